@@ -160,8 +160,10 @@ mxfp8_status mxfp8_workspace_size(int64_t B, int64_t M, int64_t N, int64_t K,
  *   step inside mxfp8_linear, mxfp8_linear_path and mxfp8_linear_noalloc
  *   (whose output only the same call's GEMM reads, after its wait), the
  *   CTA-pair GEMM when it splits K (whose partials only the same call's
- *   reduce reads, after its wait), and the small-M GEMM (whose output the
- *   next layer reads as x, after its wait).
+ *   reduce reads, after its wait), the small-M GEMM (whose output the
+ *   next layer reads as x, after its wait), and the 4-bit layer's counterparts
+ *   of these and the norm and activation calls below (whose outputs are
+ *   activations, read after the next kernel's wait).
  *   The standalone calls (mxfp8_quantize, mxfp8_quantize_packed,
  *   mxfp8_pack_scales, mxfp8_process_weights) never do, so weights they write
  *   are complete before a GEMM queued after them starts.  Kernels from other
@@ -372,6 +374,149 @@ mxfp8_status mxfp8_linear_fmt(int path, int w_format, const void* x_bf16, const 
                               const uint8_t* x_scale, int64_t B, int64_t M, int64_t N, int64_t K,
                               const uint8_t* w_packed, const uint8_t* sf_packed, const void* bias_bf16,
                               void* out_bf16, void* workspace, size_t workspace_bytes, mxfp8_stream_t stream);
+
+/*
+ * 4-bit layer: MXFP4 and NVFP4 (microscaled E2M1) quantisation and product.
+ *   No counterpart on the source pages, which stop at MXFP8 / MXFP6: the same
+ *   layer with both operands in 4 bits, for the tensor cores' 4-bit rate.
+ *   Elements are E2M1 (0, .5, 1, 1.5, 2, 3, 4, 6 and their negatives), two to
+ *   a byte, the even element in the low half: a row of K is K/2 bytes.
+ *     MXFP4: one E8M0 scale per 32 elements (OCP MX v1.0, sections 5.3.3 and
+ *       6.3): e = floor(log2 amax) - 2, scale byte e + 127, element
+ *       E2M1(x / 2^e); an Inf/NaN block gets byte 0xFF and zero codes.
+ *     NVFP4: one E4M3 scale per 16 elements and one fp32 scale g per tensor:
+ *       s = E4M3(amax / (6 g)) saturating, element = E2M1(x * (1 / (s g)))
+ *       in fp32, value = element * s * g.  A block whose s g is zero or below
+ *       what can be inverted gets zero codes, one holding Inf/NaN the scale
+ *       0x7F (NaN).  g is read on the device (float*, NULL = 1, > 0); choose
+ *       it as amax(tensor) / (448 * 6).
+ *   Elements round to nearest even and saturate to +-6.
+ *   K % 32 == 0 throughout, N % 8 == 0 for the product.
+ *   Formats of the quantising calls:
+ */
+#define MXFP8_QFMT_MXFP8 0 /* E4M3 elements, E8M0 scale per 32 */
+#define MXFP8_QFMT_MXFP4 1
+#define MXFP8_QFMT_NVFP4 2
+
+/*
+ * mxfp8_fp4_quantize - bf16 rows -> packed E2M1 codes and row-major scales.
+ *   fmt          : MXFP8_QFMT_MXFP4 or MXFP8_QFMT_NVFP4 (for every fp4 call).
+ *   x_bf16       : device, [rows, K] bf16.
+ *   tensor_scale : device, one fp32 (NVFP4), or NULL for 1; NULL for MXFP4.
+ *   x_q          : device, [rows, K/2] out.
+ *   x_scale      : device, [rows, K/32] E8M0 or [rows, K/16] E4M3 bytes out.
+ *   Pointers 16-byte aligned (tensor_scale 4).  rows = 0 is a no-op.
+ */
+mxfp8_status mxfp8_fp4_quantize(int fmt, const void* x_bf16, int64_t rows, int64_t K, const float* tensor_scale,
+                                uint8_t* x_q, uint8_t* x_scale, mxfp8_stream_t stream);
+
+/*
+ * mxfp8_fp4_quantize_packed - the same for [B, M, K], scales in the packed
+ * atoms the product reads (mxfp8_fp4_packed_sizes(fmt, B, M, K) sf bytes; an
+ * atom is 128 rows x 4 blocks as for MXFP8, so 128 elements of K for MXFP4 and
+ * 64 for NVFP4).  Bytes past a row's last block are zeroed; the padding rows
+ * of the last row tile are left as they were.
+ */
+mxfp8_status mxfp8_fp4_quantize_packed(int fmt, const void* x_bf16, int64_t B, int64_t M, int64_t K,
+                                       const float* tensor_scale, uint8_t* x_q, uint8_t* sfa_packed,
+                                       mxfp8_stream_t stream);
+
+/*
+ * mxfp8_fp4_unpack - n packed codes -> n E4M3 bytes of the same values (every
+ * E2M1 value is an E4M3 value).  An MXFP4 tensor becomes the MXFP8 tensor with
+ * the same scales, so MXFP4 weights can also be served by mxfp8_linear.
+ * n % 32 == 0; pointers 16-byte aligned.
+ */
+mxfp8_status mxfp8_fp4_unpack(const uint8_t* q, int64_t n, uint8_t* out_e4m3, mxfp8_stream_t stream);
+
+/* Bytes of the packed codes and scale atoms of B batches of [N, K]. */
+mxfp8_status mxfp8_fp4_packed_sizes(int fmt, int64_t B, int64_t N, int64_t K, size_t* w_bytes, size_t* sf_bytes);
+
+/*
+ * mxfp8_fp4_process_weights - one-time repack of 4-bit weights: the codes as
+ * they are (w_packed == w is allowed), the row-major scales [B, N, K/32] or
+ * [B, N, K/16] into packed atoms (padding zero).
+ */
+mxfp8_status mxfp8_fp4_process_weights(int fmt, const uint8_t* w, const uint8_t* w_scale, int64_t B, int64_t N,
+                                       int64_t K, uint8_t* w_packed, uint8_t* sf_packed, mxfp8_stream_t stream);
+
+/* Device workspace bytes of mxfp8_fp4_linear; with x_is_quantized it also
+ * covers mxfp8_fp4_gemm_packed. */
+mxfp8_status mxfp8_fp4_workspace_size(int fmt, int64_t B, int64_t M, int64_t N, int64_t K, int x_is_quantized,
+                                      size_t* bytes);
+
+/*
+ * mxfp8_fp4_linear - out[b, m, n] = bf16( g_x g_w sum_k x[b, m, k] w[b, n, k]
+ *                                         + bias[n] ), both operands 4-bit.
+ *   Exactly one input form: x_bf16 [B, M, K] (quantised inside the call with
+ *   x_tensor_scale), or x_q [B, M, K/2] with row-major x_scale.
+ *   w_packed, sf_packed from mxfp8_fp4_process_weights; tensor scales: device
+ *   fp32 (NVFP4) or NULL for 1, NULL for MXFP4; bias bf16 [N] or NULL;
+ *   workspace >= mxfp8_fp4_workspace_size bytes, 256-byte aligned.
+ *   fp32 accumulation; one rounding to bf16 after the tensor scales and the
+ *   bias.  Calls with few output tiles split K and add the fp32 partials in a
+ *   fixed order, so a call's result is the same every time.  Stream ordering
+ *   as mxfp8_linear: w_packed, sf_packed, bias and w_tensor_scale may be read
+ *   before the kernel ahead ends if that kernel triggers its dependents early.
+ */
+mxfp8_status mxfp8_fp4_linear(int fmt, const void* x_bf16, const uint8_t* x_q, const uint8_t* x_scale,
+                              const float* x_tensor_scale, int64_t B, int64_t M, int64_t N, int64_t K,
+                              const uint8_t* w_packed, const uint8_t* sf_packed, const float* w_tensor_scale,
+                              const void* bias_bf16, void* out_bf16, void* workspace, size_t workspace_bytes,
+                              mxfp8_stream_t stream);
+
+/*
+ * mxfp8_fp4_gemm_packed - the product alone, x already quantised with packed
+ * scales (mxfp8_fp4_quantize_packed, or the norm and activation calls below).
+ * workspace is optional: NULL, or less than mxfp8_fp4_workspace_size(...,
+ * x_is_quantized = 1) bytes, runs the call without splitting K.
+ */
+mxfp8_status mxfp8_fp4_gemm_packed(int fmt, const uint8_t* x_q, const uint8_t* sfa_packed, const float* x_tensor_scale,
+                                   int64_t B, int64_t M, int64_t N, int64_t K, const uint8_t* w_packed,
+                                   const uint8_t* sf_packed, const float* w_tensor_scale, const void* bias_bf16,
+                                   void* out_bf16, void* workspace, size_t workspace_bytes, mxfp8_stream_t stream);
+
+/*
+ * mxfp8_rmsnorm_quantize - residual addition and root-mean-square norm with
+ * the output quantised for the next layer (the QuantizedActivation input of
+ * "AiterFlyDSLMxfp8LinearKernel.apply_weights", produced by the op before it):
+ *   t = x + residual,  y = t / sqrt(mean(t^2) + eps) * weight,
+ *   (q, scale) = quantise(y),  residual_out = t.
+ *   t and y are fp32: y is rounded once, to its 8- or 4-bit elements, and t
+ *   once, to the residual's type.
+ *   fmt : MXFP8_QFMT_*.  q: [M, K] E4M3 bytes or [M, K/2] packed E2M1.
+ *   x_bf16 : device, M rows of K bf16, x_stride elements apart.
+ *   residual : device, rows of bf16 (fp32 when residual_is_f32), or NULL with
+ *     residual_out NULL: t = x.  residual_out: dense [M, K] of the same type;
+ *     it may be the residual itself when that is dense.
+ *   weight_bf16 : device, [K] (may be read before the kernel ahead ends, as a
+ *     linear layer's weights).
+ *   tensor_scale : as mxfp8_fp4_quantize (NVFP4 only).
+ *   scale : row-major [M, K/block], or with scale_packed the packed atoms of
+ *     (1, M, K), as mxfp8_quantize_packed / mxfp8_fp4_quantize_packed (bytes
+ *     past a row's last block zeroed).
+ *   y_bf16 : device, dense [M, K] bf16 out, or NULL.
+ *   A NaN in t makes every block of its row NaN, an infinity its own block
+ *   (the rest of that row becomes zero); other rows are untouched.
+ *   K % 32 == 0 and K <= 32768 (else MXFP8_ERR_UNSUPPORTED); rows start on
+ *   16-byte boundaries.
+ */
+mxfp8_status mxfp8_rmsnorm_quantize(int fmt, const void* x_bf16, int64_t x_stride, const void* residual,
+                                    int64_t residual_stride, int residual_is_f32, void* residual_out,
+                                    const void* weight_bf16, float eps, const float* tensor_scale, int64_t M, int64_t K,
+                                    uint8_t* q, uint8_t* scale, int scale_packed, void* y_bf16,
+                                    mxfp8_stream_t stream);
+
+/*
+ * mxfp8_silu_mul_quantize - the gated activation between an MLP's
+ * projections, output quantised: y = gate / (1 + exp(-gate)) * up in fp32,
+ * (q, scale) = quantise(y).  gate and up: device, M rows of K bf16 with their
+ * own strides (for a merged projection, up = gate + K and both strides 2 K).
+ * Other arguments as mxfp8_rmsnorm_quantize.
+ */
+mxfp8_status mxfp8_silu_mul_quantize(int fmt, const void* gate_bf16, int64_t gate_stride, const void* up_bf16,
+                                     int64_t up_stride, const float* tensor_scale, int64_t M, int64_t K, uint8_t* q,
+                                     uint8_t* scale, int scale_packed, mxfp8_stream_t stream);
 
 /*
  * Persistable packed weights.

@@ -6,4 +6,4 @@ this package does not load the library; the first call into :mod:`.ops` does,
 and raises if it is missing or no sm_103 GPU is present.
 """
 
-__all__ = ["ops", "synth"]
+__all__ = ["ops", "mlp", "synth"]

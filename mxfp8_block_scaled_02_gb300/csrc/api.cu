@@ -16,12 +16,27 @@
 #include <string>
 
 #include "../../include/mxfp8.h"
+#include "mx_api.h"
 #include "mx_kernels.h"
 #include "mx_layout.cuh"
 
 namespace {
 
 thread_local std::string g_last_error;
+
+struct DeviceInfo {
+  bool ok = false;
+  int sms = 0;
+  int major = 0, minor = 0;
+};
+
+constexpr int kMaxDevices = 64;
+DeviceInfo g_dev[kMaxDevices];
+std::mutex g_dev_mu;
+
+}  // namespace
+
+namespace mx {
 
 mxfp8_status fail(mxfp8_status st, const char* fmt, ...) {
   char buf[512];
@@ -37,19 +52,6 @@ mxfp8_status cuda_fail(cudaError_t e, const char* what) {
   return fail(MXFP8_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
 }
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-struct DeviceInfo {
-  bool ok = false;
-  int sms = 0;
-  int major = 0, minor = 0;
-};
-
-constexpr int kMaxDevices = 64;
-DeviceInfo g_dev[kMaxDevices];
-std::mutex g_dev_mu;
-
-// Current device, checked to be sm_103.  Returns MXFP8_OK and fills *sms.
 mxfp8_status current_device(int* sms) {
   int dev = -1;
   cudaError_t e = cudaGetDevice(&dev);
@@ -71,7 +73,27 @@ mxfp8_status current_device(int* sms) {
   return MXFP8_OK;
 }
 
-int64_t round_up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
+// Sizes are checked for range first, so the products below cannot overflow 64
+// bits.
+mxfp8_status check_block_count(int64_t B, int64_t R, int64_t K, const char* what) {
+  if (B > (1ll << 20) || R > (1ll << 31) || K > (1ll << 30) || B * R > (1ll << 31) ||
+      B * R * (K / 32) > kMaxBlocks32 || sf_packed_bytes(B, R, K) / 4 > kMaxBlocks32)
+    return fail(MXFP8_ERR_UNSUPPORTED,
+                "%s: B=%lld R=%lld K=%lld has more than 2^31 - 1 scale blocks; split the call",
+                what, (long long)B, (long long)R, (long long)K);
+  return MXFP8_OK;
+}
+
+}  // namespace mx
+
+namespace {
+
+using mx::aligned;
+using mx::check_block_count;
+using mx::cuda_fail;
+using mx::current_device;
+using mx::fail;
+using mx::round_up;
 
 constexpr int kSmallM = mx::kDecodeMaxM;  // largest M the small-M kernel takes
 
@@ -92,19 +114,6 @@ WsLayout prefill_workspace(int64_t B, int64_t M, int64_t N, int64_t K, bool quan
   w.part_bytes = splits > 1 ? round_up(static_cast<int64_t>(splits) * B * M * N * 4, 256) : 0;
   w.total = w.part_off + w.part_bytes;
   return w;
-}
-
-// The quantise and repack kernels index 32-element blocks and 4-byte packed
-// scale words with 32-bit integers: B*R*(K/32) blocks and the packed scale
-// words of (B, R, K) must each fit in 31 bits.  Sizes are checked for range
-// first, so the products below cannot overflow 64 bits.
-mxfp8_status check_block_count(int64_t B, int64_t R, int64_t K, const char* what) {
-  if (B > (1ll << 20) || R > (1ll << 31) || K > (1ll << 30) || B * R > (1ll << 31) ||
-      B * R * (K / 32) > mx::kMaxBlocks32 || mx::sf_packed_bytes(B, R, K) / 4 > mx::kMaxBlocks32)
-    return fail(MXFP8_ERR_UNSUPPORTED,
-                "%s: B=%lld R=%lld K=%lld has more than 2^31 - 1 scale blocks; split the call",
-                what, (long long)B, (long long)R, (long long)K);
-  return MXFP8_OK;
 }
 
 mxfp8_status check_weights_args(const void* w, const void* ws, int64_t B, int64_t N, int64_t K) {
@@ -601,15 +610,16 @@ mxfp8_status mxfp8_gemm_packed(const uint8_t* x_q, const uint8_t* sfa_packed, in
 mxfp8_status mxfp8_check(mxfp8_stream_t stream) {
   cudaError_t e = cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "stream synchronize");
-  unsigned int s1 = 0, s2 = 0, s3 = 0, s4 = 0, s5 = 0, s6 = 0;
+  unsigned int s1 = 0, s2 = 0, s3 = 0, s4 = 0, s5 = 0, s6 = 0, s7 = 0;
   if ((e = mx::take_status_quantize(&s1)) != cudaSuccess ||
       (e = mx::take_status_gemm(&s2)) != cudaSuccess ||
       (e = mx::take_status_decode(&s3)) != cudaSuccess ||
       (e = mx::take_status_pair(&s4)) != cudaSuccess ||
       (e = mx::take_status_fq(&s6)) != cudaSuccess ||
+      (e = mx::take_status_fp4(&s7)) != cudaSuccess ||
       (e = mx::take_status_debug(&s5)) != cudaSuccess)
     return cuda_fail(e, "status word read");
-  if ((s1 | s2 | s3 | s4 | s5 | s6) & 1u) return fail(MXFP8_ERR_TIMEOUT, "a bounded in-kernel wait ran out");
+  if ((s1 | s2 | s3 | s4 | s5 | s6 | s7) & 1u) return fail(MXFP8_ERR_TIMEOUT, "a bounded in-kernel wait ran out");
   return MXFP8_OK;
 }
 

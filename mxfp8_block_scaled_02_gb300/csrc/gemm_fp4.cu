@@ -1,0 +1,570 @@
+// gemm_fp4.cu - the 4-bit block-scaled product on CTA pairs:
+//   out[b, m, n] = bf16( g_x g_w sum_k (x sx)[b, m, k] (w sw)[b, n, k] + bias[n] )
+// with E2M1 elements and one scale per 32 (MXFP4, E8M0) or 16 (NVFP4, E4M3)
+// elements along K.  tcgen05.mma kind::mxf4 / kind::mxf4nvf4 with block scales,
+// K = 64 per instruction, fp32 accumulation in tensor memory; the result is
+// rounded once, after the tensor scales and the bias.
+//
+// A cluster of two CTAs computes one 256 x 256 output tile (cta_group::2): CTA
+// r stages rows [128 r, +128) of the activation tile and of the weight tile,
+// and receives the accumulator of its activation rows.  A stage is 128 bytes
+// (256 elements) of K per row, so one instruction reads the same bytes as an
+// 8-bit one and does twice the work; the scales are twice (MXFP4) or four
+// times (NVFP4) as many per byte, which is why they travel by TMA and
+// tcgen05.cp here: one TMA per operand fetches a stage's atoms, and one copy
+// per 512-byte atom moves them to tensor memory in the MMA issuer's own
+// instruction order (no wait between a copy and the MMAs on either side).
+//
+// Tensor memory: two accumulators of 256 columns that overlap in 64 columns
+// (0..255 and 192..447), and two scale slots of 24 columns (2 activation
+// atoms, 4 weight atoms).  The epilogue drains the shared 64 columns of a tile
+// first and releases them, so the next tile's MMAs run while the rest of the
+// tile is drained and stored.
+//
+// Warps: 0 operand TMA, 1 tensor-memory allocation and (even CTA) MMA issue,
+// 2 scale TMA, 3 idle, 4..11 epilogue.  Both CTAs' copies complete on the even
+// CTA's `full` barrier; the MMA commits free a stage in both CTAs.  Weights and
+// weight scales are loaded before griddepcontrol.wait, activations after it.
+// Every wait is bounded; the cluster barriers are reached on every path.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "mx_fp4.cuh"
+#include "mx_kernels.h"
+#include "mx_layout.cuh"
+#include "mx_ptx.cuh"
+
+namespace mx {
+
+namespace {
+
+constexpr int BM = 128;       // activation rows per CTA (256 per pair)
+constexpr int BN = 256;       // output columns per pair tile
+constexpr int BKB = 128;      // bytes of K per row and stage
+constexpr int BK = 2 * BKB;   // elements of K per stage
+constexpr int MMA_K = 64;     // elements of K per instruction
+constexpr int EPI_WARPS = 8;
+constexpr int THREADS = 128 + EPI_WARPS * 32;
+constexpr int STAGES = 5;
+constexpr int A_BYTES = BM * BKB;
+constexpr int B_BYTES = (BN / 2) * BKB;
+constexpr int OUT_BOX = 32 * 64;  // staging box: 32 rows x 64 bytes
+constexpr int ACC1 = 192;         // first column of the odd tiles' accumulator
+constexpr int T_SF = ACC1 + BN;   // scale slots
+constexpr int SLOT_COLS = 24;     // 2 activation atoms + 2 x 2 weight atoms, 4 columns each
+constexpr int TMEM_COLS = 512;
+static_assert(T_SF + 2 * SLOT_COLS <= TMEM_COLS, "tensor memory overflow");
+
+template <int FMT>
+struct Cfg {
+  // 512-byte atoms of 128 rows per stage: 128 (MXFP4) or 64 (NVFP4) elements each
+  static constexpr int ATOMS = FMT == kQNV4 ? 4 : 2;
+  static constexpr int SFA_BYTES = ATOMS * kAtomBytes;
+  static constexpr int SFB_BYTES = ATOMS * 2 * kAtomBytes;
+  static constexpr int OFF_A = 0;
+  static constexpr int OFF_B = OFF_A + STAGES * A_BYTES;
+  static constexpr int OFF_SFA = OFF_B + STAGES * B_BYTES;
+  static constexpr int OFF_SFB = OFF_SFA + STAGES * SFA_BYTES;
+  static constexpr int OFF_OUT = OFF_SFB + STAGES * SFB_BYTES;
+  static constexpr int OFF_BIAS = OFF_OUT + EPI_WARPS * 2 * OUT_BOX;
+  static constexpr int OFF_BAR = OFF_BIAS + EPI_WARPS * 4 * 32 * 2;
+  static constexpr int OFF_MISC = OFF_BAR + (2 * STAGES + 2) * 8;
+  static constexpr int SMEM = OFF_MISC + 16 + 1024;
+  static_assert(SMEM <= 232448, "shared memory overflow");
+};
+
+// Instruction descriptor of kind::mxf4 / mxf4nvf4: E2M1 A and B (type code 1
+// at bits 7 and 10), N >> 3 at bit 17, scale type at bit 23 (1 UE8M0, 0
+// UE4M3), M >> 4 at bit 24; dense K = 64.
+template <int FMT>
+__host__ __device__ constexpr uint32_t idesc_fp4(uint32_t M, uint32_t N) {
+  return (1u << 7) | (1u << 10) | ((N >> 3) << 17) | ((FMT == kQMX4 ? 1u : 0u) << 23) | ((M >> 4) << 24);
+}
+
+template <int FMT>
+__device__ __forceinline__ void mma_fp4_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
+                                             uint32_t sfb, uint32_t accumulate) {
+  if (FMT == kQMX4)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
+            d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)
+        : "memory");
+}
+
+// One scale atom of each CTA's own shared memory (same offset) into 4 columns
+// of its tensor memory, replicated over the four lane quarters.
+__device__ __forceinline__ void cp_sf_pair(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+__device__ __forceinline__ void bulk_wait_group_read1() {
+  asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+}
+
+struct Args {
+  const __nv_bfloat16* bias;
+  const float* gx;
+  const float* gw;
+  int B, M, N, K;
+  int MT, NT, KT;   // pair tiles, stages of K
+  int last_steps;   // MMA steps of the last stage
+  int units;        // tiles * splits
+  int splits;
+  int n_fast;
+};
+
+// Unit u = tile * splits + s: its tile and stages [kt_lo, kt_hi).
+__device__ __forceinline__ void unit_coords(int u, const Args& a, int& b, int& mt, int& nt, int& s, int& kt_lo,
+                                            int& kt_hi) {
+  const int tile = u / a.splits;
+  s = u - tile * a.splits;
+  const int per_b = a.MT * a.NT;
+  b = tile / per_b;
+  const int t = tile - b * per_b;
+  if (a.n_fast) {
+    mt = t / a.NT;
+    nt = t - mt * a.NT;
+  } else {
+    nt = t / a.MT;
+    mt = t - nt * a.MT;
+  }
+  kt_lo = s * a.KT / a.splits;
+  kt_hi = (s + 1) * a.KT / a.splits;
+}
+
+template <int FMT>
+__global__ void __launch_bounds__(THREADS, 1)
+    gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                    const __grid_constant__ CUtensorMap tmSFA, const __grid_constant__ CUtensorMap tmSFB,
+                    const __grid_constant__ CUtensorMap tmOut, const Args args) {
+  using C = Cfg<FMT>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  uint64_t* empty = full + STAGES;
+  uint64_t* acc_full = empty + STAGES;
+  uint64_t* acc_free = acc_full + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank() & 1u;  // clusters are (2, 1, 1)
+  const bool leader = rank == 0;
+  const int pair = blockIdx.x >> 1;
+  const int npairs = gridDim.x >> 1;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], 2);   // the even CTA's operand and scale producers (even CTA's copy is used)
+      mbar_init(&empty[s], 1);  // the even CTA's commit
+    }
+    mbar_init(acc_full, 1);
+    mbar_init(acc_free, 2 * EPI_WARPS);
+    *abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tmap(&tmA);
+    prefetch_tmap(&tmB);
+    prefetch_tmap(&tmSFA);
+    prefetch_tmap(&tmSFB);
+    prefetch_tmap(&tmOut);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_slot, TMEM_COLS);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // both CTAs' barriers exist before anyone arrives remotely
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  if (args.splits > 1 && threadIdx.x == 0) launch_dependents();  // this call's reduce waits for this grid itself
+
+  if (warp == 0 || warp == 2) {
+    // ------------------------------------------------------------ producers: operands (0), scales (2)
+    if (lane == 0) {
+      const bool op = warp == 0;
+      const uint32_t tx = op ? 2 * (A_BYTES + B_BYTES) : 2 * (C::SFA_BYTES + C::SFB_BYTES);
+      auto load_w = [&](int st, uint32_t bar, int kt, int nt, int b) {
+        if (op)
+          tma_load_3d_cluster_bar(smem + C::OFF_B + st * B_BYTES, &tmB, bar, kt * BKB,
+                                  nt * BN + static_cast<int>(rank) * (BN / 2), b);
+        else
+          tma_load_3d_cluster_bar(smem + C::OFF_SFB + st * C::SFB_BYTES, &tmSFB, bar, nt * 2 * (kAtomBytes / 4),
+                                  kt * C::ATOMS, b);
+      };
+      auto load_x = [&](int st, uint32_t bar, int kt, int mt, int b) {
+        const int rt = mt * 2 + static_cast<int>(rank);
+        if (op)
+          tma_load_3d_cluster_bar(smem + C::OFF_A + st * A_BYTES, &tmA, bar, kt * BKB, rt * BM, b);
+        else
+          tma_load_3d_cluster_bar(smem + C::OFF_SFA + st * C::SFA_BYTES, &tmSFA, bar, rt * (kAtomBytes / 4),
+                                  kt * C::ATOMS, b);
+      };
+      // First ring round: the weights, then (after the kernel before this one
+      // in the stream) the activations, its output.
+      int P0 = 0;
+      for (int pass = 0; pass < 2; ++pass) {
+        P0 = 0;
+        for (int u = pair; u < args.units && P0 < STAGES; u += npairs) {
+          int b, mt, nt, sp, kt, kt_hi;
+          unit_coords(u, args, b, mt, nt, sp, kt, kt_hi);
+          for (; kt < kt_hi && P0 < STAGES; ++kt, ++P0) {
+            const uint32_t bar = map_shared_rank(smem_u32(&full[P0]), 0);
+            if (pass == 0) {
+              if (leader) mbar_arrive_expect_tx(&full[P0], tx);
+              load_w(P0, bar, kt, nt, b);
+            } else {
+              load_x(P0, bar, kt, mt, b);
+            }
+          }
+        }
+        if (pass == 0) grid_dependency_wait();
+      }
+      int stage = 0;
+      uint32_t phase = 0;
+      int64_t issued = 0;
+      bool ok = true;
+      for (int u = pair; ok && u < args.units; u += npairs) {
+        int b, mt, nt, sp, kt, kt_hi;
+        unit_coords(u, args, b, mt, nt, sp, kt, kt_hi);
+        for (; kt < kt_hi; ++kt) {
+          if (issued >= P0) {
+            if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag)) {
+              ok = false;
+              break;
+            }
+            // The odd CTA's bytes may land before the even CTA posts the
+            // count, but not a phase early: the stage was freed by a commit
+            // behind the MMA that waited for the barrier's previous phase.
+            const uint32_t bar = map_shared_rank(smem_u32(&full[stage]), 0);
+            if (leader) mbar_arrive_expect_tx(&full[stage], tx);
+            load_x(stage, bar, kt, mt, b);
+            load_w(stage, bar, kt, nt, b);
+          }
+          ++issued;
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      // Before exit: every commit to this CTA's empty barriers has arrived; a
+      // stage's last commit follows the MMA that waited for its copies.
+      for (int s = 0; s < STAGES; ++s) {
+        if (issued <= s) continue;
+        const int64_t last = ((issued - 1 - s) / STAGES) * STAGES + s;
+        mbar_wait(&empty[s], static_cast<uint32_t>((last / STAGES) & 1), nullptr);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer (even CTA)
+    if (leader && lane == 0) {
+      constexpr uint32_t idesc = idesc_fp4<FMT>(2 * BM, BN);
+      int stage = 0, tile_no = 0;
+      uint32_t phase = 0, slot = 0;
+      bool ok = true;
+      for (int u = pair; ok && u < args.units; u += npairs, ++tile_no) {
+        const int sp = u % args.splits;
+        const int kt_lo = sp * args.KT / args.splits, kt_hi = (sp + 1) * args.KT / args.splits;
+        const uint32_t acc = tmem + ((tile_no & 1) ? ACC1 : 0);
+        // the columns shared with the previous tile's accumulator are drained
+        if (tile_no > 0 && !mbar_wait(acc_free, static_cast<uint32_t>((tile_no - 1) & 1), abort_flag)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        for (int kt = kt_lo; kt < kt_hi; ++kt) {
+          if (!mbar_wait(&full[stage], phase, abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t ad = sdesc_kmajor_sw128(smem_u32(smem + C::OFF_A + stage * A_BYTES));
+          const uint64_t bd = sdesc_kmajor_sw128(smem_u32(smem + C::OFF_B + stage * B_BYTES));
+          const uint32_t sa = smem_u32(smem + C::OFF_SFA + stage * C::SFA_BYTES);
+          const uint32_t sb = smem_u32(smem + C::OFF_SFB + stage * C::SFB_BYTES);
+          const int steps = kt == args.KT - 1 ? args.last_steps : BK / MMA_K;
+#pragma unroll
+          for (int h = 0; h < C::ATOMS / 2; ++h) {
+            // a slot: two activation atoms and their two pairs of weight atoms
+            const uint32_t t = tmem + T_SF + slot * SLOT_COLS;
+            constexpr int kStepsPerSlot = (BK / MMA_K) / (C::ATOMS / 2);
+            if (h * kStepsPerSlot < steps) {
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                cp_sf_pair(t + 4 * j, sdesc_sf(sa + (2 * h + j) * kAtomBytes));
+                cp_sf_pair(t + 8 + 8 * j, sdesc_sf(sb + (2 * h + j) * 2 * kAtomBytes));
+                cp_sf_pair(t + 12 + 8 * j, sdesc_sf(sb + ((2 * h + j) * 2 + 1) * kAtomBytes));
+              }
+#pragma unroll
+              for (int i = 0; i < kStepsPerSlot; ++i) {
+                const int kk = h * kStepsPerSlot + i;
+                if (kk >= steps) break;
+                // MXFP4: two steps share an atom (scale bytes 0-1 and 2-3)
+                const int j = FMT == kQNV4 ? i : i >> 1;
+                const uint32_t id = FMT == kQNV4 ? 0u : static_cast<uint32_t>(i & 1) * 2u;
+                mma_fp4_pair<FMT>(acc, ad + 2 * kk, bd + 2 * kk, idesc_with_sf_id(idesc, id, id), t + 4 * j,
+                                  t + 8 + 8 * j, ((kt - kt_lo) | kk) != 0);
+              }
+              slot ^= 1u;
+            }
+          }
+          tc_commit_pair_multicast(&empty[stage], 0x3);
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        tc_commit_pair_multicast(acc_full, 0x3);
+      }
+      if (!ok) __nanosleep(200000);  // let issued tensor-core work retire
+    }
+    __syncwarp();
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------ epilogue
+    // Warp e drains lanes 32 (warp % 4).. of the column groups {h, h + 2, h + 4,
+    // h + 6} of 32, h = e / 4: of the 64 shared columns each warp holds one
+    // group (the last two groups of an even tile, the first two of an odd one)
+    // and drains it first.
+    const int ew = warp - 4;
+    const int quad = warp & 3;
+    const int half = ew >> 2;
+    uint8_t* box = smem + C::OFF_OUT + ew * 2 * OUT_BOX;
+    __nv_bfloat16* bias_s = reinterpret_cast<__nv_bfloat16*>(smem + C::OFF_BIAS) + ew * 128;
+    const uint32_t acc_free_even = map_shared_rank(smem_u32(acc_free), 0);
+    grid_dependency_wait();  // g_x may be the previous kernel's output
+    float alpha = 1.f;
+    if (args.gx != nullptr) alpha = *args.gx;
+    if (args.gw != nullptr) alpha *= *args.gw;
+    int nbox = 0, tile_no = 0;
+    for (int u = pair; u < args.units; u += npairs, ++tile_no) {
+      int b, mt, nt, sp, kt_lo, kt_hi;
+      unit_coords(u, args, b, mt, nt, sp, kt_lo, kt_hi);
+      const int row0 = (mt * 2 + static_cast<int>(rank)) * BM + quad * 32;
+      const bool partial = args.splits > 1;
+      if (!partial && args.bias != nullptr) {
+        // this warp's 4 x 32 bias values (zero past N)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int n = nt * BN + (2 * c + half) * 32 + lane;
+          bias_s[c * 32 + lane] = n < args.N ? args.bias[n] : __float2bfloat16(0.f);
+        }
+        __syncwarp();
+      }
+      if (!mbar_wait(acc_full, static_cast<uint32_t>(tile_no & 1), abort_flag)) break;
+      tc_fence_after();
+      const uint32_t acc = tmem + (static_cast<uint32_t>(quad * 32) << 16) + ((tile_no & 1) ? ACC1 : 0);
+#pragma unroll 1
+      for (int i = 0; i < 4; ++i) {
+        const int c = (tile_no & 1) ? i : 3 - i;
+        const int col = (2 * c + half) * 32;
+        uint32_t r[32];
+        tmem_ld_32x32b_x32(acc + col, r);
+        tmem_ld_wait();
+        if (i == 0) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_remote(acc_free_even);
+        }
+        if (partial) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint8_t* dst = box + (nbox & 1) * OUT_BOX;
+            if (lane == 0 && nbox >= 2) bulk_wait_group_read1();
+            __syncwarp();
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const int e = 16 * h + 4 * q;
+              *reinterpret_cast<float4*>(dst + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)) =
+                  make_float4(__uint_as_float(r[e]) * alpha, __uint_as_float(r[e + 1]) * alpha,
+                              __uint_as_float(r[e + 2]) * alpha, __uint_as_float(r[e + 3]) * alpha);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_3d(&tmOut, dst, nt * BN + col + 16 * h, row0, sp * args.B + b);
+              bulk_commit_group();
+            }
+            ++nbox;
+          }
+          continue;
+        }
+        uint32_t packed[16];
+        if (args.bias != nullptr) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const uint32_t bw = reinterpret_cast<const uint32_t*>(bias_s + c * 32)[j];
+            packed[j] = pack_bf16x2(fmaf(__uint_as_float(r[2 * j]), alpha, __uint_as_float(bw << 16)),
+                                    fmaf(__uint_as_float(r[2 * j + 1]), alpha, __uint_as_float(bw & 0xFFFF0000u)));
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            packed[j] = pack_bf16x2(__uint_as_float(r[2 * j]) * alpha, __uint_as_float(r[2 * j + 1]) * alpha);
+        }
+        uint8_t* dst = box + (nbox & 1) * OUT_BOX;
+        if (lane == 0 && nbox >= 2) bulk_wait_group_read1();
+        __syncwarp();
+        // 64-byte swizzle: 16-byte chunk q of row r sits at q ^ ((r / 2) % 4),
+        // so the eight lanes of a store phase touch different banks
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *reinterpret_cast<uint4*>(dst + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)) =
+              make_uint4(packed[4 * q], packed[4 * q + 1], packed[4 * q + 2], packed[4 * q + 3]);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_3d(&tmOut, dst, nt * BN + col, row0, b);
+          bulk_commit_group();
+        }
+        ++nbox;
+      }
+    }
+    if (lane == 0) bulk_wait_group0();
+    __syncwarp();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // no CTA of the pair leaves while the other may still signal it
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, TMEM_COLS);
+  }
+}
+
+// A 3-D map: innermost extent in elements of `dtype`, the two strides in bytes.
+bool encode3(CUtensorMap* m, CUtensorMapDataType dtype, const void* base, int64_t d0, int64_t d1, int64_t d2,
+             int64_t s1, int64_t s2, int b0, int b1, CUtensorMapSwizzle sw, CUtensorMapL2promotion l2) {
+  EncodeTiledFn encode = encode_tiled_fn();
+  if (encode == nullptr) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d0), static_cast<cuuint64_t>(d1), static_cast<cuuint64_t>(d2)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(s1), static_cast<cuuint64_t>(s2)};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(b0), static_cast<cuuint32_t>(b1), 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return encode(m, dtype, 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw, l2,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int FMT>
+cudaError_t launch_t(const Fp4Problem& p, int sms, cudaStream_t stream, const char** msg) {
+  using C = Cfg<FMT>;
+  static bool attr_set[64] = {};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev >= 0 && dev < 64 && !attr_set[dev]) {
+    cudaError_t e = cudaFuncSetAttribute(gemm_fp4_kernel<FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) {
+      *msg = "cudaFuncSetAttribute(max dynamic shared memory) failed";
+      return e;
+    }
+    attr_set[dev] = true;
+  }
+  const int splits = p.part != nullptr && p.splits > 1 ? p.splits : 1;
+  const int64_t RTA = ceil_div(p.M, kAtomRows), RTB = ceil_div(p.N, kAtomRows);
+  const int64_t KA = ceil_div(fp4_scale_extent(FMT, p.K), kTileK);  // scale atoms along K
+  const int64_t kb = p.K / 2;
+  CUtensorMap ma, mb, msa, msb, mo;
+  const auto u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  const auto u32 = CU_TENSOR_MAP_DATA_TYPE_UINT32;
+  const int words = kAtomBytes / 4;
+  bool ok = encode3(&ma, u8, p.x, kb, p.M, p.B, kb, p.M * kb, BKB, BM, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B) &&
+            encode3(&mb, u8, p.w, kb, p.N, p.B, kb, p.N * kb, BKB, BN / 2, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B) &&
+            encode3(&msa, u32, p.sfx, RTA * words, KA, p.B, RTA * kAtomBytes, KA * RTA * kAtomBytes, words, C::ATOMS,
+                    CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B) &&
+            encode3(&msb, u32, p.sfw, RTB * words, KA, p.B, RTB * kAtomBytes, KA * RTB * kAtomBytes, 2 * words,
+                    C::ATOMS, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+  if (splits > 1)
+    ok = ok && encode3(&mo, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, p.part, p.N, p.M, splits * p.B, p.N * 4, p.M * p.N * 4, 16,
+                       32, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE);
+  else
+    ok = ok && encode3(&mo, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.out, p.N, p.M, p.B, p.N * 2, p.M * p.N * 2, 32, 32,
+                       CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE);
+  if (!ok) {
+    *msg = "cuTensorMapEncodeTiled rejected a 4-bit operand or output";
+    return cudaErrorInvalidValue;
+  }
+  Args a;
+  a.bias = splits > 1 ? nullptr : static_cast<const __nv_bfloat16*>(p.bias);
+  a.gx = p.gx;
+  a.gw = p.gw;
+  a.B = static_cast<int>(p.B);
+  a.M = static_cast<int>(p.M);
+  a.N = static_cast<int>(p.N);
+  a.K = static_cast<int>(p.K);
+  a.MT = static_cast<int>(ceil_div(p.M, 2 * BM));
+  a.NT = static_cast<int>(ceil_div(p.N, BN));
+  a.KT = static_cast<int>(ceil_div(p.K, BK));
+  a.last_steps = static_cast<int>(ceil_div(p.K - static_cast<int64_t>(a.KT - 1) * BK, MMA_K));
+  a.splits = splits;
+  a.units = a.B * a.MT * a.NT * splits;
+  // the operand with fewer bytes is swept fastest, so that it stays in L2
+  a.n_fast = p.M >= p.N ? 1 : 0;
+  const int pairs = a.units < sms / 2 ? a.units : sms / 2;
+
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs), 1, 1);
+  cfg.blockDim = dim3(THREADS, 1, 1);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, gemm_fp4_kernel<FMT>, ma, mb, msa, msb, mo, a);
+  if (e != cudaSuccess) {
+    *msg = "4-bit GEMM launch failed";
+    return e;
+  }
+  if (splits > 1) {
+    e = launch_splitk_reduce(p.part, splits, p.B, p.M, p.N, p.bias, p.out, nullptr, nullptr, sms, stream);
+    if (e != cudaSuccess) *msg = "split-K reduce launch failed";
+  }
+  return e;
+}
+
+}  // namespace
+
+// Few output tiles: split K so that about 64 pairs have work, with at least
+// four stages a split and at most 8 splits.  A function of the shape alone.
+int fp4_splitk_splits(int64_t B, int64_t M, int64_t N, int64_t K) {
+  const int64_t tiles = B * ceil_div(M, 2 * BM) * ceil_div(N, BN);
+  const int64_t kt = ceil_div(K, BK);
+  if (tiles <= 0 || tiles > (kt >= 32 ? 32 : 16)) return 1;
+  int64_t s = 64 / tiles;
+  if (s > kt / 4) s = kt / 4;
+  if (s > 8) s = 8;
+  return s >= 2 ? static_cast<int>(s) : 1;
+}
+
+cudaError_t launch_gemm_fp4(const Fp4Problem& p, int sms, cudaStream_t stream, const char** msg) {
+  return p.fmt == kQNV4 ? launch_t<kQNV4>(p, sms, stream, msg) : launch_t<kQMX4>(p, sms, stream, msg);
+}
+
+cudaError_t take_status_fp4(unsigned int* out) {
+  unsigned int zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(out, g_status, sizeof(unsigned int));
+  if (e != cudaSuccess) return e;
+  return cudaMemcpyToSymbol(g_status, &zero, sizeof(unsigned int));
+}
+
+}  // namespace mx

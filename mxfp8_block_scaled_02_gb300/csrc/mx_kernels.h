@@ -126,6 +126,72 @@ int decode_k_splits(int64_t M, int64_t N, int64_t K, int sms);
 cudaError_t launch_gemm_decode(const DecodeProblem& p, int sms, cudaStream_t stream, const char** msg);
 cudaError_t take_status_decode(unsigned int* out);
 
+// fp4_quant.cu: bf16 [B, M, K] -> packed E2M1 codes [B, M, K/2] and scales
+// (fmt kQMX4 / kQNV4 of mx_fp4.cuh), row-major or in packed atoms; g is NVFP4's
+// tensor scale (device, nullptr = 1).  early_trigger as launch_quantize.
+cudaError_t launch_quantize_fp4(int fmt, const void* x, int64_t B, int64_t M, int64_t K, const float* g, uint8_t* q,
+                                uint8_t* s, bool packed_scales, int sms, cudaStream_t stream, bool early_trigger);
+// n packed codes (n % 32 == 0) -> n E4M3 bytes of the same values.
+cudaError_t launch_fp4_unpack(const uint8_t* q, int64_t n, uint8_t* out, int sms, cudaStream_t stream);
+
+// fused_quant.cu: residual addition + RMS norm, and silu(gate) * up, with the
+// output quantised (fmt: MXFP8, MXFP4 or NVFP4 of mx_fp4.cuh).  Strides are in
+// elements; K % 32 == 0; the norm holds a row in one CTA (K <= kNormMaxK).
+constexpr int64_t kNormMaxK = 32768;
+struct NormProblem {
+  int fmt;
+  const void* x;  // bf16 rows
+  int64_t x_stride;
+  const void* res;  // bf16 (fp32 when res_f32) rows, or nullptr
+  int64_t res_stride;
+  bool res_f32;
+  void* res_out;  // dense [M, K] of the residual's type (with res)
+  const void* w;  // bf16 [K]
+  void* y;        // bf16 [M, K], or nullptr
+  float eps;
+  const float* g;
+  int64_t M, K;
+  uint8_t* q;
+  uint8_t* s;
+  bool packed;  // scales in packed atoms, else row-major
+};
+cudaError_t launch_rmsnorm_quantize(const NormProblem& p, int sms, cudaStream_t stream);
+struct ActProblem {
+  int fmt;
+  const void* gate;  // bf16 rows
+  int64_t gate_stride;
+  const void* up;
+  int64_t up_stride;
+  const float* g;
+  int64_t M, K;
+  uint8_t* q;
+  uint8_t* s;
+  bool packed;
+};
+cudaError_t launch_silu_mul_quantize(const ActProblem& p, int sms, cudaStream_t stream);
+
+// gemm_fp4.cu: the 4-bit block-scaled product on CTA pairs.  x / w: packed E2M1
+// codes [B, M, K/2] / [B, N, K/2]; sfx / sfw: packed scale atoms; gx / gw:
+// NVFP4 tensor scales (device, nullptr = 1); bias bf16 [N] or nullptr; out bf16
+// [B, M, N].  part (splits > 1): fp32 [splits * B][M][N].
+struct Fp4Problem {
+  int fmt;
+  const uint8_t* x;
+  const uint8_t* w;
+  const uint8_t* sfx;
+  const uint8_t* sfw;
+  const float* gx;
+  const float* gw;
+  const void* bias;
+  void* out;
+  int64_t B, M, N, K;
+  float* part = nullptr;
+  int splits = 1;
+};
+int fp4_splitk_splits(int64_t B, int64_t M, int64_t N, int64_t K);
+cudaError_t launch_gemm_fp4(const Fp4Problem& p, int sms, cudaStream_t stream, const char** msg);
+cudaError_t take_status_fp4(unsigned int* out);
+
 // debug.cu
 cudaError_t launch_expire_wait(uint64_t timeout_ns, cudaStream_t stream);
 cudaError_t take_status_debug(unsigned int* out);

@@ -61,6 +61,19 @@ SIGNATURES = {
     "mxfp8_process_weights_fmt": (_INT, [_INT, _P, _P, _I64, _I64, _I64, _P, _P, _P]),
     "mxfp8_linear_fmt": (_INT, [_INT, _INT, _P, _P, _P, _I64, _I64, _I64, _I64, _P, _P, _P, _P, _P,
                                 ctypes.c_size_t, _P]),
+    "mxfp8_fp4_quantize": (_INT, [_INT, _P, _I64, _I64, _P, _P, _P, _P]),
+    "mxfp8_fp4_quantize_packed": (_INT, [_INT, _P, _I64, _I64, _I64, _P, _P, _P, _P]),
+    "mxfp8_fp4_unpack": (_INT, [_P, _I64, _P, _P]),
+    "mxfp8_fp4_packed_sizes": (_INT, [_INT, _I64, _I64, _I64, _SIZE_P, _SIZE_P]),
+    "mxfp8_fp4_process_weights": (_INT, [_INT, _P, _P, _I64, _I64, _I64, _P, _P, _P]),
+    "mxfp8_fp4_workspace_size": (_INT, [_INT, _I64, _I64, _I64, _I64, _INT, _SIZE_P]),
+    "mxfp8_fp4_linear": (_INT, [_INT, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _P, _P, _P, _P, _P, _P,
+                                ctypes.c_size_t, _P]),
+    "mxfp8_fp4_gemm_packed": (_INT, [_INT, _P, _P, _P, _I64, _I64, _I64, _I64, _P, _P, _P, _P, _P, _P,
+                                     ctypes.c_size_t, _P]),
+    "mxfp8_rmsnorm_quantize": (_INT, [_INT, _P, _I64, _P, _I64, _INT, _P, _P, ctypes.c_float, _P, _I64, _I64,
+                                      _P, _P, _INT, _P, _P]),
+    "mxfp8_silu_mul_quantize": (_INT, [_INT, _P, _I64, _P, _I64, _P, _I64, _I64, _P, _P, _INT, _P]),
     "mxfp8_check": (_INT, [_P]),
     "mxfp8_debug_expire_wait": (_INT, [_U64, _P]),
 }
@@ -69,6 +82,11 @@ _lib = None
 
 # weight element formats (MXFP8_WFMT_*): E4M3 (MXFP8) and the MXFP6 E2M3 / E3M2
 WFMT = {"e4m3": 0, "e2m3": 1, "e3m2": 2}
+
+# formats of the quantising calls (MXFP8_QFMT_*) and their block lengths; the
+# 4-bit ones are also weight formats of linear_fp4
+QFMT = {"mxfp8": 0, "mxfp4": 1, "nvfp4": 2}
+QBLOCK = {"mxfp8": 32, "mxfp4": 32, "nvfp4": 16}
 
 
 class MxStatusError(RuntimeError):
@@ -165,15 +183,16 @@ def quantize_weights(w: torch.Tensor, fmt: str = "e4m3") -> tuple[torch.Tensor, 
 
 @dataclasses.dataclass
 class PackedWeights:
-    """Weights after the one-time repack: E4M3 bytes and scale atoms."""
+    """Weights after the one-time repack: element bytes and scale atoms."""
 
-    w_packed: torch.Tensor   # uint8, B*N*K bytes (3BNK/4 for packed FP6)
+    w_packed: torch.Tensor   # uint8, B*N*K bytes (3BNK/4 for packed FP6, BNK/2 for FP4)
     sf_packed: torch.Tensor  # uint8, packed scale atoms
     B: int
     N: int
     K: int
     batched: bool
-    fmt: str = "e4m3"        # weight element format: "e4m3", "e2m3" or "e3m2"
+    fmt: str = "e4m3"        # weight element format: "e4m3", "e2m3", "e3m2", or "mxfp4" / "nvfp4"
+    tensor_scale: torch.Tensor | None = None  # NVFP4: fp32, one element
 
 
 def process_weights(w_q: torch.Tensor, w_scale: torch.Tensor, fmt: str = "e4m3") -> PackedWeights:
@@ -208,10 +227,16 @@ def process_weights(w_q: torch.Tensor, w_scale: torch.Tensor, fmt: str = "e4m3")
     return PackedWeights(wp, sp, B, N, K, batched, fmt)
 
 
+def _not_fp4(pw: PackedWeights, what: str) -> None:
+    if pw.fmt not in WFMT:
+        raise ValueError(f"{what} does not take {pw.fmt} weights; use linear_fp4 / gemm_packed_fp4")
+
+
 def save_packed(pw: PackedWeights) -> bytes:
     """The packed weights as one self-describing blob (mxfp8_weights_serialize):
     a versioned, checksummed header, then the w_packed and sf_packed bytes.
     Write it to a file once; load_packed restores it without repacking."""
+    _not_fp4(pw, "save_packed")
     w = np.ascontiguousarray(pw.w_packed.detach().cpu().numpy())
     sf = np.ascontiguousarray(pw.sf_packed.detach().cpu().numpy())
     n = ctypes.c_size_t()
@@ -243,6 +268,7 @@ def load_packed(blob: bytes | bytearray | memoryview, device: torch.device | str
 
 
 def unpack_scales(pw: PackedWeights) -> torch.Tensor:
+    _not_fp4(pw, "unpack_scales")
     out = torch.empty((pw.B, pw.N, pw.K // BLOCK), dtype=torch.uint8, device=pw.sf_packed.device)
     _check(load().mxfp8_unpack_scales(_ptr(pw.sf_packed), pw.B, pw.N, pw.K, _ptr(out), _stream()))
     return out if pw.batched else out[0]
@@ -259,6 +285,7 @@ def _linear_rows(x: torch.Tensor, pw: PackedWeights, bias: torch.Tensor | None,
     """Check x (and x_scale, bias, out) against the packed weights; returns M,
     the rows per batch.  Shared by every linear entry point, so that none of
     them hands the library a buffer shorter than the sizes it is told."""
+    _not_fp4(pw, "this call")
     quantized = x_scale is not None
     if not quantized and x.dtype != torch.bfloat16:
         raise TypeError("x must be bfloat16 (or pass x_scale with a pre-quantised x)")
@@ -318,20 +345,28 @@ def linear(x: torch.Tensor, pw: PackedWeights, bias: torch.Tensor | None = None,
     return out
 
 
+def _mxfp8_only(pa: PackedActivation, what: str) -> None:
+    if pa.fmt != "mxfp8":
+        raise ValueError(f"{what} takes MXFP8 activations only (these are {pa.fmt}); use gemm_packed_fp4")
+
+
 def _e4m3_only(pw: PackedWeights, what: str) -> None:
     if pw.fmt != "e4m3":
-        raise ValueError(f"{what} takes E4M3 weights only (these are {pw.fmt}); use linear")
+        raise ValueError(f"{what} takes E4M3 weights only (these are {pw.fmt}); use "
+                         f"{'linear' if pw.fmt in WFMT else 'linear_fp4'}")
 
 
 @dataclasses.dataclass
 class PackedActivation:
     """Activations quantised straight into the GEMM's operand layout."""
 
-    x_q: torch.Tensor        # uint8 [B, M, K]
+    x_q: torch.Tensor        # uint8 [B, M, K] ([B, M, K/2] in the 4-bit formats)
     sf_packed: torch.Tensor  # uint8 packed scale atoms
     B: int
     M: int
     K: int
+    fmt: str = "mxfp8"       # "mxfp8", or "mxfp4" / "nvfp4" (gemm_packed_fp4)
+    tensor_scale: torch.Tensor | None = None  # NVFP4: fp32, one element
 
 
 def quantize_packed(x: torch.Tensor, B: int = 1, *, x_q: torch.Tensor | None = None,
@@ -366,6 +401,7 @@ def gemm_packed(pa: PackedActivation, pw: PackedWeights, bias: torch.Tensor | No
                 out: torch.Tensor | None = None) -> torch.Tensor:
     """The block-scaled GEMM + bias epilogue alone; returns bf16 [B, M, N]."""
     _e4m3_only(pw, "gemm_packed")
+    _mxfp8_only(pa, "gemm_packed")
     if pa.K != pw.K or pa.B != pw.B:
         raise ValueError("activation and weights disagree on K or B")
     _require_cuda(bias, out)
@@ -417,6 +453,7 @@ def gemm_packed_quantized_out(pa: PackedActivation, pw: PackedWeights, bias: tor
     """gemm_packed whose output is also handed on quantised
     (mxfp8_gemm_packed_quantized_out): the middle layer of a chain."""
     _e4m3_only(pw, "gemm_packed_quantized_out")
+    _mxfp8_only(pa, "gemm_packed_quantized_out")
     if pa.K != pw.K or pa.B != pw.B:
         raise ValueError("activation and weights disagree on K or B")
     _require_cuda(bias)
@@ -452,6 +489,315 @@ def linear_noalloc(x: torch.Tensor, pw: PackedWeights, bias: torch.Tensor | None
     _check(load().mxfp8_linear_noalloc(_ptr(x), pw.B, M, pw.N, K, _ptr(pw.w_packed),
                                        _ptr(pw.sf_packed), _ptr(bias), _ptr(out), _stream()))
     return out
+
+
+# ------------------------------------------------------------------ 4-bit layer (MXFP4, NVFP4)
+def _fmt4(fmt: str) -> int:
+    if fmt not in ("mxfp4", "nvfp4"):
+        raise ValueError(f"fmt must be 'mxfp4' or 'nvfp4', not {fmt!r}")
+    return QFMT[fmt]
+
+
+def _check_tensor_scale(fmt: str, g: torch.Tensor | None) -> None:
+    if g is None:
+        return
+    if fmt != "nvfp4":
+        raise ValueError(f"a tensor scale belongs to nvfp4, not {fmt}")
+    if g.dtype != torch.float32 or g.numel() != 1 or not g.is_cuda:
+        raise ValueError("the tensor scale must be one fp32 value on the CUDA device")
+
+
+def _rows_of(x: torch.Tensor, K: int) -> int:
+    return x.numel() // K if K else 0
+
+
+def quantize_fp4(x: torch.Tensor, fmt: str = "mxfp4", *,
+                 tensor_scale: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor]:
+    """bf16 x [..., K] -> (x_q uint8 [..., K/2], two E2M1 codes a byte, the even
+    element in the low half; x_scale uint8: "mxfp4" E8M0 [..., K/32], "nvfp4"
+    E4M3 [..., K/16]).  ``tensor_scale``: nvfp4's fp32 scale of the whole tensor
+    (one element on the device; None is 1), normally amax / (448 * 6)."""
+    f = _fmt4(fmt)
+    if x.dtype != torch.bfloat16:
+        raise TypeError("x must be bfloat16")
+    _require_cuda(x)
+    _check_tensor_scale(fmt, tensor_scale)
+    x = _aligned16(x)
+    K = x.shape[-1]
+    q = torch.empty((*x.shape[:-1], K // 2), dtype=torch.uint8, device=x.device)
+    s = torch.empty((*x.shape[:-1], K // QBLOCK[fmt]), dtype=torch.uint8, device=x.device)
+    _check(load().mxfp8_fp4_quantize(f, _ptr(x), _rows_of(x, K), K, _ptr(tensor_scale), _ptr(q), _ptr(s), _stream()))
+    return q, s
+
+
+def unpack_fp4(x_q: torch.Tensor) -> torch.Tensor:
+    """Packed E2M1 codes [..., K/2] -> the same values as float8_e4m3fn [..., K]
+    (with the same scales an MXFP4 tensor is then an MXFP8 one)."""
+    if x_q.dtype != torch.uint8:
+        raise TypeError("codes must be uint8")
+    _require_cuda(x_q)
+    x_q = _aligned16(x_q)
+    out = torch.empty((*x_q.shape[:-1], 2 * x_q.shape[-1]), dtype=torch.uint8, device=x_q.device)
+    _check(load().mxfp8_fp4_unpack(_ptr(x_q), out.numel(), _ptr(out), _stream()))
+    return out.view(torch.float8_e4m3fn)
+
+
+def packed_sizes_fp4(B: int, N: int, K: int, fmt: str) -> tuple[int, int]:
+    wb, sb = ctypes.c_size_t(), ctypes.c_size_t()
+    _check(load().mxfp8_fp4_packed_sizes(_fmt4(fmt), B, N, K, ctypes.byref(wb), ctypes.byref(sb)))
+    return wb.value, sb.value
+
+
+def process_weights_fp4(w_q: torch.Tensor, w_scale: torch.Tensor, fmt: str = "mxfp4", *,
+                        tensor_scale: torch.Tensor | None = None) -> PackedWeights:
+    """w_q uint8 [N, K/2] or [B, N, K/2], w_scale uint8 (or the scale's float8
+    type) [..., K/32] ("mxfp4") or [..., K/16] ("nvfp4"), and nvfp4's fp32
+    ``tensor_scale`` -> weights for linear_fp4.  Padded scales are sliced as in
+    process_weights."""
+    f = _fmt4(fmt)
+    if w_q.dim() not in (2, 3) or w_q.dtype != torch.uint8:
+        raise ValueError("w_q must be uint8 [N, K/2] or [B, N, K/2]")
+    batched = w_q.dim() == 3
+    B, N, K = (w_q.shape[0] if batched else 1), w_q.shape[-2], 2 * w_q.shape[-1]
+    if K % BLOCK:
+        raise ValueError(f"K={K} is not a multiple of {BLOCK}")
+    KB = K // QBLOCK[fmt]
+    if (w_scale.dim() != w_q.dim() or w_scale.element_size() != 1
+            or tuple(w_scale.shape[:-2]) != tuple(w_q.shape[:-2])
+            or w_scale.shape[-2] < N or w_scale.shape[-1] < KB):
+        raise ValueError(f"weight scale {tuple(w_scale.shape)} does not match weight {tuple(w_q.shape)}")
+    _check_tensor_scale(fmt, tensor_scale)
+    w_scale = _bytes(w_scale)[..., :N, :KB].contiguous()
+    _require_cuda(w_q, w_scale)
+    w_q, w_scale = _aligned16(w_q), _aligned16(w_scale)
+    wb, sb = packed_sizes_fp4(B, N, K, fmt)
+    wp = torch.empty(wb, dtype=torch.uint8, device=w_q.device)
+    sp = torch.empty(sb, dtype=torch.uint8, device=w_q.device)
+    _check(load().mxfp8_fp4_process_weights(f, _ptr(w_q), _ptr(w_scale), B, N, K, _ptr(wp), _ptr(sp), _stream()))
+    return PackedWeights(wp, sp, B, N, K, batched, fmt, tensor_scale)
+
+
+def workspace_size_fp4(B: int, M: int, N: int, K: int, quantized: bool, fmt: str) -> int:
+    n = ctypes.c_size_t()
+    _check(load().mxfp8_fp4_workspace_size(_fmt4(fmt), B, M, N, K, int(quantized), ctypes.byref(n)))
+    return n.value
+
+
+def _product_args(pw: PackedWeights, bias: torch.Tensor | None, out: torch.Tensor | None, rows: int) -> None:
+    if bias is not None and (bias.dtype != torch.bfloat16 or tuple(bias.shape) != (pw.N,)):
+        raise ValueError("bias must be bf16 [N]")
+    if out is not None and (out.dtype != torch.bfloat16 or out.numel() != rows * pw.N):
+        raise ValueError(f"out must be bf16 with {rows * pw.N} elements")
+
+
+def linear_fp4(x: torch.Tensor, pw: PackedWeights, bias: torch.Tensor | None = None,
+               x_scale: torch.Tensor | None = None, *, tensor_scale: torch.Tensor | None = None,
+               out: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Linear layer with both operands in 4 bits (weights from
+    process_weights_fp4).  ``x`` is bf16 [..., K] (quantised inside the call to
+    the weights' format), or with ``x_scale`` the codes uint8 [..., K/2] of
+    quantize_fp4; ``tensor_scale`` is nvfp4's scale of x either way.  For batched
+    weights x is [B, M, ...].  Returns bf16 [..., N]."""
+    fmt, quantized = pw.fmt, x_scale is not None
+    f = _fmt4(fmt)
+    _require_cuda(x, x_scale, bias, out, workspace)
+    _check_tensor_scale(fmt, tensor_scale)
+    if x.dtype != (torch.uint8 if quantized else torch.bfloat16):
+        raise TypeError("x must be bfloat16, or uint8 codes with x_scale")
+    KX = pw.K // 2 if quantized else pw.K
+    if x.dim() < 1 or x.shape[-1] != KX:
+        raise ValueError(f"x {tuple(x.shape)} does not match weights with K={pw.K}")
+    if pw.batched and (x.dim() != 3 or x.shape[0] != pw.B):
+        raise ValueError("batched weights need x of shape [B, M, K]")
+    if quantized and (x_scale.element_size() != 1
+                      or tuple(x_scale.shape) != (*x.shape[:-1], pw.K // QBLOCK[fmt])):
+        raise ValueError(f"{fmt} activation scale {tuple(x_scale.shape)} for codes {tuple(x.shape)}")
+    rows = _rows_of(x, KX)
+    _product_args(pw, bias, out, rows)
+    x, x_scale, bias = _aligned16(x), _aligned16(x_scale), _aligned16(bias)
+    if out is None:
+        out = torch.empty((*x.shape[:-1], pw.N), dtype=torch.bfloat16, device=x.device)
+    if rows == 0:
+        return out
+    M = rows // pw.B
+    if workspace is None:
+        workspace = torch.empty(workspace_size_fp4(pw.B, M, pw.N, pw.K, quantized, fmt), dtype=torch.uint8,
+                                device=x.device)
+    _check(load().mxfp8_fp4_linear(f, None if quantized else _ptr(x), _ptr(x) if quantized else None, _ptr(x_scale),
+                                   _ptr(tensor_scale), pw.B, M, pw.N, pw.K, _ptr(pw.w_packed), _ptr(pw.sf_packed),
+                                   _ptr(pw.tensor_scale), _ptr(bias), _ptr(out), _ptr(workspace),
+                                   workspace.numel() * workspace.element_size(), _stream()))
+    return out
+
+
+def quantize_packed_fp4(x: torch.Tensor, B: int = 1, fmt: str = "mxfp4", *,
+                        tensor_scale: torch.Tensor | None = None) -> PackedActivation:
+    """bf16 x ([M, K], or [B, M, K] with B given) -> codes and packed scales for gemm_packed_fp4."""
+    f = _fmt4(fmt)
+    if x.dtype != torch.bfloat16:
+        raise TypeError("x must be bfloat16")
+    _require_cuda(x)
+    _check_tensor_scale(fmt, tensor_scale)
+    x = _aligned16(x)
+    K = x.shape[-1]
+    rows = _rows_of(x, K)
+    if B < 1 or rows % B:
+        raise ValueError(f"x {tuple(x.shape)} does not split into B={B} batches")
+    pa = _packed_activation(B, rows // B, K, fmt, tensor_scale, x.device)
+    _check(load().mxfp8_fp4_quantize_packed(f, _ptr(x), B, pa.M, K, _ptr(tensor_scale), _ptr(pa.x_q),
+                                            _ptr(pa.sf_packed), _stream()))
+    return pa
+
+
+def _packed_activation(B: int, M: int, K: int, fmt: str, tensor_scale: torch.Tensor | None,
+                       device) -> PackedActivation:
+    sb = packed_sizes(B, max(M, 1), K)[1] if fmt == "mxfp8" else packed_sizes_fp4(B, max(M, 1), K, fmt)[1]
+    return PackedActivation(torch.empty((B, M, K if fmt == "mxfp8" else K // 2), dtype=torch.uint8, device=device),
+                            torch.empty(sb, dtype=torch.uint8, device=device), B, M, K, fmt, tensor_scale)
+
+
+def gemm_packed_fp4(pa: PackedActivation, pw: PackedWeights, bias: torch.Tensor | None = None,
+                    out: torch.Tensor | None = None, *, workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """The 4-bit product alone (x quantised by quantize_packed_fp4,
+    rmsnorm_quantize or silu_mul_quantize with packed scales); bf16 [B, M, N].
+    ``workspace`` (workspace_size_fp4 bytes with quantized=True) is allocated
+    when the call splits K and none is given."""
+    f = _fmt4(pw.fmt)
+    if pa.fmt != pw.fmt or pa.K != pw.K or pa.B != pw.B:
+        raise ValueError("activation and weights disagree on format, K or B")
+    _require_cuda(bias, out, workspace)
+    _product_args(pw, bias, out, pa.B * pa.M)
+    bias = _aligned16(bias)
+    if out is None:
+        out = torch.empty((pa.B, pa.M, pw.N), dtype=torch.bfloat16, device=pa.x_q.device)
+    if pa.M == 0:
+        return out
+    if workspace is None:
+        workspace = torch.empty(workspace_size_fp4(pa.B, pa.M, pw.N, pa.K, True, pw.fmt), dtype=torch.uint8,
+                                device=pa.x_q.device)
+    _check(load().mxfp8_fp4_gemm_packed(f, _ptr(pa.x_q), _ptr(pa.sf_packed), _ptr(pa.tensor_scale), pa.B, pa.M, pw.N,
+                                        pa.K, _ptr(pw.w_packed), _ptr(pw.sf_packed), _ptr(pw.tensor_scale),
+                                        _ptr(bias), _ptr(out), _ptr(workspace),
+                                        workspace.numel() * workspace.element_size(), _stream()))
+    return out
+
+
+# ------------------------------------------------------------------ steps that feed a quantised layer
+def _rows2d(x: torch.Tensor, name: str) -> tuple[torch.Tensor, int, int]:
+    """x [..., K] as rows: (tensor, row count, row stride in elements).  A view
+    whose rows are evenly spaced (a slice of a wider tensor) is taken as it is
+    when its rows start on 16-byte boundaries; anything else is copied."""
+    if not x.is_cuda:
+        raise ValueError("tensors must be on a CUDA device")
+    if x.dim() < 1 or x.shape[-1] == 0 or x.shape[-1] % BLOCK:
+        raise ValueError(f"{name} must be [..., K] with K a multiple of {BLOCK}, not {tuple(x.shape)}")
+    K = x.shape[-1]
+    rows = x.numel() // K
+    if x.is_contiguous():
+        return _aligned16(x), rows, K
+    stride, step = 0, 1  # of the merged leading axes
+    for size, st in zip(reversed(x.shape[:-1]), reversed(x.stride()[:-1])):
+        if size == 1:
+            continue
+        if step == 1:
+            stride = st
+        elif st != stride * step:
+            step = -1
+            break
+        step *= size
+    if (step < 0 or x.stride(-1) != 1 or x.data_ptr() % 16 or stride * x.element_size() % 16
+            or (rows > 1 and stride < K)):
+        return x.contiguous(), rows, K
+    return x, rows, stride
+
+
+def _quantized_out(x: torch.Tensor, rows: int, K: int, fmt: str, tensor_scale: torch.Tensor | None, packed: bool):
+    """Output tensors of a fused quantising step: (what the caller gets, codes, scales)."""
+    if packed:
+        pa = _packed_activation(1, rows, K, fmt, tensor_scale, x.device)
+        return pa, pa.x_q, pa.sf_packed
+    q = torch.empty((*x.shape[:-1], K if fmt == "mxfp8" else K // 2), dtype=torch.uint8, device=x.device)
+    s = torch.empty((*x.shape[:-1], K // QBLOCK[fmt]), dtype=torch.uint8, device=x.device)
+    return (q, s), q, s
+
+
+def _qfmt(fmt: str) -> int:
+    if fmt not in QFMT:
+        raise ValueError(f"fmt must be one of {sorted(QFMT)}, not {fmt!r}")
+    return QFMT[fmt]
+
+
+def rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None, *,
+                     eps: float = 1e-6, fmt: str = "mxfp8", tensor_scale: torch.Tensor | None = None,
+                     packed: bool = False, residual_out: torch.Tensor | None = None,
+                     y: torch.Tensor | None = None):
+    """Residual addition and RMS norm, output quantised for the next layer:
+    t = x + residual, y = t / sqrt(mean(t^2) + eps) * weight (fp32 throughout).
+
+    x bf16 [..., K], weight bf16 [K], residual bf16 or fp32 like x (or None).
+    Returns (quantised y, t rounded to the residual's type or None).  The
+    quantised y is (codes, row-major scales) as quantize / quantize_fp4 return
+    them, or with ``packed`` a PackedActivation of one batch for gemm_packed /
+    gemm_packed_fp4.  ``residual_out`` (dense; may be a dense ``residual``
+    itself) receives t; ``y`` (dense bf16) receives the norm unquantised too."""
+    f = _qfmt(fmt)
+    if x.dtype != torch.bfloat16 or weight.dtype != torch.bfloat16:
+        raise TypeError("x and weight must be bfloat16")
+    _check_tensor_scale(fmt, tensor_scale)
+    _require_cuda(weight, residual_out, y)
+    xr, rows, x_stride = _rows2d(x, "x")
+    K = x.shape[-1]
+    if tuple(weight.shape) != (K,):
+        raise ValueError(f"weight must be [{K}], not {tuple(weight.shape)}")
+    r_stride, rr = 0, None
+    if residual is not None:
+        if residual.dtype not in (torch.bfloat16, torch.float32) or residual.shape != x.shape:
+            raise ValueError("residual must be bf16 or fp32 with x's shape")
+        rr, _, r_stride = _rows2d(residual, "residual")
+        if residual_out is None:
+            residual_out = torch.empty(x.shape, dtype=residual.dtype, device=x.device)
+        elif residual_out.dtype != residual.dtype or residual_out.shape != x.shape:
+            raise ValueError("residual_out must have the residual's type and shape")
+    elif residual_out is not None:
+        raise ValueError("residual_out needs a residual")
+    if y is not None and (y.dtype != torch.bfloat16 or y.shape != x.shape):
+        raise ValueError("y must be bf16 with x's shape")
+    weight = _aligned16(weight)
+    res, q, s = _quantized_out(x, rows, K, fmt, tensor_scale, packed)
+    _check(load().mxfp8_rmsnorm_quantize(f, _ptr(xr), x_stride, _ptr(rr), r_stride,
+                                         int(residual is not None and residual.dtype == torch.float32),
+                                         _ptr(residual_out), _ptr(weight), eps, _ptr(tensor_scale), rows, K,
+                                         _ptr(q), _ptr(s), int(packed), _ptr(y), _stream()))
+    return res, residual_out
+
+
+def silu_mul_quantize(gate_up: torch.Tensor, up: torch.Tensor | None = None, *, fmt: str = "mxfp8",
+                      tensor_scale: torch.Tensor | None = None, packed: bool = False):
+    """silu(gate) * up with the output quantised for the next layer.
+
+    ``gate_up`` bf16 [..., 2 K] holds gate then up along the last axis (a merged
+    projection's output); or pass gate [..., K] and ``up`` [..., K].  Returns
+    the quantised result as rmsnorm_quantize does."""
+    f = _qfmt(fmt)
+    if up is None:
+        if gate_up.dim() < 1 or gate_up.shape[-1] % 2:
+            raise ValueError("gate_up must be [..., 2 K]")
+        half = gate_up.shape[-1] // 2
+        gate, up = gate_up[..., :half], gate_up[..., half:]
+    else:
+        gate = gate_up
+        if up.shape != gate.shape:
+            raise ValueError("gate and up must have the same shape")
+    if gate.dtype != torch.bfloat16 or up.dtype != torch.bfloat16:
+        raise TypeError("gate and up must be bfloat16")
+    _check_tensor_scale(fmt, tensor_scale)
+    gr, rows, g_stride = _rows2d(gate, "gate")
+    ur, _, u_stride = _rows2d(up, "up")
+    K = gate.shape[-1]
+    res, q, s = _quantized_out(gate, rows, K, fmt, tensor_scale, packed)
+    _check(load().mxfp8_silu_mul_quantize(f, _ptr(gr), g_stride, _ptr(ur), u_stride, _ptr(tensor_scale), rows, K,
+                                          _ptr(q), _ptr(s), int(packed), _stream()))
+    return res
 
 
 def check() -> None:

@@ -9,3 +9,5 @@ from .mx_oracle import (BLOCK, block_exponent, dequantize, e4m3_encode, e4m3_val
                         e8m0_value, linear, linear_bf16, quantize, scale_bytes)
 from .mx_oracle import (FP6_FORMATS, fp6_emax, fp6_encode, fp6_max, fp6_value,  # noqa: F401,E402
                         quantize_fp6)
+from .fp4_oracle import (dequantize4, e2m1_encode, e2m1_value, pack, quantize4,  # noqa: F401,E402
+                         quantize_any, rmsnorm, silu_mul, unpack)
