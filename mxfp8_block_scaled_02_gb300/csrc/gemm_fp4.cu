@@ -45,16 +45,13 @@ constexpr int BKB = 128;      // bytes of K per row and stage
 constexpr int BK = 2 * BKB;   // elements of K per stage
 constexpr int MMA_K = 64;     // elements of K per instruction
 constexpr int EPI_WARPS = 8;
-constexpr int THREADS = 128 + EPI_WARPS * 32;
+constexpr int SF_WARPS = 4;
+constexpr int THREADS = 128 + SF_WARPS * 32 + EPI_WARPS * 32;
 constexpr int STAGES = 5;
 constexpr int A_BYTES = BM * BKB;
 constexpr int B_BYTES = (BN / 2) * BKB;
 constexpr int OUT_BOX = 32 * 64;  // staging box: 32 rows x 64 bytes
-constexpr int ACC1 = 192;         // first column of the odd tiles' accumulator
-constexpr int T_SF = ACC1 + BN;   // scale slots
-constexpr int SLOT_COLS = 24;     // 2 activation atoms + 2 x 2 weight atoms, 4 columns each
 constexpr int TMEM_COLS = 512;
-static_assert(T_SF + 2 * SLOT_COLS <= TMEM_COLS, "tensor memory overflow");
 
 template <int FMT>
 struct Cfg {
@@ -62,6 +59,16 @@ struct Cfg {
   static constexpr int ATOMS = FMT == kQNV4 ? 4 : 2;
   static constexpr int SFA_BYTES = ATOMS * kAtomBytes;
   static constexpr int SFB_BYTES = ATOMS * 2 * kAtomBytes;
+  // tensor memory: scale slots of ATOMS activation and 2 ATOMS weight atoms, 4
+  // columns each, above the two overlapping accumulators
+  static constexpr int SLOTS = FMT == kQNV4 ? 3 : STAGES;
+  static constexpr int SLOT_COLS = ATOMS * 12;
+  static constexpr int ACC1 = FMT == kQNV4 ? 96 : 128;  // first column of the odd tiles' accumulator
+  static constexpr int T_SF = ACC1 + BN;
+  static_assert(T_SF + SLOTS * SLOT_COLS <= TMEM_COLS, "tensor memory overflow");
+  static_assert(SLOTS <= STAGES, "a slot is freed by a stage's commit");
+  // drain steps (64 columns of the tile each) that cover the shared columns
+  static constexpr int RELEASE = (BN - ACC1 + 63) / 64;
   static constexpr int OFF_A = 0;
   static constexpr int OFF_B = OFF_A + STAGES * A_BYTES;
   static constexpr int OFF_SFA = OFF_B + STAGES * B_BYTES;
@@ -69,7 +76,7 @@ struct Cfg {
   static constexpr int OFF_OUT = OFF_SFB + STAGES * SFB_BYTES;
   static constexpr int OFF_BIAS = OFF_OUT + EPI_WARPS * 2 * OUT_BOX;
   static constexpr int OFF_BAR = OFF_BIAS + EPI_WARPS * 4 * 32 * 2;
-  static constexpr int OFF_MISC = OFF_BAR + (2 * STAGES + 2) * 8;
+  static constexpr int OFF_MISC = OFF_BAR + (4 * STAGES + 2) * 8;
   static constexpr int SMEM = OFF_MISC + 16 + 1024;
   static_assert(SMEM <= 232448, "shared memory overflow");
 };
@@ -98,12 +105,6 @@ __device__ __forceinline__ void mma_fp4_pair(uint32_t d, uint64_t a, uint64_t b,
             d),
         "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)
         : "memory");
-}
-
-// One scale atom of each CTA's own shared memory (same offset) into 4 columns
-// of its tensor memory, replicated over the four lane quarters.
-__device__ __forceinline__ void cp_sf_pair(uint32_t taddr, uint64_t desc) {
-  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
 
 __device__ __forceinline__ void bulk_wait_group_read1() {
@@ -151,7 +152,9 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   uint64_t* empty = full + STAGES;
-  uint64_t* acc_full = empty + STAGES;
+  uint64_t* sf_full = empty + STAGES;
+  uint64_t* sf_ready = sf_full + STAGES;
+  uint64_t* acc_full = sf_ready + STAGES;
   uint64_t* acc_free = acc_full + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
@@ -165,8 +168,10 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(&full[s], 2);   // the even CTA's operand and scale producers (even CTA's copy is used)
-      mbar_init(&empty[s], 1);  // the even CTA's commit
+      mbar_init(&full[s], 1);     // operands of both CTAs (even CTA's copy is used)
+      mbar_init(&empty[s], 1);    // the even CTA's commit
+      mbar_init(&sf_full[s], 1);  // this CTA's scales in shared memory
+      mbar_init(&sf_ready[s], 2 * SF_WARPS);  // both CTAs' scales in tensor memory (even CTA's copy)
     }
     mbar_init(acc_full, 1);
     mbar_init(acc_free, 2 * EPI_WARPS);
@@ -192,23 +197,31 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (warp == 0 || warp == 2) {
     // ------------------------------------------------------------ producers: operands (0), scales (2)
     if (lane == 0) {
+      // Operands of both CTAs complete on the even CTA's `full`, which alone
+      // posts the count; the scales on this CTA's own sf_full.
       const bool op = warp == 0;
-      const uint32_t tx = op ? 2 * (A_BYTES + B_BYTES) : 2 * (C::SFA_BYTES + C::SFB_BYTES);
-      auto load_w = [&](int st, uint32_t bar, int kt, int nt, int b) {
-        if (op)
-          tma_load_3d_cluster_bar(smem + C::OFF_B + st * B_BYTES, &tmB, bar, kt * BKB,
-                                  nt * BN + static_cast<int>(rank) * (BN / 2), b);
-        else
-          tma_load_3d_cluster_bar(smem + C::OFF_SFB + st * C::SFB_BYTES, &tmSFB, bar, nt * 2 * (kAtomBytes / 4),
-                                  kt * C::ATOMS, b);
+      auto expect = [&](int st) {
+        if (!op)
+          mbar_arrive_expect_tx(&sf_full[st], C::SFA_BYTES + C::SFB_BYTES);
+        else if (leader)
+          mbar_arrive_expect_tx(&full[st], 2 * (A_BYTES + B_BYTES));
       };
-      auto load_x = [&](int st, uint32_t bar, int kt, int mt, int b) {
+      auto load_w = [&](int st, int kt, int nt, int b) {
+        if (op)
+          tma_load_3d_cluster_bar(smem + C::OFF_B + st * B_BYTES, &tmB, map_shared_rank(smem_u32(&full[st]), 0),
+                                  kt * BKB, nt * BN + static_cast<int>(rank) * (BN / 2), b);
+        else
+          tma_load_3d(smem + C::OFF_SFB + st * C::SFB_BYTES, &tmSFB, &sf_full[st], nt * 2 * (kAtomBytes / 4),
+                      kt * C::ATOMS, b);
+      };
+      auto load_x = [&](int st, int kt, int mt, int b) {
         const int rt = mt * 2 + static_cast<int>(rank);
         if (op)
-          tma_load_3d_cluster_bar(smem + C::OFF_A + st * A_BYTES, &tmA, bar, kt * BKB, rt * BM, b);
+          tma_load_3d_cluster_bar(smem + C::OFF_A + st * A_BYTES, &tmA, map_shared_rank(smem_u32(&full[st]), 0),
+                                  kt * BKB, rt * BM, b);
         else
-          tma_load_3d_cluster_bar(smem + C::OFF_SFA + st * C::SFA_BYTES, &tmSFA, bar, rt * (kAtomBytes / 4),
-                                  kt * C::ATOMS, b);
+          tma_load_3d(smem + C::OFF_SFA + st * C::SFA_BYTES, &tmSFA, &sf_full[st], rt * (kAtomBytes / 4),
+                      kt * C::ATOMS, b);
       };
       // First ring round: the weights, then (after the kernel before this one
       // in the stream) the activations, its output.
@@ -219,12 +232,11 @@ __global__ void __launch_bounds__(THREADS, 1)
           int b, mt, nt, sp, kt, kt_hi;
           unit_coords(u, args, b, mt, nt, sp, kt, kt_hi);
           for (; kt < kt_hi && P0 < STAGES; ++kt, ++P0) {
-            const uint32_t bar = map_shared_rank(smem_u32(&full[P0]), 0);
             if (pass == 0) {
-              if (leader) mbar_arrive_expect_tx(&full[P0], tx);
-              load_w(P0, bar, kt, nt, b);
+              expect(P0);
+              load_w(P0, kt, nt, b);
             } else {
-              load_x(P0, bar, kt, mt, b);
+              load_x(P0, kt, mt, b);
             }
           }
         }
@@ -246,10 +258,9 @@ __global__ void __launch_bounds__(THREADS, 1)
             // The odd CTA's bytes may land before the even CTA posts the
             // count, but not a phase early: the stage was freed by a commit
             // behind the MMA that waited for the barrier's previous phase.
-            const uint32_t bar = map_shared_rank(smem_u32(&full[stage]), 0);
-            if (leader) mbar_arrive_expect_tx(&full[stage], tx);
-            load_x(stage, bar, kt, mt, b);
-            load_w(stage, bar, kt, nt, b);
+            expect(stage);
+            load_x(stage, kt, mt, b);
+            load_w(stage, kt, nt, b);
           }
           ++issued;
           if (++stage == STAGES) {
@@ -271,13 +282,13 @@ __global__ void __launch_bounds__(THREADS, 1)
     // ------------------------------------------------------------ MMA issuer (even CTA)
     if (leader && lane == 0) {
       constexpr uint32_t idesc = idesc_fp4<FMT>(2 * BM, BN);
-      int stage = 0, tile_no = 0;
-      uint32_t phase = 0, slot = 0;
+      int stage = 0, tile_no = 0, slot = 0;
+      uint32_t phase = 0;
       bool ok = true;
       for (int u = pair; ok && u < args.units; u += npairs, ++tile_no) {
         const int sp = u % args.splits;
         const int kt_lo = sp * args.KT / args.splits, kt_hi = (sp + 1) * args.KT / args.splits;
-        const uint32_t acc = tmem + ((tile_no & 1) ? ACC1 : 0);
+        const uint32_t acc = tmem + ((tile_no & 1) ? C::ACC1 : 0);
         // the columns shared with the previous tile's accumulator are drained
         if (tile_no > 0 && !mbar_wait(acc_free, static_cast<uint32_t>((tile_no - 1) & 1), abort_flag)) {
           ok = false;
@@ -285,41 +296,28 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         tc_fence_after();
         for (int kt = kt_lo; kt < kt_hi; ++kt) {
-          if (!mbar_wait(&full[stage], phase, abort_flag)) {
+          // operands landed (the even CTA's scale writers waited for them) and
+          // both CTAs' scales in tensor memory
+          if (!mbar_wait(&sf_ready[stage], phase, abort_flag)) {
             ok = false;
             break;
           }
           tc_fence_after();
           const uint64_t ad = sdesc_kmajor_sw128(smem_u32(smem + C::OFF_A + stage * A_BYTES));
           const uint64_t bd = sdesc_kmajor_sw128(smem_u32(smem + C::OFF_B + stage * B_BYTES));
-          const uint32_t sa = smem_u32(smem + C::OFF_SFA + stage * C::SFA_BYTES);
-          const uint32_t sb = smem_u32(smem + C::OFF_SFB + stage * C::SFB_BYTES);
           const int steps = kt == args.KT - 1 ? args.last_steps : BK / MMA_K;
+          const uint32_t t_sfa = tmem + C::T_SF + slot * C::SLOT_COLS;
+          const uint32_t t_sfb = t_sfa + 4 * C::ATOMS;
 #pragma unroll
-          for (int h = 0; h < C::ATOMS / 2; ++h) {
-            // a slot: two activation atoms and their two pairs of weight atoms
-            const uint32_t t = tmem + T_SF + slot * SLOT_COLS;
-            constexpr int kStepsPerSlot = (BK / MMA_K) / (C::ATOMS / 2);
-            if (h * kStepsPerSlot < steps) {
-#pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                cp_sf_pair(t + 4 * j, sdesc_sf(sa + (2 * h + j) * kAtomBytes));
-                cp_sf_pair(t + 8 + 8 * j, sdesc_sf(sb + (2 * h + j) * 2 * kAtomBytes));
-                cp_sf_pair(t + 12 + 8 * j, sdesc_sf(sb + ((2 * h + j) * 2 + 1) * kAtomBytes));
-              }
-#pragma unroll
-              for (int i = 0; i < kStepsPerSlot; ++i) {
-                const int kk = h * kStepsPerSlot + i;
-                if (kk >= steps) break;
-                // MXFP4: two steps share an atom (scale bytes 0-1 and 2-3)
-                const int j = FMT == kQNV4 ? i : i >> 1;
-                const uint32_t id = FMT == kQNV4 ? 0u : static_cast<uint32_t>(i & 1) * 2u;
-                mma_fp4_pair<FMT>(acc, ad + 2 * kk, bd + 2 * kk, idesc_with_sf_id(idesc, id, id), t + 4 * j,
-                                  t + 8 + 8 * j, ((kt - kt_lo) | kk) != 0);
-              }
-              slot ^= 1u;
-            }
+          for (int kk = 0; kk < BK / MMA_K; ++kk) {
+            if (kk >= steps) break;
+            // MXFP4: two steps share an atom (scale bytes 0-1 and 2-3)
+            const int j = FMT == kQNV4 ? kk : kk >> 1;
+            const uint32_t id = FMT == kQNV4 ? 0u : static_cast<uint32_t>(kk & 1) * 2u;
+            mma_fp4_pair<FMT>(acc, ad + 2 * kk, bd + 2 * kk, idesc_with_sf_id(idesc, id, id), t_sfa + 4 * j,
+                              t_sfb + 8 * j, ((kt - kt_lo) | kk) != 0);
           }
+          if (++slot == C::SLOTS) slot = 0;
           tc_commit_pair_multicast(&empty[stage], 0x3);
           if (++stage == STAGES) {
             stage = 0;
@@ -332,13 +330,66 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (!ok) __nanosleep(200000);  // let issued tensor-core work retire
     }
     __syncwarp();
-  } else if (warp >= 4) {
+  } else if (warp >= 4 && warp < 4 + SF_WARPS) {
+    // ------------------------------------------------------------ scale writers
+    // Each warp writes its 32 lanes of every atom: line l of an atom (rows l,
+    // l + 32, l + 64, l + 96) goes to lane l of each quarter.
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + C::T_SF;
+    const uint32_t ready_even = map_shared_rank(smem_u32(sf_ready), 0);
+    int64_t total = 0;
+    for (int u = pair; u < args.units; u += npairs) {
+      const int sp = u % args.splits;
+      total += (sp + 1) * args.KT / args.splits - sp * args.KT / args.splits;
+    }
+    int stage = 0, slot = 0, fstage = 0;
+    uint32_t phase = 0, fphase = 0;
+    for (int64_t i = 0; i < total; ++i) {
+      if (!mbar_wait(&sf_full[stage], phase, abort_flag)) break;
+      // the MMAs that read this slot last, SLOTS stages ago, are done (with as
+      // many slots as stages, the stage's refill has waited for them already)
+      if (C::SLOTS < STAGES && i >= C::SLOTS) {
+        if (!mbar_wait(&empty[fstage], fphase, abort_flag)) break;
+        if (++fstage == STAGES) {
+          fstage = 0;
+          fphase ^= 1u;
+        }
+      }
+      tc_fence_after();
+      const uint4* sa = reinterpret_cast<const uint4*>(smem + C::OFF_SFA + stage * C::SFA_BYTES) + lane;
+      const uint4* sb = reinterpret_cast<const uint4*>(smem + C::OFF_SFB + stage * C::SFB_BYTES) + lane;
+      const uint32_t t = lane_base + slot * C::SLOT_COLS;
+#pragma unroll
+      for (int j = 0; j < C::ATOMS; ++j) {
+        const uint4 v = sa[j * 32];
+        tmem_st_32x32b_x4(t + 4 * j, v.x, v.y, v.z, v.w);
+      }
+#pragma unroll
+      for (int j = 0; j < 2 * C::ATOMS; ++j) {
+        const uint4 v = sb[j * 32];
+        tmem_st_32x32b_x4(t + 4 * C::ATOMS + 4 * j, v.x, v.y, v.z, v.w);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (!leader)
+          mbar_arrive_remote(ready_even + static_cast<uint32_t>(stage * 8));
+        else if (mbar_wait(&full[stage], phase, abort_flag))
+          mbar_arrive(&sf_ready[stage]);
+      }
+      if (++slot == C::SLOTS) slot = 0;
+      if (++stage == STAGES) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    }
+  } else if (warp >= 4 + SF_WARPS) {
     // ------------------------------------------------------------ epilogue
     // Warp e drains lanes 32 (warp % 4).. of the column groups {h, h + 2, h + 4,
     // h + 6} of 32, h = e / 4: of the 64 shared columns each warp holds one
     // group (the last two groups of an even tile, the first two of an odd one)
     // and drains it first.
-    const int ew = warp - 4;
+    const int ew = warp - 4 - SF_WARPS;
     const int quad = warp & 3;
     const int half = ew >> 2;
     uint8_t* box = smem + C::OFF_OUT + ew * 2 * OUT_BOX;
@@ -365,7 +416,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       if (!mbar_wait(acc_full, static_cast<uint32_t>(tile_no & 1), abort_flag)) break;
       tc_fence_after();
-      const uint32_t acc = tmem + (static_cast<uint32_t>(quad * 32) << 16) + ((tile_no & 1) ? ACC1 : 0);
+      const uint32_t acc = tmem + (static_cast<uint32_t>(quad * 32) << 16) + ((tile_no & 1) ? C::ACC1 : 0);
 #pragma unroll 1
       for (int i = 0; i < 4; ++i) {
         const int c = (tile_no & 1) ? i : 3 - i;
@@ -373,7 +424,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         uint32_t r[32];
         tmem_ld_32x32b_x32(acc + col, r);
         tmem_ld_wait();
-        if (i == 0) {
+        if (i == C::RELEASE - 1) {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_remote(acc_free_even);
