@@ -89,22 +89,36 @@ __host__ __device__ constexpr uint32_t idesc_fp4(uint32_t M, uint32_t N) {
   return (1u << 7) | (1u << 10) | ((N >> 3) << 17) | ((FMT == kQMX4 ? 1u : 0u) << 23) | ((M >> 4) << 24);
 }
 
+// Issued by the lane whose `elected` is set, as a predicated instruction in code
+// the whole warp runs: its operands then live in uniform registers (issued from
+// a one-lane branch, each instruction costs ~115 cycles of moves, close to the
+// 128 the tensor cores take for it).
 template <int FMT>
-__device__ __forceinline__ void mma_fp4_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
-                                             uint32_t sfb, uint32_t accumulate) {
+__device__ __forceinline__ void mma_fp4_pair(uint32_t elected, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                             uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
   if (FMT == kQMX4)
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %7, 0;\n\t"
+        "@q tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
+            d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb), "r"(elected)
         : "memory");
   else
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
-            d),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %7, 0;\n\t"
+        "@q tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%5], [%6], "
+        "p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb), "r"(elected)
         : "memory");
+}
+
+__device__ __forceinline__ void commit_pair_elected(uint32_t elected, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+      "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(
+          smem_u32(bar)),
+      "h"(static_cast<uint16_t>(0x3)), "r"(elected)
+      : "memory");
 }
 
 __device__ __forceinline__ void bulk_wait_group_read1() {
@@ -159,7 +173,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
 
-  const int warp = threadIdx.x >> 5;
+  const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0);  // uniform
   const int lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank() & 1u;  // clusters are (2, 1, 1)
   const bool leader = rank == 0;
@@ -191,7 +205,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   __syncthreads();
   cluster_sync();  // both CTAs' barriers exist before anyone arrives remotely
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
   if (args.splits > 1 && threadIdx.x == 0) launch_dependents();  // this call's reduce waits for this grid itself
 
   if (warp == 0 || warp == 2) {
@@ -280,8 +294,11 @@ __global__ void __launch_bounds__(THREADS, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (even CTA)
-    if (leader && lane == 0) {
+    if (leader) {
       constexpr uint32_t idesc = idesc_fp4<FMT>(2 * BM, BN);
+      const uint32_t elected = elect_one();
+      const uint64_t ad0 = sdesc_kmajor_sw128(smem_u32(smem + C::OFF_A));
+      const uint64_t bd0 = sdesc_kmajor_sw128(smem_u32(smem + C::OFF_B));
       int stage = 0, tile_no = 0, slot = 0;
       uint32_t phase = 0;
       bool ok = true;
@@ -290,7 +307,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int kt_lo = sp * args.KT / args.splits, kt_hi = (sp + 1) * args.KT / args.splits;
         const uint32_t acc = tmem + ((tile_no & 1) ? C::ACC1 : 0);
         // the columns shared with the previous tile's accumulator are drained
-        if (tile_no > 0 && !mbar_wait(acc_free, static_cast<uint32_t>((tile_no - 1) & 1), abort_flag)) {
+        if (tile_no > 0 && !mbar_wait_warp(acc_free, static_cast<uint32_t>((tile_no - 1) & 1), abort_flag)) {
           ok = false;
           break;
         }
@@ -298,34 +315,33 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int kt = kt_lo; kt < kt_hi; ++kt) {
           // operands landed (the even CTA's scale writers waited for them) and
           // both CTAs' scales in tensor memory
-          if (!mbar_wait(&sf_ready[stage], phase, abort_flag)) {
+          if (!mbar_wait_warp(&sf_ready[stage], phase, abort_flag)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint64_t ad = sdesc_kmajor_sw128(smem_u32(smem + C::OFF_A + stage * A_BYTES));
-          const uint64_t bd = sdesc_kmajor_sw128(smem_u32(smem + C::OFF_B + stage * B_BYTES));
+          const uint64_t ad = ad0 + static_cast<uint32_t>(stage * (A_BYTES >> 4));
+          const uint64_t bd = bd0 + static_cast<uint32_t>(stage * (B_BYTES >> 4));
           const int steps = kt == args.KT - 1 ? args.last_steps : BK / MMA_K;
           const uint32_t t_sfa = tmem + C::T_SF + slot * C::SLOT_COLS;
           const uint32_t t_sfb = t_sfa + 4 * C::ATOMS;
 #pragma unroll
           for (int kk = 0; kk < BK / MMA_K; ++kk) {
-            if (kk >= steps) break;
             // MXFP4: two steps share an atom (scale bytes 0-1 and 2-3)
             const int j = FMT == kQNV4 ? kk : kk >> 1;
             const uint32_t id = FMT == kQNV4 ? 0u : static_cast<uint32_t>(kk & 1) * 2u;
-            mma_fp4_pair<FMT>(acc, ad + 2 * kk, bd + 2 * kk, idesc_with_sf_id(idesc, id, id), t_sfa + 4 * j,
-                              t_sfb + 8 * j, ((kt - kt_lo) | kk) != 0);
+            mma_fp4_pair<FMT>(kk < steps ? elected : 0u, acc, ad + 2 * kk, bd + 2 * kk,
+                              idesc_with_sf_id(idesc, id, id), t_sfa + 4 * j, t_sfb + 8 * j, ((kt - kt_lo) | kk) != 0);
           }
+          commit_pair_elected(elected, &empty[stage]);
           if (++slot == C::SLOTS) slot = 0;
-          tc_commit_pair_multicast(&empty[stage], 0x3);
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1u;
           }
         }
         if (!ok) break;
-        tc_commit_pair_multicast(acc_full, 0x3);
+        commit_pair_elected(elected, acc_full);
       }
       if (!ok) __nanosleep(200000);  // let issued tensor-core work retire
     }
