@@ -63,6 +63,8 @@ struct Cfg {
   // columns each, above the two overlapping accumulators
   static constexpr int SLOTS = FMT == kQNV4 ? 3 : STAGES;
   static constexpr int SLOT_COLS = ATOMS * 12;
+  static constexpr int CP_A = FMT == kQNV4 ? 4 : 0;
+  static constexpr int CP_B = FMT == kQNV4 ? 2 : 0;
   static constexpr int ACC1 = FMT == kQNV4 ? 96 : 128;  // first column of the odd tiles' accumulator
   static constexpr int T_SF = ACC1 + BN;
   static_assert(T_SF + SLOTS * SLOT_COLS <= TMEM_COLS, "tensor memory overflow");
@@ -112,12 +114,41 @@ __device__ __forceinline__ void mma_fp4_pair(uint32_t elected, uint32_t d, uint6
         : "memory");
 }
 
+// One scale atom of each CTA's own shared memory (same offset) into 4 columns
+// of its tensor memory, replicated over the four lane quarters.
+__device__ __forceinline__ void cp_sf_pair(uint32_t elected, uint32_t taddr, uint64_t desc) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+      "@q tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr),
+      "l"(desc), "r"(elected)
+      : "memory");
+}
+
 __device__ __forceinline__ void commit_pair_elected(uint32_t elected, uint64_t* bar) {
   asm volatile(
       "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
       "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(
           smem_u32(bar)),
       "h"(static_cast<uint16_t>(0x3)), "r"(elected)
+      : "memory");
+}
+
+// TMA load by the elected lane; bar: shared-window address, either CTA of the pair.
+__device__ __forceinline__ void tma_load_elected(uint32_t elected, uint32_t dst, const CUtensorMap* m, uint32_t bar,
+                                                 int c0, int c1, int c2) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %6, 0;\n\t"
+      "@q cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];\n\t}" ::"r"(dst),
+      "l"(m), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(elected)
+      : "memory");
+}
+
+__device__ __forceinline__ void expect_tx_elected(uint32_t elected, uint32_t bar, uint32_t bytes) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+      "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar),
+      "r"(bytes), "r"(elected)
       : "memory");
 }
 
@@ -210,81 +241,79 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   if (warp == 0 || warp == 2) {
     // ------------------------------------------------------------ producers: operands (0), scales (2)
-    if (lane == 0) {
-      // Operands of both CTAs complete on the even CTA's `full`, which alone
-      // posts the count; the scales on this CTA's own sf_full.
-      const bool op = warp == 0;
-      auto expect = [&](int st) {
-        if (!op)
-          mbar_arrive_expect_tx(&sf_full[st], C::SFA_BYTES + C::SFB_BYTES);
-        else if (leader)
-          mbar_arrive_expect_tx(&full[st], 2 * (A_BYTES + B_BYTES));
-      };
-      auto load_w = [&](int st, int kt, int nt, int b) {
-        if (op)
-          tma_load_3d_cluster_bar(smem + C::OFF_B + st * B_BYTES, &tmB, map_shared_rank(smem_u32(&full[st]), 0),
-                                  kt * BKB, nt * BN + static_cast<int>(rank) * (BN / 2), b);
-        else
-          tma_load_3d(smem + C::OFF_SFB + st * C::SFB_BYTES, &tmSFB, &sf_full[st], nt * 2 * (kAtomBytes / 4),
-                      kt * C::ATOMS, b);
-      };
-      auto load_x = [&](int st, int kt, int mt, int b) {
-        const int rt = mt * 2 + static_cast<int>(rank);
-        if (op)
-          tma_load_3d_cluster_bar(smem + C::OFF_A + st * A_BYTES, &tmA, map_shared_rank(smem_u32(&full[st]), 0),
-                                  kt * BKB, rt * BM, b);
-        else
-          tma_load_3d(smem + C::OFF_SFA + st * C::SFA_BYTES, &tmSFA, &sf_full[st], rt * (kAtomBytes / 4),
-                      kt * C::ATOMS, b);
-      };
-      // First ring round: the weights, then (after the kernel before this one
-      // in the stream) the activations, its output.
-      int P0 = 0;
-      for (int pass = 0; pass < 2; ++pass) {
-        P0 = 0;
-        for (int u = pair; u < args.units && P0 < STAGES; u += npairs) {
-          int b, mt, nt, sp, kt, kt_hi;
-          unit_coords(u, args, b, mt, nt, sp, kt, kt_hi);
-          for (; kt < kt_hi && P0 < STAGES; ++kt, ++P0) {
-            if (pass == 0) {
-              expect(P0);
-              load_w(P0, kt, nt, b);
-            } else {
-              load_x(P0, kt, mt, b);
-            }
-          }
-        }
-        if (pass == 0) grid_dependency_wait();
-      }
-      int stage = 0;
-      uint32_t phase = 0;
-      int64_t issued = 0;
-      bool ok = true;
-      for (int u = pair; ok && u < args.units; u += npairs) {
+    // Operands of both CTAs complete on the even CTA's `full`, which alone
+    // posts the count; the scales on this CTA's own sf_full.
+    const bool op = warp == 0;
+    const uint32_t elected = elect_one();
+    const uint32_t base = smem_u32(smem);
+    const uint32_t bar0 = smem_u32(op ? full : sf_full);
+    const uint32_t bar_to = op ? map_shared_rank(bar0, 0) : map_shared_rank(bar0, rank);
+    const uint32_t poster = op && !leader ? 0u : elected;
+    const uint32_t tx = op ? 2 * (A_BYTES + B_BYTES) : C::SFA_BYTES + C::SFB_BYTES;
+    const CUtensorMap* tm_x = op ? &tmA : &tmSFA;
+    const CUtensorMap* tm_w = op ? &tmB : &tmSFB;
+    const uint32_t dst_x = base + (op ? C::OFF_A : C::OFF_SFA), dst_w = base + (op ? C::OFF_B : C::OFF_SFB);
+    const uint32_t step_x = op ? A_BYTES : C::SFA_BYTES, step_w = op ? B_BYTES : C::SFB_BYTES;
+    // operands: {byte of K, row}; scales: {word of the atom row, atom along K}
+    auto load_w = [&](int st, int kt, int nt, int b) {
+      const int c0 = op ? kt * BKB : nt * 2 * (kAtomBytes / 4);
+      const int c1 = op ? nt * BN + static_cast<int>(rank) * (BN / 2) : kt * C::ATOMS;
+      tma_load_elected(elected, dst_w + st * step_w, tm_w, bar_to + st * 8, c0, c1, b);
+    };
+    auto load_x = [&](int st, int kt, int mt, int b) {
+      const int rt = mt * 2 + static_cast<int>(rank);
+      tma_load_elected(elected, dst_x + st * step_x, tm_x, bar_to + st * 8, op ? kt * BKB : rt * (kAtomBytes / 4),
+                       op ? rt * BM : kt * C::ATOMS, b);
+    };
+    // First ring round: the weights, then (after the kernel before this one
+    // in the stream) the activations, its output.
+    int P0 = 0;
+    for (int pass = 0; pass < 2; ++pass) {
+      P0 = 0;
+      for (int u = pair; u < args.units && P0 < STAGES; u += npairs) {
         int b, mt, nt, sp, kt, kt_hi;
         unit_coords(u, args, b, mt, nt, sp, kt, kt_hi);
-        for (; kt < kt_hi; ++kt) {
-          if (issued >= P0) {
-            if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag)) {
-              ok = false;
-              break;
-            }
-            // The odd CTA's bytes may land before the even CTA posts the
-            // count, but not a phase early: the stage was freed by a commit
-            // behind the MMA that waited for the barrier's previous phase.
-            expect(stage);
-            load_x(stage, kt, mt, b);
-            load_w(stage, kt, nt, b);
-          }
-          ++issued;
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1u;
+        for (; kt < kt_hi && P0 < STAGES; ++kt, ++P0) {
+          if (pass == 0) {
+            expect_tx_elected(poster, bar0 + P0 * 8, tx);
+            load_w(P0, kt, nt, b);
+          } else {
+            load_x(P0, kt, mt, b);
           }
         }
       }
-      // Before exit: every commit to this CTA's empty barriers has arrived; a
-      // stage's last commit follows the MMA that waited for its copies.
+      if (pass == 0) grid_dependency_wait();
+    }
+    int stage = 0;
+    uint32_t phase = 0;
+    int64_t issued = 0;
+    bool ok = true;
+    for (int u = pair; ok && u < args.units; u += npairs) {
+      int b, mt, nt, sp, kt, kt_hi;
+      unit_coords(u, args, b, mt, nt, sp, kt, kt_hi);
+      for (; kt < kt_hi; ++kt) {
+        if (issued >= P0) {
+          if (!mbar_wait_warp(&empty[stage], phase ^ 1u, abort_flag)) {
+            ok = false;
+            break;
+          }
+          // The odd CTA's bytes may land before the even CTA posts the
+          // count, but not a phase early: the stage was freed by a commit
+          // behind the MMA that waited for the barrier's previous phase.
+          expect_tx_elected(poster, bar0 + stage * 8, tx);
+          load_x(stage, kt, mt, b);
+          load_w(stage, kt, nt, b);
+        }
+        ++issued;
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    // Before exit: every commit to this CTA's empty barriers has arrived; a
+    // stage's last commit follows the MMA that waited for its copies.
+    if (lane == 0) {
       for (int s = 0; s < STAGES; ++s) {
         if (issued <= s) continue;
         const int64_t last = ((issued - 1 - s) / STAGES) * STAGES + s;
@@ -325,6 +354,12 @@ __global__ void __launch_bounds__(THREADS, 1)
           const int steps = kt == args.KT - 1 ? args.last_steps : BK / MMA_K;
           const uint32_t t_sfa = tmem + C::T_SF + slot * C::SLOT_COLS;
           const uint32_t t_sfb = t_sfa + 4 * C::ATOMS;
+          const uint64_t sa = sdesc_sf(smem_u32(smem + C::OFF_SFA)) + static_cast<uint32_t>(stage * (C::SFA_BYTES >> 4));
+          const uint64_t sb = sdesc_sf(smem_u32(smem + C::OFF_SFB)) + static_cast<uint32_t>(stage * (C::SFB_BYTES >> 4));
+#pragma unroll
+          for (int j = 0; j < C::CP_A; ++j) cp_sf_pair(elected, t_sfa + 4 * j, sa + j * (kAtomBytes >> 4));
+#pragma unroll
+          for (int j = 0; j < C::CP_B; ++j) cp_sf_pair(elected, t_sfb + 4 * j, sb + j * (kAtomBytes >> 4));
 #pragma unroll
           for (int kk = 0; kk < BK / MMA_K; ++kk) {
             // MXFP4: two steps share an atom (scale bytes 0-1 and 2-3)
@@ -375,12 +410,12 @@ __global__ void __launch_bounds__(THREADS, 1)
       const uint4* sb = reinterpret_cast<const uint4*>(smem + C::OFF_SFB + stage * C::SFB_BYTES) + lane;
       const uint32_t t = lane_base + slot * C::SLOT_COLS;
 #pragma unroll
-      for (int j = 0; j < C::ATOMS; ++j) {
+      for (int j = C::CP_A; j < C::ATOMS; ++j) {
         const uint4 v = sa[j * 32];
         tmem_st_32x32b_x4(t + 4 * j, v.x, v.y, v.z, v.w);
       }
 #pragma unroll
-      for (int j = 0; j < 2 * C::ATOMS; ++j) {
+      for (int j = C::CP_B; j < 2 * C::ATOMS; ++j) {
         const uint4 v = sb[j * 32];
         tmem_st_32x32b_x4(t + 4 * C::ATOMS + 4 * j, v.x, v.y, v.z, v.w);
       }
@@ -416,11 +451,66 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (args.gx != nullptr) alpha = *args.gx;
     if (args.gw != nullptr) alpha *= *args.gw;
     int nbox = 0, tile_no = 0;
+    const bool partial = args.splits > 1;
+    // 32 columns of this warp's rows: scale, bias, round, store through a box
+    auto store_group = [&](const uint32_t (&r)[32], int b, int c, int col, int row0, int nt, int sp) {
+      if (partial) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint8_t* dst = box + (nbox & 1) * OUT_BOX;
+          if (lane == 0 && nbox >= 2) bulk_wait_group_read1();
+          __syncwarp();
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int e = 16 * h + 4 * q;
+            *reinterpret_cast<float4*>(dst + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)) =
+                make_float4(__uint_as_float(r[e]) * alpha, __uint_as_float(r[e + 1]) * alpha,
+                            __uint_as_float(r[e + 2]) * alpha, __uint_as_float(r[e + 3]) * alpha);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_3d(&tmOut, dst, nt * BN + col + 16 * h, row0, sp * args.B + b);
+            bulk_commit_group();
+          }
+          ++nbox;
+        }
+        return;
+      }
+      uint32_t packed[16];
+      if (args.bias != nullptr) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const uint32_t bw = reinterpret_cast<const uint32_t*>(bias_s + c * 32)[j];
+          packed[j] = pack_bf16x2(fmaf(__uint_as_float(r[2 * j]), alpha, __uint_as_float(bw << 16)),
+                                  fmaf(__uint_as_float(r[2 * j + 1]), alpha, __uint_as_float(bw & 0xFFFF0000u)));
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          packed[j] = pack_bf16x2(__uint_as_float(r[2 * j]) * alpha, __uint_as_float(r[2 * j + 1]) * alpha);
+      }
+      uint8_t* dst = box + (nbox & 1) * OUT_BOX;
+      if (lane == 0 && nbox >= 2) bulk_wait_group_read1();
+      __syncwarp();
+      // 64-byte swizzle: 16-byte chunk q of row r sits at q ^ ((r / 2) % 4),
+      // so the eight lanes of a store phase touch different banks
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<uint4*>(dst + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)) =
+            make_uint4(packed[4 * q], packed[4 * q + 1], packed[4 * q + 2], packed[4 * q + 3]);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        tma_store_3d(&tmOut, dst, nt * BN + col, row0, b);
+        bulk_commit_group();
+      }
+      ++nbox;
+    };
     for (int u = pair; u < args.units; u += npairs, ++tile_no) {
       int b, mt, nt, sp, kt_lo, kt_hi;
       unit_coords(u, args, b, mt, nt, sp, kt_lo, kt_hi);
       const int row0 = (mt * 2 + static_cast<int>(rank)) * BM + quad * 32;
-      const bool partial = args.splits > 1;
       if (!partial && args.bias != nullptr) {
         // this warp's 4 x 32 bias values (zero past N)
 #pragma unroll
@@ -433,70 +523,26 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (!mbar_wait(acc_full, static_cast<uint32_t>(tile_no & 1), abort_flag)) break;
       tc_fence_after();
       const uint32_t acc = tmem + (static_cast<uint32_t>(quad * 32) << 16) + ((tile_no & 1) ? C::ACC1 : 0);
-#pragma unroll 1
+      // the columns shared with the next tile's accumulator, all into registers
+      uint32_t r[C::RELEASE][32];
+#pragma unroll
+      for (int i = 0; i < C::RELEASE; ++i) {
+        const int c = (tile_no & 1) ? i : 3 - i;
+        tmem_ld_32x32b_x32(acc + (2 * c + half) * 32, r[i]);
+      }
+      tmem_ld_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_remote(acc_free_even);
+#pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int c = (tile_no & 1) ? i : 3 - i;
         const int col = (2 * c + half) * 32;
-        uint32_t r[32];
-        tmem_ld_32x32b_x32(acc + col, r);
-        tmem_ld_wait();
-        if (i == C::RELEASE - 1) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_remote(acc_free_even);
+        if (i >= C::RELEASE) {
+          tmem_ld_32x32b_x32(acc + col, r[0]);
+          tmem_ld_wait();
         }
-        if (partial) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint8_t* dst = box + (nbox & 1) * OUT_BOX;
-            if (lane == 0 && nbox >= 2) bulk_wait_group_read1();
-            __syncwarp();
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const int e = 16 * h + 4 * q;
-              *reinterpret_cast<float4*>(dst + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)) =
-                  make_float4(__uint_as_float(r[e]) * alpha, __uint_as_float(r[e + 1]) * alpha,
-                              __uint_as_float(r[e + 2]) * alpha, __uint_as_float(r[e + 3]) * alpha);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              tma_store_3d(&tmOut, dst, nt * BN + col + 16 * h, row0, sp * args.B + b);
-              bulk_commit_group();
-            }
-            ++nbox;
-          }
-          continue;
-        }
-        uint32_t packed[16];
-        if (args.bias != nullptr) {
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const uint32_t bw = reinterpret_cast<const uint32_t*>(bias_s + c * 32)[j];
-            packed[j] = pack_bf16x2(fmaf(__uint_as_float(r[2 * j]), alpha, __uint_as_float(bw << 16)),
-                                    fmaf(__uint_as_float(r[2 * j + 1]), alpha, __uint_as_float(bw & 0xFFFF0000u)));
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < 16; ++j)
-            packed[j] = pack_bf16x2(__uint_as_float(r[2 * j]) * alpha, __uint_as_float(r[2 * j + 1]) * alpha);
-        }
-        uint8_t* dst = box + (nbox & 1) * OUT_BOX;
-        if (lane == 0 && nbox >= 2) bulk_wait_group_read1();
-        __syncwarp();
-        // 64-byte swizzle: 16-byte chunk q of row r sits at q ^ ((r / 2) % 4),
-        // so the eight lanes of a store phase touch different banks
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          *reinterpret_cast<uint4*>(dst + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)) =
-              make_uint4(packed[4 * q], packed[4 * q + 1], packed[4 * q + 2], packed[4 * q + 3]);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          tma_store_3d(&tmOut, dst, nt * BN + col, row0, b);
-          bulk_commit_group();
-        }
-        ++nbox;
+        store_group(r[i < C::RELEASE ? i : 0], b, c, col, row0, nt, sp);
       }
     }
     if (lane == 0) bulk_wait_group0();
