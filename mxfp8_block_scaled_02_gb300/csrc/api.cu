@@ -610,16 +610,17 @@ mxfp8_status mxfp8_gemm_packed(const uint8_t* x_q, const uint8_t* sfa_packed, in
 mxfp8_status mxfp8_check(mxfp8_stream_t stream) {
   cudaError_t e = cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "stream synchronize");
-  unsigned int s1 = 0, s2 = 0, s3 = 0, s4 = 0, s5 = 0, s6 = 0, s7 = 0;
+  unsigned int s1 = 0, s2 = 0, s3 = 0, s4 = 0, s5 = 0, s6 = 0, s7 = 0, s8 = 0;
   if ((e = mx::take_status_quantize(&s1)) != cudaSuccess ||
       (e = mx::take_status_gemm(&s2)) != cudaSuccess ||
       (e = mx::take_status_decode(&s3)) != cudaSuccess ||
       (e = mx::take_status_pair(&s4)) != cudaSuccess ||
       (e = mx::take_status_fq(&s6)) != cudaSuccess ||
       (e = mx::take_status_fp4(&s7)) != cudaSuccess ||
+      (e = mx::take_status_fp4_small(&s8)) != cudaSuccess ||
       (e = mx::take_status_debug(&s5)) != cudaSuccess)
     return cuda_fail(e, "status word read");
-  if ((s1 | s2 | s3 | s4 | s5 | s6 | s7) & 1u) return fail(MXFP8_ERR_TIMEOUT, "a bounded in-kernel wait ran out");
+  if ((s1 | s2 | s3 | s4 | s5 | s6 | s7 | s8) & 1u) return fail(MXFP8_ERR_TIMEOUT, "a bounded in-kernel wait ran out");
   return MXFP8_OK;
 }
 

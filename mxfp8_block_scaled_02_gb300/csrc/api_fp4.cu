@@ -60,6 +60,14 @@ mxfp8_status quantize_impl(int fmt, const void* x, int64_t B, int64_t M, int64_t
   return e == cudaSuccess ? MXFP8_OK : cuda_fail(e, "4-bit quantise launch");
 }
 
+// One batch of few rows runs the small-M kernel, the rest the CTA-pair kernel,
+// with its K split when the shape has few output tiles.
+bool use_small(int64_t B, int64_t M) { return B == 1 && M <= mx::kFp4SmallMaxM; }
+
+int product_splits(int64_t B, int64_t M, int64_t N, int64_t K) {
+  return use_small(B, M) ? 1 : mx::fp4_splitk_splits(B, M, N, K);
+}
+
 // Workspace of a call: codes and packed scales of x (bf16 x; the scales also
 // for row-major x_scale), then the split-K partials.
 struct WsLayout {
@@ -117,7 +125,8 @@ mxfp8_status run_product(int fmt, const Operands& o, int64_t B, int64_t M, int64
   p.part = part;
   p.splits = splits;
   const char* msg = "";
-  cudaError_t e = mx::launch_gemm_fp4(p, sms, as_stream(stream), &msg);
+  cudaError_t e = use_small(B, M) ? mx::launch_gemm_fp4_small(p, sms, as_stream(stream), &msg)
+                                  : mx::launch_gemm_fp4(p, sms, as_stream(stream), &msg);
   return e == cudaSuccess ? MXFP8_OK : cuda_fail(e, msg);
 }
 
@@ -203,7 +212,7 @@ mxfp8_status mxfp8_fp4_workspace_size(int fmt, int64_t B, int64_t M, int64_t N, 
   mxfp8_status st = check_product(fmt, B, M, N, K);
   if (st != MXFP8_OK) return st;
   *bytes = static_cast<size_t>(
-      workspace_layout(fmt, B, M, N, K, x_is_quantized != 0, false, mx::fp4_splitk_splits(B, M, N, K)).total);
+      workspace_layout(fmt, B, M, N, K, x_is_quantized != 0, false, product_splits(B, M, N, K)).total);
   return MXFP8_OK;
 }
 
@@ -222,7 +231,7 @@ mxfp8_status mxfp8_fp4_linear(int fmt, const void* x_bf16, const uint8_t* x_q, c
   Operands o{x_q, x_scale, x_tensor_scale, w_packed, sf_packed, w_tensor_scale, bias_bf16, out_bf16};
   if ((st = check_operands(fmt, o)) != MXFP8_OK) return st;
   if (!aligned(x_bf16, 16)) return fail(MXFP8_ERR_INVALID_ARG, "tensor pointers must be 16-byte aligned");
-  const int splits = mx::fp4_splitk_splits(B, M, N, K);
+  const int splits = product_splits(B, M, N, K);
   const WsLayout ws = workspace_layout(fmt, B, M, N, K, have_q, false, splits);
   if (static_cast<int64_t>(workspace_bytes) < ws.total)
     return fail(MXFP8_ERR_INVALID_ARG, "workspace has %zu bytes, needs %lld", workspace_bytes, (long long)ws.total);
@@ -255,7 +264,7 @@ mxfp8_status mxfp8_fp4_gemm_packed(int fmt, const uint8_t* x_q, const uint8_t* s
   if (x_q == nullptr || sfa_packed == nullptr) return fail(MXFP8_ERR_INVALID_ARG, "null pointer");
   const Operands o{x_q, sfa_packed, x_tensor_scale, w_packed, sf_packed, w_tensor_scale, bias_bf16, out_bf16};
   if ((st = check_operands(fmt, o)) != MXFP8_OK) return st;
-  int splits = mx::fp4_splitk_splits(B, M, N, K);
+  int splits = product_splits(B, M, N, K);
   const WsLayout ws = workspace_layout(fmt, B, M, N, K, true, true, splits);
   if (workspace != nullptr && !aligned(workspace, 256))
     return fail(MXFP8_ERR_INVALID_ARG, "workspace must be 256-byte aligned");

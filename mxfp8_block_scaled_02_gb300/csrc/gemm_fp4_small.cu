@@ -1,0 +1,453 @@
+// gemm_fp4_small.cu - the 4-bit product for few tokens (M <= 128, one batch):
+//   out[m, n] = bf16( g_x g_w sum_k (x sx)[m, k] (w sw)[n, k] + bias[n] ).
+//
+// Bound by reading the weights once, and at decode sizes by the chain launch ->
+// weights -> MMA -> reduction -> store.  So the weights are the MMA's M side
+// (128 rows per CTA) and the tokens its N side (16, 32, 64 or 128 >= M), no MMA
+// row is padding, and K is split over a cluster of S CTAs so that every SM
+// streams from the start: each holds a ring of 128-row x 128-byte weight tiles
+// in flight before the tokens arrive (they are the previous kernel's output,
+// waited for with griddepcontrol.wait; weights, scales and bias are not).
+// Codes and scale atoms of both operands come by TMA, the atoms go to tensor
+// memory by tcgen05.cp in the MMA warp's own order.
+//
+// The S fp32 partials meet in distributed shared memory: CTA r owns weight rows
+// [r 128/S, (r+1) 128/S) and adds the partials in the order 0..S-1, so the
+// result is the same on every call; with S = 1 the epilogue stores straight
+// from tensor memory.
+//
+// Warps: 0 weight TMA, 1 tensor-memory allocation and MMA issue, 2 token TMA,
+// 3 idle, 4..7 epilogue; all eight reduce.  Every wait is bounded and the
+// cluster barrier is reached on every path.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "mx_fp4.cuh"
+#include "mx_kernels.h"
+#include "mx_layout.cuh"
+#include "mx_ptx.cuh"
+
+namespace mx {
+
+namespace {
+
+constexpr int ROWS = 128;   // weight rows per CTA
+constexpr int BKB = 128;    // bytes of K per row and stage
+constexpr int BK = 2 * BKB;
+constexpr int MMA_K = 64;
+constexpr int THREADS = 256;
+constexpr int W_BYTES = ROWS * BKB;
+constexpr int SMEM_MAX = 232448;
+
+template <int FMT, int NTOK>
+struct Cfg {
+  static constexpr int ATOMS = FMT == kQNV4 ? 4 : 2;
+  static constexpr int SF_BYTES = ATOMS * kAtomBytes;  // scales of one operand and stage
+  static constexpr int X_BYTES = NTOK * BKB;
+  static constexpr int STAGE_BYTES = W_BYTES + X_BYTES + 2 * SF_BYTES;
+  static constexpr int RECV_BYTES = NTOK * ROWS * 4;  // [S][NTOK][ROWS / S] fp32
+  static constexpr int FIT = (SMEM_MAX - 1024 - 512 - RECV_BYTES) / STAGE_BYTES;
+  static constexpr int STAGES = FIT < 12 ? FIT : 12;
+  static constexpr int OFF_W = 0;
+  static constexpr int OFF_X = OFF_W + STAGES * W_BYTES;
+  static constexpr int OFF_SFW = OFF_X + STAGES * X_BYTES;
+  static constexpr int OFF_SFX = OFF_SFW + STAGES * SF_BYTES;
+  static constexpr int OFF_RECV = OFF_SFX + STAGES * SF_BYTES;
+  static constexpr int OFF_BAR = OFF_RECV + RECV_BYTES;
+  static constexpr int OFF_MISC = OFF_BAR + (3 * STAGES + 1) * 8;
+  static constexpr int SMEM = OFF_MISC + 16 + 1024;
+  static_assert(SMEM <= SMEM_MAX && STAGES >= 4, "shared memory");
+  // tensor memory: accumulator, then two scale slots (weight and token atoms)
+  static constexpr int SLOT_COLS = 8 * ATOMS;
+  static constexpr int T_SF = NTOK < 32 ? 32 : NTOK;
+  static constexpr int T_END = T_SF + 2 * SLOT_COLS;
+  static constexpr int TMEM_COLS = T_END <= 64 ? 64 : (T_END <= 128 ? 128 : 256);
+  static_assert(T_END <= 256, "tensor memory");
+};
+
+template <int FMT>
+__device__ __forceinline__ void mma_fp4(uint32_t elected, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                        uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+  if (FMT == kQMX4)
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %7, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
+            d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb), "r"(elected)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %7, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%5], [%6], "
+        "p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb), "r"(elected)
+        : "memory");
+}
+
+__device__ __forceinline__ void cp_sf(uint32_t elected, uint32_t taddr, uint64_t desc) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+      "@q tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr),
+      "l"(desc), "r"(elected)
+      : "memory");
+}
+
+__device__ __forceinline__ void commit_elected(uint32_t elected, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"(elected)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_load_elected(uint32_t elected, uint32_t dst, const CUtensorMap* m, uint32_t bar,
+                                                 int c0, int c1) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];\n\t}" ::
+          "r"(dst),
+      "l"(m), "r"(bar), "r"(c0), "r"(c1), "r"(elected)
+      : "memory");
+}
+
+__device__ __forceinline__ void expect_tx_elected(uint32_t elected, uint32_t bar, uint32_t bytes) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+      "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar),
+      "r"(bytes), "r"(elected)
+      : "memory");
+}
+
+struct Args {
+  const __nv_bfloat16* bias;
+  const float* gx;
+  const float* gw;
+  __nv_bfloat16* out;
+  int M, N;
+  int KT;          // stages of K
+  int last_steps;  // MMA steps of the last one
+  int splits;      // cluster size S
+};
+
+template <int FMT, int NTOK>
+__global__ void __launch_bounds__(THREADS, 1)
+    gemm_fp4_small_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                          const __grid_constant__ CUtensorMap tmSFW, const __grid_constant__ CUtensorMap tmSFX,
+                          const Args a) {
+  using C = Cfg<FMT, NTOK>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint64_t* full_w = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  uint64_t* full_x = full_w + C::STAGES;
+  uint64_t* empty = full_x + C::STAGES;
+  uint64_t* acc_full = empty + C::STAGES;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
+
+  const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0);  // uniform
+  const int lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_ctarank());
+  const int tile = static_cast<int>(blockIdx.x) / a.splits;
+  const int kt0 = rank * a.KT / a.splits;
+  const int nk = (rank + 1) * a.KT / a.splits - kt0;  // >= 1: splits <= KT
+  const uint32_t base = smem_u32(smem);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(&full_w[s], 1);
+      mbar_init(&full_x[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(acc_full, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  const uint32_t elected = elect_one();
+  auto load_w = [&](int i, int st) {
+    const uint32_t bar = smem_u32(&full_w[st]);
+    expect_tx_elected(elected, bar, W_BYTES + C::SF_BYTES);
+    tma_load_elected(elected, base + C::OFF_W + st * W_BYTES, &tmW, bar, (kt0 + i) * BKB, tile * ROWS);
+    tma_load_elected(elected, base + C::OFF_SFW + st * C::SF_BYTES, &tmSFW, bar, tile * (kAtomBytes / 4),
+                     (kt0 + i) * C::ATOMS);
+  };
+  const int first = nk < C::STAGES ? nk : C::STAGES;
+  if (warp == 0) {
+    // the first ring round needs nothing but the barriers this warp has made
+    __syncwarp();
+    for (int i = 0; i < first; ++i) load_w(i, i);
+    launch_dependents();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
+  // the output row this thread finishes: its bias and the weights' scale are
+  // read before the dependency wait, like the weights
+  const int per = ROWS / a.splits;
+  const int my_n = a.splits == 1 ? tile * ROWS + (warp & 3) * 32 + lane
+                                 : tile * ROWS + rank * per + static_cast<int>(threadIdx.x) % per;
+  float bias_n = 0.f, alpha = 1.f;
+
+  if (warp == 0) {
+    // ------------------------------------------------ weight producer, later rounds
+    int st = 0, issued = first;
+    uint32_t ph = 0;
+    for (int i = first; i < nk; ++i) {
+      if (!mbar_wait_warp(&empty[st], ph, abort_flag)) break;
+      load_w(i, st);
+      ++issued;
+      if (++st == C::STAGES) {
+        st = 0;
+        ph ^= 1u;
+      }
+    }
+    if (*abort_flag) {  // leave with no copy in flight
+      for (int s = 0; s < C::STAGES && s < issued; ++s)
+        mbar_wait(&full_w[s], static_cast<uint32_t>(((issued - 1 - s) / C::STAGES) & 1), nullptr);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------ MMA issuer
+    constexpr uint32_t idesc = (1u << 7) | (1u << 10) | (static_cast<uint32_t>(NTOK >> 3) << 17) |
+                               ((FMT == kQMX4 ? 1u : 0u) << 23) | (static_cast<uint32_t>(ROWS >> 4) << 24);
+    const uint64_t wd0 = sdesc_kmajor_sw128(base + C::OFF_W), xd0 = sdesc_kmajor_sw128(base + C::OFF_X);
+    const uint64_t sw0 = sdesc_sf(base + C::OFF_SFW), sx0 = sdesc_sf(base + C::OFF_SFX);
+    int st = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    for (int i = 0; i < nk; ++i) {
+      if (!mbar_wait_warp(&full_w[st], ph, abort_flag) || !mbar_wait_warp(&full_x[st], ph, abort_flag)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const uint32_t t_sfw = tmem + C::T_SF + (i & 1) * C::SLOT_COLS;
+      const uint32_t t_sfx = t_sfw + 4 * C::ATOMS;
+#pragma unroll
+      for (int j = 0; j < C::ATOMS; ++j) {
+        cp_sf(elected, t_sfw + 4 * j, sw0 + static_cast<uint32_t>((st * C::SF_BYTES + j * kAtomBytes) >> 4));
+        cp_sf(elected, t_sfx + 4 * j, sx0 + static_cast<uint32_t>((st * C::SF_BYTES + j * kAtomBytes) >> 4));
+      }
+      const uint64_t wd = wd0 + static_cast<uint32_t>(st * (W_BYTES >> 4));
+      const uint64_t xd = xd0 + static_cast<uint32_t>(st * (C::X_BYTES >> 4));
+      const int steps = kt0 + i == a.KT - 1 ? a.last_steps : BK / MMA_K;
+#pragma unroll
+      for (int kk = 0; kk < BK / MMA_K; ++kk) {
+        const int j = FMT == kQNV4 ? kk : kk >> 1;
+        const uint32_t id = FMT == kQNV4 ? 0u : static_cast<uint32_t>(kk & 1) * 2u;
+        mma_fp4<FMT>(kk < steps ? elected : 0u, tmem, wd + 2 * kk, xd + 2 * kk, idesc_with_sf_id(idesc, id, id),
+                     t_sfw + 4 * j, t_sfx + 4 * j, (i | kk) != 0);
+      }
+      commit_elected(elected, &empty[st]);
+      if (++st == C::STAGES) {
+        st = 0;
+        ph ^= 1u;
+      }
+    }
+    if (ok)
+      commit_elected(elected, acc_full);
+    else
+      __nanosleep(200000);  // let issued tensor-core work retire
+    __syncwarp();
+  } else if (warp == 2) {
+    // ------------------------------------------------ token producer
+    grid_dependency_wait();
+    int st = 0, issued = 0;
+    uint32_t ph = 1;  // the first round's slots are free
+    for (int i = 0; i < nk; ++i) {
+      if (i >= C::STAGES && !mbar_wait_warp(&empty[st], ph, abort_flag)) break;
+      const uint32_t bar = smem_u32(&full_x[st]);
+      expect_tx_elected(elected, bar, C::X_BYTES + C::SF_BYTES);
+      tma_load_elected(elected, base + C::OFF_X + st * C::X_BYTES, &tmX, bar, (kt0 + i) * BKB, 0);
+      tma_load_elected(elected, base + C::OFF_SFX + st * C::SF_BYTES, &tmSFX, bar, 0, (kt0 + i) * C::ATOMS);
+      ++issued;
+      if (++st == C::STAGES) {
+        st = 0;
+        ph ^= 1u;
+      }
+    }
+    if (*abort_flag) {
+      for (int s = 0; s < C::STAGES && s < issued; ++s)
+        mbar_wait(&full_x[s], static_cast<uint32_t>(((issued - 1 - s) / C::STAGES) & 1), nullptr);
+    }
+    __syncwarp();
+  }
+  if (warp >= 4 || a.splits > 1) {
+    if (a.bias != nullptr && my_n < a.N) bias_n = __bfloat162float(a.bias[my_n]);
+    if (a.gw != nullptr) alpha = *a.gw;
+    grid_dependency_wait();  // g_x and the output belong to the kernels before
+    if (a.gx != nullptr) alpha *= *a.gx;
+  }
+  if (warp >= 4 && mbar_wait_warp(acc_full, 0, abort_flag)) {
+    // ------------------------------------------------ epilogue: lane = weight row
+    tc_fence_after();
+    const uint32_t lrow = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const int wrow = (warp & 3) * 32 + lane;
+    const int owner = wrow / per;
+    const uint32_t dst = a.splits == 1 ? 0u
+                                       : map_shared_rank(base + C::OFF_RECV, static_cast<uint32_t>(owner)) +
+                                             static_cast<uint32_t>(((rank * NTOK) * per + wrow - owner * per) * 4);
+    for (int c = 0; c < a.M; c += 16) {
+      uint32_t r[16];
+      tmem_ld_32x32b_x16(lrow + c, r);
+      tmem_ld_wait();
+      if (a.splits == 1) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          if (c + j < a.M && my_n < a.N)
+            a.out[static_cast<int64_t>(c + j) * a.N + my_n] =
+                __float2bfloat16_rn(fmaf(__uint_as_float(r[j]), alpha, bias_n));
+      } else {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) st_shared_cluster_u32(dst + static_cast<uint32_t>((c + j) * per * 4), r[j]);
+      }
+    }
+  }
+
+  tc_fence_before();
+  cluster_sync();  // all partials are in their owners' buffers
+  if (a.splits > 1 && !*abort_flag && my_n < a.N) {
+    const float* recv = reinterpret_cast<const float*>(smem + C::OFF_RECV);
+    const int nl = static_cast<int>(threadIdx.x) % per;
+    for (int m = static_cast<int>(threadIdx.x) / per; m < a.M; m += THREADS / per) {
+      float acc = 0.f;
+      for (int s = 0; s < a.splits; ++s) acc += recv[(s * NTOK + m) * per + nl];
+      a.out[static_cast<int64_t>(m) * a.N + my_n] = __float2bfloat16_rn(fmaf(acc, alpha, bias_n));
+    }
+  }
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+bool encode2(CUtensorMap* m, CUtensorMapDataType dtype, const void* base, int64_t d0, int64_t d1, int64_t s1, int b0,
+             int b1, CUtensorMapSwizzle sw) {
+  EncodeTiledFn encode = encode_tiled_fn();
+  if (encode == nullptr) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(d0), static_cast<cuuint64_t>(d1)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(s1)};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(b0), static_cast<cuuint32_t>(b1)};
+  const cuuint32_t estr[2] = {1, 1};
+  return encode(m, dtype, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+void fill_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, int grid, int splits, int smem, cudaStream_t s) {
+  *cfg = cudaLaunchConfig_t{};
+  cfg->gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+  cfg->blockDim = dim3(THREADS, 1, 1);
+  cfg->dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg->stream = s;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(splits);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg->attrs = attr;
+  cfg->numAttrs = 2;
+}
+
+// Clusters of S CTAs that fit on the GPU at once, per device (asked once).
+template <int FMT, int NTOK>
+int max_clusters(int splits, int sms) {
+  static int cache[64][4] = {};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  const int slot = splits == 8 ? 3 : (splits == 4 ? 2 : (splits == 2 ? 1 : 0));
+  if (dev < 0 || dev >= 64) return sms / splits;
+  if (cache[dev][slot] == 0) {
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr[2];
+    fill_config(&cfg, attr, splits, splits, Cfg<FMT, NTOK>::SMEM, nullptr);
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, gemm_fp4_small_kernel<FMT, NTOK>, &cfg) != cudaSuccess || n < 1) {
+      cudaGetLastError();  // the query's own error
+      n = sms / splits;
+    }
+    cache[dev][slot] = n;
+  }
+  return cache[dev][slot];
+}
+
+template <int FMT, int NTOK>
+cudaError_t launch_t(const Fp4Problem& p, int sms, cudaStream_t stream, const char** msg) {
+  using C = Cfg<FMT, NTOK>;
+  static bool attr_set[64] = {};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64 || !attr_set[dev]) {
+    cudaError_t e =
+        cudaFuncSetAttribute(gemm_fp4_small_kernel<FMT, NTOK>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) {
+      *msg = "cudaFuncSetAttribute(max dynamic shared memory) failed";
+      return e;
+    }
+    if (dev >= 0 && dev < 64) attr_set[dev] = true;
+  }
+  const int64_t kb = p.K / 2, RTW = ceil_div(p.N, kAtomRows), RTX = ceil_div(p.M, kAtomRows);
+  const int64_t KA = ceil_div(fp4_scale_extent(FMT, p.K), kTileK);
+  const int words = kAtomBytes / 4;
+  CUtensorMap mw, mx, msw, msx;
+  const auto u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8, u32 = CU_TENSOR_MAP_DATA_TYPE_UINT32;
+  if (!encode2(&mw, u8, p.w, kb, p.N, kb, BKB, ROWS, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode2(&mx, u8, p.x, kb, p.M, kb, BKB, NTOK, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode2(&msw, u32, p.sfw, RTW * words, KA, RTW * kAtomBytes, words, C::ATOMS, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+      !encode2(&msx, u32, p.sfx, RTX * words, KA, RTX * kAtomBytes, words, C::ATOMS, CU_TENSOR_MAP_SWIZZLE_NONE)) {
+    *msg = "cuTensorMapEncodeTiled rejected a 4-bit operand";
+    return cudaErrorInvalidValue;
+  }
+  Args a;
+  a.bias = static_cast<const __nv_bfloat16*>(p.bias);
+  a.gx = p.gx;
+  a.gw = p.gw;
+  a.out = static_cast<__nv_bfloat16*>(p.out);
+  a.M = static_cast<int>(p.M);
+  a.N = static_cast<int>(p.N);
+  a.KT = static_cast<int>(ceil_div(p.K, BK));
+  a.last_steps = static_cast<int>(ceil_div(p.K - static_cast<int64_t>(a.KT - 1) * BK, MMA_K));
+  // the largest K split whose clusters all run at once
+  a.splits = 8;
+  while (a.splits > 1 && (a.splits > a.KT || RTW > max_clusters<FMT, NTOK>(a.splits, sms))) a.splits >>= 1;
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr[2];
+  fill_config(&cfg, attr, static_cast<int>(RTW) * a.splits, a.splits, C::SMEM, stream);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, gemm_fp4_small_kernel<FMT, NTOK>, mw, mx, msw, msx, a);
+  if (e != cudaSuccess) *msg = "small-M 4-bit GEMM launch failed";
+  return e;
+}
+
+template <int FMT>
+cudaError_t launch_fmt(const Fp4Problem& p, int sms, cudaStream_t stream, const char** msg) {
+  if (p.M <= 16) return launch_t<FMT, 16>(p, sms, stream, msg);
+  if (p.M <= 32) return launch_t<FMT, 32>(p, sms, stream, msg);
+  if (p.M <= 64) return launch_t<FMT, 64>(p, sms, stream, msg);
+  return launch_t<FMT, 128>(p, sms, stream, msg);
+}
+
+}  // namespace
+
+cudaError_t launch_gemm_fp4_small(const Fp4Problem& p, int sms, cudaStream_t stream, const char** msg) {
+  if (p.B != 1 || p.M < 1 || p.M > kFp4SmallMaxM) {
+    *msg = "small-M 4-bit GEMM: B and M out of range";
+    return cudaErrorInvalidValue;
+  }
+  return p.fmt == kQNV4 ? launch_fmt<kQNV4>(p, sms, stream, msg) : launch_fmt<kQMX4>(p, sms, stream, msg);
+}
+
+cudaError_t take_status_fp4_small(unsigned int* out) {
+  unsigned int zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(out, g_status, sizeof(unsigned int));
+  if (e != cudaSuccess) return e;
+  return cudaMemcpyToSymbol(g_status, &zero, sizeof(unsigned int));
+}
+
+}  // namespace mx

@@ -191,6 +191,11 @@ struct Fp4Problem {
 int fp4_splitk_splits(int64_t B, int64_t M, int64_t N, int64_t K);
 cudaError_t launch_gemm_fp4(const Fp4Problem& p, int sms, cudaStream_t stream, const char** msg);
 cudaError_t take_status_fp4(unsigned int* out);
+// gemm_fp4_small.cu: the same for one batch of at most kFp4SmallMaxM rows, the
+// weights on the MMA's M side (part and splits are not used).
+constexpr int64_t kFp4SmallMaxM = 128;
+cudaError_t launch_gemm_fp4_small(const Fp4Problem& p, int sms, cudaStream_t stream, const char** msg);
+cudaError_t take_status_fp4_small(unsigned int* out);
 
 // debug.cu
 cudaError_t launch_expire_wait(uint64_t timeout_ns, cudaStream_t stream);

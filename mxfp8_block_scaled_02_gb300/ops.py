@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import functools
 import os
 
 import numpy as np
@@ -117,6 +118,10 @@ def _check(status: int) -> None:
 
 
 def _stream() -> int:
+    # the handle alone: torch.cuda.current_stream() builds a Stream object
+    # (2.9 us per call on the Grace host, of ~10 for a whole call)
+    if torch.cuda.is_initialized():
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return torch.cuda.current_stream().cuda_stream
 
 
@@ -537,11 +542,12 @@ def unpack_fp4(x_q: torch.Tensor) -> torch.Tensor:
         raise TypeError("codes must be uint8")
     _require_cuda(x_q)
     x_q = _aligned16(x_q)
-    out = torch.empty((*x_q.shape[:-1], 2 * x_q.shape[-1]), dtype=torch.uint8, device=x_q.device)
-    _check(load().mxfp8_fp4_unpack(_ptr(x_q), out.numel(), _ptr(out), _stream()))
-    return out.view(torch.float8_e4m3fn)
+    out = torch.empty((*x_q.shape[:-1], 2 * x_q.shape[-1]), dtype=torch.float8_e4m3fn, device=x_q.device)
+    _check(load().mxfp8_fp4_unpack(x_q.data_ptr(), out.numel(), out.data_ptr(), _stream()))
+    return out
 
 
+@functools.lru_cache(maxsize=4096)
 def packed_sizes_fp4(B: int, N: int, K: int, fmt: str) -> tuple[int, int]:
     wb, sb = ctypes.c_size_t(), ctypes.c_size_t()
     _check(load().mxfp8_fp4_packed_sizes(_fmt4(fmt), B, N, K, ctypes.byref(wb), ctypes.byref(sb)))
@@ -577,6 +583,7 @@ def process_weights_fp4(w_q: torch.Tensor, w_scale: torch.Tensor, fmt: str = "mx
     return PackedWeights(wp, sp, B, N, K, batched, fmt, tensor_scale)
 
 
+@functools.lru_cache(maxsize=4096)
 def workspace_size_fp4(B: int, M: int, N: int, K: int, quantized: bool, fmt: str) -> int:
     n = ctypes.c_size_t()
     _check(load().mxfp8_fp4_workspace_size(_fmt4(fmt), B, M, N, K, int(quantized), ctypes.byref(n)))
@@ -649,9 +656,14 @@ def quantize_packed_fp4(x: torch.Tensor, B: int = 1, fmt: str = "mxfp4", *,
     return pa
 
 
+@functools.lru_cache(maxsize=4096)
+def _packed_sizes_mx8(B: int, M: int, K: int, fmt: str) -> tuple[int, int]:
+    return packed_sizes(B, M, K)
+
+
 def _packed_activation(B: int, M: int, K: int, fmt: str, tensor_scale: torch.Tensor | None,
                        device) -> PackedActivation:
-    sb = packed_sizes(B, max(M, 1), K)[1] if fmt == "mxfp8" else packed_sizes_fp4(B, max(M, 1), K, fmt)[1]
+    sb = (_packed_sizes_mx8 if fmt == "mxfp8" else packed_sizes_fp4)(B, max(M, 1), K, fmt)[1]
     return PackedActivation(torch.empty((B, M, K if fmt == "mxfp8" else K // 2), dtype=torch.uint8, device=device),
                             torch.empty(sb, dtype=torch.uint8, device=device), B, M, K, fmt, tensor_scale)
 
@@ -711,13 +723,13 @@ def _rows2d(x: torch.Tensor, name: str) -> tuple[torch.Tensor, int, int]:
     return x, rows, stride
 
 
-def _quantized_out(x: torch.Tensor, rows: int, K: int, fmt: str, tensor_scale: torch.Tensor | None, packed: bool):
+def _quantized_out(lead, device, rows: int, K: int, fmt: str, tensor_scale: torch.Tensor | None, packed: bool):
     """Output tensors of a fused quantising step: (what the caller gets, codes, scales)."""
     if packed:
-        pa = _packed_activation(1, rows, K, fmt, tensor_scale, x.device)
+        pa = _packed_activation(1, rows, K, fmt, tensor_scale, device)
         return pa, pa.x_q, pa.sf_packed
-    q = torch.empty((*x.shape[:-1], K if fmt == "mxfp8" else K // 2), dtype=torch.uint8, device=x.device)
-    s = torch.empty((*x.shape[:-1], K // QBLOCK[fmt]), dtype=torch.uint8, device=x.device)
+    q = torch.empty((*lead, K if fmt == "mxfp8" else K // 2), dtype=torch.uint8, device=device)
+    s = torch.empty((*lead, K // QBLOCK[fmt]), dtype=torch.uint8, device=device)
     return (q, s), q, s
 
 
@@ -763,7 +775,7 @@ def rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tens
     if y is not None and (y.dtype != torch.bfloat16 or y.shape != x.shape):
         raise ValueError("y must be bf16 with x's shape")
     weight = _aligned16(weight)
-    res, q, s = _quantized_out(x, rows, K, fmt, tensor_scale, packed)
+    res, q, s = _quantized_out(x.shape[:-1], x.device, rows, K, fmt, tensor_scale, packed)
     _check(load().mxfp8_rmsnorm_quantize(f, _ptr(xr), x_stride, _ptr(rr), r_stride,
                                          int(residual is not None and residual.dtype == torch.float32),
                                          _ptr(residual_out), _ptr(weight), eps, _ptr(tensor_scale), rows, K,
@@ -779,24 +791,27 @@ def silu_mul_quantize(gate_up: torch.Tensor, up: torch.Tensor | None = None, *, 
     projection's output); or pass gate [..., K] and ``up`` [..., K].  Returns
     the quantised result as rmsnorm_quantize does."""
     f = _qfmt(fmt)
-    if up is None:
-        if gate_up.dim() < 1 or gate_up.shape[-1] % 2:
-            raise ValueError("gate_up must be [..., 2 K]")
-        half = gate_up.shape[-1] // 2
-        gate, up = gate_up[..., :half], gate_up[..., half:]
-    else:
-        gate = gate_up
-        if up.shape != gate.shape:
-            raise ValueError("gate and up must have the same shape")
-    if gate.dtype != torch.bfloat16 or up.dtype != torch.bfloat16:
+    if gate_up.dtype != torch.bfloat16 or (up is not None and up.dtype != torch.bfloat16):
         raise TypeError("gate and up must be bfloat16")
     _check_tensor_scale(fmt, tensor_scale)
-    gr, rows, g_stride = _rows2d(gate, "gate")
-    ur, _, u_stride = _rows2d(up, "up")
-    K = gate.shape[-1]
-    res, q, s = _quantized_out(gate, rows, K, fmt, tensor_scale, packed)
-    _check(load().mxfp8_silu_mul_quantize(f, _ptr(gr), g_stride, _ptr(ur), u_stride, _ptr(tensor_scale), rows, K,
-                                          _ptr(q), _ptr(s), int(packed), _stream()))
+    if up is None:
+        if gate_up.dim() < 1 or gate_up.shape[-1] % (2 * BLOCK):
+            raise ValueError(f"gate_up must be [..., 2 K] with K a multiple of {BLOCK}, not {tuple(gate_up.shape)}")
+        both, rows, stride = _rows2d(gate_up, "gate_up")
+        K = gate_up.shape[-1] // 2
+        lead = gate_up.shape[:-1]
+        gate_ptr, gate_stride = both.data_ptr(), stride
+        up_ptr, up_stride = gate_ptr + 2 * K, stride
+    else:
+        if up.shape != gate_up.shape:
+            raise ValueError("gate and up must have the same shape")
+        gr, rows, gate_stride = _rows2d(gate_up, "gate")
+        ur, _, up_stride = _rows2d(up, "up")
+        K, lead = gate_up.shape[-1], gate_up.shape[:-1]
+        gate_ptr, up_ptr = gr.data_ptr(), ur.data_ptr()
+    res, q, s = _quantized_out(lead, gate_up.device, rows, K, fmt, tensor_scale, packed)
+    _check(load().mxfp8_silu_mul_quantize(f, gate_ptr, gate_stride, up_ptr, up_stride, _ptr(tensor_scale), rows, K,
+                                          q.data_ptr(), s.data_ptr(), packed, _stream()))
     return res
 
 
