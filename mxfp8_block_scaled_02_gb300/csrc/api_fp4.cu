@@ -60,12 +60,9 @@ mxfp8_status quantize_impl(int fmt, const void* x, int64_t B, int64_t M, int64_t
   return e == cudaSuccess ? MXFP8_OK : cuda_fail(e, "4-bit quantise launch");
 }
 
-// One batch of few rows runs the small-M kernel, the rest the CTA-pair kernel,
-// with its K split when the shape has few output tiles.
-bool use_small(int64_t B, int64_t M) { return B == 1 && M <= mx::kFp4SmallMaxM; }
-
+// K splits of the CTA-pair kernel (1 where the small-M kernel runs).
 int product_splits(int64_t B, int64_t M, int64_t N, int64_t K) {
-  return use_small(B, M) ? 1 : mx::fp4_splitk_splits(B, M, N, K);
+  return mx::fp4_use_small(B, M, N, K) ? 1 : mx::fp4_splitk_splits(B, M, N, K);
 }
 
 // Workspace of a call: codes and packed scales of x (bf16 x; the scales also
@@ -125,7 +122,7 @@ mxfp8_status run_product(int fmt, const Operands& o, int64_t B, int64_t M, int64
   p.part = part;
   p.splits = splits;
   const char* msg = "";
-  cudaError_t e = use_small(B, M) ? mx::launch_gemm_fp4_small(p, sms, as_stream(stream), &msg)
+  cudaError_t e = mx::fp4_use_small(B, M, N, K) ? mx::launch_gemm_fp4_small(p, sms, as_stream(stream), &msg)
                                   : mx::launch_gemm_fp4(p, sms, as_stream(stream), &msg);
   return e == cudaSuccess ? MXFP8_OK : cuda_fail(e, msg);
 }

@@ -558,19 +558,6 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
 }
 
-// A 3-D map: innermost extent in elements of `dtype`, the two strides in bytes.
-bool encode3(CUtensorMap* m, CUtensorMapDataType dtype, const void* base, int64_t d0, int64_t d1, int64_t d2,
-             int64_t s1, int64_t s2, int b0, int b1, CUtensorMapSwizzle sw, CUtensorMapL2promotion l2) {
-  EncodeTiledFn encode = encode_tiled_fn();
-  if (encode == nullptr) return false;
-  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d0), static_cast<cuuint64_t>(d1), static_cast<cuuint64_t>(d2)};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(s1), static_cast<cuuint64_t>(s2)};
-  const cuuint32_t box[3] = {static_cast<cuuint32_t>(b0), static_cast<cuuint32_t>(b1), 1};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  return encode(m, dtype, 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw, l2,
-                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int FMT>
 cudaError_t launch_t(const Fp4Problem& p, int sms, cudaStream_t stream, const char** msg) {
   using C = Cfg<FMT>;
@@ -593,19 +580,19 @@ cudaError_t launch_t(const Fp4Problem& p, int sms, cudaStream_t stream, const ch
   const auto u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
   const auto u32 = CU_TENSOR_MAP_DATA_TYPE_UINT32;
   const int words = kAtomBytes / 4;
-  bool ok = encode3(&ma, u8, p.x, kb, p.M, p.B, kb, p.M * kb, BKB, BM, CU_TENSOR_MAP_SWIZZLE_128B,
+  bool ok = encode_map3(&ma, u8, p.x, kb, p.M, p.B, kb, p.M * kb, BKB, BM, CU_TENSOR_MAP_SWIZZLE_128B,
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B) &&
-            encode3(&mb, u8, p.w, kb, p.N, p.B, kb, p.N * kb, BKB, BN / 2, CU_TENSOR_MAP_SWIZZLE_128B,
+            encode_map3(&mb, u8, p.w, kb, p.N, p.B, kb, p.N * kb, BKB, BN / 2, CU_TENSOR_MAP_SWIZZLE_128B,
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B) &&
-            encode3(&msa, u32, p.sfx, RTA * words, KA, p.B, RTA * kAtomBytes, KA * RTA * kAtomBytes, words, C::ATOMS,
+            encode_map3(&msa, u32, p.sfx, RTA * words, KA, p.B, RTA * kAtomBytes, KA * RTA * kAtomBytes, words, C::ATOMS,
                     CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B) &&
-            encode3(&msb, u32, p.sfw, RTB * words, KA, p.B, RTB * kAtomBytes, KA * RTB * kAtomBytes, 2 * words,
+            encode_map3(&msb, u32, p.sfw, RTB * words, KA, p.B, RTB * kAtomBytes, KA * RTB * kAtomBytes, 2 * words,
                     C::ATOMS, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
   if (splits > 1)
-    ok = ok && encode3(&mo, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, p.part, p.N, p.M, splits * p.B, p.N * 4, p.M * p.N * 4, 16,
+    ok = ok && encode_map3(&mo, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, p.part, p.N, p.M, splits * p.B, p.N * 4, p.M * p.N * 4, 16,
                        32, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE);
   else
-    ok = ok && encode3(&mo, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.out, p.N, p.M, p.B, p.N * 2, p.M * p.N * 2, 32, 32,
+    ok = ok && encode_map3(&mo, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.out, p.N, p.M, p.B, p.N * 2, p.M * p.N * 2, 32, 32,
                        CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE);
   if (!ok) {
     *msg = "cuTensorMapEncodeTiled rejected a 4-bit operand or output";
@@ -656,6 +643,18 @@ cudaError_t launch_t(const Fp4Problem& p, int sms, cudaStream_t stream, const ch
 }
 
 }  // namespace
+
+bool encode_map3(CUtensorMap* m, CUtensorMapDataType dtype, const void* base, int64_t d0, int64_t d1, int64_t d2,
+             int64_t s1, int64_t s2, int b0, int b1, CUtensorMapSwizzle sw, CUtensorMapL2promotion l2) {
+  EncodeTiledFn encode = encode_tiled_fn();
+  if (encode == nullptr) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d0), static_cast<cuuint64_t>(d1), static_cast<cuuint64_t>(d2)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(s1), static_cast<cuuint64_t>(s2)};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(b0), static_cast<cuuint32_t>(b1), 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return encode(m, dtype, 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw, l2,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 // Few output tiles: split K so that about 64 pairs have work, with at least
 // four stages a split and at most 8 splits.  A function of the shape alone.

@@ -102,12 +102,12 @@ __device__ __forceinline__ void commit_elected(uint32_t elected, uint64_t* bar) 
 }
 
 __device__ __forceinline__ void tma_load_elected(uint32_t elected, uint32_t dst, const CUtensorMap* m, uint32_t bar,
-                                                 int c0, int c1) {
+                                                 int c0, int c1, int c2) {
   asm volatile(
-      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-      "@q cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];\n\t}" ::
-          "r"(dst),
-      "l"(m), "r"(bar), "r"(c0), "r"(c1), "r"(elected)
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %6, 0;\n\t"
+      "@q cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], "
+      "[%2];\n\t}" ::"r"(dst),
+      "l"(m), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(elected)
       : "memory");
 }
 
@@ -125,6 +125,7 @@ struct Args {
   const float* gw;
   __nv_bfloat16* out;
   int M, N;
+  int RTW, TT;     // weight row tiles, token tiles
   int KT;          // stages of K
   int last_steps;  // MMA steps of the last one
   int splits;      // cluster size S
@@ -148,7 +149,13 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0);  // uniform
   const int lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_ctarank());
-  const int tile = static_cast<int>(blockIdx.x) / a.splits;
+  // cluster = ((batch * TT) + token tile) * RTW + weight tile
+  const int cluster = static_cast<int>(blockIdx.x) / a.splits;
+  const int tile = cluster % a.RTW;
+  const int tt = cluster / a.RTW % a.TT;
+  const int b = cluster / a.RTW / a.TT;
+  const int m0 = tt * NTOK;
+  const int M = min(NTOK, a.M - m0);  // rows of this tile
   const int kt0 = rank * a.KT / a.splits;
   const int nk = (rank + 1) * a.KT / a.splits - kt0;  // >= 1: splits <= KT
   const uint32_t base = smem_u32(smem);
@@ -167,9 +174,9 @@ __global__ void __launch_bounds__(THREADS, 1)
   auto load_w = [&](int i, int st) {
     const uint32_t bar = smem_u32(&full_w[st]);
     expect_tx_elected(elected, bar, W_BYTES + C::SF_BYTES);
-    tma_load_elected(elected, base + C::OFF_W + st * W_BYTES, &tmW, bar, (kt0 + i) * BKB, tile * ROWS);
+    tma_load_elected(elected, base + C::OFF_W + st * W_BYTES, &tmW, bar, (kt0 + i) * BKB, tile * ROWS, b);
     tma_load_elected(elected, base + C::OFF_SFW + st * C::SF_BYTES, &tmSFW, bar, tile * (kAtomBytes / 4),
-                     (kt0 + i) * C::ATOMS);
+                     (kt0 + i) * C::ATOMS, b);
   };
   const int first = nk < C::STAGES ? nk : C::STAGES;
   if (warp == 0) {
@@ -192,6 +199,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int my_n = a.splits == 1 ? tile * ROWS + (warp & 3) * 32 + lane
                                  : tile * ROWS + rank * per + static_cast<int>(threadIdx.x) % per;
   float bias_n = 0.f, alpha = 1.f;
+  __nv_bfloat16* out = a.out + (static_cast<int64_t>(b) * a.M + m0) * a.N;
 
   if (warp == 0) {
     // ------------------------------------------------ weight producer, later rounds
@@ -263,8 +271,9 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (i >= C::STAGES && !mbar_wait_warp(&empty[st], ph, abort_flag)) break;
       const uint32_t bar = smem_u32(&full_x[st]);
       expect_tx_elected(elected, bar, C::X_BYTES + C::SF_BYTES);
-      tma_load_elected(elected, base + C::OFF_X + st * C::X_BYTES, &tmX, bar, (kt0 + i) * BKB, 0);
-      tma_load_elected(elected, base + C::OFF_SFX + st * C::SF_BYTES, &tmSFX, bar, 0, (kt0 + i) * C::ATOMS);
+      tma_load_elected(elected, base + C::OFF_X + st * C::X_BYTES, &tmX, bar, (kt0 + i) * BKB, m0, b);
+      tma_load_elected(elected, base + C::OFF_SFX + st * C::SF_BYTES, &tmSFX, bar, tt * (kAtomBytes / 4),
+                       (kt0 + i) * C::ATOMS, b);
       ++issued;
       if (++st == C::STAGES) {
         st = 0;
@@ -292,15 +301,15 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t dst = a.splits == 1 ? 0u
                                        : map_shared_rank(base + C::OFF_RECV, static_cast<uint32_t>(owner)) +
                                              static_cast<uint32_t>(((rank * NTOK) * per + wrow - owner * per) * 4);
-    for (int c = 0; c < a.M; c += 16) {
+    for (int c = 0; c < M; c += 16) {
       uint32_t r[16];
       tmem_ld_32x32b_x16(lrow + c, r);
       tmem_ld_wait();
       if (a.splits == 1) {
 #pragma unroll
         for (int j = 0; j < 16; ++j)
-          if (c + j < a.M && my_n < a.N)
-            a.out[static_cast<int64_t>(c + j) * a.N + my_n] =
+          if (c + j < M && my_n < a.N)
+            out[static_cast<int64_t>(c + j) * a.N + my_n] =
                 __float2bfloat16_rn(fmaf(__uint_as_float(r[j]), alpha, bias_n));
       } else {
 #pragma unroll
@@ -314,10 +323,10 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (a.splits > 1 && !*abort_flag && my_n < a.N) {
     const float* recv = reinterpret_cast<const float*>(smem + C::OFF_RECV);
     const int nl = static_cast<int>(threadIdx.x) % per;
-    for (int m = static_cast<int>(threadIdx.x) / per; m < a.M; m += THREADS / per) {
+    for (int m = static_cast<int>(threadIdx.x) / per; m < M; m += THREADS / per) {
       float acc = 0.f;
       for (int s = 0; s < a.splits; ++s) acc += recv[(s * NTOK + m) * per + nl];
-      a.out[static_cast<int64_t>(m) * a.N + my_n] = __float2bfloat16_rn(fmaf(acc, alpha, bias_n));
+      out[static_cast<int64_t>(m) * a.N + my_n] = __float2bfloat16_rn(fmaf(acc, alpha, bias_n));
     }
   }
   __syncthreads();
@@ -325,18 +334,6 @@ __global__ void __launch_bounds__(THREADS, 1)
     tc_fence_after();
     tmem_dealloc(tmem, C::TMEM_COLS);
   }
-}
-
-bool encode2(CUtensorMap* m, CUtensorMapDataType dtype, const void* base, int64_t d0, int64_t d1, int64_t s1, int b0,
-             int b1, CUtensorMapSwizzle sw) {
-  EncodeTiledFn encode = encode_tiled_fn();
-  if (encode == nullptr) return false;
-  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(d0), static_cast<cuuint64_t>(d1)};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(s1)};
-  const cuuint32_t box[2] = {static_cast<cuuint32_t>(b0), static_cast<cuuint32_t>(b1)};
-  const cuuint32_t estr[2] = {1, 1};
-  return encode(m, dtype, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
-                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 void fill_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, int grid, int splits, int smem, cudaStream_t s) {
@@ -398,10 +395,14 @@ cudaError_t launch_t(const Fp4Problem& p, int sms, cudaStream_t stream, const ch
   const int words = kAtomBytes / 4;
   CUtensorMap mw, mx, msw, msx;
   const auto u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8, u32 = CU_TENSOR_MAP_DATA_TYPE_UINT32;
-  if (!encode2(&mw, u8, p.w, kb, p.N, kb, BKB, ROWS, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !encode2(&mx, u8, p.x, kb, p.M, kb, BKB, NTOK, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !encode2(&msw, u32, p.sfw, RTW * words, KA, RTW * kAtomBytes, words, C::ATOMS, CU_TENSOR_MAP_SWIZZLE_NONE) ||
-      !encode2(&msx, u32, p.sfx, RTX * words, KA, RTX * kAtomBytes, words, C::ATOMS, CU_TENSOR_MAP_SWIZZLE_NONE)) {
+  const auto sw = CU_TENSOR_MAP_SWIZZLE_128B, flat = CU_TENSOR_MAP_SWIZZLE_NONE;
+  const auto l2 = CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
+  if (!encode_map3(&mw, u8, p.w, kb, p.N, p.B, kb, p.N * kb, BKB, ROWS, sw, l2) ||
+      !encode_map3(&mx, u8, p.x, kb, p.M, p.B, kb, p.M * kb, BKB, NTOK, sw, l2) ||
+      !encode_map3(&msw, u32, p.sfw, RTW * words, KA, p.B, RTW * kAtomBytes, KA * RTW * kAtomBytes, words, C::ATOMS,
+                   flat, l2) ||
+      !encode_map3(&msx, u32, p.sfx, RTX * words, KA, p.B, RTX * kAtomBytes, KA * RTX * kAtomBytes, words, C::ATOMS,
+                   flat, l2)) {
     *msg = "cuTensorMapEncodeTiled rejected a 4-bit operand";
     return cudaErrorInvalidValue;
   }
@@ -412,14 +413,17 @@ cudaError_t launch_t(const Fp4Problem& p, int sms, cudaStream_t stream, const ch
   a.out = static_cast<__nv_bfloat16*>(p.out);
   a.M = static_cast<int>(p.M);
   a.N = static_cast<int>(p.N);
+  a.RTW = static_cast<int>(RTW);
+  a.TT = static_cast<int>(ceil_div(p.M, NTOK));
   a.KT = static_cast<int>(ceil_div(p.K, BK));
   a.last_steps = static_cast<int>(ceil_div(p.K - static_cast<int64_t>(a.KT - 1) * BK, MMA_K));
   // the largest K split whose clusters all run at once
+  const int64_t tiles = p.B * a.TT * RTW;
   a.splits = 8;
-  while (a.splits > 1 && (a.splits > a.KT || RTW > max_clusters<FMT, NTOK>(a.splits, sms))) a.splits >>= 1;
+  while (a.splits > 1 && (a.splits > a.KT || tiles > max_clusters<FMT, NTOK>(a.splits, sms))) a.splits >>= 1;
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[2];
-  fill_config(&cfg, attr, static_cast<int>(RTW) * a.splits, a.splits, C::SMEM, stream);
+  fill_config(&cfg, attr, static_cast<int>(tiles) * a.splits, a.splits, C::SMEM, stream);
   cudaError_t e = cudaLaunchKernelEx(&cfg, gemm_fp4_small_kernel<FMT, NTOK>, mw, mx, msw, msx, a);
   if (e != cudaSuccess) *msg = "small-M 4-bit GEMM launch failed";
   return e;
@@ -435,11 +439,24 @@ cudaError_t launch_fmt(const Fp4Problem& p, int sms, cudaStream_t stream, const 
 
 }  // namespace
 
+// Where this kernel is the faster one (a function of the shape alone: the
+// workspace size depends on it).  It wins while each CTA's chain is short; the
+// CTA-pair kernel moves fewer bytes per MMA and wins on long ones.  Measured
+// (us, MXFP4, this kernel / CTA pairs): N = K = 4096, M = 128 7.1 / 9.5, 256
+// 10.1 / 11.3, 512 (16 stages a CTA) 11.1 / 10.3; N = 14336, K = 4096, M = 64
+// 9.2 / 10.5, 128 11.1 / 10.5; N = 4096, K = 14336, M = 128 10.1 / 12.6, 256
+// (28 stages) 16.1 / 14.5; N = 1000, K = 4128, M = 1024 10.6 / 12.2; two waves
+// of tiles (N = 28672), M = 16 15.0 / 17.9, 64 17.7 / 15.4; 16 x [M, 512, 7168],
+// M = 16 7.8 / 13.4, 128 12.0 / 13.5, 256 14.7 / 13.5.
+bool fp4_use_small(int64_t B, int64_t M, int64_t N, int64_t K) {
+  if (M <= 32) return true;
+  const int64_t tiles = B * ceil_div(M, 128) * ceil_div(N, ROWS);
+  if (tiles > 152) return false;  // more than one CTA an SM
+  const int64_t splits = tiles <= 14 ? 8 : (tiles <= 36 ? 4 : (tiles <= 75 ? 2 : 1));
+  return ceil_div(ceil_div(K, BK), splits) <= (M <= 64 ? 16 : 14);
+}
+
 cudaError_t launch_gemm_fp4_small(const Fp4Problem& p, int sms, cudaStream_t stream, const char** msg) {
-  if (p.B != 1 || p.M < 1 || p.M > kFp4SmallMaxM) {
-    *msg = "small-M 4-bit GEMM: B and M out of range";
-    return cudaErrorInvalidValue;
-  }
   return p.fmt == kQNV4 ? launch_fmt<kQNV4>(p, sms, stream, msg) : launch_fmt<kQMX4>(p, sms, stream, msg);
 }
 
