@@ -56,7 +56,7 @@ mxfp8_status quantize_impl(int fmt, const void* x, int64_t B, int64_t M, int64_t
     return fail(MXFP8_ERR_INVALID_ARG, "x, codes and scales must be 16-byte aligned");
   int sms = 0;
   if ((st = mx::current_device(&sms)) != MXFP8_OK) return st;
-  cudaError_t e = mx::launch_quantize_fp4(fmt, x, B, M, K, g, q, s, packed, sms, as_stream(stream), false);
+  cudaError_t e = mx::launch_quantize_fp4(fmt, x, B, M, K, g, q, s, packed, as_stream(stream), false);
   return e == cudaSuccess ? MXFP8_OK : cuda_fail(e, "4-bit quantise launch");
 }
 
@@ -167,7 +167,7 @@ mxfp8_status mxfp8_fp4_unpack(const uint8_t* q, int64_t n, uint8_t* out_e4m3, mx
   int sms = 0;
   mxfp8_status st = mx::current_device(&sms);
   if (st != MXFP8_OK) return st;
-  cudaError_t e = mx::launch_fp4_unpack(q, n, out_e4m3, sms, as_stream(stream));
+  cudaError_t e = mx::launch_fp4_unpack(q, n, out_e4m3, as_stream(stream));
   return e == cudaSuccess ? MXFP8_OK : cuda_fail(e, "4-bit unpack launch");
 }
 
@@ -239,8 +239,8 @@ mxfp8_status mxfp8_fp4_linear(int fmt, const void* x_bf16, const uint8_t* x_q, c
   uint8_t* wsb = static_cast<uint8_t*>(workspace);
   cudaError_t e;
   if (have_x) {
-    e = mx::launch_quantize_fp4(fmt, x_bf16, B, M, K, x_tensor_scale, wsb + ws.xq, wsb + ws.sfx, true, sms,
-                                as_stream(stream), true);
+    e = mx::launch_quantize_fp4(fmt, x_bf16, B, M, K, x_tensor_scale, wsb + ws.xq, wsb + ws.sfx, true, as_stream(stream),
+                                true);
     o.x = wsb + ws.xq;
   } else {
     e = mx::launch_sf_pack(x_scale, B, M, fp4_scale_extent(fmt, K), wsb + ws.sfx, sms, as_stream(stream), true);
@@ -299,7 +299,7 @@ mxfp8_status mxfp8_rmsnorm_quantize(int fmt, const void* x_bf16, int64_t x_strid
   if ((st = mx::current_device(&sms)) != MXFP8_OK) return st;
   const mx::NormProblem p{fmt,         x_bf16, x_stride, residual, residual_stride, residual_is_f32 != 0,
                           residual_out, weight_bf16, y_bf16, eps, tensor_scale, M, K, q, scale, scale_packed != 0};
-  cudaError_t e = mx::launch_rmsnorm_quantize(p, sms, as_stream(stream));
+  cudaError_t e = mx::launch_rmsnorm_quantize(p, as_stream(stream));
   return e == cudaSuccess ? MXFP8_OK : cuda_fail(e, "norm launch");
 }
 
@@ -321,7 +321,7 @@ mxfp8_status mxfp8_silu_mul_quantize(int fmt, const void* gate_bf16, int64_t gat
   if ((st = mx::current_device(&sms)) != MXFP8_OK) return st;
   const mx::ActProblem p{fmt, gate_bf16, gate_stride, up_bf16, up_stride, tensor_scale, M, K, q, scale,
                          scale_packed != 0};
-  cudaError_t e = mx::launch_silu_mul_quantize(p, sms, as_stream(stream));
+  cudaError_t e = mx::launch_silu_mul_quantize(p, as_stream(stream));
   return e == cudaSuccess ? MXFP8_OK : cuda_fail(e, "activation launch");
 }
 

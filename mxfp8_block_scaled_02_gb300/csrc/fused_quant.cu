@@ -4,15 +4,18 @@
 //   rmsnorm : t = x + residual (fp32), y = t * rsqrt(mean(t^2) + eps) * w,
 //             outputs quantise(y), t rounded once to the residual's type, and
 //             optionally y as bf16;
-//   silu_mul: y = gate / (1 + exp(-gate)) * up, output quantise(y).
+//   silu_mul: y = gate / (1 + exp(-gate)) * up, output quantise(y);
+//   fp4     : y = x, the plain 4-bit quantise call;
+// and the exact widening of packed E2M1 codes to E4M3 bytes.
 //
 // y stays in fp32 from the sum to the element's rounding: it is rounded once.
-// Both read each input once and write each output once, and are bound by HBM
+// All read each input once and write each output once, and are bound by HBM
 // on long inputs and by one round trip to memory on short ones.
 //
-// A thread owns chunks of 8 consecutive elements (one 16-byte load of bf16), so
-// a 32-element block is 4 neighbouring lanes and its amax two shuffles; the
-// codes of a warp's chunks are contiguous.
+// A thread owns chunks of 16 consecutive elements: one NVFP4 block, or half a
+// 32-element one, so a block's scale is worked out once or twice.  The scale
+// bytes of four blocks are gathered into one word by shuffles (a byte at a time
+// into the packed atoms cost the activation 5 us of 52 at 4096 x 14336).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -30,48 +33,107 @@ namespace {
 struct QuantOut {
   uint8_t* q;
   uint8_t* s;
-  const float* g;  // NVFP4 tensor scale, or nullptr for 1
-  int64_t K;       // elements per row
-  int64_t RT;      // atom row tiles (packed scales)
+  const float* g;      // NVFP4 tensor scale, or nullptr for 1
+  int64_t K;           // elements per row
+  int64_t RT;          // packed scales: atom row tiles of a batch,
+  uint32_t rows_per_b;  // its rows (0: one batch)
+  int64_t b_stride;    // and its bytes
 };
 
-__device__ __forceinline__ void unpack_bf16x8(const uint4 v, float (&f)[8]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+QuantOut quant_out(int fmt, uint8_t* q, uint8_t* s, const float* g, int64_t B, int64_t M, int64_t K, bool packed) {
+  const int64_t ext = fp4_scale_extent(fmt, K);
+  return QuantOut{q, s, g, K, packed ? ceil_div(M, kAtomRows) : 0, B == 1 ? 0u : static_cast<uint32_t>(M), sf_packed_bytes(1, M, ext)};
+}
+
+// Chunk c of a row: 32 bytes of bf16 (64 of fp32), as whole sectors when the
+// rows start on 32-byte boundaries (wide; uniform over the grid), else as
+// 16-byte pieces.
+struct Chunk {
+  uint32_t w[8];
+};
+
+__device__ __forceinline__ Chunk zero_chunk() { return Chunk{{0, 0, 0, 0, 0, 0, 0, 0}}; }
+
+__device__ __forceinline__ Chunk load_32(const void* p, bool wide) {
+  Chunk r;
+  if (wide) {
+    ld_global_32(p, r.w);
+  } else {
+    const uint4* q = static_cast<const uint4*>(p);
+    const uint4 lo = q[0], hi = q[1];
+    r = Chunk{{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w}};
+  }
+  return r;
+}
+
+__device__ __forceinline__ void store_32(void* p, const uint32_t (&w)[8], bool wide) {
+  if (wide) {
+    st_global_32(p, w);
+  } else {
+    uint4* q = static_cast<uint4*>(p);
+    q[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    q[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
+__device__ __forceinline__ Chunk load16(const __nv_bfloat16* row, int c, bool wide) {
+  return load_32(row + 16 * static_cast<int64_t>(c), wide);
+}
+
+__device__ __forceinline__ void unpack16(const Chunk& v, float (&f)[16]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(w[i] << 16);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  for (int i = 0; i < 8; ++i) {
+    f[2 * i] = __uint_as_float(v.w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(v.w[i] & 0xFFFF0000u);
   }
 }
 
-__device__ __forceinline__ uint4 pack_bf16x8(const float (&f)[8]) {
-  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+__device__ __forceinline__ void store16(__nv_bfloat16* row, int c, const float (&f)[16], bool wide) {
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
+  store_32(row + 16 * static_cast<int64_t>(c), w, wide);
 }
 
-// Quantise chunk `c` (8 elements) of row `row` and store it.  Every lane of the
-// warp calls; only valid lanes store.  A row is whole blocks, so the lanes of a
-// block are valid together.
+// Quantise chunk `c` (16 elements) of row `row` and store it.  Every lane of the
+// warp calls with consecutive chunks, lane 0's a multiple of 32; only valid lanes
+// store.  A row is whole 32-element blocks.
 template <int FMT>
-__device__ __forceinline__ void quantize_store(const QuantOut& o, int64_t row, int c, bool valid, const float (&y)[8],
-                                               float six_g, float g) {
-  uint2 codes;
-  const uint32_t sb = quantize_lane8<FMT>(y, six_g, g, codes);
-  if (!valid) return;
-  constexpr int kLanes = q_block(FMT) / 8;
-  if (FMT == kQMX8)
-    *reinterpret_cast<uint2*>(o.q + row * o.K + 8 * static_cast<int64_t>(c)) = codes;
-  else
-    *reinterpret_cast<uint32_t*>(o.q + (row * o.K + 8 * static_cast<int64_t>(c)) / 2) = codes.x;
-  if (c % kLanes != 0) return;
-  const int64_t KB = o.K / q_block(FMT), kb = c / kLanes;
-  if (o.RT == 0) {
-    o.s[row * KB + kb] = static_cast<uint8_t>(sb);
-    return;
+__device__ __forceinline__ void quantize_store(const QuantOut& o, int64_t row, int c, bool valid, const float (&y)[16],
+                                               const TensorScale& ts) {
+  uint32_t codes[4];
+  const uint32_t sb = quantize_lane16<FMT>(y, ts, codes);
+  if (valid) {
+    const int64_t e = row * o.K + 16 * static_cast<int64_t>(c);
+    if (FMT == kQMX8)
+      *reinterpret_cast<uint4*>(o.q + e) = make_uint4(codes[0], codes[1], codes[2], codes[3]);
+    else
+      *reinterpret_cast<uint2*>(o.q + e / 2) = make_uint2(codes[0], codes[1]);
   }
-  uint8_t* word = o.s + ((kb >> 2) * o.RT + (row >> 7)) * kAtomBytes + (row & 31) * 16 + ((row >> 5) & 3) * 4;
-  word[kb & 3] = static_cast<uint8_t>(sb);
-  if (kb + 1 == KB)  // the bytes that pad the row to whole scale words are zero
-    for (int64_t p = (kb & 3) + 1; p < 4; ++p) word[p] = 0;
+  // word: the scale bytes of four consecutive blocks, zero past the row's end
+  constexpr int kLanes = q_block(FMT) / 16;  // lanes of a block
+  uint32_t word = valid ? sb : 0u;
+  word |= __shfl_xor_sync(0xFFFFFFFFu, word, kLanes) << 8;
+  word |= __shfl_xor_sync(0xFFFFFFFFu, word, 2 * kLanes) << 16;
+  if (!valid) return;
+  const int KB = static_cast<int>(o.K / q_block(FMT)), kb = c / kLanes;
+  if (o.RT != 0) {
+    if (c % (4 * kLanes) == 0) {
+      uint8_t* s = o.s;
+      int64_t r = row;
+      if (o.rows_per_b != 0) {  // more than one batch
+        const uint32_t b = static_cast<uint32_t>(row) / o.rows_per_b;
+        s += static_cast<int64_t>(b) * o.b_stride;
+        r -= static_cast<int64_t>(b) * o.rows_per_b;
+      }
+      *reinterpret_cast<uint32_t*>(s + ((kb >> 2) * o.RT + (r >> 7)) * kAtomBytes + (r & 31) * 16 + ((r >> 5) & 3) * 4) =
+          word;
+    }
+  } else if ((KB & 3) == 0) {
+    if (c % (4 * kLanes) == 0) *reinterpret_cast<uint32_t*>(o.s + row * KB + kb) = word;
+  } else if (c % kLanes == 0) {
+    o.s[row * KB + kb] = static_cast<uint8_t>(sb);
+  }
 }
 
 struct NormArgs {
@@ -83,79 +145,66 @@ struct NormArgs {
   const __nv_bfloat16* w;
   __nv_bfloat16* y;  // dense bf16 rows, or nullptr
   float eps;
+  bool wide;        // every row starts on a 32-byte boundary
   QuantOut o;
 };
 
-enum { kResNone = 0, kResBf16 = 1, kResF32 = 2 };
+constexpr int kNormThreads = 512;
 
-constexpr int norm_max_threads(int ch) { return ch == 1 ? 1024 : 512; }
-// With few chunks a thread the weight is loaded up front (a short call's
-// latency); with many, each SM has other rows to run while it is fetched from
-// L2, and the registers are worth more.
-template <int CH>
-constexpr bool kPreloadW = CH <= 2;
+enum { kResNone = 0, kResBf16 = 1, kResF32 = 2 };
 
 // One CTA per row, the row held in registers (CH chunks a thread) between the
 // sum of squares and the output, so x and the residual are read once.  The
-// norm's weight and the tensor scale depend on nothing the kernel before this
-// one writes and are read before the dependency wait; the next kernel in the
-// stream may start at once (a GEMM that reads the output after its own wait).
+// norm's weight depends on nothing the kernel before this one writes and is
+// read before the dependency wait; the next kernel in the stream may start at
+// once (a GEMM that reads the output after its own wait).
 template <int FMT, int CH, int RES>
-__global__ void __launch_bounds__(norm_max_threads(CH)) rmsnorm_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(kNormThreads, CH == 1 ? 3 : (CH == 2 ? 2 : 1)) rmsnorm_kernel(const NormArgs a) {
   __shared__ float part[32];
   launch_dependents();
   const int64_t row = blockIdx.x;
-  const int nchunks = static_cast<int>(a.o.K / 8);
+  const int nchunks = static_cast<int>(a.o.K / 16);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const uint4* wp = reinterpret_cast<const uint4*>(a.w);
-  uint4 w[kPreloadW<CH> ? CH : 1];
-  if (kPreloadW<CH>) {
+  Chunk w = zero_chunk();
+  if (CH == 1) w = static_cast<int>(threadIdx.x) < nchunks ? load16(a.w, threadIdx.x, a.wide) : zero_chunk();
+  grid_dependency_wait();
+  // all loads first, so that they are in flight together
+  const float g = FMT == kQNV4 && a.o.g != nullptr ? *a.o.g : 1.f;
+  Chunk xv[CH], rv[CH][RES == kResF32 ? 2 : 1];
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      const int c = threadIdx.x + i * blockDim.x;
-      w[i] = c < nchunks ? __ldg(wp + c) : make_uint4(0, 0, 0, 0);
+  for (int i = 0; i < CH; ++i) {
+    const int c = threadIdx.x + i * blockDim.x;
+    const bool valid = c < nchunks;
+    xv[i] = valid ? load16(a.x + row * a.x_stride, c, a.wide) : zero_chunk();
+    if (RES == kResBf16)
+      rv[i][0] =
+          valid ? load16(static_cast<const __nv_bfloat16*>(a.res) + row * a.res_stride, c, a.wide) : zero_chunk();
+    if (RES == kResF32) {
+      const float* rp = static_cast<const float*>(a.res) + row * a.res_stride + 16 * static_cast<int64_t>(c);
+#pragma unroll
+      for (int h = 0; h < (RES == kResF32 ? 2 : 1); ++h) rv[i][h] = valid ? load_32(rp + 8 * h, a.wide) : zero_chunk();
     }
   }
-  grid_dependency_wait();
-  float t[CH][8];
-  {
-    uint4 xv[CH], r0[CH], r1[CH];
+  float t[CH][16];
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      const int c = threadIdx.x + i * blockDim.x;
-      const uint4 z = make_uint4(0, 0, 0, 0);
-      xv[i] = r0[i] = r1[i] = z;
-      if (c >= nchunks) continue;
-      xv[i] = *(reinterpret_cast<const uint4*>(a.x + row * a.x_stride) + c);
-      if (RES == kResBf16)
-        r0[i] = *(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.res) + row * a.res_stride) + c);
-      if (RES == kResF32) {
-        const uint4* rp = reinterpret_cast<const uint4*>(static_cast<const float*>(a.res) + row * a.res_stride) + 2 * c;
-        r0[i] = rp[0];
-        r1[i] = rp[1];
-      }
+  for (int i = 0; i < CH; ++i) {
+    unpack16(xv[i], t[i]);
+    if (RES == kResBf16) {
+      float r[16];
+      unpack16(rv[i][0], r);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) t[i][j] += r[j];
     }
+    if (RES == kResF32) {
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      unpack_bf16x8(xv[i], t[i]);
-      if (RES == kResBf16) {
-        float r[8];
-        unpack_bf16x8(r0[i], r);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) t[i][j] += r[j];
-      }
-      if (RES == kResF32) {
-        const uint32_t r[8] = {r0[i].x, r0[i].y, r0[i].z, r0[i].w, r1[i].x, r1[i].y, r1[i].z, r1[i].w};
-#pragma unroll
-        for (int j = 0; j < 8; ++j) t[i][j] += __uint_as_float(r[j]);
-      }
+      for (int j = 0; j < 16; ++j) t[i][j] += __uint_as_float(rv[i][RES == kResF32 ? j >> 3 : 0].w[j & 7]);
     }
   }
   float ss = 0.f;
 #pragma unroll
   for (int i = 0; i < CH; ++i)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) ss = fmaf(t[i][j], t[i][j], ss);
+    for (int j = 0; j < 16; ++j) ss = fmaf(t[i][j], t[i][j], ss);
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, d);
   if (lane == 0) part[warp] = ss;
@@ -165,77 +214,132 @@ __global__ void __launch_bounds__(norm_max_threads(CH)) rmsnorm_kernel(const Nor
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, d);
   const float rstd = rsqrtf(ss / static_cast<float>(a.o.K) + a.eps);
-  const float g = FMT == kQNV4 && a.o.g != nullptr ? *a.o.g : 1.f;
-  const float six_g = 6.f * g;
+  const TensorScale ts = tensor_scale(g);
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
     const int c = threadIdx.x + i * blockDim.x;
     if (i > 0 && (c & ~31) >= nchunks) break;  // the whole warp is past the row
     const bool valid = c < nchunks;
-    if (RES == kResBf16 && valid)
-      *(reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.res_out) + row * a.o.K) + c) = pack_bf16x8(t[i]);
+    if (RES == kResBf16 && valid) store16(static_cast<__nv_bfloat16*>(a.res_out) + row * a.o.K, c, t[i], a.wide);
     if (RES == kResF32 && valid) {
-      float4* rp = reinterpret_cast<float4*>(static_cast<float*>(a.res_out) + row * a.o.K) + 2 * c;
-      rp[0] = make_float4(t[i][0], t[i][1], t[i][2], t[i][3]);
-      rp[1] = make_float4(t[i][4], t[i][5], t[i][6], t[i][7]);
-    }
-    float wf[8], y[8];
-    unpack_bf16x8(kPreloadW<CH> ? w[kPreloadW<CH> ? i : 0] : (valid ? __ldg(wp + c) : make_uint4(0, 0, 0, 0)), wf);
+      float* rp = static_cast<float*>(a.res_out) + row * a.o.K + 16 * static_cast<int64_t>(c);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) y[j] = t[i][j] * rstd * wf[j];
-    if (a.y != nullptr && valid) *(reinterpret_cast<uint4*>(a.y + row * a.o.K) + c) = pack_bf16x8(y);
-    quantize_store<FMT>(a.o, row, c, valid, y, six_g, g);
+      for (int h = 0; h < 2; ++h) {
+        uint32_t r[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) r[j] = __float_as_uint(t[i][8 * h + j]);
+        store_32(rp + 8 * h, r, a.wide);
+      }
+    }
+    float wf[16];
+    unpack16(CH == 1 ? w : (valid ? load16(a.w, c, a.wide) : zero_chunk()), wf);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) t[i][j] = t[i][j] * rstd * wf[j];
+    if (a.y != nullptr && valid) store16(a.y + row * a.o.K, c, t[i], a.wide);
+    quantize_store<FMT>(a.o, row, c, valid, t[i], ts);
   }
 }
+
+constexpr int kRowThreads = 128;
 
 struct ActArgs {
   const __nv_bfloat16* gate;
   const __nv_bfloat16* up;
   int64_t gate_stride, up_stride;
-  int segs;  // CTAs per row
+  int segs;   // CTAs per row
+  bool wide;  // every row starts on a 32-byte boundary
   QuantOut o;
 };
 
-constexpr int kActThreads = 128;
 
-// kActThreads x CH chunks of one row per CTA.
+// A CTA takes CH x blockDim.x chunks of one row (a row is `segs` CTAs).
 template <int FMT, int CH>
-__global__ void __launch_bounds__(kActThreads) silu_mul_kernel(const ActArgs a) {
+__global__ void __launch_bounds__(kRowThreads, 12) silu_mul_kernel(const ActArgs a) {
   launch_dependents();
   const int64_t row = blockIdx.x / a.segs;
-  const int c0 = static_cast<int>(blockIdx.x - row * a.segs) * (kActThreads * CH) + threadIdx.x;
-  const int nchunks = static_cast<int>(a.o.K / 8);
+  const int c0 = static_cast<int>(blockIdx.x - row * a.segs) * (CH * blockDim.x) + threadIdx.x;
+  const int nchunks = static_cast<int>(a.o.K / 16);
   grid_dependency_wait();
-  uint4 gv[CH], uv[CH];
+  Chunk gv[CH], uv[CH];
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
-    const int c = c0 + i * kActThreads;
-    gv[i] = uv[i] = make_uint4(0, 0, 0, 0);
-    if (c >= nchunks) continue;
-    gv[i] = *(reinterpret_cast<const uint4*>(a.gate + row * a.gate_stride) + c);
-    uv[i] = *(reinterpret_cast<const uint4*>(a.up + row * a.up_stride) + c);
+    const int c = c0 + i * blockDim.x;
+    gv[i] = c < nchunks ? load16(a.gate + row * a.gate_stride, c, a.wide) : zero_chunk();
+    uv[i] = c < nchunks ? load16(a.up + row * a.up_stride, c, a.wide) : zero_chunk();
   }
-  const float g = FMT == kQNV4 && a.o.g != nullptr ? *a.o.g : 1.f;
-  const float six_g = 6.f * g;
+  const TensorScale ts = tensor_scale(FMT == kQNV4 && a.o.g != nullptr ? *a.o.g : 1.f);
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
-    const int c = c0 + i * kActThreads;
-    if ((c & ~31) >= nchunks) break;
-    float gt[8], up[8], y[8];
-    unpack_bf16x8(gv[i], gt);
-    unpack_bf16x8(uv[i], up);
+    const int c = c0 + i * blockDim.x;
+    if ((c & ~31) >= nchunks) return;  // the whole warp is past the row
+    float gt[16], up[16];
+    unpack16(gv[i], gt);
+    unpack16(uv[i], up);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < 16; ++j) {
       // gate / (1 + exp(-gate)) with the exponential's argument <= 0, so that
       // nothing overflows and very negative gates keep their value
       const float e = __expf(-fabsf(gt[j]));
-      y[j] = gt[j] * __fdividef(gt[j] >= 0.f ? 1.f : e, 1.f + e) * up[j];
+      gt[j] = gt[j] * __fdividef(gt[j] >= 0.f ? 1.f : e, 1.f + e) * up[j];
     }
-    quantize_store<FMT>(a.o, row, c, c < nchunks, y, six_g, g);
+    quantize_store<FMT>(a.o, row, c, c < nchunks, gt, ts);
   }
 }
 
-cudaError_t launch_pdl(void* kern, int64_t grid, int threads, void* args, cudaStream_t stream) {
+struct Fp4Args {
+  const __nv_bfloat16* x;  // dense rows
+  int segs;                // CTAs per row
+  bool wide;
+  QuantOut o;
+};
+
+// kEarly as in quantize.cu: only the activation quantise inside a linear call
+// lets the next kernel start early, never the call that may make weights.
+template <int FMT, bool kEarly, int CH>
+__global__ void __launch_bounds__(kRowThreads, 12) quantize_fp4_kernel(const Fp4Args a) {
+  if (kEarly) {
+    launch_dependents();
+    grid_dependency_wait();
+  }
+  const int64_t row = blockIdx.x / a.segs;
+  const int c0 = static_cast<int>(blockIdx.x - row * a.segs) * (CH * blockDim.x) + threadIdx.x;
+  const int nchunks = static_cast<int>(a.o.K / 16);
+  Chunk v[CH];
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int c = c0 + i * blockDim.x;
+    v[i] = c < nchunks ? load16(a.x + row * a.o.K, c, a.wide) : zero_chunk();
+  }
+  const TensorScale ts = tensor_scale(FMT == kQNV4 && a.o.g != nullptr ? *a.o.g : 1.f);
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int c = c0 + i * blockDim.x;
+    if ((c & ~31) >= nchunks) return;  // the whole warp is past the row
+    float x[16];
+    unpack16(v[i], x);
+    quantize_store<FMT>(a.o, row, c, c < nchunks, x, ts);
+  }
+}
+
+// Four E2M1 codes (the low 16 bits of w) -> four E4M3 bytes, a table lookup by
+// byte permute; the signs move from bit 3 of a nibble to bit 7 of a byte.
+__device__ __forceinline__ uint32_t e2m1x4_to_e4m3(uint32_t w) {
+  const uint32_t mag = __byte_perm(0x3C383000u, 0x4C484440u, w & 0x7777u);
+  const uint32_t sign = ((w & 0x8u) << 4) | ((w & 0x80u) << 8) | ((w & 0x800u) << 12) | ((w & 0x8000u) << 16);
+  return mag | sign;
+}
+
+// 16 codes a lane: 8 bytes in, 16 out, both contiguous over the warp.
+__global__ void __launch_bounds__(256) fp4_unpack_kernel(const uint2* __restrict__ q, uint4* __restrict__ out,
+                                                         uint64_t n) {
+  const uint64_t i = static_cast<uint64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+  if (i >= n) return;
+  const uint2 v = __ldg(q + i);
+  out[i] = make_uint4(e2m1x4_to_e4m3(v.x), e2m1x4_to_e4m3(v.x >> 16), e2m1x4_to_e4m3(v.y), e2m1x4_to_e4m3(v.y >> 16));
+}
+
+cudaError_t launch_pdl(const void* kern, int64_t grid, int threads, void* args, cudaStream_t stream,
+                       bool programmatic = true) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
   cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
@@ -244,9 +348,42 @@ cudaError_t launch_pdl(void* kern, int64_t grid, int threads, void* args, cudaSt
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = programmatic ? 1 : 0;
   void* params[1] = {args};
   return cudaLaunchKernelExC(&cfg, kern, params);
+}
+
+// Chunks a thread, threads and CTAs for M rows of K elements, the CTAs of a row
+// as even as whole warps allow.  Two chunks a thread keep more bytes in flight
+// on long inputs (4-bit quantise, 14336 x 4096: 25.6 -> 24.3 us) and one starts
+// more CTAs on short ones (activation, 512 x 14336: 7.0 -> 6.6 us).
+int row_split(int64_t M, int64_t K, int* threads, int* segs) {
+  const int64_t chunks = K / 16;
+  const int ch = chunks >= 64 && M * chunks >= 152ll * 32 * 2 * kRowThreads ? 2 : 1;
+  *segs = static_cast<int>(ceil_div(chunks, ch * kRowThreads));
+  *threads = static_cast<int>(ceil_div(ceil_div(chunks, *segs * ch), 32) * 32);
+  return ch;
+}
+
+// Whether rows of `elem`-byte elements at p, `stride` elements apart, all start
+// on 32-byte boundaries (absent tensors do).
+bool rows_32(const void* p, int64_t stride, int elem) {
+  return p == nullptr || (reinterpret_cast<uintptr_t>(p) % 32 == 0 && stride * elem % 32 == 0);
+}
+
+template <int FMT>
+const void* act_kernel(int ch) {
+  return ch == 2 ? reinterpret_cast<const void*>(silu_mul_kernel<FMT, 2>)
+                 : reinterpret_cast<const void*>(silu_mul_kernel<FMT, 1>);
+}
+
+template <int FMT>
+const void* fp4_kernel(bool early, int ch) {
+  if (early)
+    return ch == 2 ? reinterpret_cast<const void*>(quantize_fp4_kernel<FMT, true, 2>)
+                   : reinterpret_cast<const void*>(quantize_fp4_kernel<FMT, true, 1>);
+  return ch == 2 ? reinterpret_cast<const void*>(quantize_fp4_kernel<FMT, false, 2>)
+                 : reinterpret_cast<const void*>(quantize_fp4_kernel<FMT, false, 1>);
 }
 
 template <int FMT, int CH>
@@ -258,12 +395,12 @@ void* norm_kernel(int res) {
 
 template <int FMT>
 void* norm_kernel(int ch, int res) {
-  return ch == 1 ? norm_kernel<FMT, 1>(res) : (ch == 2 ? norm_kernel<FMT, 2>(res) : (ch == 4 ? norm_kernel<FMT, 4>(res) : norm_kernel<FMT, 8>(res)));
+  return ch == 1 ? norm_kernel<FMT, 1>(res) : (ch == 2 ? norm_kernel<FMT, 2>(res) : norm_kernel<FMT, 4>(res));
 }
 
 }  // namespace
 
-cudaError_t launch_rmsnorm_quantize(const NormProblem& p, int sms, cudaStream_t stream) {
+cudaError_t launch_rmsnorm_quantize(const NormProblem& p, cudaStream_t stream) {
   if (p.M == 0) return cudaSuccess;
   NormArgs a;
   a.x = static_cast<const __nv_bfloat16*>(p.x);
@@ -274,44 +411,61 @@ cudaError_t launch_rmsnorm_quantize(const NormProblem& p, int sms, cudaStream_t 
   a.w = static_cast<const __nv_bfloat16*>(p.w);
   a.y = static_cast<__nv_bfloat16*>(p.y);
   a.eps = p.eps;
-  a.o = QuantOut{p.q, p.s, p.g, p.K, p.packed ? ceil_div(p.M, kAtomRows) : 0};
+  a.o = quant_out(p.fmt, p.q, p.s, p.g, 1, p.M, p.K, p.packed);
+  const int re = p.res_f32 ? 4 : 2;
+  a.wide = rows_32(p.x, p.x_stride, 2) && rows_32(p.res, p.res_stride, re) && rows_32(p.res_out, p.K, re) &&
+           rows_32(p.w, 0, 2) && rows_32(p.y, p.K, 2);
   const int res = p.res == nullptr ? kResNone : (p.res_f32 ? kResF32 : kResBf16);
-  const int64_t chunks = p.K / 8;
-  // One chunk a thread while that fits a CTA; with more rows than the GPU runs
-  // at once, four, so that each SM has several rows' loads in flight.
-  int ch = p.M >= 4 * sms ? 4 : 1;
-  while (ceil_div(chunks, ch) > norm_max_threads(ch)) ch *= 2;
-  if (ch > 8) return cudaErrorInvalidValue;  // the host refuses these first
+  const int64_t chunks = p.K / 16;
+  // one chunk a thread while that fits a CTA
+  int ch = 1;
+  while (ceil_div(chunks, ch) > kNormThreads) ch *= 2;
+  if (ch > 4) return cudaErrorInvalidValue;  // the host refuses these first
   const int threads = static_cast<int>(ceil_div(ceil_div(chunks, ch), 32) * 32);
   void* k = p.fmt == kQMX8 ? norm_kernel<kQMX8>(ch, res)
                            : (p.fmt == kQMX4 ? norm_kernel<kQMX4>(ch, res) : norm_kernel<kQNV4>(ch, res));
   return launch_pdl(k, p.M, threads, &a, stream);
 }
 
-cudaError_t launch_silu_mul_quantize(const ActProblem& p, int sms, cudaStream_t stream) {
+cudaError_t launch_silu_mul_quantize(const ActProblem& p, cudaStream_t stream) {
   if (p.M == 0) return cudaSuccess;
   ActArgs a;
   a.gate = static_cast<const __nv_bfloat16*>(p.gate);
   a.up = static_cast<const __nv_bfloat16*>(p.up);
   a.gate_stride = p.gate_stride;
   a.up_stride = p.up_stride;
-  a.o = QuantOut{p.q, p.s, p.g, p.K, p.packed ? ceil_div(p.M, kAtomRows) : 0};
-  const int64_t chunks = p.K / 8;
-  // two chunks a thread once that still gives every SM work
-  const bool two = p.M * ceil_div(chunks, 2 * kActThreads) >= 4 * static_cast<int64_t>(sms);
-  a.segs = static_cast<int>(ceil_div(chunks, two ? 2 * kActThreads : kActThreads));
+  a.o = quant_out(p.fmt, p.q, p.s, p.g, 1, p.M, p.K, p.packed);
+  a.wide = rows_32(p.gate, p.gate_stride, 2) && rows_32(p.up, p.up_stride, 2);
+  int threads;
+  const int ch = row_split(p.M, p.K, &threads, &a.segs);
   const int64_t grid = p.M * a.segs;
   if (grid > 0x7FFFFFFFll) return cudaErrorInvalidValue;  // the host refuses these first
-  void* k;
-  if (two)
-    k = p.fmt == kQMX8 ? reinterpret_cast<void*>(silu_mul_kernel<kQMX8, 2>)
-                       : (p.fmt == kQMX4 ? reinterpret_cast<void*>(silu_mul_kernel<kQMX4, 2>)
-                                         : reinterpret_cast<void*>(silu_mul_kernel<kQNV4, 2>));
-  else
-    k = p.fmt == kQMX8 ? reinterpret_cast<void*>(silu_mul_kernel<kQMX8, 1>)
-                       : (p.fmt == kQMX4 ? reinterpret_cast<void*>(silu_mul_kernel<kQMX4, 1>)
-                                         : reinterpret_cast<void*>(silu_mul_kernel<kQNV4, 1>));
-  return launch_pdl(k, grid, kActThreads, &a, stream);
+  const void* k = p.fmt == kQMX8 ? act_kernel<kQMX8>(ch) : (p.fmt == kQMX4 ? act_kernel<kQMX4>(ch) : act_kernel<kQNV4>(ch));
+  return launch_pdl(k, grid, threads, &a, stream);
+}
+
+cudaError_t launch_quantize_fp4(int fmt, const void* x, int64_t B, int64_t M, int64_t K, const float* g, uint8_t* q,
+                                uint8_t* s, bool packed_scales, cudaStream_t stream, bool early_trigger) {
+  if (B * M == 0) return cudaSuccess;
+  Fp4Args a;
+  a.x = static_cast<const __nv_bfloat16*>(x);
+  a.wide = rows_32(x, K, 2);
+  a.o = quant_out(fmt, q, s, g, B, M, K, packed_scales);
+  int threads;
+  const int ch = row_split(B * M, K, &threads, &a.segs);
+  const int64_t grid = B * M * a.segs;
+  if (grid > 0x7FFFFFFFll) return cudaErrorInvalidValue;  // the host refuses these first
+  const void* k = fmt == kQNV4 ? fp4_kernel<kQNV4>(early_trigger, ch) : fp4_kernel<kQMX4>(early_trigger, ch);
+  return launch_pdl(k, grid, threads, &a, stream, early_trigger);
+}
+
+cudaError_t launch_fp4_unpack(const uint8_t* q, int64_t n, uint8_t* out, cudaStream_t stream) {
+  const int64_t chunks = n / 16, grid = ceil_div(chunks, 256);
+  if (grid == 0) return cudaSuccess;
+  if (grid > 0x7FFFFFFFll) return cudaErrorInvalidValue;  // the host refuses these first
+  fp4_unpack_kernel<<<static_cast<unsigned>(grid), 256, 0, stream>>>(
+      reinterpret_cast<const uint2*>(q), reinterpret_cast<uint4*>(out), static_cast<uint64_t>(chunks));
+  return cudaGetLastError();
 }
 
 }  // namespace mx

@@ -55,14 +55,33 @@ __device__ __forceinline__ float e4m3_to_f32(uint32_t b) {
   return e ? __uint_as_float(((e + 120u) << 23) | (m << 20)) : static_cast<float>(m) * 0.001953125f;  // 2^-9
 }
 
+// NVFP4's tensor scale g and what the blocks share of it.
+struct TensorScale {
+  float g, six_g, inv_lo, inv_hi;
+};
+
+__device__ __forceinline__ TensorScale tensor_scale(float g) {
+  const float six_g = 6.f * g;
+  const float inv = __fdividef(1.f, six_g);
+  // an interval around 1 / (6 g), wider than inv's (2 ulp) and a product's rounding
+  return TensorScale{g, six_g, inv * (1.f - 9.53674316e-7f), inv * (1.f + 9.53674316e-7f)};
+}
+
 // A block's scale byte and the factor its elements are multiplied by, from the
 // block's amax as a bit pattern of |x| in fp32 (integer order is value order;
-// >= 0x7F800000 is Inf or NaN).  six_g and g are NVFP4's tensor scale.
+// >= 0x7F800000 is Inf or NaN).
 template <int FMT>
-__device__ __forceinline__ uint32_t block_scale(uint32_t amax_bits, float six_g, float g, float* mul, bool* nonfinite) {
+__device__ __forceinline__ uint32_t block_scale(uint32_t amax_bits, const TensorScale& ts, float* mul,
+                                                bool* nonfinite) {
   *nonfinite = amax_bits >= 0x7F800000u;
   if (FMT == kQNV4) {
-    const uint32_t sb = cvt_e4m3x2(__fdiv_rn(__uint_as_float(amax_bits), six_g), 0.f) & 0xFFu;
+    // E4M3(amax / (6 g)) without the division, wherever both ends of the
+    // interval around the quotient round to the same code
+    const float amax = __uint_as_float(amax_bits);
+    const uint32_t both = cvt_e4m3x2(amax * ts.inv_lo, amax * ts.inv_hi);
+    uint32_t sb = both & 0xFFu;
+    if (sb != both >> 8) sb = cvt_e4m3x2(__fdiv_rn(amax, ts.six_g), 0.f) & 0xFFu;
+    const float g = ts.g;
     const float unit = e4m3_to_f32(sb & 0x7Fu) * g;
     const float inv = __frcp_rn(unit);
     // a zero (or NaN) unit, or one so small that its inverse overflows: zero codes
@@ -76,78 +95,35 @@ __device__ __forceinline__ uint32_t block_scale(uint32_t amax_bits, float six_g,
   return sb;
 }
 
-// Quantise eight fp32 values per lane; a block is 4 (16-element NVFP4: 2)
-// consecutive lanes.  Every lane of the warp takes part.  codes: 8 bytes of
-// E4M3, or 4 bytes of E2M1 in codes.x.  Returns the block's scale byte (the
-// same in its lanes).
+// Quantise sixteen fp32 values per lane: a 16-element block is one lane, a
+// 32-element block two neighbouring ones.  Every lane of the warp takes part.
+// codes: 16 bytes of E4M3, or 8 bytes of E2M1 in codes[0..1].  Returns the
+// block's scale byte (the same in its lanes).
 template <int FMT>
-__device__ __forceinline__ uint32_t quantize_lane8(const float (&v)[8], float six_g, float g, uint2& codes) {
+__device__ __forceinline__ uint32_t quantize_lane16(const float (&v)[16], const TensorScale& ts, uint32_t (&codes)[4]) {
   uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-  m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-  if (FMT != kQNV4) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+  for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+  if (FMT != kQNV4) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
   float mul;
   bool nonfinite;
-  const uint32_t sb = block_scale<FMT>(m, six_g, g, &mul, &nonfinite);
-  float t[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) t[i] = v[i] * mul;
-  if (FMT == kQMX8) {
-    codes.x = cvt_e4m3x2(t[0], t[1]) | (cvt_e4m3x2(t[2], t[3]) << 16);
-    codes.y = cvt_e4m3x2(t[4], t[5]) | (cvt_e4m3x2(t[6], t[7]) << 16);
-    if (nonfinite) codes.x = codes.y = 0x7F7F7F7Fu;
-  } else {
-    codes.x = nonfinite ? 0u : cvt_e2m1x8(t);
-    codes.y = 0u;
-  }
-  return sb;
-}
-
-// 32 consecutive bf16 values in one lane (16 words) -> 16 bytes of E2M1 codes.
-// The scale byte(s): MXFP4 one in bits [0, 8), NVFP4 two (the second block of
-// 16 in bits [8, 16)).
-template <int FMT>
-__device__ __forceinline__ uint32_t quantize_fp4_32(const uint4 (&v)[4], float six_g, float g, uint4& codes) {
-  uint32_t w[16];
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    w[4 * q] = v[q].x;
-    w[4 * q + 1] = v[q].y;
-    w[4 * q + 2] = v[q].z;
-    w[4 * q + 3] = v[q].w;
-  }
-  uint32_t m[2];
+  const uint32_t sb = block_scale<FMT>(m, ts, &mul, &nonfinite);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    uint32_t a = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) a = __vmaxu2(a, w[8 * h + i] & 0x7FFF7FFFu);
-    m[h] = max(a & 0xFFFFu, a >> 16) << 16;  // the bf16 amax as fp32 bits
-  }
-  float mul[2];
-  bool bad[2];
-  uint32_t sb;
-  if (FMT == kQNV4) {
-    sb = block_scale<FMT>(m[0], six_g, g, &mul[0], &bad[0]);
-    sb |= block_scale<FMT>(m[1], six_g, g, &mul[1], &bad[1]) << 8;
-  } else {
-    sb = block_scale<FMT>(max(m[0], m[1]), six_g, g, &mul[0], &bad[0]);
-    mul[1] = mul[0];
-    bad[1] = bad[0];
-  }
-  uint32_t o[4];
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
     float t[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      t[2 * i] = __uint_as_float(w[4 * q + i] << 16) * mul[q >> 1];
-      t[2 * i + 1] = __uint_as_float(w[4 * q + i] & 0xFFFF0000u) * mul[q >> 1];
+    for (int i = 0; i < 8; ++i) t[i] = v[8 * h + i] * mul;
+    if (FMT == kQMX8) {
+      codes[2 * h] = cvt_e4m3x2(t[0], t[1]) | (cvt_e4m3x2(t[2], t[3]) << 16);
+      codes[2 * h + 1] = cvt_e4m3x2(t[4], t[5]) | (cvt_e4m3x2(t[6], t[7]) << 16);
+    } else {
+      codes[h] = cvt_e2m1x8(t);
     }
-    o[q] = bad[q >> 1] ? 0u : cvt_e2m1x8(t);
   }
-  codes = make_uint4(o[0], o[1], o[2], o[3]);
+  if (nonfinite) {
+#pragma unroll
+    for (int i = 0; i < (FMT == kQMX8 ? 4 : 2); ++i) codes[i] = FMT == kQMX8 ? 0x7F7F7F7Fu : 0u;
+  }
   return sb;
 }
 

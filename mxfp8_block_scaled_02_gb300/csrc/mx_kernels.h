@@ -126,16 +126,8 @@ int decode_k_splits(int64_t M, int64_t N, int64_t K, int sms);
 cudaError_t launch_gemm_decode(const DecodeProblem& p, int sms, cudaStream_t stream, const char** msg);
 cudaError_t take_status_decode(unsigned int* out);
 
-// fp4_quant.cu: bf16 [B, M, K] -> packed E2M1 codes [B, M, K/2] and scales
-// (fmt kQMX4 / kQNV4 of mx_fp4.cuh), row-major or in packed atoms; g is NVFP4's
-// tensor scale (device, nullptr = 1).  early_trigger as launch_quantize.
-cudaError_t launch_quantize_fp4(int fmt, const void* x, int64_t B, int64_t M, int64_t K, const float* g, uint8_t* q,
-                                uint8_t* s, bool packed_scales, int sms, cudaStream_t stream, bool early_trigger);
-// n packed codes (n % 32 == 0) -> n E4M3 bytes of the same values.
-cudaError_t launch_fp4_unpack(const uint8_t* q, int64_t n, uint8_t* out, int sms, cudaStream_t stream);
-
-// fused_quant.cu: residual addition + RMS norm, and silu(gate) * up, with the
-// output quantised (fmt: MXFP8, MXFP4 or NVFP4 of mx_fp4.cuh).  Strides are in
+// fused_quant.cu: 4-bit quantisation, and residual addition + RMS norm and
+// silu(gate) * up with the output quantised (fmt: MXFP8, MXFP4 or NVFP4 of mx_fp4.cuh).  Strides are in
 // elements; K % 32 == 0; the norm holds a row in one CTA (K <= kNormMaxK).
 constexpr int64_t kNormMaxK = 32768;
 struct NormProblem {
@@ -155,7 +147,7 @@ struct NormProblem {
   uint8_t* s;
   bool packed;  // scales in packed atoms, else row-major
 };
-cudaError_t launch_rmsnorm_quantize(const NormProblem& p, int sms, cudaStream_t stream);
+cudaError_t launch_rmsnorm_quantize(const NormProblem& p, cudaStream_t stream);
 struct ActProblem {
   int fmt;
   const void* gate;  // bf16 rows
@@ -168,7 +160,14 @@ struct ActProblem {
   uint8_t* s;
   bool packed;
 };
-cudaError_t launch_silu_mul_quantize(const ActProblem& p, int sms, cudaStream_t stream);
+cudaError_t launch_silu_mul_quantize(const ActProblem& p, cudaStream_t stream);
+// bf16 [B, M, K] -> packed E2M1 codes [B, M, K/2] and scales (kQMX4 / kQNV4),
+// row-major or in packed atoms; g is NVFP4's tensor scale (device, nullptr =
+// 1).  early_trigger as launch_quantize.
+cudaError_t launch_quantize_fp4(int fmt, const void* x, int64_t B, int64_t M, int64_t K, const float* g, uint8_t* q,
+                                uint8_t* s, bool packed_scales, cudaStream_t stream, bool early_trigger);
+// n packed codes (n % 32 == 0) -> n E4M3 bytes of the same values.
+cudaError_t launch_fp4_unpack(const uint8_t* q, int64_t n, uint8_t* out, cudaStream_t stream);
 
 // gemm_fp4.cu: the 4-bit block-scaled product on CTA pairs.  x / w: packed E2M1
 // codes [B, M, K/2] / [B, N, K/2]; sfx / sfw: packed scale atoms; gx / gw:
