@@ -440,10 +440,14 @@ mxfp8_status mxfp8_fp4_packed_sizes(int fmt, int64_t B, int64_t N, int64_t K, si
 mxfp8_status mxfp8_fp4_process_weights(int fmt, const uint8_t* w, const uint8_t* w_scale, int64_t B, int64_t N,
                                        int64_t K, uint8_t* w_packed, uint8_t* sf_packed, mxfp8_stream_t stream);
 
-/* Device workspace bytes of mxfp8_fp4_linear; with x_is_quantized it also
- * covers mxfp8_fp4_gemm_packed. */
+/* Device workspace bytes of mxfp8_fp4_linear (0 where few rows of bf16 x are
+ * quantised inside the product's kernel). */
 mxfp8_status mxfp8_fp4_workspace_size(int fmt, int64_t B, int64_t M, int64_t N, int64_t K, int x_is_quantized,
                                       size_t* bytes);
+
+/* Device workspace bytes with which mxfp8_fp4_gemm_packed splits K (0 for the
+ * shapes it does not split). */
+mxfp8_status mxfp8_fp4_product_workspace_size(int fmt, int64_t B, int64_t M, int64_t N, int64_t K, size_t* bytes);
 
 /*
  * mxfp8_fp4_linear - out[b, m, n] = bf16( g_x g_w sum_k x[b, m, k] w[b, n, k]
@@ -452,7 +456,8 @@ mxfp8_status mxfp8_fp4_workspace_size(int fmt, int64_t B, int64_t M, int64_t N, 
  *   x_tensor_scale), or x_q [B, M, K/2] with row-major x_scale.
  *   w_packed, sf_packed from mxfp8_fp4_process_weights; tensor scales: device
  *   fp32 (NVFP4) or NULL for 1, NULL for MXFP4; bias bf16 [N] or NULL;
- *   workspace >= mxfp8_fp4_workspace_size bytes, 256-byte aligned.
+ *   workspace >= mxfp8_fp4_workspace_size bytes, 256-byte aligned (NULL when
+ *   that is 0).
  *   fp32 accumulation; one rounding to bf16 after the tensor scales and the
  *   bias.  Calls with few output tiles split K and add the fp32 partials in a
  *   fixed order, so a call's result is the same every time.  Stream ordering
@@ -468,8 +473,8 @@ mxfp8_status mxfp8_fp4_linear(int fmt, const void* x_bf16, const uint8_t* x_q, c
 /*
  * mxfp8_fp4_gemm_packed - the product alone, x already quantised with packed
  * scales (mxfp8_fp4_quantize_packed, or the norm and activation calls below).
- * workspace is optional: NULL, or less than mxfp8_fp4_workspace_size(...,
- * x_is_quantized = 1) bytes, runs the call without splitting K.
+ * workspace is optional: NULL, or less than mxfp8_fp4_product_workspace_size
+ * bytes, runs the call without splitting K.
  */
 mxfp8_status mxfp8_fp4_gemm_packed(int fmt, const uint8_t* x_q, const uint8_t* sfa_packed, const float* x_tensor_scale,
                                    int64_t B, int64_t M, int64_t N, int64_t K, const uint8_t* w_packed,

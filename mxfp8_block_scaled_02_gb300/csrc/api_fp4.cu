@@ -208,8 +208,20 @@ mxfp8_status mxfp8_fp4_workspace_size(int fmt, int64_t B, int64_t M, int64_t N, 
   if (bytes == nullptr) return fail(MXFP8_ERR_INVALID_ARG, "null output pointer");
   mxfp8_status st = check_product(fmt, B, M, N, K);
   if (st != MXFP8_OK) return st;
+  if (x_is_quantized == 0 && mx::fp4_quantizes_inside(B, M, N, K)) {
+    *bytes = 0;
+    return MXFP8_OK;
+  }
   *bytes = static_cast<size_t>(
       workspace_layout(fmt, B, M, N, K, x_is_quantized != 0, false, product_splits(B, M, N, K)).total);
+  return MXFP8_OK;
+}
+
+mxfp8_status mxfp8_fp4_product_workspace_size(int fmt, int64_t B, int64_t M, int64_t N, int64_t K, size_t* bytes) {
+  if (bytes == nullptr) return fail(MXFP8_ERR_INVALID_ARG, "null output pointer");
+  mxfp8_status st = check_product(fmt, B, M, N, K);
+  if (st != MXFP8_OK) return st;
+  *bytes = static_cast<size_t>(workspace_layout(fmt, B, M, N, K, true, true, product_splits(B, M, N, K)).total);
   return MXFP8_OK;
 }
 
@@ -228,13 +240,21 @@ mxfp8_status mxfp8_fp4_linear(int fmt, const void* x_bf16, const uint8_t* x_q, c
   Operands o{x_q, x_scale, x_tensor_scale, w_packed, sf_packed, w_tensor_scale, bias_bf16, out_bf16};
   if ((st = check_operands(fmt, o)) != MXFP8_OK) return st;
   if (!aligned(x_bf16, 16)) return fail(MXFP8_ERR_INVALID_ARG, "tensor pointers must be 16-byte aligned");
+  int sms = 0;
+  if (have_x && mx::fp4_quantizes_inside(B, M, N, K)) {
+    if ((st = mx::current_device(&sms)) != MXFP8_OK) return st;
+    mx::Fp4Problem p{fmt, nullptr, o.w, nullptr, o.sfw, o.gx, o.gw, o.bias, o.out, B, M, N, K};
+    p.x_bf16 = x_bf16;
+    const char* msg = "";
+    cudaError_t e = mx::launch_gemm_fp4_small(p, sms, as_stream(stream), &msg);
+    return e == cudaSuccess ? MXFP8_OK : cuda_fail(e, msg);
+  }
   const int splits = product_splits(B, M, N, K);
   const WsLayout ws = workspace_layout(fmt, B, M, N, K, have_q, false, splits);
   if (static_cast<int64_t>(workspace_bytes) < ws.total)
     return fail(MXFP8_ERR_INVALID_ARG, "workspace has %zu bytes, needs %lld", workspace_bytes, (long long)ws.total);
   if (workspace == nullptr || !aligned(workspace, 256))
     return fail(MXFP8_ERR_INVALID_ARG, "workspace must be non-null and 256-byte aligned");
-  int sms = 0;
   if ((st = mx::current_device(&sms)) != MXFP8_OK) return st;
   uint8_t* wsb = static_cast<uint8_t*>(workspace);
   cudaError_t e;

@@ -9,15 +9,18 @@
 // in flight before the tokens arrive (they are the previous kernel's output,
 // waited for with griddepcontrol.wait; weights, scales and bias are not).
 // Codes and scale atoms of both operands come by TMA, the atoms go to tensor
-// memory by tcgen05.cp in the MMA warp's own order.
+// memory by tcgen05.cp in the MMA warp's own order.  A few bf16 tokens can
+// also be quantised here (kQuant): six warps load the CTA's K range and write
+// codes and scales where TMA would have put them, the bytes of the quantise
+// call, which saves a launch and a workspace.
 //
 // The S fp32 partials meet in distributed shared memory: CTA r owns weight rows
 // [r 128/S, (r+1) 128/S) and adds the partials in the order 0..S-1, so the
 // result is the same on every call; with S = 1 the epilogue stores straight
 // from tensor memory.
 //
-// Warps: 0 weight TMA, 1 tensor-memory allocation and MMA issue, 2 token TMA,
-// 3 idle, 4..7 epilogue; all eight reduce.  Every wait is bounded and the
+// Warps: 0 weight TMA, 1 tensor-memory allocation and MMA issue, 2 token TMA
+// (kQuant: 2..7 quantise the tokens), 4..7 epilogue; all eight reduce.  Every wait is bounded and the
 // cluster barrier is reached on every path.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -119,7 +122,13 @@ __device__ __forceinline__ void expect_tx_elected(uint32_t elected, uint32_t bar
       : "memory");
 }
 
+constexpr int QUANT_WARPS = 6;
+constexpr int QUANT_MAX_M = 16;
+constexpr int QUANT_AHEAD = 4;  // loads ahead, in tasks of two rows and a stage
+
 struct Args {
+  const __nv_bfloat16* x;  // kQuant: bf16 [M, K]
+  int K;
   const __nv_bfloat16* bias;
   const float* gx;
   const float* gw;
@@ -131,7 +140,7 @@ struct Args {
   int splits;      // cluster size S
 };
 
-template <int FMT, int NTOK>
+template <int FMT, int NTOK, bool kQuant>
 __global__ void __launch_bounds__(THREADS, 1)
     gemm_fp4_small_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                           const __grid_constant__ CUtensorMap tmSFW, const __grid_constant__ CUtensorMap tmSFX,
@@ -262,7 +271,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     else
       __nanosleep(200000);  // let issued tensor-core work retire
     __syncwarp();
-  } else if (warp == 2) {
+  } else if (!kQuant && warp == 2) {
     // ------------------------------------------------ token producer
     grid_dependency_wait();
     int st = 0, issued = 0;
@@ -283,6 +292,76 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (*abort_flag) {
       for (int s = 0; s < C::STAGES && s < issued; ++s)
         mbar_wait(&full_x[s], static_cast<uint32_t>(((issued - 1 - s) / C::STAGES) & 1), nullptr);
+    }
+    __syncwarp();
+  }
+  if (kQuant && warp >= 2) {
+    // ------------------------------------------------ token quantiser
+    // A warp takes every sixth stage; a task is two rows of it, 16 elements a
+    // lane.  Task n of the warp: stage warp - 2 + 6 (n / T), rows 2 (n % T) and
+    // the one after, T = ceil(M / 2).
+    grid_dependency_wait();
+    const TensorScale ts = tensor_scale(FMT == kQNV4 && a.gx != nullptr ? *a.gx : 1.f);
+    constexpr int kLanes = q_block(FMT) / 16;
+    const int j = lane & 15, T = (a.M + 1) >> 1;
+    const int ntasks = (nk - (warp - 2) + QUANT_WARPS - 1) / QUANT_WARPS * T;  // <= 0: none
+    int lt = 0, li = warp - 2;  // task the next load belongs to
+    auto load = [&](uint4 (&v)[2]) {
+      const int r = 2 * lt + (lane >> 4), k = (kt0 + li) * BK + 16 * j;
+      const bool valid = li < nk && r < a.M && k < a.K;
+      const uint4* src = reinterpret_cast<const uint4*>(a.x + (valid ? static_cast<int64_t>(r) * a.K + k : 0));
+      v[0] = valid ? src[0] : make_uint4(0, 0, 0, 0);
+      v[1] = valid ? src[1] : make_uint4(0, 0, 0, 0);
+      if (++lt == T) {
+        lt = 0;
+        li += QUANT_WARPS;
+      }
+    };
+    uint4 buf[QUANT_AHEAD][2];
+#pragma unroll
+    for (int d = 0; d < QUANT_AHEAD; ++d) load(buf[d]);
+    int t = 0, i = warp - 2;
+    bool ok = true;
+    for (int n0 = 0; ok && n0 < ntasks; n0 += QUANT_AHEAD) {
+#pragma unroll
+      for (int d = 0; d < QUANT_AHEAD; ++d) {
+        if (!ok || n0 + d >= ntasks) break;
+        const int st = i % C::STAGES;
+        if (t == 0 && i >= C::STAGES &&
+            !mbar_wait_warp(&empty[st], static_cast<uint32_t>((i / C::STAGES - 1) & 1), abort_flag)) {
+          ok = false;
+          break;
+        }
+        const int r = 2 * t + (lane >> 4);
+        const uint32_t w[8] = {buf[d][0].x, buf[d][0].y, buf[d][0].z, buf[d][0].w,
+                               buf[d][1].x, buf[d][1].y, buf[d][1].z, buf[d][1].w};
+        float f[16];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          f[2 * e] = __uint_as_float(w[e] << 16);
+          f[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+        }
+        load(buf[d]);
+        uint32_t codes[4];
+        uint32_t word = quantize_lane16<FMT>(f, ts, codes);
+        word |= __shfl_xor_sync(0xFFFFFFFFu, word, kLanes) << 8;
+        word |= __shfl_xor_sync(0xFFFFFFFFu, word, 2 * kLanes) << 16;
+        if (r < a.M) {
+          // 128-byte swizzle: 16-byte piece q of row r sits at q ^ (r % 8)
+          *reinterpret_cast<uint2*>(smem + C::OFF_X + st * C::X_BYTES + r * BKB + (((j >> 1) ^ (r & 7)) << 4) +
+                                    (j & 1) * 8) = make_uint2(codes[0], codes[1]);
+          if (j % (4 * kLanes) == 0)
+            *reinterpret_cast<uint32_t*>(smem + C::OFF_SFX + st * C::SF_BYTES + j / (4 * kLanes) * kAtomBytes + r * 16) =
+                word;
+        }
+        if (++t == T) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&full_x[st]);
+          t = 0;
+          i += QUANT_WARPS;
+        }
+      }
     }
     __syncwarp();
   }
@@ -353,7 +432,7 @@ void fill_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, int grid, i
 }
 
 // Clusters of S CTAs that fit on the GPU at once, per device (asked once).
-template <int FMT, int NTOK>
+template <int FMT, int NTOK, bool kQuant>
 int max_clusters(int splits, int sms) {
   static int cache[64][4] = {};
   int dev = 0;
@@ -366,7 +445,7 @@ int max_clusters(int splits, int sms) {
     fill_config(&cfg, attr, splits, splits, Cfg<FMT, NTOK>::SMEM, nullptr);
     cfg.numAttrs = 1;
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, gemm_fp4_small_kernel<FMT, NTOK>, &cfg) != cudaSuccess || n < 1) {
+    if (cudaOccupancyMaxActiveClusters(&n, gemm_fp4_small_kernel<FMT, NTOK, kQuant>, &cfg) != cudaSuccess || n < 1) {
       cudaGetLastError();  // the query's own error
       n = sms / splits;
     }
@@ -375,7 +454,7 @@ int max_clusters(int splits, int sms) {
   return cache[dev][slot];
 }
 
-template <int FMT, int NTOK>
+template <int FMT, int NTOK, bool kQuant>
 cudaError_t launch_t(const Fp4Problem& p, int sms, cudaStream_t stream, const char** msg) {
   using C = Cfg<FMT, NTOK>;
   static bool attr_set[64] = {};
@@ -383,7 +462,7 @@ cudaError_t launch_t(const Fp4Problem& p, int sms, cudaStream_t stream, const ch
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64 || !attr_set[dev]) {
     cudaError_t e =
-        cudaFuncSetAttribute(gemm_fp4_small_kernel<FMT, NTOK>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+        cudaFuncSetAttribute(gemm_fp4_small_kernel<FMT, NTOK, kQuant>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) {
       *msg = "cudaFuncSetAttribute(max dynamic shared memory) failed";
       return e;
@@ -398,15 +477,22 @@ cudaError_t launch_t(const Fp4Problem& p, int sms, cudaStream_t stream, const ch
   const auto sw = CU_TENSOR_MAP_SWIZZLE_128B, flat = CU_TENSOR_MAP_SWIZZLE_NONE;
   const auto l2 = CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
   if (!encode_map3(&mw, u8, p.w, kb, p.N, p.B, kb, p.N * kb, BKB, ROWS, sw, l2) ||
-      !encode_map3(&mx, u8, p.x, kb, p.M, p.B, kb, p.M * kb, BKB, NTOK, sw, l2) ||
       !encode_map3(&msw, u32, p.sfw, RTW * words, KA, p.B, RTW * kAtomBytes, KA * RTW * kAtomBytes, words, C::ATOMS,
                    flat, l2) ||
-      !encode_map3(&msx, u32, p.sfx, RTX * words, KA, p.B, RTX * kAtomBytes, KA * RTX * kAtomBytes, words, C::ATOMS,
-                   flat, l2)) {
+      (!kQuant &&
+       (!encode_map3(&mx, u8, p.x, kb, p.M, p.B, kb, p.M * kb, BKB, NTOK, sw, l2) ||
+        !encode_map3(&msx, u32, p.sfx, RTX * words, KA, p.B, RTX * kAtomBytes, KA * RTX * kAtomBytes, words, C::ATOMS,
+                     flat, l2)))) {
     *msg = "cuTensorMapEncodeTiled rejected a 4-bit operand";
     return cudaErrorInvalidValue;
   }
+  if (kQuant) {  // not used
+    mx = mw;
+    msx = msw;
+  }
   Args a;
+  a.x = static_cast<const __nv_bfloat16*>(p.x_bf16);
+  a.K = static_cast<int>(p.K);
   a.bias = static_cast<const __nv_bfloat16*>(p.bias);
   a.gx = p.gx;
   a.gw = p.gw;
@@ -420,24 +506,42 @@ cudaError_t launch_t(const Fp4Problem& p, int sms, cudaStream_t stream, const ch
   // the largest K split whose clusters all run at once
   const int64_t tiles = p.B * a.TT * RTW;
   a.splits = 8;
-  while (a.splits > 1 && (a.splits > a.KT || tiles > max_clusters<FMT, NTOK>(a.splits, sms))) a.splits >>= 1;
+  while (a.splits > 1 && (a.splits > a.KT || tiles > max_clusters<FMT, NTOK, kQuant>(a.splits, sms))) a.splits >>= 1;
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[2];
   fill_config(&cfg, attr, static_cast<int>(tiles) * a.splits, a.splits, C::SMEM, stream);
-  cudaError_t e = cudaLaunchKernelEx(&cfg, gemm_fp4_small_kernel<FMT, NTOK>, mw, mx, msw, msx, a);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, gemm_fp4_small_kernel<FMT, NTOK, kQuant>, mw, mx, msw, msx, a);
   if (e != cudaSuccess) *msg = "small-M 4-bit GEMM launch failed";
   return e;
 }
 
 template <int FMT>
 cudaError_t launch_fmt(const Fp4Problem& p, int sms, cudaStream_t stream, const char** msg) {
-  if (p.M <= 16) return launch_t<FMT, 16>(p, sms, stream, msg);
-  if (p.M <= 32) return launch_t<FMT, 32>(p, sms, stream, msg);
-  if (p.M <= 64) return launch_t<FMT, 64>(p, sms, stream, msg);
-  return launch_t<FMT, 128>(p, sms, stream, msg);
+  if (p.x_bf16 != nullptr) return launch_t<FMT, 16, true>(p, sms, stream, msg);
+  if (p.M <= 16) return launch_t<FMT, 16, false>(p, sms, stream, msg);
+  if (p.M <= 32) return launch_t<FMT, 32, false>(p, sms, stream, msg);
+  if (p.M <= 64) return launch_t<FMT, 64, false>(p, sms, stream, msg);
+  return launch_t<FMT, 128, false>(p, sms, stream, msg);
 }
 
 }  // namespace
+
+namespace {
+
+// The K split the launcher comes to on this GPU's 152 SMs, by the tile count.
+int64_t splits_estimate(int64_t tiles) { return tiles <= 14 ? 8 : (tiles <= 36 ? 4 : (tiles <= 75 ? 2 : 1)); }
+
+}  // namespace
+
+// Quantising inside repeats the work in every CTA of the same K range, and
+// saves a launch and the workspace (5 us of host time): used while a CTA's share
+// is small.  Measured in a graph (us, quantise call first / inside, MXFP4):
+// N = K = 4096 (4 stages a CTA), M = 1 4.7 / 4.2, 4 4.7 / 4.5, 8 4.8 / 5.2, 16
+// 5.0 / 6.2; N = 14336, K = 4096 (16 stages), M = 2 8.0 / 8.1, 4 8.0 / 8.7.
+bool fp4_quantizes_inside(int64_t B, int64_t M, int64_t N, int64_t K) {
+  if (B != 1 || M > QUANT_MAX_M) return false;
+  return M <= 2 || M * ceil_div(ceil_div(K, BK), splits_estimate(ceil_div(N, ROWS))) <= 32;
+}
 
 // Where this kernel is the faster one (a function of the shape alone: the
 // workspace size depends on it).  It wins while each CTA's chain is short; the
@@ -452,8 +556,7 @@ bool fp4_use_small(int64_t B, int64_t M, int64_t N, int64_t K) {
   if (M <= 32) return true;
   const int64_t tiles = B * ceil_div(M, 128) * ceil_div(N, ROWS);
   if (tiles > 152) return false;  // more than one CTA an SM
-  const int64_t splits = tiles <= 14 ? 8 : (tiles <= 36 ? 4 : (tiles <= 75 ? 2 : 1));
-  return ceil_div(ceil_div(K, BK), splits) <= (M <= 64 ? 16 : 14);
+  return ceil_div(ceil_div(K, BK), splits_estimate(tiles)) <= (M <= 64 ? 16 : 14);
 }
 
 cudaError_t launch_gemm_fp4_small(const Fp4Problem& p, int sms, cudaStream_t stream, const char** msg) {

@@ -186,6 +186,7 @@ struct Fp4Problem {
   int64_t B, M, N, K;
   float* part = nullptr;
   int splits = 1;
+  const void* x_bf16 = nullptr;  // small-M kernel, fp4_quantizes_inside: bf16 x instead of x and sfx
 };
 int fp4_splitk_splits(int64_t B, int64_t M, int64_t N, int64_t K);
 cudaError_t launch_gemm_fp4(const Fp4Problem& p, int sms, cudaStream_t stream, const char** msg);
@@ -197,6 +198,7 @@ bool encode_map3(CUtensorMap* m, CUtensorMapDataType dtype, const void* base, in
 // gemm_fp4_small.cu: the same product on 128 x (16, 32, 64 or 128) tiles of one
 // CTA each, the weights on the MMA's M side and K split over a cluster (part
 // and splits are not used); fp4_use_small: the shapes it is meant for.
+bool fp4_quantizes_inside(int64_t B, int64_t M, int64_t N, int64_t K);
 bool fp4_use_small(int64_t B, int64_t M, int64_t N, int64_t K);
 cudaError_t launch_gemm_fp4_small(const Fp4Problem& p, int sms, cudaStream_t stream, const char** msg);
 cudaError_t take_status_fp4_small(unsigned int* out);

@@ -68,6 +68,7 @@ SIGNATURES = {
     "mxfp8_fp4_packed_sizes": (_INT, [_INT, _I64, _I64, _I64, _SIZE_P, _SIZE_P]),
     "mxfp8_fp4_process_weights": (_INT, [_INT, _P, _P, _I64, _I64, _I64, _P, _P, _P]),
     "mxfp8_fp4_workspace_size": (_INT, [_INT, _I64, _I64, _I64, _I64, _INT, _SIZE_P]),
+    "mxfp8_fp4_product_workspace_size": (_INT, [_INT, _I64, _I64, _I64, _I64, _SIZE_P]),
     "mxfp8_fp4_linear": (_INT, [_INT, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _P, _P, _P, _P, _P, _P,
                                 ctypes.c_size_t, _P]),
     "mxfp8_fp4_gemm_packed": (_INT, [_INT, _P, _P, _P, _I64, _I64, _I64, _I64, _P, _P, _P, _P, _P, _P,
@@ -590,6 +591,23 @@ def workspace_size_fp4(B: int, M: int, N: int, K: int, quantized: bool, fmt: str
     return n.value
 
 
+@functools.lru_cache(maxsize=4096)
+def product_workspace_fp4(B: int, M: int, N: int, K: int, fmt: str) -> int:
+    """Bytes gemm_packed_fp4 needs to split K (0 where it does not)."""
+    n = ctypes.c_size_t()
+    _check(load().mxfp8_fp4_product_workspace_size(_fmt4(fmt), B, M, N, K, ctypes.byref(n)))
+    return n.value
+
+
+def _workspace(given: torch.Tensor | None, need: int, device) -> tuple[int | None, int, torch.Tensor | None]:
+    """(pointer, bytes, the tensor to keep alive during the call)."""
+    if given is None:
+        if need == 0:
+            return None, 0, None
+        given = torch.empty(need, dtype=torch.uint8, device=device)
+    return given.data_ptr(), given.numel() * given.element_size(), given
+
+
 def _product_args(pw: PackedWeights, bias: torch.Tensor | None, out: torch.Tensor | None, rows: int) -> None:
     if bias is not None and (bias.dtype != torch.bfloat16 or tuple(bias.shape) != (pw.N,)):
         raise ValueError("bias must be bf16 [N]")
@@ -627,13 +645,12 @@ def linear_fp4(x: torch.Tensor, pw: PackedWeights, bias: torch.Tensor | None = N
     if rows == 0:
         return out
     M = rows // pw.B
-    if workspace is None:
-        workspace = torch.empty(workspace_size_fp4(pw.B, M, pw.N, pw.K, quantized, fmt), dtype=torch.uint8,
-                                device=x.device)
-    _check(load().mxfp8_fp4_linear(f, None if quantized else _ptr(x), _ptr(x) if quantized else None, _ptr(x_scale),
-                                   _ptr(tensor_scale), pw.B, M, pw.N, pw.K, _ptr(pw.w_packed), _ptr(pw.sf_packed),
-                                   _ptr(pw.tensor_scale), _ptr(bias), _ptr(out), _ptr(workspace),
-                                   workspace.numel() * workspace.element_size(), _stream()))
+    ws_ptr, ws_bytes, workspace = _workspace(workspace, workspace_size_fp4(pw.B, M, pw.N, pw.K, quantized, fmt),
+                                             x.device)
+    _check(load().mxfp8_fp4_linear(f, None if quantized else x.data_ptr(), x.data_ptr() if quantized else None,
+                                   _ptr(x_scale), _ptr(tensor_scale), pw.B, M, pw.N, pw.K, pw.w_packed.data_ptr(),
+                                   pw.sf_packed.data_ptr(), _ptr(pw.tensor_scale), _ptr(bias), out.data_ptr(),
+                                   ws_ptr, ws_bytes, _stream()))
     return out
 
 
@@ -672,8 +689,8 @@ def gemm_packed_fp4(pa: PackedActivation, pw: PackedWeights, bias: torch.Tensor 
                     out: torch.Tensor | None = None, *, workspace: torch.Tensor | None = None) -> torch.Tensor:
     """The 4-bit product alone (x quantised by quantize_packed_fp4,
     rmsnorm_quantize or silu_mul_quantize with packed scales); bf16 [B, M, N].
-    ``workspace`` (workspace_size_fp4 bytes with quantized=True) is allocated
-    when the call splits K and none is given."""
+    ``workspace`` (product_workspace_fp4 bytes) is allocated when the call splits
+    K and none is given."""
     f = _fmt4(pw.fmt)
     if pa.fmt != pw.fmt or pa.K != pw.K or pa.B != pw.B:
         raise ValueError("activation and weights disagree on format, K or B")
@@ -684,13 +701,12 @@ def gemm_packed_fp4(pa: PackedActivation, pw: PackedWeights, bias: torch.Tensor 
         out = torch.empty((pa.B, pa.M, pw.N), dtype=torch.bfloat16, device=pa.x_q.device)
     if pa.M == 0:
         return out
-    if workspace is None:
-        workspace = torch.empty(workspace_size_fp4(pa.B, pa.M, pw.N, pa.K, True, pw.fmt), dtype=torch.uint8,
-                                device=pa.x_q.device)
-    _check(load().mxfp8_fp4_gemm_packed(f, _ptr(pa.x_q), _ptr(pa.sf_packed), _ptr(pa.tensor_scale), pa.B, pa.M, pw.N,
-                                        pa.K, _ptr(pw.w_packed), _ptr(pw.sf_packed), _ptr(pw.tensor_scale),
-                                        _ptr(bias), _ptr(out), _ptr(workspace),
-                                        workspace.numel() * workspace.element_size(), _stream()))
+    ws_ptr, ws_bytes, workspace = _workspace(workspace, product_workspace_fp4(pa.B, pa.M, pw.N, pa.K, pw.fmt),
+                                             pa.x_q.device)
+    _check(load().mxfp8_fp4_gemm_packed(f, pa.x_q.data_ptr(), pa.sf_packed.data_ptr(), _ptr(pa.tensor_scale), pa.B,
+                                        pa.M, pw.N, pa.K, pw.w_packed.data_ptr(), pw.sf_packed.data_ptr(),
+                                        _ptr(pw.tensor_scale), _ptr(bias), out.data_ptr(), ws_ptr, ws_bytes,
+                                        _stream()))
     return out
 
 

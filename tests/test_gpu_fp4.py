@@ -175,6 +175,29 @@ def test_linear_on_bf16_against_the_oracle(fmt, B, M, N, K):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M,N,K", [(1, 4096, 4096), (3, 264, 96), (7, 1000, 4128), (12, 136, 8224), (13, 520, 2080),
+                                   (16, 72, 14336), (16, 14336, 512)])
+def test_few_tokens_are_quantised_inside_to_the_same_bytes(fmt, M, N, K):
+    """Up to 16 bf16 rows are quantised in the product's own kernel: the output is bit for bit that of the codes
+    the quantise call gives, whatever a block holds."""
+    dev = device()
+    rng = np.random.default_rng(M + N + K)
+    x = rand_bf16(rng, M, K)[1] * np.exp2(rng.integers(-8, 9, size=(M, K // 32)).repeat(32, axis=1))
+    x[M // 2, :32] = 0.0
+    x[0, K - 1] = np.inf
+    xt = bf16_to_dev(bf16_bits_of(x), dev)
+    wt = bf16_to_dev(rand_bf16(rng, N, K)[0], dev)
+    g = scale_tensor(None if fmt == "mxfp4" else 0.37, dev)
+    pw = ops.process_weights_fp4(*ops.quantize_fp4(wt, fmt), fmt)
+    inside = ops.linear_fp4(xt, pw, tensor_scale=g)
+    q, s = ops.quantize_fp4(xt, fmt, tensor_scale=g)
+    codes = ops.linear_fp4(q, pw, x_scale=s, tensor_scale=g)
+    ops.check()
+    assert torch.equal(inside.view(torch.int16), codes.view(torch.int16))
+    assert torch.isnan(inside[0]).all() and torch.isfinite(inside[1:]).all()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("M", [20, 200])
 def test_nan_blocks_stay_in_their_row_and_column(fmt, M):
     dev = device()
@@ -272,7 +295,7 @@ def test_refusals():
     with pytest.raises(ValueError):
         ops.linear_fp4(x, pw, out=torch.empty(4, 8, dtype=torch.bfloat16, device=dev))
     with pytest.raises(ops.MxStatusError, match="workspace"):
-        ops.linear_fp4(x, pw, workspace=torch.empty(16, dtype=torch.uint8, device=dev))
+        ops.linear_fp4(x.repeat(5, 1), pw, workspace=torch.empty(16, dtype=torch.uint8, device=dev))
 
 
 def test_misaligned_views_are_taken():
