@@ -263,7 +263,10 @@ mxfp8_status mxfp8_fp4_linear(int fmt, const void* x_bf16, const uint8_t* x_q, c
                                 true);
     o.x = wsb + ws.xq;
   } else {
-    e = mx::launch_sf_pack(x_scale, B, M, fp4_scale_extent(fmt, K), wsb + ws.sfx, sms, as_stream(stream), true);
+    const int64_t KB = K / mx::q_block(fmt);
+    e = KB % 4 == 0 && B <= 65535 && M <= 65535 * mx::kAtomRows
+            ? mx::launch_sf_repack(x_scale, B, M, KB, wsb + ws.sfx, as_stream(stream))
+            : mx::launch_sf_pack(x_scale, B, M, fp4_scale_extent(fmt, K), wsb + ws.sfx, sms, as_stream(stream), true);
   }
   if (e != cudaSuccess) return cuda_fail(e, have_x ? "4-bit quantise launch" : "activation scale repack launch");
   o.sfx = wsb + ws.sfx;

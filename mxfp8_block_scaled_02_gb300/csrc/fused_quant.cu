@@ -6,7 +6,8 @@
 //             optionally y as bf16;
 //   silu_mul: y = gate / (1 + exp(-gate)) * up, output quantise(y);
 //   fp4     : y = x, the plain 4-bit quantise call;
-// and the exact widening of packed E2M1 codes to E4M3 bytes.
+// the exact widening of packed E2M1 codes to E4M3 bytes, and the repack of
+// row-major activation scales into atoms.
 //
 // y stays in fp32 from the sum to the element's rounding: it is rounded once.
 // All read each input once and write each output once, and are bound by HBM
@@ -296,7 +297,7 @@ struct Fp4Args {
 // kEarly as in quantize.cu: only the activation quantise inside a linear call
 // lets the next kernel start early, never the call that may make weights.
 template <int FMT, bool kEarly, int CH>
-__global__ void __launch_bounds__(kRowThreads, 12) quantize_fp4_kernel(const Fp4Args a) {
+__global__ void __launch_bounds__(kRowThreads, CH == 1 ? 12 : 8) quantize_fp4_kernel(const Fp4Args a) {
   if (kEarly) {
     launch_dependents();
     grid_dependency_wait();
@@ -338,6 +339,49 @@ __global__ void __launch_bounds__(256) fp4_unpack_kernel(const uint2* __restrict
   out[i] = make_uint4(e2m1x4_to_e4m3(v.x), e2m1x4_to_e4m3(v.x >> 16), e2m1x4_to_e4m3(v.y), e2m1x4_to_e4m3(v.y >> 16));
 }
 
+// Row-major scales [B, R, KB] -> packed atoms, for pre-quantised activations.  A
+// CTA turns 128 rows x 32 bytes into 8 atoms through shared memory, so that both
+// sides move whole sectors (V bytes a load, KB % V == 0).
+constexpr int kRepackThreads = 256;
+
+template <int V>
+__global__ void __launch_bounds__(kRepackThreads) sf_repack_kernel(const uint8_t* __restrict__ src, int64_t R, int KB,
+                                                                   int KT, int RT, uint8_t* __restrict__ dst) {
+  __shared__ uint32_t tile[kAtomRows][9];  // 8 words a row, one of padding
+  launch_dependents();
+  grid_dependency_wait();
+  const int kt0 = blockIdx.x * 8, rt = blockIdx.y;
+  const int64_t b = blockIdx.z;
+  constexpr int kPieces = 32 / V;
+  for (int p = threadIdx.x; p < kAtomRows * kPieces; p += kRepackThreads) {
+    const int r = p / kPieces, o = p % kPieces * V;
+    const int64_t row = static_cast<int64_t>(rt) * kAtomRows + r;
+    const int byte = kt0 * 4 + o;
+    uint32_t w[V / 4];
+#pragma unroll
+    for (int i = 0; i < V / 4; ++i) w[i] = 0;
+    if (row < R && byte < KB) {
+      const uint8_t* s = src + (b * R + row) * KB + byte;
+      if constexpr (V == 16) {
+        const uint4 v = *reinterpret_cast<const uint4*>(s);
+        w[0] = v.x;
+        w[1] = v.y;
+        w[2] = v.z;
+        w[3] = v.w;
+      } else {
+        w[0] = *reinterpret_cast<const uint32_t*>(s);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < V / 4; ++i) tile[r][o / 4 + i] = w[i];
+  }
+  __syncthreads();
+  const int a = threadIdx.x >> 5, l = threadIdx.x & 31;
+  if (kt0 + a < KT)
+    *reinterpret_cast<uint4*>(dst + ((b * KT + kt0 + a) * RT + rt) * kAtomBytes + l * 16) =
+        make_uint4(tile[l][a], tile[l + 32][a], tile[l + 64][a], tile[l + 96][a]);
+}
+
 cudaError_t launch_pdl(const void* kern, int64_t grid, int threads, void* args, cudaStream_t stream,
                        bool programmatic = true) {
   cudaLaunchConfig_t cfg = {};
@@ -354,12 +398,13 @@ cudaError_t launch_pdl(const void* kern, int64_t grid, int threads, void* args, 
 }
 
 // Chunks a thread, threads and CTAs for M rows of K elements, the CTAs of a row
-// as even as whole warps allow.  Two chunks a thread keep more bytes in flight
-// on long inputs (4-bit quantise, 14336 x 4096: 25.6 -> 24.3 us) and one starts
-// more CTAs on short ones (activation, 512 x 14336: 7.0 -> 6.6 us).
-int row_split(int64_t M, int64_t K, int* threads, int* segs) {
+// as even as whole warps allow.  `most` chunks a thread keep more bytes in
+// flight on long inputs (4-bit quantise, 14336 x 4096: 25.6 -> 24.1 us, NVFP4
+// 31.4 -> 26.3) and one starts more CTAs on short ones (activation, 512 x 14336:
+// 7.0 -> 6.6 us).
+int row_split(int64_t M, int64_t K, int most, int* threads, int* segs) {
   const int64_t chunks = K / 16;
-  const int ch = chunks >= 64 && M * chunks >= 152ll * 32 * 2 * kRowThreads ? 2 : 1;
+  const int ch = chunks >= 32 * most && M * chunks >= 152ll * 32 * 2 * kRowThreads ? most : 1;
   *segs = static_cast<int>(ceil_div(chunks, ch * kRowThreads));
   *threads = static_cast<int>(ceil_div(ceil_div(chunks, *segs * ch), 32) * 32);
   return ch;
@@ -380,9 +425,9 @@ const void* act_kernel(int ch) {
 template <int FMT>
 const void* fp4_kernel(bool early, int ch) {
   if (early)
-    return ch == 2 ? reinterpret_cast<const void*>(quantize_fp4_kernel<FMT, true, 2>)
+    return ch == 4 ? reinterpret_cast<const void*>(quantize_fp4_kernel<FMT, true, 4>)
                    : reinterpret_cast<const void*>(quantize_fp4_kernel<FMT, true, 1>);
-  return ch == 2 ? reinterpret_cast<const void*>(quantize_fp4_kernel<FMT, false, 2>)
+  return ch == 4 ? reinterpret_cast<const void*>(quantize_fp4_kernel<FMT, false, 4>)
                  : reinterpret_cast<const void*>(quantize_fp4_kernel<FMT, false, 1>);
 }
 
@@ -437,7 +482,7 @@ cudaError_t launch_silu_mul_quantize(const ActProblem& p, cudaStream_t stream) {
   a.o = quant_out(p.fmt, p.q, p.s, p.g, 1, p.M, p.K, p.packed);
   a.wide = rows_32(p.gate, p.gate_stride, 2) && rows_32(p.up, p.up_stride, 2);
   int threads;
-  const int ch = row_split(p.M, p.K, &threads, &a.segs);
+  const int ch = row_split(p.M, p.K, 2, &threads, &a.segs);
   const int64_t grid = p.M * a.segs;
   if (grid > 0x7FFFFFFFll) return cudaErrorInvalidValue;  // the host refuses these first
   const void* k = p.fmt == kQMX8 ? act_kernel<kQMX8>(ch) : (p.fmt == kQMX4 ? act_kernel<kQMX4>(ch) : act_kernel<kQNV4>(ch));
@@ -452,11 +497,27 @@ cudaError_t launch_quantize_fp4(int fmt, const void* x, int64_t B, int64_t M, in
   a.wide = rows_32(x, K, 2);
   a.o = quant_out(fmt, q, s, g, B, M, K, packed_scales);
   int threads;
-  const int ch = row_split(B * M, K, &threads, &a.segs);
+  const int ch = row_split(B * M, K, 4, &threads, &a.segs);
   const int64_t grid = B * M * a.segs;
   if (grid > 0x7FFFFFFFll) return cudaErrorInvalidValue;  // the host refuses these first
   const void* k = fmt == kQNV4 ? fp4_kernel<kQNV4>(early_trigger, ch) : fp4_kernel<kQMX4>(early_trigger, ch);
   return launch_pdl(k, grid, threads, &a, stream, early_trigger);
+}
+
+cudaError_t launch_sf_repack(const uint8_t* src, int64_t B, int64_t R, int64_t KB, uint8_t* dst, cudaStream_t stream) {
+  const int64_t RT = ceil_div(R, kAtomRows), KT = ceil_div(KB, 4);
+  if (KB % 4 != 0 || RT > 65535 || B > 65535) return cudaErrorInvalidValue;  // the caller takes sf_pack then
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(ceil_div(KT, 8)), static_cast<unsigned>(RT), static_cast<unsigned>(B));
+  cfg.blockDim = dim3(kRepackThreads, 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  auto k = KB % 16 == 0 ? sf_repack_kernel<16> : sf_repack_kernel<4>;
+  return cudaLaunchKernelEx(&cfg, k, src, R, static_cast<int>(KB), static_cast<int>(KT), static_cast<int>(RT), dst);
 }
 
 cudaError_t launch_fp4_unpack(const uint8_t* q, int64_t n, uint8_t* out, cudaStream_t stream) {

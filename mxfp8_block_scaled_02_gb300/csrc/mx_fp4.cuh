@@ -49,10 +49,15 @@ __device__ __forceinline__ uint32_t cvt_e2m1x8(const float (&v)[8]) {
   return r;
 }
 
-// E4M3 byte (finite, non-negative) -> fp32, by its fields: exact.
-__device__ __forceinline__ float e4m3_to_f32(uint32_t b) {
-  const uint32_t e = b >> 3, m = b & 7u;
-  return e ? __uint_as_float(((e + 120u) << 23) | (m << 20)) : static_cast<float>(m) * 0.001953125f;  // 2^-9
+// E4M3 byte (finite, non-negative) -> fp32: its fields moved to fp32's, then the
+// exponent rebiased by 2^(127 - 7), exactly (subnormals too).
+__device__ __forceinline__ float e4m3_to_f32(uint32_t b) { return __uint_as_float(b << 20) * 1.329227996e36f; }
+
+// max(|a|, |b|), NaN if either is.
+__device__ __forceinline__ float max_abs(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)));
+  return r;
 }
 
 // NVFP4's tensor scale g and what the blocks share of it.
@@ -101,9 +106,10 @@ __device__ __forceinline__ uint32_t block_scale(uint32_t amax_bits, const Tensor
 // block's scale byte (the same in its lanes).
 template <int FMT>
 __device__ __forceinline__ uint32_t quantize_lane16(const float (&v)[16], const TensorScale& ts, uint32_t (&codes)[4]) {
-  uint32_t m = 0;
+  float m4[4];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+  for (int i = 0; i < 4; ++i) m4[i] = max_abs(max_abs(v[4 * i], v[4 * i + 1]), max_abs(v[4 * i + 2], v[4 * i + 3]));
+  uint32_t m = __float_as_uint(max_abs(max_abs(m4[0], m4[1]), max_abs(m4[2], m4[3]))) & 0x7FFFFFFFu;
   if (FMT != kQNV4) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
   float mul;
   bool nonfinite;

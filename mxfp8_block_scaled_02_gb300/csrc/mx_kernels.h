@@ -166,6 +166,9 @@ cudaError_t launch_silu_mul_quantize(const ActProblem& p, cudaStream_t stream);
 // 1).  early_trigger as launch_quantize.
 cudaError_t launch_quantize_fp4(int fmt, const void* x, int64_t B, int64_t M, int64_t K, const float* g, uint8_t* q,
                                 uint8_t* s, bool packed_scales, cudaStream_t stream, bool early_trigger);
+// Row-major scales [B, R, KB] (KB % 4 == 0, at most 65535 row tiles and
+// batches) -> packed atoms, for activations: programmatic, triggers early.
+cudaError_t launch_sf_repack(const uint8_t* src, int64_t B, int64_t R, int64_t KB, uint8_t* dst, cudaStream_t stream);
 // n packed codes (n % 32 == 0) -> n E4M3 bytes of the same values.
 cudaError_t launch_fp4_unpack(const uint8_t* q, int64_t n, uint8_t* out, cudaStream_t stream);
 

@@ -504,9 +504,7 @@ def _fmt4(fmt: str) -> int:
     return QFMT[fmt]
 
 
-def _check_tensor_scale(fmt: str, g: torch.Tensor | None) -> None:
-    if g is None:
-        return
+def _check_tensor_scale(fmt: str, g: torch.Tensor) -> None:
     if fmt != "nvfp4":
         raise ValueError(f"a tensor scale belongs to nvfp4, not {fmt}")
     if g.dtype != torch.float32 or g.numel() != 1 or not g.is_cuda:
@@ -527,7 +525,8 @@ def quantize_fp4(x: torch.Tensor, fmt: str = "mxfp4", *,
     if x.dtype != torch.bfloat16:
         raise TypeError("x must be bfloat16")
     _require_cuda(x)
-    _check_tensor_scale(fmt, tensor_scale)
+    if tensor_scale is not None:
+        _check_tensor_scale(fmt, tensor_scale)
     x = _aligned16(x)
     K = x.shape[-1]
     q = torch.empty((*x.shape[:-1], K // 2), dtype=torch.uint8, device=x.device)
@@ -573,7 +572,8 @@ def process_weights_fp4(w_q: torch.Tensor, w_scale: torch.Tensor, fmt: str = "mx
             or tuple(w_scale.shape[:-2]) != tuple(w_q.shape[:-2])
             or w_scale.shape[-2] < N or w_scale.shape[-1] < KB):
         raise ValueError(f"weight scale {tuple(w_scale.shape)} does not match weight {tuple(w_q.shape)}")
-    _check_tensor_scale(fmt, tensor_scale)
+    if tensor_scale is not None:
+        _check_tensor_scale(fmt, tensor_scale)
     w_scale = _bytes(w_scale)[..., :N, :KB].contiguous()
     _require_cuda(w_q, w_scale)
     w_q, w_scale = _aligned16(w_q), _aligned16(w_scale)
@@ -626,7 +626,8 @@ def linear_fp4(x: torch.Tensor, pw: PackedWeights, bias: torch.Tensor | None = N
     fmt, quantized = pw.fmt, x_scale is not None
     f = _fmt4(fmt)
     _require_cuda(x, x_scale, bias, out, workspace)
-    _check_tensor_scale(fmt, tensor_scale)
+    if tensor_scale is not None:
+        _check_tensor_scale(fmt, tensor_scale)
     if x.dtype != (torch.uint8 if quantized else torch.bfloat16):
         raise TypeError("x must be bfloat16, or uint8 codes with x_scale")
     KX = pw.K // 2 if quantized else pw.K
@@ -661,7 +662,8 @@ def quantize_packed_fp4(x: torch.Tensor, B: int = 1, fmt: str = "mxfp4", *,
     if x.dtype != torch.bfloat16:
         raise TypeError("x must be bfloat16")
     _require_cuda(x)
-    _check_tensor_scale(fmt, tensor_scale)
+    if tensor_scale is not None:
+        _check_tensor_scale(fmt, tensor_scale)
     x = _aligned16(x)
     K = x.shape[-1]
     rows = _rows_of(x, K)
@@ -717,12 +719,13 @@ def _rows2d(x: torch.Tensor, name: str) -> tuple[torch.Tensor, int, int]:
     when its rows start on 16-byte boundaries; anything else is copied."""
     if not x.is_cuda:
         raise ValueError("tensors must be on a CUDA device")
-    if x.dim() < 1 or x.shape[-1] == 0 or x.shape[-1] % BLOCK:
-        raise ValueError(f"{name} must be [..., K] with K a multiple of {BLOCK}, not {tuple(x.shape)}")
-    K = x.shape[-1]
+    shape = x.shape
+    K = shape[-1] if shape else 0
+    if K == 0 or K % BLOCK:
+        raise ValueError(f"{name} must be [..., K] with K a multiple of {BLOCK}, not {tuple(shape)}")
     rows = x.numel() // K
     if x.is_contiguous():
-        return _aligned16(x), rows, K
+        return (x if x.data_ptr() % 16 == 0 else _aligned16(x)), rows, K
     stride, step = 0, 1  # of the merged leading axes
     for size, st in zip(reversed(x.shape[:-1]), reversed(x.stride()[:-1])):
         if size == 1:
@@ -771,31 +774,34 @@ def rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tens
     f = _qfmt(fmt)
     if x.dtype != torch.bfloat16 or weight.dtype != torch.bfloat16:
         raise TypeError("x and weight must be bfloat16")
-    _check_tensor_scale(fmt, tensor_scale)
+    if tensor_scale is not None:
+        _check_tensor_scale(fmt, tensor_scale)
     _require_cuda(weight, residual_out, y)
+    shape = x.shape
     xr, rows, x_stride = _rows2d(x, "x")
-    K = x.shape[-1]
-    if tuple(weight.shape) != (K,):
+    K = shape[-1]
+    if weight.dim() != 1 or weight.shape[0] != K:
         raise ValueError(f"weight must be [{K}], not {tuple(weight.shape)}")
-    r_stride, rr = 0, None
+    r_ptr, r_stride, r_f32, t_ptr = None, 0, 0, None
     if residual is not None:
-        if residual.dtype not in (torch.bfloat16, torch.float32) or residual.shape != x.shape:
+        r_f32 = residual.dtype == torch.float32
+        if not (r_f32 or residual.dtype == torch.bfloat16) or residual.shape != shape:
             raise ValueError("residual must be bf16 or fp32 with x's shape")
         rr, _, r_stride = _rows2d(residual, "residual")
         if residual_out is None:
-            residual_out = torch.empty(x.shape, dtype=residual.dtype, device=x.device)
-        elif residual_out.dtype != residual.dtype or residual_out.shape != x.shape:
+            residual_out = torch.empty(shape, dtype=residual.dtype, device=x.device)
+        elif residual_out.dtype != residual.dtype or residual_out.shape != shape:
             raise ValueError("residual_out must have the residual's type and shape")
+        r_ptr, t_ptr = rr.data_ptr(), residual_out.data_ptr()
     elif residual_out is not None:
         raise ValueError("residual_out needs a residual")
-    if y is not None and (y.dtype != torch.bfloat16 or y.shape != x.shape):
+    if y is not None and (y.dtype != torch.bfloat16 or y.shape != shape):
         raise ValueError("y must be bf16 with x's shape")
     weight = _aligned16(weight)
-    res, q, s = _quantized_out(x.shape[:-1], x.device, rows, K, fmt, tensor_scale, packed)
-    _check(load().mxfp8_rmsnorm_quantize(f, _ptr(xr), x_stride, _ptr(rr), r_stride,
-                                         int(residual is not None and residual.dtype == torch.float32),
-                                         _ptr(residual_out), _ptr(weight), eps, _ptr(tensor_scale), rows, K,
-                                         _ptr(q), _ptr(s), int(packed), _ptr(y), _stream()))
+    res, q, s = _quantized_out(shape[:-1], x.device, rows, K, fmt, tensor_scale, packed)
+    _check(load().mxfp8_rmsnorm_quantize(f, xr.data_ptr(), x_stride, r_ptr, r_stride, r_f32, t_ptr, weight.data_ptr(),
+                                         eps, _ptr(tensor_scale), rows, K, q.data_ptr(), s.data_ptr(), packed,
+                                         _ptr(y), _stream()))
     return res, residual_out
 
 
@@ -809,7 +815,8 @@ def silu_mul_quantize(gate_up: torch.Tensor, up: torch.Tensor | None = None, *, 
     f = _qfmt(fmt)
     if gate_up.dtype != torch.bfloat16 or (up is not None and up.dtype != torch.bfloat16):
         raise TypeError("gate and up must be bfloat16")
-    _check_tensor_scale(fmt, tensor_scale)
+    if tensor_scale is not None:
+        _check_tensor_scale(fmt, tensor_scale)
     if up is None:
         if gate_up.dim() < 1 or gate_up.shape[-1] % (2 * BLOCK):
             raise ValueError(f"gate_up must be [..., 2 K] with K a multiple of {BLOCK}, not {tuple(gate_up.shape)}")
