@@ -50,7 +50,7 @@ constexpr int THREADS = 128 + SF_WARPS * 32 + EPI_WARPS * 32;
 constexpr int STAGES = 5;
 constexpr int A_BYTES = BM * BKB;
 constexpr int B_BYTES = (BN / 2) * BKB;
-constexpr int OUT_BOX = 32 * 64;  // staging box: 32 rows x 64 bytes
+constexpr int OUT_BOX = 32 * 128;  // staging box of an epilogue warp: 32 rows x 128 bytes, whole cache lines
 constexpr int TMEM_COLS = 512;
 
 template <int FMT>
@@ -69,14 +69,12 @@ struct Cfg {
   static constexpr int T_SF = ACC1 + BN;
   static_assert(T_SF + SLOTS * SLOT_COLS <= TMEM_COLS, "tensor memory overflow");
   static_assert(SLOTS <= STAGES, "a slot is freed by a stage's commit");
-  // drain steps (64 columns of the tile each) that cover the shared columns
-  static constexpr int RELEASE = (BN - ACC1 + 63) / 64;
   static constexpr int OFF_A = 0;
   static constexpr int OFF_B = OFF_A + STAGES * A_BYTES;
   static constexpr int OFF_SFA = OFF_B + STAGES * B_BYTES;
   static constexpr int OFF_SFB = OFF_SFA + STAGES * SFA_BYTES;
   static constexpr int OFF_OUT = OFF_SFB + STAGES * SFB_BYTES;
-  static constexpr int OFF_BIAS = OFF_OUT + EPI_WARPS * 2 * OUT_BOX;
+  static constexpr int OFF_BIAS = OFF_OUT + EPI_WARPS * OUT_BOX;
   static constexpr int OFF_BAR = OFF_BIAS + EPI_WARPS * 4 * 32 * 2;
   static constexpr int OFF_MISC = OFF_BAR + (4 * STAGES + 2) * 8;
   static constexpr int SMEM = OFF_MISC + 16 + 1024;
@@ -152,10 +150,6 @@ __device__ __forceinline__ void expect_tx_elected(uint32_t elected, uint32_t bar
       : "memory");
 }
 
-__device__ __forceinline__ void bulk_wait_group_read1() {
-  asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-}
-
 struct Args {
   const __nv_bfloat16* bias;
   const float* gx;
@@ -165,7 +159,7 @@ struct Args {
   int last_steps;   // MMA steps of the last stage
   int units;        // tiles * splits
   int splits;
-  int n_fast;
+  int n_fast;       // tile order: 1 = column tiles vary fastest
 };
 
 // Unit u = tile * splits + s: its tile and stages [kt_lo, kt_hi).
@@ -436,113 +430,108 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
   } else if (warp >= 4 + SF_WARPS) {
     // ------------------------------------------------------------ epilogue
-    // Warp e drains lanes 32 (warp % 4).. of the column groups {h, h + 2, h + 4,
-    // h + 6} of 32, h = e / 4: of the 64 shared columns each warp holds one
-    // group (the last two groups of an even tile, the first two of an odd one)
-    // and drains it first.
+    // Warp e drains lanes 32 (warp % 4).. of two of the tile's four groups of 64
+    // columns: e / 4 and the one two further.  The group that shares columns
+    // with the next tile's accumulator comes first (the upper one of an even
+    // tile, the lower one of an odd one), and the shared columns are released
+    // once all of them are in registers, before anything is stored.
     const int ew = warp - 4 - SF_WARPS;
     const int quad = warp & 3;
     const int half = ew >> 2;
-    uint8_t* box = smem + C::OFF_OUT + ew * 2 * OUT_BOX;
+    uint8_t* box = smem + C::OFF_OUT + ew * OUT_BOX;
     __nv_bfloat16* bias_s = reinterpret_cast<__nv_bfloat16*>(smem + C::OFF_BIAS) + ew * 128;
     const uint32_t acc_free_even = map_shared_rank(smem_u32(acc_free), 0);
     grid_dependency_wait();  // g_x may be the previous kernel's output
     float alpha = 1.f;
     if (args.gx != nullptr) alpha = *args.gx;
     if (args.gw != nullptr) alpha *= *args.gw;
-    int nbox = 0, tile_no = 0;
     const bool partial = args.splits > 1;
-    // 32 columns of this warp's rows: scale, bias, round, store through a box
-    auto store_group = [&](const uint32_t (&r)[32], int b, int c, int col, int row0, int nt, int sp) {
-      if (partial) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint8_t* dst = box + (nbox & 1) * OUT_BOX;
-          if (lane == 0 && nbox >= 2) bulk_wait_group_read1();
-          __syncwarp();
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int e = 16 * h + 4 * q;
-            *reinterpret_cast<float4*>(dst + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)) =
-                make_float4(__uint_as_float(r[e]) * alpha, __uint_as_float(r[e + 1]) * alpha,
-                            __uint_as_float(r[e + 2]) * alpha, __uint_as_float(r[e + 3]) * alpha);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            tma_store_3d(&tmOut, dst, nt * BN + col + 16 * h, row0, sp * args.B + b);
-            bulk_commit_group();
-          }
-          ++nbox;
-        }
-        return;
-      }
-      uint32_t packed[16];
-      if (args.bias != nullptr) {
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const uint32_t bw = reinterpret_cast<const uint32_t*>(bias_s + c * 32)[j];
-          packed[j] = pack_bf16x2(fmaf(__uint_as_float(r[2 * j]), alpha, __uint_as_float(bw << 16)),
-                                  fmaf(__uint_as_float(r[2 * j + 1]), alpha, __uint_as_float(bw & 0xFFFF0000u)));
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-          packed[j] = pack_bf16x2(__uint_as_float(r[2 * j]) * alpha, __uint_as_float(r[2 * j + 1]) * alpha);
-      }
-      uint8_t* dst = box + (nbox & 1) * OUT_BOX;
-      if (lane == 0 && nbox >= 2) bulk_wait_group_read1();
+    bool pending = false;
+    // 16-byte piece q of this lane's row: 128-byte swizzle, so the eight lanes
+    // of a store phase touch different banks
+    auto piece = [&](int q) { return reinterpret_cast<uint4*>(box + lane * 128 + ((q ^ (lane & 7)) << 4)); };
+    auto box_free = [&]() {
+      if (lane == 0 && pending) bulk_wait_group_read0();
       __syncwarp();
-      // 64-byte swizzle: 16-byte chunk q of row r sits at q ^ ((r / 2) % 4),
-      // so the eight lanes of a store phase touch different banks
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        *reinterpret_cast<uint4*>(dst + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)) =
-            make_uint4(packed[4 * q], packed[4 * q + 1], packed[4 * q + 2], packed[4 * q + 3]);
+    };
+    auto store_box = [&](int col, int row, int z) {
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        tma_store_3d(&tmOut, dst, nt * BN + col, row0, b);
+        tma_store_3d(&tmOut, box, col, row, z);
         bulk_commit_group();
+        pending = true;
       }
-      ++nbox;
     };
+    int tile_no = 0;
     for (int u = pair; u < args.units; u += npairs, ++tile_no) {
       int b, mt, nt, sp, kt_lo, kt_hi;
       unit_coords(u, args, b, mt, nt, sp, kt_lo, kt_hi);
       const int row0 = (mt * 2 + static_cast<int>(rank)) * BM + quad * 32;
       if (!partial && args.bias != nullptr) {
-        // this warp's 4 x 32 bias values (zero past N)
+        // the bias of this warp's two groups (zero past N)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int n = nt * BN + (2 * c + half) * 32 + lane;
-          bias_s[c * 32 + lane] = n < args.N ? args.bias[n] : __float2bfloat16(0.f);
+        for (int i = 0; i < 4; ++i) {
+          const int n = nt * BN + (half + (i & 2)) * 64 + (i & 1) * 32 + lane;
+          bias_s[i * 32 + lane] = n < args.N ? args.bias[n] : __float2bfloat16(0.f);
         }
         __syncwarp();
       }
       if (!mbar_wait(acc_full, static_cast<uint32_t>(tile_no & 1), abort_flag)) break;
       tc_fence_after();
-      const uint32_t acc = tmem + (static_cast<uint32_t>(quad * 32) << 16) + ((tile_no & 1) ? C::ACC1 : 0);
-      // the columns shared with the next tile's accumulator, all into registers
-      uint32_t r[C::RELEASE][32];
-#pragma unroll
-      for (int i = 0; i < C::RELEASE; ++i) {
-        const int c = (tile_no & 1) ? i : 3 - i;
-        tmem_ld_32x32b_x32(acc + (2 * c + half) * 32, r[i]);
-      }
-      tmem_ld_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_remote(acc_free_even);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int c = (tile_no & 1) ? i : 3 - i;
-        const int col = (2 * c + half) * 32;
-        if (i >= C::RELEASE) {
-          tmem_ld_32x32b_x32(acc + col, r[0]);
-          tmem_ld_wait();
+      const bool odd = tile_no & 1;
+      const uint32_t acc = tmem + (static_cast<uint32_t>(quad * 32) << 16) + (odd ? C::ACC1 : 0);
+      // whether the second group also holds shared columns
+      const bool both = odd ? (half + 2) * 64 < BN - C::ACC1 : (half + 1) * 64 > C::ACC1;
+#pragma unroll 1
+      for (int i = 0; i < 2; ++i) {
+        const int up = (i == 0) != odd;  // the upper of this warp's groups
+        const int col = (half + 2 * up) * 64;
+        uint32_t r[2][32];
+        tmem_ld_32x32b_x32(acc + col, r[0]);
+        tmem_ld_32x32b_x32(acc + col + 32, r[1]);
+        tmem_ld_wait();
+        if (i == (both ? 1 : 0)) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_remote(acc_free_even);
         }
-        store_group(r[i < C::RELEASE ? i : 0], b, c, col, row0, nt, sp);
+        if (partial) {
+          // fp32 partial of this K split: 32 columns a box
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            box_free();
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              *piece(q) = make_uint4(__float_as_uint(__uint_as_float(r[h][4 * q]) * alpha),
+                                     __float_as_uint(__uint_as_float(r[h][4 * q + 1]) * alpha),
+                                     __float_as_uint(__uint_as_float(r[h][4 * q + 2]) * alpha),
+                                     __float_as_uint(__uint_as_float(r[h][4 * q + 3]) * alpha));
+            store_box(nt * BN + col + 32 * h, row0, sp * args.B + b);
+          }
+          continue;
+        }
+        const uint32_t* bw = reinterpret_cast<const uint32_t*>(bias_s + up * 64);
+        box_free();
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          uint32_t o[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int j = 4 * q + e;  // columns 2 j and 2 j + 1 of the group
+            float lo = __uint_as_float(r[j >> 4][2 * (j & 15)]), hi = __uint_as_float(r[j >> 4][2 * (j & 15) + 1]);
+            if (args.bias != nullptr) {
+              lo = fmaf(lo, alpha, __uint_as_float(bw[j] << 16));
+              hi = fmaf(hi, alpha, __uint_as_float(bw[j] & 0xFFFF0000u));
+            } else {
+              lo *= alpha;
+              hi *= alpha;
+            }
+            o[e] = pack_bf16x2(lo, hi);
+          }
+          *piece(q) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+        store_box(nt * BN + col, row0, b);
       }
     }
     if (lane == 0) bulk_wait_group0();
@@ -589,11 +578,11 @@ cudaError_t launch_t(const Fp4Problem& p, int sms, cudaStream_t stream, const ch
             encode_map3(&msb, u32, p.sfw, RTB * words, KA, p.B, RTB * kAtomBytes, KA * RTB * kAtomBytes, 2 * words,
                     C::ATOMS, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
   if (splits > 1)
-    ok = ok && encode_map3(&mo, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, p.part, p.N, p.M, splits * p.B, p.N * 4, p.M * p.N * 4, 16,
-                       32, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE);
+    ok = ok && encode_map3(&mo, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, p.part, p.N, p.M, splits * p.B, p.N * 4, p.M * p.N * 4, 32,
+                       32, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE);
   else
-    ok = ok && encode_map3(&mo, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.out, p.N, p.M, p.B, p.N * 2, p.M * p.N * 2, 32, 32,
-                       CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE);
+    ok = ok && encode_map3(&mo, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.out, p.N, p.M, p.B, p.N * 2, p.M * p.N * 2, 64, 32,
+                       CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE);
   if (!ok) {
     *msg = "cuTensorMapEncodeTiled rejected a 4-bit operand or output";
     return cudaErrorInvalidValue;
@@ -612,8 +601,11 @@ cudaError_t launch_t(const Fp4Problem& p, int sms, cudaStream_t stream, const ch
   a.last_steps = static_cast<int>(ceil_div(p.K - static_cast<int64_t>(a.KT - 1) * BK, MMA_K));
   a.splits = splits;
   a.units = a.B * a.MT * a.NT * splits;
-  // the operand with fewer bytes is swept fastest, so that it stays in L2
-  a.n_fast = p.M >= p.N ? 1 : 0;
+  // Column tiles fastest while a sweep of the weights stays in L2 (two dies:
+  // half of it), else the operand with fewer bytes: M = 4096, N = 14336, K =
+  // 4096 76.2 -> 74.1 us, M = 8192, N = 4096, K = 14336 133.8 -> 126.8 us; at
+  // N = 28672, K = 4096 (59 MB of weights) row tiles fastest 151.9 against 161.5.
+  a.n_fast = p.M >= p.N || p.N * p.K / 2 <= (32ll << 20) ? 1 : 0;
   const int pairs = a.units < sms / 2 ? a.units : sms / 2;
 
   cudaLaunchConfig_t cfg = {};
