@@ -344,3 +344,18 @@ def test_graph_capture_and_two_streams(fmt):
         assert all(torch.equal(2 * a, b) for a, b in zip(ref, captured))
     else:
         assert all(torch.equal(a, b) for a, b in zip(run(), captured))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_outputs_past_two_billion_elements(fmt):
+    """M N beyond 32 bits: the last rows equal the same rows multiplied alone (every tile sums K in the same order)."""
+    dev = device()
+    M, N, K = 140000, 16384, 128
+    gen = torch.Generator(device=dev).manual_seed(2)
+    x = torch.randn(M, K, device=dev, generator=gen).to(torch.bfloat16)
+    w = torch.randn(N, K, device=dev, generator=gen).to(torch.bfloat16)
+    pw = ops.process_weights_fp4(*ops.quantize_fp4(w, fmt), fmt)
+    out = ops.linear_fp4(x, pw)
+    tail = ops.linear_fp4(x[-300:].clone(), pw)
+    ops.check()
+    assert torch.equal(out[-300:], tail) and torch.equal(out[:300], ops.linear_fp4(x[:300].clone(), pw))

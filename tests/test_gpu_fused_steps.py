@@ -284,3 +284,71 @@ def test_mlp_in_a_graph_and_refusals():
     other, *_ = make_mlp("mxfp4", 256, 512, dev)
     with pytest.raises(ValueError):
         mlp.GatedMLP(nw, block.gate_up, other.down)
+
+
+def banded(n_bytes, dev):
+    """A buffer of n_bytes inside 4 KB bands of a known byte: (buffer, check that the bands are untouched)."""
+    raw = torch.full((n_bytes + 8192,), 0xA5, dtype=torch.uint8, device=dev)
+    return raw[4096:4096 + n_bytes], lambda: bool((raw[:4096] == 0xA5).all() and (raw[4096 + n_bytes:] == 0xA5).all())
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("packed", [0, 1])
+@pytest.mark.parametrize("M,K", [(3, 96), (130, 1056)])
+def test_every_call_writes_its_documented_bytes_only(fmt, packed, M, K):
+    dev = device()
+    lib, st = ops.load(), torch.cuda.current_stream().cuda_stream
+    f = ops.QFMT[fmt]
+    x = torch.randn(M, 2 * K, device=dev).to(torch.bfloat16)
+    w = torch.randn(K, device=dev).to(torch.bfloat16)
+    res = torch.randn(M, K, device=dev)
+    qb = M * K // (1 if fmt == "mxfp8" else 2)
+    sizes = ops.packed_sizes(1, M, K) if fmt == "mxfp8" else ops.packed_sizes_fp4(1, M, K, fmt)
+    sb = sizes[1] if packed else M * K // ops.QBLOCK[fmt]
+    ok = []
+
+    def buf(n):
+        b, check = banded(n, dev)
+        ok.append(check)
+        return b.data_ptr()
+
+    assert lib.mxfp8_rmsnorm_quantize(f, x.data_ptr(), 2 * K, res.data_ptr(), K, 1, buf(4 * M * K), w.data_ptr(), 1e-6,
+                                      None, M, K, buf(qb), buf(sb), packed, buf(2 * M * K), st) == 0
+    assert lib.mxfp8_silu_mul_quantize(f, x.data_ptr(), 2 * K, x.data_ptr() + 2 * K, 2 * K, None, M, K, buf(qb), buf(sb),
+                                       packed, st) == 0
+    if fmt != "mxfp8":
+        xd = x[:, :K].contiguous()
+        if packed:
+            assert lib.mxfp8_fp4_quantize_packed(f, xd.data_ptr(), 1, M, K, None, buf(qb), buf(sb), st) == 0
+        else:
+            assert lib.mxfp8_fp4_quantize(f, xd.data_ptr(), M, K, None, buf(qb), buf(sb), st) == 0
+            q, s = ops.quantize_fp4(xd, fmt)
+            assert lib.mxfp8_fp4_unpack(q.data_ptr(), M * K, buf(M * K), st) == 0
+            assert lib.mxfp8_fp4_process_weights(f, q.data_ptr(), s.data_ptr(), 1, M, K, buf(qb), buf(sizes[1]), st) == 0
+    torch.cuda.synchronize()
+    assert all(check() for check in ok)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_tensors_past_two_billion_elements(fmt):
+    """Offsets beyond 32 bits: the last rows of a 2.2 G-element input come out as they do alone."""
+    dev = device()
+    M, K = 66000, 32768
+    gen = torch.Generator(device=dev).manual_seed(1)
+    x = torch.empty(M, K, dtype=torch.bfloat16, device=dev)
+    x[:-4] = 1.0
+    x[-4:] = torch.randn(4, K, device=dev, generator=gen).to(torch.bfloat16)
+    w = torch.randn(K, device=dev, generator=gen).to(torch.bfloat16)
+    (q, s), _ = ops.rmsnorm_quantize(x, w, fmt=fmt)
+    (q1, s1), _ = ops.rmsnorm_quantize(x[-4:].clone(), w, fmt=fmt)
+    assert torch.equal(q[-4:], q1) and torch.equal(s[-4:], s1)
+    del q, s
+    q, s = ops.silu_mul_quantize(x[:, :K // 2], x[:, K // 2:], fmt=fmt)
+    q1, s1 = ops.silu_mul_quantize(x[-4:].clone(), fmt=fmt)
+    assert torch.equal(q[-4:], q1) and torch.equal(s[-4:], s1)
+    del q, s
+    if fmt != "mxfp8":
+        q, s = ops.quantize_fp4(x, fmt)
+        q1, s1 = ops.quantize_fp4(x[-4:].clone(), fmt)
+        assert torch.equal(q[-4:], q1) and torch.equal(s[-4:], s1)
+        assert torch.equal(ops.unpack_fp4(q)[-4:].view(torch.uint8), ops.unpack_fp4(q1).view(torch.uint8))
