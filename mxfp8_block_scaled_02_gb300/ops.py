@@ -498,6 +498,13 @@ def linear_noalloc(x: torch.Tensor, pw: PackedWeights, bias: torch.Tensor | None
 
 
 # ------------------------------------------------------------------ 4-bit layer (MXFP4, NVFP4)
+# On the Grace host a short call costs as much in Python as in its launches, so
+# the functions below look things up once and call few helpers.
+_BF16, _F32, _U8 = torch.bfloat16, torch.float32, torch.uint8
+# (MXFP8_QFMT code, elements per code byte, block length) of the quantising formats
+_QSPEC = {"mxfp8": (0, 1, 32), "mxfp4": (1, 2, 32), "nvfp4": (2, 2, 16)}
+
+
 def _fmt4(fmt: str) -> int:
     if fmt not in ("mxfp4", "nvfp4"):
         raise ValueError(f"fmt must be 'mxfp4' or 'nvfp4', not {fmt!r}")
@@ -522,16 +529,19 @@ def quantize_fp4(x: torch.Tensor, fmt: str = "mxfp4", *,
     E4M3 [..., K/16]).  ``tensor_scale``: nvfp4's fp32 scale of the whole tensor
     (one element on the device; None is 1), normally amax / (448 * 6)."""
     f = _fmt4(fmt)
-    if x.dtype != torch.bfloat16:
+    if x.dtype is not _BF16:
         raise TypeError("x must be bfloat16")
     _require_cuda(x)
     if tensor_scale is not None:
         _check_tensor_scale(fmt, tensor_scale)
     x = _aligned16(x)
-    K = x.shape[-1]
-    q = torch.empty((*x.shape[:-1], K // 2), dtype=torch.uint8, device=x.device)
-    s = torch.empty((*x.shape[:-1], K // QBLOCK[fmt]), dtype=torch.uint8, device=x.device)
-    _check(load().mxfp8_fp4_quantize(f, _ptr(x), _rows_of(x, K), K, _ptr(tensor_scale), _ptr(q), _ptr(s), _stream()))
+    shape, dev = x.shape, x.device
+    lead, K = shape[:-1], shape[-1]
+    q = torch.empty(lead + (K // 2,), dtype=_U8, device=dev)
+    s = torch.empty(lead + (K // QBLOCK[fmt],), dtype=_U8, device=dev)
+    _check(load().mxfp8_fp4_quantize(f, x.data_ptr(), x.numel() // K if K else 0, K,
+                                     None if tensor_scale is None else tensor_scale.data_ptr(), q.data_ptr(),
+                                     s.data_ptr(), _stream()))
     return q, s
 
 
@@ -623,35 +633,35 @@ def linear_fp4(x: torch.Tensor, pw: PackedWeights, bias: torch.Tensor | None = N
     the weights' format), or with ``x_scale`` the codes uint8 [..., K/2] of
     quantize_fp4; ``tensor_scale`` is nvfp4's scale of x either way.  For batched
     weights x is [B, M, ...].  Returns bf16 [..., N]."""
-    fmt, quantized = pw.fmt, x_scale is not None
+    fmt, quantized, K, N, B = pw.fmt, x_scale is not None, pw.K, pw.N, pw.B
     f = _fmt4(fmt)
     _require_cuda(x, x_scale, bias, out, workspace)
     if tensor_scale is not None:
         _check_tensor_scale(fmt, tensor_scale)
-    if x.dtype != (torch.uint8 if quantized else torch.bfloat16):
+    if x.dtype is not (_U8 if quantized else _BF16):
         raise TypeError("x must be bfloat16, or uint8 codes with x_scale")
-    KX = pw.K // 2 if quantized else pw.K
-    if x.dim() < 1 or x.shape[-1] != KX:
-        raise ValueError(f"x {tuple(x.shape)} does not match weights with K={pw.K}")
-    if pw.batched and (x.dim() != 3 or x.shape[0] != pw.B):
+    shape, dev = x.shape, x.device
+    KX = K // 2 if quantized else K
+    if not shape or shape[-1] != KX:
+        raise ValueError(f"x {tuple(shape)} does not match weights with K={K}")
+    if pw.batched and (len(shape) != 3 or shape[0] != B):
         raise ValueError("batched weights need x of shape [B, M, K]")
-    if quantized and (x_scale.element_size() != 1
-                      or tuple(x_scale.shape) != (*x.shape[:-1], pw.K // QBLOCK[fmt])):
-        raise ValueError(f"{fmt} activation scale {tuple(x_scale.shape)} for codes {tuple(x.shape)}")
-    rows = _rows_of(x, KX)
+    lead = shape[:-1]
+    if quantized and (x_scale.element_size() != 1 or x_scale.shape != lead + (K // QBLOCK[fmt],)):
+        raise ValueError(f"{fmt} activation scale {tuple(x_scale.shape)} for codes {tuple(shape)}")
+    rows = x.numel() // KX
     _product_args(pw, bias, out, rows)
     x, x_scale, bias = _aligned16(x), _aligned16(x_scale), _aligned16(bias)
     if out is None:
-        out = torch.empty((*x.shape[:-1], pw.N), dtype=torch.bfloat16, device=x.device)
+        out = torch.empty(lead + (N,), dtype=_BF16, device=dev)
     if rows == 0:
         return out
-    M = rows // pw.B
-    ws_ptr, ws_bytes, workspace = _workspace(workspace, workspace_size_fp4(pw.B, M, pw.N, pw.K, quantized, fmt),
-                                             x.device)
-    _check(load().mxfp8_fp4_linear(f, None if quantized else x.data_ptr(), x.data_ptr() if quantized else None,
-                                   _ptr(x_scale), _ptr(tensor_scale), pw.B, M, pw.N, pw.K, pw.w_packed.data_ptr(),
-                                   pw.sf_packed.data_ptr(), _ptr(pw.tensor_scale), _ptr(bias), out.data_ptr(),
-                                   ws_ptr, ws_bytes, _stream()))
+    M = rows // B
+    ws_ptr, ws_bytes, workspace = _workspace(workspace, workspace_size_fp4(B, M, N, K, quantized, fmt), dev)
+    xp = x.data_ptr()
+    _check(load().mxfp8_fp4_linear(f, None if quantized else xp, xp if quantized else None, _ptr(x_scale),
+                                   _ptr(tensor_scale), B, M, N, K, pw.w_packed.data_ptr(), pw.sf_packed.data_ptr(),
+                                   _ptr(pw.tensor_scale), _ptr(bias), out.data_ptr(), ws_ptr, ws_bytes, _stream()))
     return out
 
 
@@ -747,15 +757,16 @@ def _quantized_out(lead, device, rows: int, K: int, fmt: str, tensor_scale: torc
     if packed:
         pa = _packed_activation(1, rows, K, fmt, tensor_scale, device)
         return pa, pa.x_q, pa.sf_packed
-    q = torch.empty((*lead, K if fmt == "mxfp8" else K // 2), dtype=torch.uint8, device=device)
-    s = torch.empty((*lead, K // QBLOCK[fmt]), dtype=torch.uint8, device=device)
+    _, per, block = _QSPEC[fmt]
+    q = torch.empty(lead + (K // per,), dtype=_U8, device=device)
+    s = torch.empty(lead + (K // block,), dtype=_U8, device=device)
     return (q, s), q, s
 
 
 def _qfmt(fmt: str) -> int:
-    if fmt not in QFMT:
-        raise ValueError(f"fmt must be one of {sorted(QFMT)}, not {fmt!r}")
-    return QFMT[fmt]
+    if fmt not in _QSPEC:
+        raise ValueError(f"fmt must be one of {sorted(_QSPEC)}, not {fmt!r}")
+    return _QSPEC[fmt][0]
 
 
 def rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None, *,
@@ -772,7 +783,7 @@ def rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tens
     gemm_packed_fp4.  ``residual_out`` (dense; may be a dense ``residual``
     itself) receives t; ``y`` (dense bf16) receives the norm unquantised too."""
     f = _qfmt(fmt)
-    if x.dtype != torch.bfloat16 or weight.dtype != torch.bfloat16:
+    if x.dtype is not _BF16 or weight.dtype is not _BF16:
         raise TypeError("x and weight must be bfloat16")
     if tensor_scale is not None:
         _check_tensor_scale(fmt, tensor_scale)
@@ -782,26 +793,29 @@ def rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tens
     K = shape[-1]
     if weight.dim() != 1 or weight.shape[0] != K:
         raise ValueError(f"weight must be [{K}], not {tuple(weight.shape)}")
-    r_ptr, r_stride, r_f32, t_ptr = None, 0, 0, None
+    r_ptr, r_stride, r_f32, t_ptr = None, 0, False, None
+    dev = x.device
     if residual is not None:
-        r_f32 = residual.dtype == torch.float32
-        if not (r_f32 or residual.dtype == torch.bfloat16) or residual.shape != shape:
+        rt = residual.dtype
+        r_f32 = rt is _F32
+        if not (r_f32 or rt is _BF16) or residual.shape != shape:
             raise ValueError("residual must be bf16 or fp32 with x's shape")
         rr, _, r_stride = _rows2d(residual, "residual")
         if residual_out is None:
-            residual_out = torch.empty(shape, dtype=residual.dtype, device=x.device)
-        elif residual_out.dtype != residual.dtype or residual_out.shape != shape:
+            residual_out = torch.empty(shape, dtype=rt, device=dev)
+        elif residual_out.dtype is not rt or residual_out.shape != shape:
             raise ValueError("residual_out must have the residual's type and shape")
         r_ptr, t_ptr = rr.data_ptr(), residual_out.data_ptr()
     elif residual_out is not None:
         raise ValueError("residual_out needs a residual")
-    if y is not None and (y.dtype != torch.bfloat16 or y.shape != shape):
+    if y is not None and (y.dtype is not _BF16 or y.shape != shape):
         raise ValueError("y must be bf16 with x's shape")
     weight = _aligned16(weight)
-    res, q, s = _quantized_out(shape[:-1], x.device, rows, K, fmt, tensor_scale, packed)
+    res, q, s = _quantized_out(shape[:-1], dev, rows, K, fmt, tensor_scale, packed)
     _check(load().mxfp8_rmsnorm_quantize(f, xr.data_ptr(), x_stride, r_ptr, r_stride, r_f32, t_ptr, weight.data_ptr(),
-                                         eps, _ptr(tensor_scale), rows, K, q.data_ptr(), s.data_ptr(), packed,
-                                         _ptr(y), _stream()))
+                                         eps, None if tensor_scale is None else tensor_scale.data_ptr(), rows, K,
+                                         q.data_ptr(), s.data_ptr(), packed, None if y is None else y.data_ptr(),
+                                         _stream()))
     return res, residual_out
 
 
@@ -813,7 +827,7 @@ def silu_mul_quantize(gate_up: torch.Tensor, up: torch.Tensor | None = None, *, 
     projection's output); or pass gate [..., K] and ``up`` [..., K].  Returns
     the quantised result as rmsnorm_quantize does."""
     f = _qfmt(fmt)
-    if gate_up.dtype != torch.bfloat16 or (up is not None and up.dtype != torch.bfloat16):
+    if gate_up.dtype is not _BF16 or (up is not None and up.dtype is not _BF16):
         raise TypeError("gate and up must be bfloat16")
     if tensor_scale is not None:
         _check_tensor_scale(fmt, tensor_scale)
@@ -833,7 +847,8 @@ def silu_mul_quantize(gate_up: torch.Tensor, up: torch.Tensor | None = None, *, 
         K, lead = gate_up.shape[-1], gate_up.shape[:-1]
         gate_ptr, up_ptr = gr.data_ptr(), ur.data_ptr()
     res, q, s = _quantized_out(lead, gate_up.device, rows, K, fmt, tensor_scale, packed)
-    _check(load().mxfp8_silu_mul_quantize(f, gate_ptr, gate_stride, up_ptr, up_stride, _ptr(tensor_scale), rows, K,
+    _check(load().mxfp8_silu_mul_quantize(f, gate_ptr, gate_stride, up_ptr, up_stride,
+                                          None if tensor_scale is None else tensor_scale.data_ptr(), rows, K,
                                           q.data_ptr(), s.data_ptr(), packed, _stream()))
     return res
 
