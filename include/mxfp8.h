@@ -524,6 +524,34 @@ mxfp8_status mxfp8_silu_mul_quantize(int fmt, const void* gate_bf16, int64_t gat
                                      uint8_t* scale, int scale_packed, mxfp8_stream_t stream);
 
 /*
+ * mxfp8_gated_mlp - the four steps of a gated MLP block in one call:
+ *   t = x + residual, a = quantise(rmsnorm(t)), h = a . gate_up^T (bf16),
+ *   c = quantise(silu(h[:, :F]) * h[:, F:]), out = c . down^T (bf16),
+ * by the calls above (mxfp8_rmsnorm_quantize, the packed product of fmt,
+ * mxfp8_silu_mul_quantize, the packed product) with the intermediates in the
+ * workspace; the outputs are theirs bit for bit.
+ *   fmt : MXFP8_QFMT_*, of both weights and of a and c.
+ *   x, residual, residual_out, norm_weight, eps, M, K : as
+ *     mxfp8_rmsnorm_quantize.
+ *   gate_up_packed, gate_up_sf : weights [2 F, K] (gate rows first) after
+ *     mxfp8_process_weights (MXFP8) or mxfp8_fp4_process_weights; down_packed,
+ *     down_sf : [K, F].  Their tensor scales, and those of a and c
+ *     (a_tensor_scale, c_tensor_scale): NVFP4 only, device fp32 or NULL for 1.
+ *   out_bf16 : device, dense [M, K].
+ *   workspace : >= mxfp8_gated_mlp_workspace_size bytes, 256-byte aligned.
+ *   K and F: multiples of 128 for MXFP8, of 32 for the 4-bit formats
+ *   (otherwise the products' errors).
+ */
+mxfp8_status mxfp8_gated_mlp_workspace_size(int fmt, int64_t M, int64_t K, int64_t F, size_t* bytes);
+mxfp8_status mxfp8_gated_mlp(int fmt, const void* x_bf16, int64_t x_stride, const void* residual,
+                             int64_t residual_stride, int residual_is_f32, void* residual_out,
+                             const void* norm_weight_bf16, float eps, int64_t M, int64_t K, int64_t F,
+                             const uint8_t* gate_up_packed, const uint8_t* gate_up_sf,
+                             const float* gate_up_tensor_scale, const uint8_t* down_packed, const uint8_t* down_sf,
+                             const float* down_tensor_scale, const float* a_tensor_scale, const float* c_tensor_scale,
+                             void* out_bf16, void* workspace, size_t workspace_bytes, mxfp8_stream_t stream);
+
+/*
  * Persistable packed weights.
  *   Source: the Mxfp8LinearKernel page: supports_pre_processed_weights and the
  *   weight-cache daemon that hands weights, already processed, to later

@@ -349,3 +349,107 @@ mxfp8_status mxfp8_silu_mul_quantize(int fmt, const void* gate_bf16, int64_t gat
 }
 
 }  // extern "C"
+
+namespace {
+
+// The intermediates of a gated MLP block.
+struct MlpLayout {
+  int64_t aq, asf, h, cq, csf, part, part_bytes, total;
+};
+
+mxfp8_status mlp_layout(int fmt, int64_t M, int64_t K, int64_t F, MlpLayout* w) {
+  mxfp8_status st = check_qfmt(fmt);
+  if (st != MXFP8_OK || (st = check_blocks(fmt, 1, M, K, "MLP")) != MXFP8_OK ||
+      (st = check_blocks(fmt, 1, M, F, "MLP")) != MXFP8_OK)
+    return st;
+  const int64_t per = fmt == MXFP8_QFMT_MXFP8 ? 1 : 2;
+  int64_t p1 = 0, p2 = 0;
+  if (fmt != MXFP8_QFMT_MXFP8 && M > 0) {
+    if ((st = check_product(fmt, 1, M, 2 * F, K)) != MXFP8_OK || (st = check_product(fmt, 1, M, K, F)) != MXFP8_OK)
+      return st;
+    p1 = workspace_layout(fmt, 1, M, 2 * F, K, true, true, product_splits(1, M, 2 * F, K)).total;
+    p2 = workspace_layout(fmt, 1, M, K, F, true, true, product_splits(1, M, K, F)).total;
+  }
+  int64_t at = 0;
+  auto take = [&](int64_t bytes) {
+    const int64_t o = at;
+    at += round_up(bytes, 256);
+    return o;
+  };
+  w->aq = take(M * K / per);
+  w->asf = take(mx::sf_packed_bytes(1, M, fp4_scale_extent(fmt, K)));
+  w->h = take(4 * M * F);
+  w->cq = take(M * F / per);
+  w->csf = take(mx::sf_packed_bytes(1, M, fp4_scale_extent(fmt, F)));
+  w->part_bytes = p1 > p2 ? p1 : p2;
+  w->part = take(w->part_bytes);
+  w->total = at;
+  return MXFP8_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+mxfp8_status mxfp8_gated_mlp_workspace_size(int fmt, int64_t M, int64_t K, int64_t F, size_t* bytes) {
+  if (bytes == nullptr) return fail(MXFP8_ERR_INVALID_ARG, "null output pointer");
+  MlpLayout w;
+  mxfp8_status st = mlp_layout(fmt, M, K, F, &w);
+  if (st == MXFP8_OK) *bytes = static_cast<size_t>(w.total);
+  return st;
+}
+
+mxfp8_status mxfp8_gated_mlp(int fmt, const void* x_bf16, int64_t x_stride, const void* residual,
+                             int64_t residual_stride, int residual_is_f32, void* residual_out,
+                             const void* norm_weight_bf16, float eps, int64_t M, int64_t K, int64_t F,
+                             const uint8_t* gate_up_packed, const uint8_t* gate_up_sf,
+                             const float* gate_up_tensor_scale, const uint8_t* down_packed, const uint8_t* down_sf,
+                             const float* down_tensor_scale, const float* a_tensor_scale, const float* c_tensor_scale,
+                             void* out_bf16, void* workspace, size_t workspace_bytes, mxfp8_stream_t stream) {
+  MlpLayout w;
+  mxfp8_status st = mlp_layout(fmt, M, K, F, &w);
+  if (st != MXFP8_OK) return st;
+  // everything a later step would refuse is refused before the first launch
+  const bool mx8 = fmt == MXFP8_QFMT_MXFP8;
+  if (mx8 && (K % 128 != 0 || F % 128 != 0))
+    return fail(MXFP8_ERR_UNSUPPORTED, "MLP: K=%lld and F=%lld must be multiples of 128 in MXFP8", (long long)K,
+                (long long)F);
+  if ((st = check_tensor_scale(fmt, gate_up_tensor_scale)) != MXFP8_OK ||
+      (st = check_tensor_scale(fmt, down_tensor_scale)) != MXFP8_OK ||
+      (st = check_tensor_scale(fmt, a_tensor_scale)) != MXFP8_OK ||
+      (st = check_tensor_scale(fmt, c_tensor_scale)) != MXFP8_OK)
+    return st;
+  if (M == 0) return MXFP8_OK;
+  if (mx8 && ((st = mx::check_block_count(1, 2 * F, K, "MLP")) != MXFP8_OK ||
+              (st = mx::check_block_count(1, K, F, "MLP")) != MXFP8_OK))
+    return st;
+  if (gate_up_packed == nullptr || gate_up_sf == nullptr || down_packed == nullptr || down_sf == nullptr ||
+      out_bf16 == nullptr)
+    return fail(MXFP8_ERR_INVALID_ARG, "null pointer");
+  if (!aligned(gate_up_packed, 16) || !aligned(gate_up_sf, 16) || !aligned(down_packed, 16) || !aligned(down_sf, 16) ||
+      !aligned(out_bf16, 16))
+    return fail(MXFP8_ERR_INVALID_ARG, "tensor pointers must be 16-byte aligned");
+  if (static_cast<int64_t>(workspace_bytes) < w.total)
+    return fail(MXFP8_ERR_INVALID_ARG, "workspace has %zu bytes, needs %lld", workspace_bytes, (long long)w.total);
+  if (workspace == nullptr || !aligned(workspace, 256))
+    return fail(MXFP8_ERR_INVALID_ARG, "workspace must be non-null and 256-byte aligned");
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  uint8_t *aq = ws + w.aq, *asf = ws + w.asf, *h = ws + w.h, *cq = ws + w.cq, *csf = ws + w.csf;
+  auto product = [&](const uint8_t* q, const uint8_t* sf, const float* g, int64_t N, int64_t Kp, const uint8_t* wp,
+                     const uint8_t* wsf, const float* gw, void* out) {
+    return mx8 ? mxfp8_gemm_packed(q, sf, 1, M, N, Kp, wp, wsf, nullptr, out, stream)
+               : mxfp8_fp4_gemm_packed(fmt, q, sf, g, 1, M, N, Kp, wp, wsf, gw, nullptr, out,
+                                       w.part_bytes > 0 ? ws + w.part : nullptr, static_cast<size_t>(w.part_bytes),
+                                       stream);
+  };
+  st = mxfp8_rmsnorm_quantize(fmt, x_bf16, x_stride, residual, residual_stride, residual_is_f32, residual_out,
+                              norm_weight_bf16, eps, a_tensor_scale, M, K, aq, asf, 1, nullptr, stream);
+  if (st != MXFP8_OK) return st;
+  st = product(aq, asf, a_tensor_scale, 2 * F, K, gate_up_packed, gate_up_sf, gate_up_tensor_scale, h);
+  if (st != MXFP8_OK) return st;
+  st = mxfp8_silu_mul_quantize(fmt, h, 2 * F, h + 2 * F, 2 * F, c_tensor_scale, M, F, cq, csf, 1, stream);
+  if (st != MXFP8_OK) return st;
+  return product(cq, csf, c_tensor_scale, K, F, down_packed, down_sf, down_tensor_scale, out_bf16);
+}
+
+}  // extern "C"

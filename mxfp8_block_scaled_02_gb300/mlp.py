@@ -5,7 +5,8 @@
 
 Four steps, each handing its output to the next already quantised in the
 weights' format (MXFP8, MXFP4 or NVFP4): norm with the residual's addition,
-merged gate and up projection, gated activation, down projection.
+merged gate and up projection, gated activation, down projection.  One library
+call (ops.gated_mlp) launches them.
 """
 
 from __future__ import annotations
@@ -30,14 +31,9 @@ class GatedMLP:
             raise ValueError(f"gate_up [{gate_up.N}, {gate_up.K}] and down [{down.N}, {down.K}] are not [2 F, K] and [K, F]")
         self.norm_weight, self.gate_up, self.down, self.eps = norm_weight, gate_up, down, eps
         self.x_tensor_scale, self.h_tensor_scale = x_tensor_scale, h_tensor_scale
-        self.fmt = "mxfp8" if gate_up.fmt == "e4m3" else gate_up.fmt
-        self._gemm = ops.gemm_packed if self.fmt == "mxfp8" else ops.gemm_packed_fp4
 
     def __call__(self, x: torch.Tensor, residual: torch.Tensor | None = None
                  ) -> tuple[torch.Tensor, torch.Tensor | None]:
         """x bf16 [..., K], residual bf16 or fp32 like x -> (bf16 [..., K], x + residual)."""
-        a, residual = ops.rmsnorm_quantize(x, self.norm_weight, residual, eps=self.eps, fmt=self.fmt,
-                                           tensor_scale=self.x_tensor_scale, packed=True)
-        h = self._gemm(a, self.gate_up)
-        a = ops.silu_mul_quantize(h, fmt=self.fmt, tensor_scale=self.h_tensor_scale, packed=True)
-        return self._gemm(a, self.down).view(x.shape), residual
+        return ops.gated_mlp(x, self.norm_weight, self.gate_up, self.down, residual, eps=self.eps,
+                             x_tensor_scale=self.x_tensor_scale, h_tensor_scale=self.h_tensor_scale)

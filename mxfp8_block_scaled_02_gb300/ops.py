@@ -76,6 +76,9 @@ SIGNATURES = {
     "mxfp8_rmsnorm_quantize": (_INT, [_INT, _P, _I64, _P, _I64, _INT, _P, _P, ctypes.c_float, _P, _I64, _I64,
                                       _P, _P, _INT, _P, _P]),
     "mxfp8_silu_mul_quantize": (_INT, [_INT, _P, _I64, _P, _I64, _P, _I64, _I64, _P, _P, _INT, _P]),
+    "mxfp8_gated_mlp_workspace_size": (_INT, [_INT, _I64, _I64, _I64, _SIZE_P]),
+    "mxfp8_gated_mlp": (_INT, [_INT, _P, _I64, _P, _I64, _INT, _P, _P, ctypes.c_float, _I64, _I64, _I64, _P, _P, _P,
+                               _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
     "mxfp8_check": (_INT, [_P]),
     "mxfp8_debug_expire_wait": (_INT, [_U64, _P]),
 }
@@ -851,6 +854,57 @@ def silu_mul_quantize(gate_up: torch.Tensor, up: torch.Tensor | None = None, *, 
                                           None if tensor_scale is None else tensor_scale.data_ptr(), rows, K,
                                           q.data_ptr(), s.data_ptr(), packed, _stream()))
     return res
+
+
+@functools.lru_cache(maxsize=4096)
+def gated_mlp_workspace_size(fmt: str, M: int, K: int, F: int) -> int:
+    n = ctypes.c_size_t()
+    _check(load().mxfp8_gated_mlp_workspace_size(_qfmt(fmt), M, K, F, ctypes.byref(n)))
+    return n.value
+
+
+def gated_mlp(x: torch.Tensor, norm_weight: torch.Tensor, gate_up: PackedWeights, down: PackedWeights,
+              residual: torch.Tensor | None = None, *, eps: float = 1e-6,
+              x_tensor_scale: torch.Tensor | None = None, h_tensor_scale: torch.Tensor | None = None,
+              workspace: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor | None]:
+    """A gated MLP block in one call (mxfp8_gated_mlp): rmsnorm_quantize of x (+
+    residual), the gate_up product, silu_mul_quantize and the down product, all
+    in the weights' format.  Returns (bf16 out like x, x + residual or None).
+    x_tensor_scale / h_tensor_scale: nvfp4's scales of the norm's and the
+    activation's output.  mlp.GatedMLP keeps the weights and checks them once."""
+    fmt = "mxfp8" if gate_up.fmt == "e4m3" else gate_up.fmt
+    f, K, F = _qfmt(fmt), gate_up.K, down.K
+    if gate_up.fmt != down.fmt or gate_up.batched or down.batched or gate_up.N != 2 * F or down.N != K:
+        raise ValueError(f"gate_up [{gate_up.N}, {K}] {gate_up.fmt} and down [{down.N}, {F}] {down.fmt} are not "
+                         "[2 F, K] and [K, F] of one format")
+    if x.dtype is not _BF16 or norm_weight.dtype is not _BF16:
+        raise TypeError("x and norm_weight must be bfloat16")
+    _require_cuda(norm_weight, workspace)
+    for g in (x_tensor_scale, h_tensor_scale):
+        if g is not None:
+            _check_tensor_scale(fmt, g)
+    shape, dev = x.shape, x.device
+    xr, rows, x_stride = _rows2d(x, "x")
+    if shape[-1] != K or tuple(norm_weight.shape) != (K,):
+        raise ValueError(f"x {tuple(shape)} and norm_weight {tuple(norm_weight.shape)} do not match K={K}")
+    r_ptr, r_stride, r_f32, t, t_ptr = None, 0, False, None, None
+    if residual is not None:
+        rt = residual.dtype
+        r_f32 = rt is _F32
+        if not (r_f32 or rt is _BF16) or residual.shape != shape:
+            raise ValueError("residual must be bf16 or fp32 with x's shape")
+        rr, _, r_stride = _rows2d(residual, "residual")
+        t = torch.empty(shape, dtype=rt, device=dev)
+        r_ptr, t_ptr = rr.data_ptr(), t.data_ptr()
+    norm_weight = _aligned16(norm_weight)
+    out = torch.empty(shape, dtype=_BF16, device=dev)
+    ws_ptr, ws_bytes, workspace = _workspace(workspace, gated_mlp_workspace_size(fmt, rows, K, F), dev)
+    _check(load().mxfp8_gated_mlp(f, xr.data_ptr(), x_stride, r_ptr, r_stride, r_f32, t_ptr, norm_weight.data_ptr(), eps,
+                                  rows, K, F, gate_up.w_packed.data_ptr(), gate_up.sf_packed.data_ptr(),
+                                  _ptr(gate_up.tensor_scale), down.w_packed.data_ptr(), down.sf_packed.data_ptr(),
+                                  _ptr(down.tensor_scale), _ptr(x_tensor_scale), _ptr(h_tensor_scale), out.data_ptr(),
+                                  ws_ptr, ws_bytes, _stream()))
+    return out, t
 
 
 def check() -> None:

@@ -233,8 +233,8 @@ def make_mlp(fmt, K, F, dev, seed=0):
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("M", [1, 40, 300])
 def test_mlp_block_is_its_steps_and_is_near_fp64(fmt, M):
-    """Every step is bit-identical to the separate calls (row-major scales and bf16 x into the layers);
-    against fp64 the block differs by the 8- or 4-bit roundings that two fp32 paths take differently,
+    """The one call is bit-identical to the separate packed calls, and up to the order of fp32 sums to those with
+    row-major scales; against fp64 the block differs by the 8- or 4-bit roundings that two fp32 paths take differently,
     which is rare: the rms of the difference stays under 1 % of the output's (bf16's own is 0.2 %)."""
     dev = device()
     K, F = 256, 640
@@ -244,6 +244,12 @@ def test_mlp_block_is_its_steps_and_is_near_fp64(fmt, M):
     res = (2 * torch.randn(M, K, device=dev)).to(torch.bfloat16)
     out, t = block(x, res)
     ops.check()
+    gemm = ops.gemm_packed if fmt == "mxfp8" else ops.gemm_packed_fp4
+    a, t2 = ops.rmsnorm_quantize(x, nw, res, fmt=fmt, tensor_scale=tx, packed=True)
+    c = ops.silu_mul_quantize(gemm(a, block.gate_up), fmt=fmt, tensor_scale=th, packed=True)
+    assert torch.equal(out, gemm(c, block.down)[0]) and torch.equal(t, t2)
+    alone, none = block(x)
+    assert none is None and alone.shape == x.shape
     (q, s), t2 = ops.rmsnorm_quantize(x, nw, res, fmt=fmt, tensor_scale=tx)
     lin = (lambda q, p, s, g: ops.linear(q, p, None, s)) if fmt == "mxfp8" else \
         (lambda q, p, s, g: ops.linear_fp4(q, p, None, s, tensor_scale=g))
@@ -284,6 +290,16 @@ def test_mlp_in_a_graph_and_refusals():
     other, *_ = make_mlp("mxfp4", 256, 512, dev)
     with pytest.raises(ValueError):
         mlp.GatedMLP(nw, block.gate_up, other.down)
+    for bad in (lambda: block(x[..., :128]), lambda: block(x, res[:1]), lambda: block(x, res.half()),
+                lambda: ops.gated_mlp(x, nw[:128], block.gate_up, block.down),
+                lambda: ops.gated_mlp(x, nw, block.down, block.gate_up),
+                lambda: ops.gated_mlp(x, nw, other.gate_up, other.down, x_tensor_scale=tx)):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(ops.MxStatusError, match="workspace"):
+        ops.gated_mlp(x, nw, block.gate_up, block.down, workspace=torch.empty(256, dtype=torch.uint8, device=dev))
+    empty, t = block(x[:0], res[:0])
+    assert empty.shape == (0, 4, 256) and t.shape == (0, 4, 256)
 
 
 def banded(n_bytes, dev):
