@@ -8,23 +8,35 @@
 // A cluster of two CTAs computes one 256 x 256 output tile (cta_group::2): CTA
 // r stages rows [128 r, +128) of the activation tile and of the weight tile,
 // and receives the accumulator of its activation rows.  A stage is 128 bytes
-// (256 elements) of K per row, so one instruction reads the same bytes as an
-// 8-bit one and does twice the work; the scales are twice (MXFP4) or four
-// times (NVFP4) as many per byte, which is why they travel by TMA and
-// tcgen05.cp here: one TMA per operand fetches a stage's atoms, and one copy
-// per 512-byte atom moves them to tensor memory in the MMA issuer's own
-// instruction order (no wait between a copy and the MMAs on either side).
+// (256 elements) of K per row: four instructions, 512 cycles of the tensor
+// cores.  One instruction reads the same bytes as an 8-bit one and does twice
+// the work, and there are twice (MXFP4) or four times (NVFP4) as many scales
+// per byte, which decides the rest:
+//   scales: one TMA per operand brings a stage's atoms.  A tcgen05.cp moves an
+//     atom to tensor memory in ~64 cycles, so MXFP4's 6 atoms a stage would
+//     just fit beside the MMAs and NVFP4's 12 would not; four warps write
+//     MXFP4's atoms and half of NVFP4's with tcgen05.st instead, into scale
+//     slots ahead of the MMAs.  (All by cp, M = 4096, N = 14336, K = 4096: MXFP4
+//     116 -> 89 us and NVFP4 145 -> 94 us when the writers came in; NVFP4 half by
+//     cp 86.8 -> 80.4.)
+//   issue: the MMA warp stays converged and its instructions are predicated
+//     (below): 89 -> 79 us.
+//   tensor memory: two accumulators of 256 columns that overlap (from column
+//     ACC1 on) and the scale slots beside them.  The epilogue drains a tile's
+//     shared columns first and releases them, so the next tile's MMAs run while
+//     the rest is drained and stored.
+// What bounds it (M = 4096, N = 14336, K = 4096, MXFP4 71.4 us, 6.7 PFLOP/s;
+// NVFP4 78.6): the way between L2 and the SMs, which operand loads (1.0 GB) and
+// output stores share: without the stores 66 of then 76 us, without the loads
+// 68, without both 62; the tensor cores alone need 50.  Longer K writes less:
+// M = 8192, N = 4096, K = 14336 124 us, 7.7 PFLOP/s.  192-column tiles with two
+// whole accumulators (86.8 against 73.1 us) load more; clusters of four would
+// share loads, but 144 of the 152 SMs hold them.
 //
-// Tensor memory: two accumulators of 256 columns that overlap in 64 columns
-// (0..255 and 192..447), and two scale slots of 24 columns (2 activation
-// atoms, 4 weight atoms).  The epilogue drains the shared 64 columns of a tile
-// first and releases them, so the next tile's MMAs run while the rest of the
-// tile is drained and stored.
-//
-// Warps: 0 operand TMA, 1 tensor-memory allocation and (even CTA) MMA issue,
-// 2 scale TMA, 3 idle, 4..11 epilogue.  Both CTAs' copies complete on the even
-// CTA's `full` barrier; the MMA commits free a stage in both CTAs.  Weights and
-// weight scales are loaded before griddepcontrol.wait, activations after it.
+// Warps: 0 weight TMA, 1 tensor-memory allocation and (even CTA) MMA issue,
+// 2 weight-scale TMA, 3 activation and activation-scale TMA, 4..7 scales into
+// tensor memory, 8..15 epilogue.  Both CTAs' operand copies complete on the
+// even CTA's `full` barrier; the MMA commits free a stage in both CTAs.
 // Every wait is bounded; the cluster barriers are reached on every path.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -216,89 +228,75 @@ __global__ void __launch_bounds__(THREADS, 1)
     mbar_init(acc_free, 2 * EPI_WARPS);
     *abort_flag = 0;
     fence_mbar_init();
-    prefetch_tmap(&tmA);
+  }
+  if (threadIdx.x == 64) {
     prefetch_tmap(&tmB);
-    prefetch_tmap(&tmSFA);
     prefetch_tmap(&tmSFB);
+    prefetch_tmap(&tmA);
+    prefetch_tmap(&tmSFA);
     prefetch_tmap(&tmOut);
   }
-  if (warp == 1) {
-    tmem_alloc_pair(tmem_slot, TMEM_COLS);
-    tmem_relinquish_pair();
-  }
-  tc_fence_before();
-  __syncthreads();
-  cluster_sync();  // both CTAs' barriers exist before anyone arrives remotely
-  tc_fence_after();
-  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
-  if (args.splits > 1 && threadIdx.x == 0) launch_dependents();  // this call's reduce waits for this grid itself
-
-  if (warp == 0 || warp == 2) {
-    // ------------------------------------------------------------ producers: operands (0), scales (2)
-    // Operands of both CTAs complete on the even CTA's `full`, which alone
-    // posts the count; the scales on this CTA's own sf_full.
-    const bool op = warp == 0;
-    const uint32_t elected = elect_one();
-    const uint32_t base = smem_u32(smem);
-    const uint32_t bar0 = smem_u32(op ? full : sf_full);
-    const uint32_t bar_to = op ? map_shared_rank(bar0, 0) : map_shared_rank(bar0, rank);
-    const uint32_t poster = op && !leader ? 0u : elected;
-    const uint32_t tx = op ? 2 * (A_BYTES + B_BYTES) : C::SFA_BYTES + C::SFB_BYTES;
-    const CUtensorMap* tm_x = op ? &tmA : &tmSFA;
-    const CUtensorMap* tm_w = op ? &tmB : &tmSFB;
-    const uint32_t dst_x = base + (op ? C::OFF_A : C::OFF_SFA), dst_w = base + (op ? C::OFF_B : C::OFF_SFB);
-    const uint32_t step_x = op ? A_BYTES : C::SFA_BYTES, step_w = op ? B_BYTES : C::SFB_BYTES;
-    // operands: {byte of K, row}; scales: {word of the atom row, atom along K}
-    auto load_w = [&](int st, int kt, int nt, int b) {
-      const int c0 = op ? kt * BKB : nt * 2 * (kAtomBytes / 4);
-      const int c1 = op ? nt * BN + static_cast<int>(rank) * (BN / 2) : kt * C::ATOMS;
-      tma_load_elected(elected, dst_w + st * step_w, tm_w, bar_to + st * 8, c0, c1, b);
-    };
-    auto load_x = [&](int st, int kt, int mt, int b) {
-      const int rt = mt * 2 + static_cast<int>(rank);
-      tma_load_elected(elected, dst_x + st * step_x, tm_x, bar_to + st * 8, op ? kt * BKB : rt * (kAtomBytes / 4),
-                       op ? rt * BM : kt * C::ATOMS, b);
-    };
-    // First ring round: the weights, then (after the kernel before this one
-    // in the stream) the activations, its output.
-    int P0 = 0;
-    for (int pass = 0; pass < 2; ++pass) {
-      P0 = 0;
-      for (int u = pair; u < args.units && P0 < STAGES; u += npairs) {
-        int b, mt, nt, sp, kt, kt_hi;
-        unit_coords(u, args, b, mt, nt, sp, kt, kt_hi);
-        for (; kt < kt_hi && P0 < STAGES; ++kt, ++P0) {
-          if (pass == 0) {
-            expect_tx_elected(poster, bar0 + P0 * 8, tx);
-            load_w(P0, kt, nt, b);
-          } else {
-            load_x(P0, kt, mt, b);
-          }
-        }
-      }
-      if (pass == 0) grid_dependency_wait();
+  // both CTAs' barriers exist before anyone signals them (this also joins the
+  // threads of the block)
+  cluster_sync();
+  // This call's reduce waits for this grid itself.  Without a split the next
+  // kernel is not let in early: a quantise or activation kernel that starts
+  // beside this one keeps its shared-memory split of the SM, and with the L1
+  // that is left a 8192 x 14336 quantise took 59 us instead of 46.
+  if (args.splits > 1 && threadIdx.x == 0) launch_dependents();
+  uint32_t tmem = 0;
+  if (warp == 1 || warp >= 4) {
+    // the loads start without waiting for the allocation
+    if (warp == 1) {
+      tmem_alloc_pair(tmem_slot, TMEM_COLS);
+      tmem_relinquish_pair();
     }
+    tc_fence_before();
+    asm volatile("bar.sync 1, %0;" ::"n"(THREADS - 96) : "memory");
+    tc_fence_after();
+    tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
+  }
+
+  if (warp == 0 || warp == 2 || warp == 3) {
+    // ------------------------------------------------------------ producers
+    // Warp 0 the weights, 2 their scales, 3 the activations and theirs (after
+    // the kernel before this one in the stream, whose output they are).
+    // Operands of both CTAs complete on the even CTA's `full`, whose count the
+    // even CTA alone posts, the scales on this CTA's own sf_full.  Bytes may
+    // land before the count is posted, but not a phase early: the stage was
+    // freed by a commit behind the MMA that waited for the previous phase.
+    const uint32_t elected = elect_one();
+    const uint32_t poster = leader ? elected : 0u;
+    const uint32_t base = smem_u32(smem);
+    const uint32_t full_even = map_shared_rank(smem_u32(full), 0), sf_own = map_shared_rank(smem_u32(sf_full), rank);
+    if (warp == 3) grid_dependency_wait();
     int stage = 0;
-    uint32_t phase = 0;
+    uint32_t phase = 1;  // the first round's slots are free
     int64_t issued = 0;
     bool ok = true;
     for (int u = pair; ok && u < args.units; u += npairs) {
       int b, mt, nt, sp, kt, kt_hi;
       unit_coords(u, args, b, mt, nt, sp, kt, kt_hi);
-      for (; kt < kt_hi; ++kt) {
-        if (issued >= P0) {
-          if (!mbar_wait_warp(&empty[stage], phase ^ 1u, abort_flag)) {
-            ok = false;
-            break;
-          }
-          // The odd CTA's bytes may land before the even CTA posts the
-          // count, but not a phase early: the stage was freed by a commit
-          // behind the MMA that waited for the barrier's previous phase.
-          expect_tx_elected(poster, bar0 + stage * 8, tx);
-          load_x(stage, kt, mt, b);
-          load_w(stage, kt, nt, b);
+      const int rt = mt * 2 + static_cast<int>(rank);
+      for (; kt < kt_hi; ++kt, ++issued) {
+        if (!mbar_wait_warp(&empty[stage], phase, abort_flag)) {
+          ok = false;
+          break;
         }
-        ++issued;
+        if (warp == 0) {
+          expect_tx_elected(poster, smem_u32(&full[stage]), 2 * (A_BYTES + B_BYTES));
+          tma_load_elected(elected, base + C::OFF_B + stage * B_BYTES, &tmB, full_even + stage * 8, kt * BKB,
+                           nt * BN + static_cast<int>(rank) * (BN / 2), b);
+        } else if (warp == 2) {
+          expect_tx_elected(elected, smem_u32(&sf_full[stage]), C::SFA_BYTES + C::SFB_BYTES);
+          tma_load_elected(elected, base + C::OFF_SFB + stage * C::SFB_BYTES, &tmSFB, sf_own + stage * 8,
+                           nt * 2 * (kAtomBytes / 4), kt * C::ATOMS, b);
+        } else {
+          tma_load_elected(elected, base + C::OFF_A + stage * A_BYTES, &tmA, full_even + stage * 8, kt * BKB, rt * BM,
+                           b);
+          tma_load_elected(elected, base + C::OFF_SFA + stage * C::SFA_BYTES, &tmSFA, sf_own + stage * 8,
+                           rt * (kAtomBytes / 4), kt * C::ATOMS, b);
+        }
         if (++stage == STAGES) {
           stage = 0;
           phase ^= 1u;
@@ -534,12 +532,12 @@ __global__ void __launch_bounds__(THREADS, 1)
         store_box(nt * BN + col, row0, b);
       }
     }
-    if (lane == 0) bulk_wait_group0();
+    if (lane == 0) bulk_wait_group_read0();  // the boxes are read; the end of the grid completes the stores
     __syncwarp();
   }
 
   tc_fence_before();
-  __syncthreads();
+  __syncwarp();
   cluster_sync();  // no CTA of the pair leaves while the other may still signal it
   if (warp == 1) {
     tc_fence_after();
@@ -648,16 +646,40 @@ bool encode_map3(CUtensorMap* m, CUtensorMapDataType dtype, const void* base, in
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Few output tiles: split K so that about 64 pairs have work, with at least
-// four stages a split and at most 8 splits.  A function of the shape alone.
-int fp4_splitk_splits(int64_t B, int64_t M, int64_t N, int64_t K) {
-  const int64_t tiles = B * ceil_div(M, 2 * BM) * ceil_div(N, BN);
-  const int64_t kt = ceil_div(K, BK);
-  if (tiles <= 0 || tiles > (kt >= 32 ? 32 : 16)) return 1;
-  int64_t s = 64 / tiles;
-  if (s > kt / 4) s = kt / 4;
+namespace {
+
+// What a product costs on CTA pairs, in 0.01 us, and the K split that gives it.
+// A stage of K takes 0.26 us (0.36 where a row of K/2 bytes is not a whole
+// number of 128-byte lines: K = 4128 11.5 us against 9.4 at 4096), the rest of a
+// call 5.4 us; partial sums and the kernel that adds them 2.3 us + 0.16 us a
+// tile + 0.1 us a split.  Measured (us, MXFP4, without a split / split in s): 8 tiles of K = 28672 34.7 / 13.4 (8); 16
+// tiles, K = 14336 20.0 / 14.2 (4); 32 tiles, K = 14336 20.3 / 20.7 (2); 32
+// tiles, K = 8192 14.0 / 17.1 (2).
+int64_t pair_cost(int64_t tiles, int64_t K, int* splits) {
+  const int64_t stages = ceil_div(K, BK), stage = K % BK != 0 ? 36 : 26;
+  int64_t s = tiles > 0 ? 64 / tiles : 1;  // about 64 pairs at work, at least four stages each
+  if (s > stages / 4) s = stages / 4;
   if (s > 8) s = 8;
-  return s >= 2 ? static_cast<int>(s) : 1;
+  const int64_t whole = 540 + stage * stages * (tiles > 76 ? ceil_div(tiles, 76) : 1);
+  *splits = 1;
+  if (s < 2) return whole;
+  const int64_t split = 540 + stage * ceil_div(stages, s) + 230 + 16 * tiles + 10 * s;
+  if (split >= whole) return whole;
+  *splits = static_cast<int>(s);
+  return split;
+}
+
+}  // namespace
+
+int fp4_splitk_splits(int64_t B, int64_t M, int64_t N, int64_t K) {
+  int s;
+  pair_cost(B * ceil_div(M, 2 * BM) * ceil_div(N, BN), K, &s);
+  return s;
+}
+
+int64_t fp4_pair_cost(int64_t B, int64_t M, int64_t N, int64_t K) {
+  int s;
+  return pair_cost(B * ceil_div(M, 2 * BM) * ceil_div(N, BN), K, &s);
 }
 
 cudaError_t launch_gemm_fp4(const Fp4Problem& p, int sms, cudaStream_t stream, const char** msg) {

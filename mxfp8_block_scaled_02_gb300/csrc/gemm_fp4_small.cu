@@ -544,19 +544,22 @@ bool fp4_quantizes_inside(int64_t B, int64_t M, int64_t N, int64_t K) {
 }
 
 // Where this kernel is the faster one (a function of the shape alone: the
-// workspace size depends on it).  It wins while each CTA's chain is short; the
-// CTA-pair kernel moves fewer bytes per MMA and wins on long ones.  Measured
-// (us, MXFP4, this kernel / CTA pairs): N = K = 4096, M = 128 7.1 / 9.5, 256
-// 10.1 / 11.3, 512 (16 stages a CTA) 11.1 / 10.3; N = 14336, K = 4096, M = 64
-// 9.2 / 10.5, 128 11.1 / 10.5; N = 4096, K = 14336, M = 128 10.1 / 12.6, 256
-// (28 stages) 16.1 / 14.5; N = 1000, K = 4128, M = 1024 10.6 / 12.2; two waves
-// of tiles (N = 28672), M = 16 15.0 / 17.9, 64 17.7 / 15.4; 16 x [M, 512, 7168],
-// M = 16 7.8 / 13.4, 128 12.0 / 13.5, 256 14.7 / 13.5.
+// workspace size depends on it): its time by the stages of a CTA's K range and
+// by the split, which shares the epilogue out but adds an exchange, against the
+// CTA-pair kernel's.  Measured (us, MXFP4, this kernel / CTA pairs): N = K =
+// 4096, M = 64 5.5 / 9.1, 128 7.1 / 9.4, 256 10.1 / 9.5, 512 11.1 / 9.7; N = K =
+// 8192, M = 128 12.5 / 13.9, 256 15.8 / 14.0; N = K = 2048, M = 256 6.3 / 7.4,
+// 512 8.9 / 7.5; N = 14336, K = 4096, M = 64 9.2 / 9.4, 128 11.0 / 9.9; N = 4096,
+// K = 14336, M = 128 10.2 / 20.0, 256 16.2 / 14.2; two waves of tiles (N =
+// 28672, K = 4096), M = 16 15.0 / 17.0, 64 17.9 / 14.5; 16 x [M, 512, 7168], M =
+// 16 7.8 / 12.2, 128 11.9 / 12.9, 256 14.7 / 13.1.
 bool fp4_use_small(int64_t B, int64_t M, int64_t N, int64_t K) {
   if (M <= 32) return true;
   const int64_t tiles = B * ceil_div(M, 128) * ceil_div(N, ROWS);
   if (tiles > 152) return false;  // more than one CTA an SM
-  return ceil_div(ceil_div(K, BK), splits_estimate(tiles)) <= (M <= 64 ? 16 : 14);
+  const int64_t splits = splits_estimate(tiles);
+  const int64_t fixed = M <= 64 ? 440 : (splits == 1 ? 640 : (splits == 2 ? 740 : (splits == 4 ? 590 : 530)));
+  return fixed + 31 * ceil_div(ceil_div(K, BK), splits) <= fp4_pair_cost(B, M, N, K);  // 0.01 us
 }
 
 cudaError_t launch_gemm_fp4_small(const Fp4Problem& p, int sms, cudaStream_t stream, const char** msg) {

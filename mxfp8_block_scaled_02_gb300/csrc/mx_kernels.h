@@ -192,6 +192,7 @@ struct Fp4Problem {
   const void* x_bf16 = nullptr;  // small-M kernel, fp4_quantizes_inside: bf16 x instead of x and sfx
 };
 int fp4_splitk_splits(int64_t B, int64_t M, int64_t N, int64_t K);
+int64_t fp4_pair_cost(int64_t B, int64_t M, int64_t N, int64_t K);  // with that split, in 0.01 us
 cudaError_t launch_gemm_fp4(const Fp4Problem& p, int sms, cudaStream_t stream, const char** msg);
 cudaError_t take_status_fp4(unsigned int* out);
 // A 3-D tensor map: innermost extent d0 in elements of `dtype`, strides s1 and
