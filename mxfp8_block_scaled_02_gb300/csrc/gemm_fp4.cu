@@ -5,8 +5,8 @@
 // K = 64 per instruction, fp32 accumulation in tensor memory; the result is
 // rounded once, after the tensor scales and the bias.
 //
-// A cluster of two CTAs computes one 256 x 256 output tile (cta_group::2): CTA
-// r stages rows [128 r, +128) of the activation tile and of the weight tile,
+// A cluster of two CTAs computes one 256 x 256 output tile (or 256 x 128, see
+// pair_plan) with cta_group::2: CTA r stages rows [128 r, +128) of the activation tile and of the weight tile,
 // and receives the accumulator of its activation rows.  A stage is 128 bytes
 // (256 elements) of K per row: four instructions, 512 cycles of the tensor
 // cores.  One instruction reads the same bytes as an 8-bit one and does twice
@@ -52,32 +52,33 @@ namespace mx {
 namespace {
 
 constexpr int BM = 128;       // activation rows per CTA (256 per pair)
-constexpr int BN = 256;       // output columns per pair tile
 constexpr int BKB = 128;      // bytes of K per row and stage
 constexpr int BK = 2 * BKB;   // elements of K per stage
 constexpr int MMA_K = 64;     // elements of K per instruction
 constexpr int EPI_WARPS = 8;
 constexpr int SF_WARPS = 4;
 constexpr int THREADS = 128 + SF_WARPS * 32 + EPI_WARPS * 32;
-constexpr int STAGES = 5;
 constexpr int A_BYTES = BM * BKB;
-constexpr int B_BYTES = (BN / 2) * BKB;
 constexpr int OUT_BOX = 32 * 128;  // staging box of an epilogue warp: 32 rows x 128 bytes, whole cache lines
 constexpr int TMEM_COLS = 512;
 
-template <int FMT>
+// BN: output columns of a pair's tile, 256 or (few tiles) 128
+template <int FMT, int BN>
 struct Cfg {
+  static constexpr int STAGES = BN == 256 ? 5 : (FMT == kQNV4 ? 6 : 7);
+  static constexpr int NB = BN / 128;  // row tiles of the weights
+  static constexpr int B_BYTES = (BN / 2) * BKB;
   // 512-byte atoms of 128 rows per stage: 128 (MXFP4) or 64 (NVFP4) elements each
   static constexpr int ATOMS = FMT == kQNV4 ? 4 : 2;
   static constexpr int SFA_BYTES = ATOMS * kAtomBytes;
-  static constexpr int SFB_BYTES = ATOMS * 2 * kAtomBytes;
-  // tensor memory: scale slots of ATOMS activation and 2 ATOMS weight atoms, 4
-  // columns each, above the two overlapping accumulators
-  static constexpr int SLOTS = FMT == kQNV4 ? 3 : STAGES;
-  static constexpr int SLOT_COLS = ATOMS * 12;
-  static constexpr int CP_A = FMT == kQNV4 ? 4 : 0;
-  static constexpr int CP_B = FMT == kQNV4 ? 2 : 0;
-  static constexpr int ACC1 = FMT == kQNV4 ? 96 : 128;  // first column of the odd tiles' accumulator
+  static constexpr int SFB_BYTES = ATOMS * NB * kAtomBytes;
+  // tensor memory: scale slots of ATOMS activation and NB ATOMS weight atoms, 4
+  // columns each, above the two accumulators (of 256 columns they overlap)
+  static constexpr int SLOTS = FMT == kQNV4 && BN == 256 ? 3 : STAGES;
+  static constexpr int SLOT_COLS = ATOMS * 4 * (1 + NB);
+  static constexpr int CP_A = FMT == kQNV4 && BN == 256 ? 4 : 0;
+  static constexpr int CP_B = FMT == kQNV4 && BN == 256 ? 2 : 0;
+  static constexpr int ACC1 = FMT == kQNV4 && BN == 256 ? 96 : 128;  // first column of the odd tiles' accumulator
   static constexpr int T_SF = ACC1 + BN;
   static_assert(T_SF + SLOTS * SLOT_COLS <= TMEM_COLS, "tensor memory overflow");
   static_assert(SLOTS <= STAGES, "a slot is freed by a stage's commit");
@@ -193,12 +194,13 @@ __device__ __forceinline__ void unit_coords(int u, const Args& a, int& b, int& m
   kt_hi = (s + 1) * a.KT / a.splits;
 }
 
-template <int FMT>
+template <int FMT, int BN>
 __global__ void __launch_bounds__(THREADS, 1)
     gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                     const __grid_constant__ CUtensorMap tmSFA, const __grid_constant__ CUtensorMap tmSFB,
                     const __grid_constant__ CUtensorMap tmOut, const Args args) {
-  using C = Cfg<FMT>;
+  using C = Cfg<FMT, BN>;
+  constexpr int STAGES = C::STAGES, B_BYTES = C::B_BYTES;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
@@ -290,7 +292,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         } else if (warp == 2) {
           expect_tx_elected(elected, smem_u32(&sf_full[stage]), C::SFA_BYTES + C::SFB_BYTES);
           tma_load_elected(elected, base + C::OFF_SFB + stage * C::SFB_BYTES, &tmSFB, sf_own + stage * 8,
-                           nt * 2 * (kAtomBytes / 4), kt * C::ATOMS, b);
+                           nt * C::NB * (kAtomBytes / 4), kt * C::ATOMS, b);
         } else {
           tma_load_elected(elected, base + C::OFF_A + stage * A_BYTES, &tmA, full_even + stage * 8, kt * BKB, rt * BM,
                            b);
@@ -358,7 +360,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int j = FMT == kQNV4 ? kk : kk >> 1;
             const uint32_t id = FMT == kQNV4 ? 0u : static_cast<uint32_t>(kk & 1) * 2u;
             mma_fp4_pair<FMT>(kk < steps ? elected : 0u, acc, ad + 2 * kk, bd + 2 * kk,
-                              idesc_with_sf_id(idesc, id, id), t_sfa + 4 * j, t_sfb + 8 * j, ((kt - kt_lo) | kk) != 0);
+                              idesc_with_sf_id(idesc, id, id), t_sfa + 4 * j, t_sfb + 4 * C::NB * j, ((kt - kt_lo) | kk) != 0);
           }
           commit_pair_elected(elected, &empty[stage]);
           if (++slot == C::SLOTS) slot = 0;
@@ -407,7 +409,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         tmem_st_32x32b_x4(t + 4 * j, v.x, v.y, v.z, v.w);
       }
 #pragma unroll
-      for (int j = C::CP_B; j < 2 * C::ATOMS; ++j) {
+      for (int j = C::CP_B; j < C::NB * C::ATOMS; ++j) {
         const uint4 v = sb[j * 32];
         tmem_st_32x32b_x4(t + 4 * C::ATOMS + 4 * j, v.x, v.y, v.z, v.w);
       }
@@ -428,8 +430,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
   } else if (warp >= 4 + SF_WARPS) {
     // ------------------------------------------------------------ epilogue
-    // Warp e drains lanes 32 (warp % 4).. of two of the tile's four groups of 64
-    // columns: e / 4 and the one two further.  The group that shares columns
+    // Warp e drains lanes 32 (warp % 4).. of the tile's group e / 4 of 64 columns
+    // and, of 256 columns, the one two further.  The group that shares columns
     // with the next tile's accumulator comes first (the upper one of an even
     // tile, the lower one of an odd one), and the shared columns are released
     // once all of them are in registers, before anything is stored.
@@ -469,7 +471,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (!partial && args.bias != nullptr) {
         // the bias of this warp's two groups (zero past N)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 2 * C::NB; ++i) {
           const int n = nt * BN + (half + (i & 2)) * 64 + (i & 1) * 32 + lane;
           bias_s[i * 32 + lane] = n < args.N ? args.bias[n] : __float2bfloat16(0.f);
         }
@@ -482,8 +484,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       // whether the second group also holds shared columns
       const bool both = odd ? (half + 2) * 64 < BN - C::ACC1 : (half + 1) * 64 > C::ACC1;
 #pragma unroll 1
-      for (int i = 0; i < 2; ++i) {
-        const int up = (i == 0) != odd;  // the upper of this warp's groups
+      for (int i = 0; i < C::NB; ++i) {
+        const int up = C::NB == 2 && (i == 0) != odd;  // the upper of this warp's groups
         const int col = (half + 2 * up) * 64;
         uint32_t r[2][32];
         tmem_ld_32x32b_x32(acc + col, r[0]);
@@ -545,14 +547,14 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
 }
 
-template <int FMT>
+template <int FMT, int BN>
 cudaError_t launch_t(const Fp4Problem& p, int sms, cudaStream_t stream, const char** msg) {
-  using C = Cfg<FMT>;
+  using C = Cfg<FMT, BN>;
   static bool attr_set[64] = {};
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev >= 0 && dev < 64 && !attr_set[dev]) {
-    cudaError_t e = cudaFuncSetAttribute(gemm_fp4_kernel<FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    cudaError_t e = cudaFuncSetAttribute(gemm_fp4_kernel<FMT, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) {
       *msg = "cudaFuncSetAttribute(max dynamic shared memory) failed";
       return e;
@@ -573,7 +575,7 @@ cudaError_t launch_t(const Fp4Problem& p, int sms, cudaStream_t stream, const ch
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B) &&
             encode_map3(&msa, u32, p.sfx, RTA * words, KA, p.B, RTA * kAtomBytes, KA * RTA * kAtomBytes, words, C::ATOMS,
                     CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B) &&
-            encode_map3(&msb, u32, p.sfw, RTB * words, KA, p.B, RTB * kAtomBytes, KA * RTB * kAtomBytes, 2 * words,
+            encode_map3(&msb, u32, p.sfw, RTB * words, KA, p.B, RTB * kAtomBytes, KA * RTB * kAtomBytes, C::NB * words,
                     C::ATOMS, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
   if (splits > 1)
     ok = ok && encode_map3(&mo, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, p.part, p.N, p.M, splits * p.B, p.N * 4, p.M * p.N * 4, 32,
@@ -620,7 +622,7 @@ cudaError_t launch_t(const Fp4Problem& p, int sms, cudaStream_t stream, const ch
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, gemm_fp4_kernel<FMT>, ma, mb, msa, msb, mo, a);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, gemm_fp4_kernel<FMT, BN>, ma, mb, msa, msb, mo, a);
   if (e != cudaSuccess) {
     *msg = "4-bit GEMM launch failed";
     return e;
@@ -648,42 +650,52 @@ bool encode_map3(CUtensorMap* m, CUtensorMapDataType dtype, const void* base, in
 
 namespace {
 
-// What a product costs on CTA pairs, in 0.01 us, and the K split that gives it.
-// A stage of K takes 0.26 us (0.36 where a row of K/2 bytes is not a whole
-// number of 128-byte lines: K = 4128 11.5 us against 9.4 at 4096), the rest of a
-// call 5.4 us; partial sums and the kernel that adds them 2.3 us + 0.16 us a
-// tile + 0.1 us a split.  Measured (us, MXFP4, without a split / split in s): 8 tiles of K = 28672 34.7 / 13.4 (8); 16
-// tiles, K = 14336 20.0 / 14.2 (4); 32 tiles, K = 14336 20.3 / 20.7 (2); 32
-// tiles, K = 8192 14.0 / 17.1 (2).
-int64_t pair_cost(int64_t tiles, int64_t K, int* splits) {
-  const int64_t stages = ceil_div(K, BK), stage = K % BK != 0 ? 36 : 26;
-  int64_t s = tiles > 0 ? 64 / tiles : 1;  // about 64 pairs at work, at least four stages each
+// How a product runs on CTA pairs (a function of the shape alone) and what it
+// costs, in 0.01 us: the least of
+//   256-column tiles: 5.4 us + 0.26 us a stage of K (0.36 where a row of K/2
+//     bytes is not a whole number of 128-byte lines);
+//   128-column tiles, where one a pair covers the output: 4.7 us + 0.25 (0.29)
+//     us a stage.  A CTA still loads 24 of the 32 KB a stage, so only the
+//     epilogue and the misaligned loads get shorter;
+//   256-column tiles with K split over about 64 pairs, at least four stages
+//     each: partial sums and the kernel that adds them cost 2.3 us + 0.16 us a
+//     tile + 0.1 us a split more.
+// Measured (us, MXFP4, 256 / 128 columns / split): N = K = 4096, M = 512 9.7 /
+// 9.0 / 15.2, M = 768 (one tile a pair / two) 9.8 / 13.5; N = K = 2048, M = 512
+// 7.5 / 6.6 / 10.7; N = 1000, K = 4128, M = 768 11.8 / 9.6 / 11.6; N = 4096, K =
+// 14336, M = 256 20.0 / 18.9 / 14.1, M = 512 20.2 / 19.2 / 20.8; N = 1024, K =
+// 28672, M = 512 34.6 / 33.0 / 13.5.
+struct PairPlan {
+  int bn, splits;
+  int64_t cost;
+};
+
+PairPlan pair_plan(int64_t B, int64_t M, int64_t N, int64_t K, bool may_split) {
+  const int64_t stages = ceil_div(K, BK), rows = B * ceil_div(M, 2 * BM), tiles = rows * ceil_div(N, 256);
+  const bool lines = K % BK == 0;
+  const int64_t stage = lines ? 26 : 36;
+  PairPlan p = {256, 1, 540 + stage * stages * (tiles > 76 ? ceil_div(tiles, 76) : 1)};
+  const int64_t narrow = 470 + (lines ? 25 : 29) * stages;
+  if (rows * ceil_div(N, 128) <= 76 && narrow < p.cost) p = {128, 1, narrow};
+  int64_t s = tiles > 0 ? 64 / tiles : 1;
   if (s > stages / 4) s = stages / 4;
   if (s > 8) s = 8;
-  const int64_t whole = 540 + stage * stages * (tiles > 76 ? ceil_div(tiles, 76) : 1);
-  *splits = 1;
-  if (s < 2) return whole;
+  if (!may_split || s < 2) return p;
   const int64_t split = 540 + stage * ceil_div(stages, s) + 230 + 16 * tiles + 10 * s;
-  if (split >= whole) return whole;
-  *splits = static_cast<int>(s);
-  return split;
+  if (split < p.cost) p = {256, static_cast<int>(s), split};
+  return p;
 }
 
 }  // namespace
 
-int fp4_splitk_splits(int64_t B, int64_t M, int64_t N, int64_t K) {
-  int s;
-  pair_cost(B * ceil_div(M, 2 * BM) * ceil_div(N, BN), K, &s);
-  return s;
-}
+int fp4_splitk_splits(int64_t B, int64_t M, int64_t N, int64_t K) { return pair_plan(B, M, N, K, true).splits; }
 
-int64_t fp4_pair_cost(int64_t B, int64_t M, int64_t N, int64_t K) {
-  int s;
-  return pair_cost(B * ceil_div(M, 2 * BM) * ceil_div(N, BN), K, &s);
-}
+int64_t fp4_pair_cost(int64_t B, int64_t M, int64_t N, int64_t K) { return pair_plan(B, M, N, K, true).cost; }
 
 cudaError_t launch_gemm_fp4(const Fp4Problem& p, int sms, cudaStream_t stream, const char** msg) {
-  return p.fmt == kQNV4 ? launch_t<kQNV4>(p, sms, stream, msg) : launch_t<kQMX4>(p, sms, stream, msg);
+  if (pair_plan(p.B, p.M, p.N, p.K, p.part != nullptr && p.splits > 1).bn == 128)
+    return p.fmt == kQNV4 ? launch_t<kQNV4, 128>(p, sms, stream, msg) : launch_t<kQMX4, 128>(p, sms, stream, msg);
+  return p.fmt == kQNV4 ? launch_t<kQNV4, 256>(p, sms, stream, msg) : launch_t<kQMX4, 256>(p, sms, stream, msg);
 }
 
 cudaError_t take_status_fp4(unsigned int* out) {
