@@ -60,7 +60,7 @@ mxfp8_status quantize_impl(int fmt, const void* x, int64_t B, int64_t M, int64_t
   return e == cudaSuccess ? MXFP8_OK : cuda_fail(e, "4-bit quantise launch");
 }
 
-// K splits of the CTA-pair kernel (1 where the small-M kernel runs).
+// K splits of the CTA-pair kernel that meet in workspace partials (else 1).
 int product_splits(int64_t B, int64_t M, int64_t N, int64_t K) {
   return mx::fp4_use_small(B, M, N, K) ? 1 : mx::fp4_splitk_splits(B, M, N, K);
 }

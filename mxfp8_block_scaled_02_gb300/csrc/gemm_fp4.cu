@@ -135,12 +135,12 @@ __device__ __forceinline__ void cp_sf_pair(uint32_t elected, uint32_t taddr, uin
       : "memory");
 }
 
-__device__ __forceinline__ void commit_pair_elected(uint32_t elected, uint64_t* bar) {
+__device__ __forceinline__ void commit_pair_elected(uint32_t elected, uint64_t* bar, uint16_t mask) {
   asm volatile(
       "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
       "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(
           smem_u32(bar)),
-      "h"(static_cast<uint16_t>(0x3)), "r"(elected)
+      "h"(mask), "r"(elected)
       : "memory");
 }
 
@@ -172,6 +172,7 @@ struct Args {
   int last_steps;   // MMA steps of the last stage
   int units;        // tiles * splits
   int splits;
+  int exchange;     // 1: the two splits of a tile meet in a cluster of two pairs
   int n_fast;       // tile order: 1 = column tiles vary fastest
 };
 
@@ -214,7 +215,9 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0);  // uniform
   const int lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_ctarank() & 1u;  // clusters are (2, 1, 1)
+  // clusters are (2, 1, 1), or (4, 1, 1) with the two K splits of a tile
+  const uint32_t crank = cluster_ctarank() & 3u;
+  const uint32_t rank = crank & 1u, even = crank & 2u;
   const bool leader = rank == 0;
   const int pair = blockIdx.x >> 1;
   const int npairs = gridDim.x >> 1;
@@ -245,7 +248,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   // kernel is not let in early: a quantise or activation kernel that starts
   // beside this one keeps its shared-memory split of the SM, and with the L1
   // that is left a 8192 x 14336 quantise took 59 us instead of 46.
-  if (args.splits > 1 && threadIdx.x == 0) launch_dependents();
+  if (args.splits > 1 && !args.exchange && threadIdx.x == 0) launch_dependents();
   uint32_t tmem = 0;
   if (warp == 1 || warp >= 4) {
     // the loads start without waiting for the allocation
@@ -270,7 +273,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t elected = elect_one();
     const uint32_t poster = leader ? elected : 0u;
     const uint32_t base = smem_u32(smem);
-    const uint32_t full_even = map_shared_rank(smem_u32(full), 0), sf_own = map_shared_rank(smem_u32(sf_full), rank);
+    const uint32_t full_even = map_shared_rank(smem_u32(full), even), sf_own = map_shared_rank(smem_u32(sf_full), crank);
     if (warp == 3) grid_dependency_wait();
     int stage = 0;
     uint32_t phase = 1;  // the first round's slots are free
@@ -320,6 +323,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (leader) {
       constexpr uint32_t idesc = idesc_fp4<FMT>(2 * BM, BN);
       const uint32_t elected = elect_one();
+      const uint16_t pair_mask = static_cast<uint16_t>(0x3u << even);
       const uint64_t ad0 = sdesc_kmajor_sw128(smem_u32(smem + C::OFF_A));
       const uint64_t bd0 = sdesc_kmajor_sw128(smem_u32(smem + C::OFF_B));
       int stage = 0, tile_no = 0, slot = 0;
@@ -362,7 +366,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             mma_fp4_pair<FMT>(kk < steps ? elected : 0u, acc, ad + 2 * kk, bd + 2 * kk,
                               idesc_with_sf_id(idesc, id, id), t_sfa + 4 * j, t_sfb + 4 * C::NB * j, ((kt - kt_lo) | kk) != 0);
           }
-          commit_pair_elected(elected, &empty[stage]);
+          commit_pair_elected(elected, &empty[stage], pair_mask);
           if (++slot == C::SLOTS) slot = 0;
           if (++stage == STAGES) {
             stage = 0;
@@ -370,7 +374,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
         }
         if (!ok) break;
-        commit_pair_elected(elected, acc_full);
+        commit_pair_elected(elected, acc_full, pair_mask);
       }
       if (!ok) __nanosleep(200000);  // let issued tensor-core work retire
     }
@@ -380,7 +384,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     // Each warp writes its 32 lanes of every atom: line l of an atom (rows l,
     // l + 32, l + 64, l + 96) goes to lane l of each quarter.
     const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + C::T_SF;
-    const uint32_t ready_even = map_shared_rank(smem_u32(sf_ready), 0);
+    const uint32_t ready_even = map_shared_rank(smem_u32(sf_ready), even);
     int64_t total = 0;
     for (int u = pair; u < args.units; u += npairs) {
       const int sp = u % args.splits;
@@ -440,12 +444,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int half = ew >> 2;
     uint8_t* box = smem + C::OFF_OUT + ew * OUT_BOX;
     __nv_bfloat16* bias_s = reinterpret_cast<__nv_bfloat16*>(smem + C::OFF_BIAS) + ew * 128;
-    const uint32_t acc_free_even = map_shared_rank(smem_u32(acc_free), 0);
+    const uint32_t acc_free_even = map_shared_rank(smem_u32(acc_free), even);
     grid_dependency_wait();  // g_x may be the previous kernel's output
     float alpha = 1.f;
     if (args.gx != nullptr) alpha = *args.gx;
     if (args.gw != nullptr) alpha *= *args.gw;
-    const bool partial = args.splits > 1;
+    const bool partial = args.splits > 1 && !args.exchange;
     bool pending = false;
     // 16-byte piece q of this lane's row: 128-byte swizzle, so the eight lanes
     // of a store phase touch different banks
@@ -463,75 +467,134 @@ __global__ void __launch_bounds__(THREADS, 1)
         pending = true;
       }
     };
-    int tile_no = 0;
-    for (int u = pair; u < args.units; u += npairs, ++tile_no) {
-      int b, mt, nt, sp, kt_lo, kt_hi;
-      unit_coords(u, args, b, mt, nt, sp, kt_lo, kt_hi);
-      const int row0 = (mt * 2 + static_cast<int>(rank)) * BM + quad * 32;
-      if (!partial && args.bias != nullptr) {
-        // the bias of this warp's two groups (zero past N)
+    // bias and rounding of a 64-column group of this lane's row, and its store
+    auto finish = [&](const uint32_t (&r)[2][32], const __nv_bfloat16* bias_g, int col, int row, int z) {
+      const uint32_t* bw = reinterpret_cast<const uint32_t*>(bias_g);
+      box_free();
 #pragma unroll
-        for (int i = 0; i < 2 * C::NB; ++i) {
-          const int n = nt * BN + (half + (i & 2)) * 64 + (i & 1) * 32 + lane;
+      for (int q = 0; q < 8; ++q) {
+        uint32_t o[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int j = 4 * q + e;  // columns 2 j and 2 j + 1 of the group
+          float lo = __uint_as_float(r[j >> 4][2 * (j & 15)]), hi = __uint_as_float(r[j >> 4][2 * (j & 15) + 1]);
+          if (args.bias != nullptr) {
+            lo = fmaf(lo, alpha, __uint_as_float(bw[j] << 16));
+            hi = fmaf(hi, alpha, __uint_as_float(bw[j] & 0xFFFF0000u));
+          } else {
+            lo *= alpha;
+            hi *= alpha;
+          }
+          o[e] = pack_bf16x2(lo, hi);
+        }
+        *piece(q) = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+      store_box(col, row, z);
+    };
+    if (BN == 256 && args.exchange) {
+      // The pair's sum over its half of K; each of the two pairs of the cluster
+      // finishes half of the columns and sends the other half, in fp32, to the
+      // other pair's stage buffers (all their copies and MMAs are done at the
+      // first barrier).  Warp e of a CTA writes what warp e of the other reads:
+      // 32 rows of one group, 16-byte piece q of lane l at 512 q + 16 l.
+      int b, mt, nt, sp, kt_lo, kt_hi;
+      unit_coords(pair, args, b, mt, nt, sp, kt_lo, kt_hi);
+      const int row0 = (mt * 2 + static_cast<int>(rank)) * BM + quad * 32;
+      const int keep = (2 * sp + half) * 64, send = (2 * (1 - sp) + half) * 64;
+      if (args.bias != nullptr) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int n = nt * BN + keep + i * 32 + lane;
           bias_s[i * 32 + lane] = n < args.N ? args.bias[n] : __float2bfloat16(0.f);
         }
-        __syncwarp();
       }
-      if (!mbar_wait(acc_full, static_cast<uint32_t>(tile_no & 1), abort_flag)) break;
+      const bool got = mbar_wait(acc_full, 0, abort_flag);
+      __syncwarp();
+      cluster_sync();
+      const uint32_t acc = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+      uint32_t r[2][32];
+      const uint32_t mine = smem_u32(smem + C::OFF_A) + ew * 8192 + lane * 16;
+      const uint32_t theirs = map_shared_rank(mine, crank ^ 2u);
       tc_fence_after();
-      const bool odd = tile_no & 1;
-      const uint32_t acc = tmem + (static_cast<uint32_t>(quad * 32) << 16) + (odd ? C::ACC1 : 0);
-      // whether the second group also holds shared columns
-      const bool both = odd ? (half + 2) * 64 < BN - C::ACC1 : (half + 1) * 64 > C::ACC1;
-#pragma unroll 1
-      for (int i = 0; i < C::NB; ++i) {
-        const int up = C::NB == 2 && (i == 0) != odd;  // the upper of this warp's groups
-        const int col = (half + 2 * up) * 64;
-        uint32_t r[2][32];
-        tmem_ld_32x32b_x32(acc + col, r[0]);
-        tmem_ld_32x32b_x32(acc + col + 32, r[1]);
+      if (__all_sync(0xFFFFFFFFu, got)) {
+        tmem_ld_32x32b_x32(acc + send, r[0]);
+        tmem_ld_32x32b_x32(acc + send + 32, r[1]);
         tmem_ld_wait();
-        if (i == (both ? 1 : 0)) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_remote(acc_free_even);
-        }
-        if (partial) {
-          // fp32 partial of this K split: 32 columns a box
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            box_free();
+        for (int q = 0; q < 16; ++q)
+          st_shared_cluster_v4(theirs + q * 512, r[q >> 3][4 * (q & 7)], r[q >> 3][4 * (q & 7) + 1],
+                               r[q >> 3][4 * (q & 7) + 2], r[q >> 3][4 * (q & 7) + 3]);
+        tmem_ld_32x32b_x32(acc + keep, r[0]);
+        tmem_ld_32x32b_x32(acc + keep + 32, r[1]);
+        tmem_ld_wait();
+      }
+      __syncwarp();
+      cluster_sync();
+      if (__all_sync(0xFFFFFFFFu, got)) {
+        const uint4* in = reinterpret_cast<const uint4*>(smem + C::OFF_A + ew * 8192) + lane;
 #pragma unroll
-            for (int q = 0; q < 8; ++q)
-              *piece(q) = make_uint4(__float_as_uint(__uint_as_float(r[h][4 * q]) * alpha),
-                                     __float_as_uint(__uint_as_float(r[h][4 * q + 1]) * alpha),
-                                     __float_as_uint(__uint_as_float(r[h][4 * q + 2]) * alpha),
-                                     __float_as_uint(__uint_as_float(r[h][4 * q + 3]) * alpha));
-            store_box(nt * BN + col + 32 * h, row0, sp * args.B + b);
-          }
-          continue;
-        }
-        const uint32_t* bw = reinterpret_cast<const uint32_t*>(bias_s + up * 64);
-        box_free();
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          uint32_t o[4];
+        for (int q = 0; q < 16; ++q) {
+          const uint4 v = in[q * 32];
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int j = 4 * q + e;  // columns 2 j and 2 j + 1 of the group
-            float lo = __uint_as_float(r[j >> 4][2 * (j & 15)]), hi = __uint_as_float(r[j >> 4][2 * (j & 15) + 1]);
-            if (args.bias != nullptr) {
-              lo = fmaf(lo, alpha, __uint_as_float(bw[j] << 16));
-              hi = fmaf(hi, alpha, __uint_as_float(bw[j] & 0xFFFF0000u));
-            } else {
-              lo *= alpha;
-              hi *= alpha;
-            }
-            o[e] = pack_bf16x2(lo, hi);
+            uint32_t& x = r[q >> 3][4 * (q & 7) + e];
+            x = __float_as_uint(__uint_as_float(x) + __uint_as_float(w[e]));
           }
-          *piece(q) = make_uint4(o[0], o[1], o[2], o[3]);
         }
-        store_box(nt * BN + col, row0, b);
+        finish(r, bias_s, nt * BN + keep, row0, b);
+      }
+    } else {
+      int tile_no = 0;
+      for (int u = pair; u < args.units; u += npairs, ++tile_no) {
+        int b, mt, nt, sp, kt_lo, kt_hi;
+        unit_coords(u, args, b, mt, nt, sp, kt_lo, kt_hi);
+        const int row0 = (mt * 2 + static_cast<int>(rank)) * BM + quad * 32;
+        if (!partial && args.bias != nullptr) {
+          // the bias of this warp's two groups (zero past N)
+#pragma unroll
+          for (int i = 0; i < 2 * C::NB; ++i) {
+            const int n = nt * BN + (half + (i & 2)) * 64 + (i & 1) * 32 + lane;
+            bias_s[i * 32 + lane] = n < args.N ? args.bias[n] : __float2bfloat16(0.f);
+          }
+          __syncwarp();
+        }
+        if (!mbar_wait(acc_full, static_cast<uint32_t>(tile_no & 1), abort_flag)) break;
+        tc_fence_after();
+        const bool odd = tile_no & 1;
+        const uint32_t acc = tmem + (static_cast<uint32_t>(quad * 32) << 16) + (odd ? C::ACC1 : 0);
+        // whether the second group also holds shared columns
+        const bool both = odd ? (half + 2) * 64 < BN - C::ACC1 : (half + 1) * 64 > C::ACC1;
+#pragma unroll 1
+        for (int i = 0; i < C::NB; ++i) {
+          const int up = C::NB == 2 && (i == 0) != odd;  // the upper of this warp's groups
+          const int col = (half + 2 * up) * 64;
+          uint32_t r[2][32];
+          tmem_ld_32x32b_x32(acc + col, r[0]);
+          tmem_ld_32x32b_x32(acc + col + 32, r[1]);
+          tmem_ld_wait();
+          if (i == (both ? 1 : 0)) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote(acc_free_even);
+          }
+          if (partial) {
+            // fp32 partial of this K split: 32 columns a box
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              box_free();
+#pragma unroll
+              for (int q = 0; q < 8; ++q)
+                *piece(q) = make_uint4(__float_as_uint(__uint_as_float(r[h][4 * q]) * alpha),
+                                       __float_as_uint(__uint_as_float(r[h][4 * q + 1]) * alpha),
+                                       __float_as_uint(__uint_as_float(r[h][4 * q + 2]) * alpha),
+                                       __float_as_uint(__uint_as_float(r[h][4 * q + 3]) * alpha));
+              store_box(nt * BN + col + 32 * h, row0, sp * args.B + b);
+            }
+            continue;
+          }
+          finish(r, bias_s + up * 64, nt * BN + col, row0, b);
+        }
       }
     }
     if (lane == 0) bulk_wait_group_read0();  // the boxes are read; the end of the grid completes the stores
@@ -540,6 +603,10 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   tc_fence_before();
   __syncwarp();
+  if (BN == 256 && args.exchange && warp < 4 + SF_WARPS) {  // the epilogue's two barriers
+    cluster_sync();
+    cluster_sync();
+  }
   cluster_sync();  // no CTA of the pair leaves while the other may still signal it
   if (warp == 1) {
     tc_fence_after();
@@ -547,8 +614,14 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
 }
 
+struct PairPlan {
+  int bn, splits;
+  bool exchange;  // the two splits meet in a cluster, without partials in memory
+  int64_t cost;
+};
+
 template <int FMT, int BN>
-cudaError_t launch_t(const Fp4Problem& p, int sms, cudaStream_t stream, const char** msg) {
+cudaError_t launch_t(const Fp4Problem& p, const PairPlan& plan, int sms, cudaStream_t stream, const char** msg) {
   using C = Cfg<FMT, BN>;
   static bool attr_set[64] = {};
   int dev = 0;
@@ -561,7 +634,9 @@ cudaError_t launch_t(const Fp4Problem& p, int sms, cudaStream_t stream, const ch
     }
     attr_set[dev] = true;
   }
-  const int splits = p.part != nullptr && p.splits > 1 ? p.splits : 1;
+  const bool exchange = plan.exchange;
+  const int splits = plan.splits;
+  const bool partials = splits > 1 && !exchange;
   const int64_t RTA = ceil_div(p.M, kAtomRows), RTB = ceil_div(p.N, kAtomRows);
   const int64_t KA = ceil_div(fp4_scale_extent(FMT, p.K), kTileK);  // scale atoms along K
   const int64_t kb = p.K / 2;
@@ -577,7 +652,7 @@ cudaError_t launch_t(const Fp4Problem& p, int sms, cudaStream_t stream, const ch
                     CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B) &&
             encode_map3(&msb, u32, p.sfw, RTB * words, KA, p.B, RTB * kAtomBytes, KA * RTB * kAtomBytes, C::NB * words,
                     C::ATOMS, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
-  if (splits > 1)
+  if (partials)
     ok = ok && encode_map3(&mo, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, p.part, p.N, p.M, splits * p.B, p.N * 4, p.M * p.N * 4, 32,
                        32, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE);
   else
@@ -588,7 +663,7 @@ cudaError_t launch_t(const Fp4Problem& p, int sms, cudaStream_t stream, const ch
     return cudaErrorInvalidValue;
   }
   Args a;
-  a.bias = splits > 1 ? nullptr : static_cast<const __nv_bfloat16*>(p.bias);
+  a.bias = partials ? nullptr : static_cast<const __nv_bfloat16*>(p.bias);
   a.gx = p.gx;
   a.gw = p.gw;
   a.B = static_cast<int>(p.B);
@@ -600,13 +675,14 @@ cudaError_t launch_t(const Fp4Problem& p, int sms, cudaStream_t stream, const ch
   a.KT = static_cast<int>(ceil_div(p.K, BK));
   a.last_steps = static_cast<int>(ceil_div(p.K - static_cast<int64_t>(a.KT - 1) * BK, MMA_K));
   a.splits = splits;
+  a.exchange = exchange ? 1 : 0;
   a.units = a.B * a.MT * a.NT * splits;
   // Column tiles fastest while a sweep of the weights stays in L2 (two dies:
   // half of it), else the operand with fewer bytes: M = 4096, N = 14336, K =
   // 4096 76.2 -> 74.1 us, M = 8192, N = 4096, K = 14336 133.8 -> 126.8 us; at
   // N = 28672, K = 4096 (59 MB of weights) row tiles fastest 151.9 against 161.5.
   a.n_fast = p.M >= p.N || p.N * p.K / 2 <= (32ll << 20) ? 1 : 0;
-  const int pairs = a.units < sms / 2 ? a.units : sms / 2;
+  const int pairs = exchange || a.units < sms / 2 ? a.units : sms / 2;
 
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs), 1, 1);
@@ -615,7 +691,7 @@ cudaError_t launch_t(const Fp4Problem& p, int sms, cudaStream_t stream, const ch
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.x = exchange ? 4 : 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -627,7 +703,7 @@ cudaError_t launch_t(const Fp4Problem& p, int sms, cudaStream_t stream, const ch
     *msg = "4-bit GEMM launch failed";
     return e;
   }
-  if (splits > 1) {
+  if (partials) {
     e = launch_splitk_reduce(p.part, splits, p.B, p.M, p.N, p.bias, p.out, nullptr, nullptr, sms, stream);
     if (e != cudaSuccess) *msg = "split-K reduce launch failed";
   }
@@ -657,45 +733,52 @@ namespace {
 //   128-column tiles, where one a pair covers the output: 4.7 us + 0.25 (0.29)
 //     us a stage.  A CTA still loads 24 of the 32 KB a stage, so only the
 //     epilogue and the misaligned loads get shorter;
+//   256-column tiles with K split in two, the halves meeting in a cluster of two
+//     pairs: 2.2 us + 0.05 us a tile more;
 //   256-column tiles with K split over about 64 pairs, at least four stages
 //     each: partial sums and the kernel that adds them cost 2.3 us + 0.16 us a
 //     tile + 0.1 us a split more.
-// Measured (us, MXFP4, 256 / 128 columns / split): N = K = 4096, M = 512 9.7 /
-// 9.0 / 15.2, M = 768 (one tile a pair / two) 9.8 / 13.5; N = K = 2048, M = 512
-// 7.5 / 6.6 / 10.7; N = 1000, K = 4128, M = 768 11.8 / 9.6 / 11.6; N = 4096, K =
-// 14336, M = 256 20.0 / 18.9 / 14.1, M = 512 20.2 / 19.2 / 20.8; N = 1024, K =
-// 28672, M = 512 34.6 / 33.0 / 13.5.
-struct PairPlan {
-  int bn, splits;
-  int64_t cost;
-};
-
+// Measured (us, MXFP4, 256 / 128 columns / in two / split): N = K = 4096, M = 512
+// 9.7 / 9.0 / 10.4 / 15.2, M = 768 (one tile a pair / two) 9.8 / 13.5; N = K =
+// 2048, M = 512 7.5 / 6.6 / 8.6 / 10.7; N = 1000, K = 4128, M = 768 11.8 / 9.6 /
+// 10.9 / 11.6; N = 4096, K = 14336, M = 256 20.0 / 18.9 / 15.2 / 14.1, M = 512
+// 20.2 / 19.2 / 16.5 / 20.8; N = 1024, K = 28672, M = 512 34.6 / 33.0 / 22.6 /
+// 13.5; N = 3584, K = 18944, M = 512 25.0 / 23.7 / 18.9 / 21.9.
 PairPlan pair_plan(int64_t B, int64_t M, int64_t N, int64_t K, bool may_split) {
   const int64_t stages = ceil_div(K, BK), rows = B * ceil_div(M, 2 * BM), tiles = rows * ceil_div(N, 256);
   const bool lines = K % BK == 0;
   const int64_t stage = lines ? 26 : 36;
-  PairPlan p = {256, 1, 540 + stage * stages * (tiles > 76 ? ceil_div(tiles, 76) : 1)};
+  PairPlan p = {256, 1, false, 540 + stage * stages * (tiles > 76 ? ceil_div(tiles, 76) : 1)};
   const int64_t narrow = 470 + (lines ? 25 : 29) * stages;
-  if (rows * ceil_div(N, 128) <= 76 && narrow < p.cost) p = {128, 1, narrow};
+  if (rows * ceil_div(N, 128) <= 76 && narrow < p.cost) p = {128, 1, false, narrow};
+  // 36 clusters of four CTAs run at a time
+  const int64_t exchange = 540 + stage * ceil_div(stages, 2) + 220 + 5 * tiles;
+  if (tiles <= 36 && stages >= 2 && exchange < p.cost) p = {256, 2, true, exchange};
   int64_t s = tiles > 0 ? 64 / tiles : 1;
   if (s > stages / 4) s = stages / 4;
   if (s > 8) s = 8;
   if (!may_split || s < 2) return p;
   const int64_t split = 540 + stage * ceil_div(stages, s) + 230 + 16 * tiles + 10 * s;
-  if (split < p.cost) p = {256, static_cast<int>(s), split};
+  if (split < p.cost) p = {256, static_cast<int>(s), false, split};
   return p;
 }
 
 }  // namespace
 
-int fp4_splitk_splits(int64_t B, int64_t M, int64_t N, int64_t K) { return pair_plan(B, M, N, K, true).splits; }
+int fp4_splitk_splits(int64_t B, int64_t M, int64_t N, int64_t K) {
+  const PairPlan p = pair_plan(B, M, N, K, true);
+  return p.exchange ? 1 : p.splits;
+}
 
 int64_t fp4_pair_cost(int64_t B, int64_t M, int64_t N, int64_t K) { return pair_plan(B, M, N, K, true).cost; }
 
 cudaError_t launch_gemm_fp4(const Fp4Problem& p, int sms, cudaStream_t stream, const char** msg) {
-  if (pair_plan(p.B, p.M, p.N, p.K, p.part != nullptr && p.splits > 1).bn == 128)
-    return p.fmt == kQNV4 ? launch_t<kQNV4, 128>(p, sms, stream, msg) : launch_t<kQMX4, 128>(p, sms, stream, msg);
-  return p.fmt == kQNV4 ? launch_t<kQNV4, 256>(p, sms, stream, msg) : launch_t<kQMX4, 256>(p, sms, stream, msg);
+  const PairPlan plan = pair_plan(p.B, p.M, p.N, p.K, p.part != nullptr && p.splits > 1);
+  if (plan.bn == 128)
+    return p.fmt == kQNV4 ? launch_t<kQNV4, 128>(p, plan, sms, stream, msg)
+                          : launch_t<kQMX4, 128>(p, plan, sms, stream, msg);
+  return p.fmt == kQNV4 ? launch_t<kQNV4, 256>(p, plan, sms, stream, msg)
+                        : launch_t<kQMX4, 256>(p, plan, sms, stream, msg);
 }
 
 cudaError_t take_status_fp4(unsigned int* out) {

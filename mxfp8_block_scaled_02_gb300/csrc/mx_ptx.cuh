@@ -397,6 +397,11 @@ __device__ __forceinline__ void st_shared_cluster_u32(uint32_t addr, uint32_t v)
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
+__device__ __forceinline__ void st_shared_cluster_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
+
 // ---------------------------------------------------------------- 32-byte global accesses
 // One 32-byte access per lane (p 32-byte aligned): whole sectors, where two
 // 16-byte stores a lane apart write half sectors.
