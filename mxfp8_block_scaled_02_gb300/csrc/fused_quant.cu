@@ -17,6 +17,12 @@
 // 32-element one, so a block's scale is worked out once or twice.  The scale
 // bytes of four blocks are gathered into one word by shuffles (a byte at a time
 // into the packed atoms cost the activation 5 us of 52 at 4096 x 14336).
+//
+// Measured (us, back to back in a CUDA graph; MXFP8 unless named): rmsnorm with
+// a bf16 residual 8192 x 4096 34.9 (6.76 TB/s), 4 x 4096 1.7; silu_mul 4096 x
+// 14336 44.7 (6.6 TB/s), MXFP4 42.9 (6.2), NVFP4 48.4 (5.5: twice the block
+// scales, each with a reciprocal), 16 x 14336 1.6; fp4 14336 x 4096 23.3 (6.4
+// TB/s), NVFP4 24.5 (6.2); unpack of those codes 12.9 (6.8 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>

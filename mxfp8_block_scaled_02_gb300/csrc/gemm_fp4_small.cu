@@ -1,9 +1,9 @@
-// gemm_fp4_small.cu - the 4-bit product for few tokens (M <= 128, one batch):
-//   out[m, n] = bf16( g_x g_w sum_k (x sx)[m, k] (w sw)[n, k] + bias[n] ).
+// gemm_fp4_small.cu - the 4-bit product for few tokens or few output tiles:
+//   out[b, m, n] = bf16( g_x g_w sum_k (x sx)[b, m, k] (w sw)[b, n, k] + bias[n] ).
 //
 // Bound by reading the weights once, and at decode sizes by the chain launch ->
 // weights -> MMA -> reduction -> store.  So the weights are the MMA's M side
-// (128 rows per CTA) and the tokens its N side (16, 32, 64 or 128 >= M), no MMA
+// (128 rows per CTA) and the tokens its N side (16, 32, 64 or 128 a CTA), no MMA
 // row is padding, and K is split over a cluster of S CTAs so that every SM
 // streams from the start: each holds a ring of 128-row x 128-byte weight tiles
 // in flight before the tokens arrive (they are the previous kernel's output,
@@ -19,9 +19,15 @@
 // result is the same on every call; with S = 1 the epilogue stores straight
 // from tensor memory.
 //
+// Measured in a CUDA graph (us, MXFP4 / NVFP4): N = K = 4096, M = 1 3.9 / 4.0
+// (bf16 x 4.2), 16 4.1 / 4.2, 64 5.4 / 5.6, 128 7.1 / 7.2; N = 14336, K = 4096, M
+// = 16 7.8 / 8.3 (31 MB, 4.0 TB/s: ~3.5 us of chain, then the rate at which the
+// 112 of 152 SMs that hold a row tile take it in).  On CTA pairs M = 1 takes
+// 10.7 and 15.0.
+//
 // Warps: 0 weight TMA, 1 tensor-memory allocation and MMA issue, 2 token TMA
-// (kQuant: 2..7 quantise the tokens), 4..7 epilogue; all eight reduce.  Every wait is bounded and the
-// cluster barrier is reached on every path.
+// (kQuant: 2..7 quantise the tokens), 4..7 epilogue; all eight reduce.  Every
+// wait is bounded and the cluster barrier is reached on every path.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
