@@ -17,13 +17,13 @@
 // The S fp32 partials meet in distributed shared memory: CTA r owns weight rows
 // [r 128/S, (r+1) 128/S) and adds the partials in the order 0..S-1, so the
 // result is the same on every call; with S = 1 the epilogue stores straight
-// from tensor memory.
+// from tensor memory.  With more tiles than SMs two CTAs share an SM (kTwo).
 //
 // Measured in a CUDA graph (us, MXFP4 / NVFP4): N = K = 4096, M = 1 3.9 / 4.0
 // (bf16 x 4.2), 16 4.1 / 4.2, 64 5.4 / 5.6, 128 7.1 / 7.2; N = 14336, K = 4096, M
 // = 16 7.8 / 8.3 (31 MB, 4.0 TB/s: ~3.5 us of chain, then the rate at which the
-// 112 of 152 SMs that hold a row tile take it in).  On CTA pairs M = 1 takes
-// 10.7 and 15.0.
+// 112 of 152 SMs that hold a row tile take it in); N = 28672, K = 4096, M = 16
+// 11.7 from HBM (62 MB, 5.3 TB/s).  On CTA pairs M = 1 takes 9.6, 13.1 and 21.9.
 //
 // Warps: 0 weight TMA, 1 tensor-memory allocation and MMA issue, 2 token TMA
 // (kQuant: 2..7 quantise the tokens), 4..7 epilogue; all eight reduce.  Every
@@ -47,15 +47,16 @@ constexpr int BK = 2 * BKB;
 constexpr int MMA_K = 64;
 constexpr int THREADS = 256;
 constexpr int W_BYTES = ROWS * BKB;
-constexpr int SMEM_MAX = 232448;
 
-template <int FMT, int NTOK>
+// kTwo: two CTAs an SM, each with a whole tile (no K split, so nothing received)
+template <int FMT, int NTOK, bool kTwo>
 struct Cfg {
+  static constexpr int SMEM_MAX = kTwo ? 115712 : 232448;
   static constexpr int ATOMS = FMT == kQNV4 ? 4 : 2;
   static constexpr int SF_BYTES = ATOMS * kAtomBytes;  // scales of one operand and stage
   static constexpr int X_BYTES = NTOK * BKB;
   static constexpr int STAGE_BYTES = W_BYTES + X_BYTES + 2 * SF_BYTES;
-  static constexpr int RECV_BYTES = NTOK * ROWS * 4;  // [S][NTOK][ROWS / S] fp32
+  static constexpr int RECV_BYTES = kTwo ? 0 : NTOK * ROWS * 4;  // [S][NTOK][ROWS / S] fp32
   static constexpr int FIT = (SMEM_MAX - 1024 - 512 - RECV_BYTES) / STAGE_BYTES;
   static constexpr int STAGES = FIT < 12 ? FIT : 12;
   static constexpr int OFF_W = 0;
@@ -66,7 +67,7 @@ struct Cfg {
   static constexpr int OFF_BAR = OFF_RECV + RECV_BYTES;
   static constexpr int OFF_MISC = OFF_BAR + (3 * STAGES + 1) * 8;
   static constexpr int SMEM = OFF_MISC + 16 + 1024;
-  static_assert(SMEM <= SMEM_MAX && STAGES >= 4, "shared memory");
+  static_assert(SMEM <= SMEM_MAX && STAGES >= 3, "shared memory");
   // tensor memory: accumulator, then two scale slots (weight and token atoms)
   static constexpr int SLOT_COLS = 8 * ATOMS;
   static constexpr int T_SF = NTOK < 32 ? 32 : NTOK;
@@ -146,12 +147,12 @@ struct Args {
   int splits;      // cluster size S
 };
 
-template <int FMT, int NTOK, bool kQuant>
-__global__ void __launch_bounds__(THREADS, 1)
+template <int FMT, int NTOK, bool kQuant, bool kTwo>
+__global__ void __launch_bounds__(THREADS, kTwo ? 2 : 1)
     gemm_fp4_small_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                           const __grid_constant__ CUtensorMap tmSFW, const __grid_constant__ CUtensorMap tmSFX,
                           const Args a) {
-  using C = Cfg<FMT, NTOK>;
+  using C = Cfg<FMT, NTOK, kTwo>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t* full_w = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
@@ -303,14 +304,17 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
   if (kQuant && warp >= 2) {
     // ------------------------------------------------ token quantiser
-    // A warp takes every sixth stage; a task is two rows of it, 16 elements a
-    // lane.  Task n of the warp: stage warp - 2 + 6 (n / T), rows 2 (n % T) and
-    // the one after, T = ceil(M / 2).
+    // QW warps take every QW-th stage; a task is two rows of it, 16 elements a
+    // lane.  Task n of the warp: stage warp - 2 + QW (n / T), rows 2 (n % T) and
+    // the one after, T = ceil(M / 2).  QW is at most the ring's length: a warp
+    // that waits for stage i's slot has seen stage i - QW - STAGES consumed, and
+    // the wait's parity is only right if that covers i - 2 STAGES.
+    constexpr int QW = C::STAGES < QUANT_WARPS ? C::STAGES : QUANT_WARPS;
     grid_dependency_wait();
     const TensorScale ts = tensor_scale(FMT == kQNV4 && a.gx != nullptr ? *a.gx : 1.f);
     constexpr int kLanes = q_block(FMT) / 16;
     const int j = lane & 15, T = (a.M + 1) >> 1;
-    const int ntasks = (nk - (warp - 2) + QUANT_WARPS - 1) / QUANT_WARPS * T;  // <= 0: none
+    const int ntasks = warp - 2 < QW ? (nk - (warp - 2) + QW - 1) / QW * T : 0;  // <= 0: none
     int lt = 0, li = warp - 2;  // task the next load belongs to
     auto load = [&](uint4 (&v)[2]) {
       const int r = 2 * lt + (lane >> 4), k = (kt0 + li) * BK + 16 * j;
@@ -320,7 +324,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       v[1] = valid ? src[1] : make_uint4(0, 0, 0, 0);
       if (++lt == T) {
         lt = 0;
-        li += QUANT_WARPS;
+        li += QW;
       }
     };
     uint4 buf[QUANT_AHEAD][2];
@@ -365,7 +369,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(&full_x[st]);
           t = 0;
-          i += QUANT_WARPS;
+          i += QW;
         }
       }
     }
@@ -448,10 +452,10 @@ int max_clusters(int splits, int sms) {
   if (cache[dev][slot] == 0) {
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[2];
-    fill_config(&cfg, attr, splits, splits, Cfg<FMT, NTOK>::SMEM, nullptr);
+    fill_config(&cfg, attr, splits, splits, Cfg<FMT, NTOK, false>::SMEM, nullptr);
     cfg.numAttrs = 1;
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, gemm_fp4_small_kernel<FMT, NTOK, kQuant>, &cfg) != cudaSuccess || n < 1) {
+    if (cudaOccupancyMaxActiveClusters(&n, gemm_fp4_small_kernel<FMT, NTOK, kQuant, false>, &cfg) != cudaSuccess || n < 1) {
       cudaGetLastError();  // the query's own error
       n = sms / splits;
     }
@@ -460,15 +464,15 @@ int max_clusters(int splits, int sms) {
   return cache[dev][slot];
 }
 
-template <int FMT, int NTOK, bool kQuant>
+template <int FMT, int NTOK, bool kQuant, bool kTwo>
 cudaError_t launch_t(const Fp4Problem& p, int sms, cudaStream_t stream, const char** msg) {
-  using C = Cfg<FMT, NTOK>;
+  using C = Cfg<FMT, NTOK, kTwo>;
   static bool attr_set[64] = {};
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64 || !attr_set[dev]) {
     cudaError_t e =
-        cudaFuncSetAttribute(gemm_fp4_small_kernel<FMT, NTOK, kQuant>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+        cudaFuncSetAttribute(gemm_fp4_small_kernel<FMT, NTOK, kQuant, kTwo>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) {
       *msg = "cudaFuncSetAttribute(max dynamic shared memory) failed";
       return e;
@@ -509,25 +513,40 @@ cudaError_t launch_t(const Fp4Problem& p, int sms, cudaStream_t stream, const ch
   a.TT = static_cast<int>(ceil_div(p.M, NTOK));
   a.KT = static_cast<int>(ceil_div(p.K, BK));
   a.last_steps = static_cast<int>(ceil_div(p.K - static_cast<int64_t>(a.KT - 1) * BK, MMA_K));
-  // the largest K split whose clusters all run at once
   const int64_t tiles = p.B * a.TT * RTW;
-  a.splits = 8;
-  while (a.splits > 1 && (a.splits > a.KT || tiles > max_clusters<FMT, NTOK, kQuant>(a.splits, sms))) a.splits >>= 1;
+  a.splits = 1;
+  if (!kTwo) {  // the largest K split whose clusters all run at once
+    a.splits = 8;
+    while (a.splits > 1 && (a.splits > a.KT || tiles > max_clusters<FMT, NTOK, kQuant>(a.splits, sms))) a.splits >>= 1;
+  }
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[2];
   fill_config(&cfg, attr, static_cast<int>(tiles) * a.splits, a.splits, C::SMEM, stream);
-  cudaError_t e = cudaLaunchKernelEx(&cfg, gemm_fp4_small_kernel<FMT, NTOK, kQuant>, mw, mx, msw, msx, a);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, gemm_fp4_small_kernel<FMT, NTOK, kQuant, kTwo>, mw, mx, msw, msx, a);
   if (e != cudaSuccess) *msg = "small-M 4-bit GEMM launch failed";
   return e;
 }
 
+// More tiles than SMs: two CTAs an SM, each with half the ring, so that the
+// tiles past the first wave stream from the start and their chains overlap
+// instead of following.  Measured (us, one / two, weights from HBM): N = 28672, K
+// = 4096, M = 1 15.4 / 11.5, 32 17.2 / 12.4; N = 20480, K = 5120, M = 16 17.4 /
+// 11.8.  Where the tiles fit one wave the K split makes up for it: N = 14336, K =
+// 4096, M = 16 8.4 with one, 8.8 with two and twice the split.
+template <int FMT, int NTOK, bool kQuant>
+cudaError_t launch_n(const Fp4Problem& p, int sms, cudaStream_t stream, const char** msg) {
+  return p.B * ceil_div(p.M, NTOK) * ceil_div(p.N, ROWS) > sms
+             ? launch_t<FMT, NTOK, kQuant, true>(p, sms, stream, msg)
+             : launch_t<FMT, NTOK, kQuant, false>(p, sms, stream, msg);
+}
+
 template <int FMT>
 cudaError_t launch_fmt(const Fp4Problem& p, int sms, cudaStream_t stream, const char** msg) {
-  if (p.x_bf16 != nullptr) return launch_t<FMT, 16, true>(p, sms, stream, msg);
-  if (p.M <= 16) return launch_t<FMT, 16, false>(p, sms, stream, msg);
-  if (p.M <= 32) return launch_t<FMT, 32, false>(p, sms, stream, msg);
-  if (p.M <= 64) return launch_t<FMT, 64, false>(p, sms, stream, msg);
-  return launch_t<FMT, 128, false>(p, sms, stream, msg);
+  if (p.x_bf16 != nullptr) return launch_n<FMT, 16, true>(p, sms, stream, msg);
+  if (p.M <= 16) return launch_n<FMT, 16, false>(p, sms, stream, msg);
+  if (p.M <= 32) return launch_n<FMT, 32, false>(p, sms, stream, msg);
+  if (p.M <= 64) return launch_n<FMT, 64, false>(p, sms, stream, msg);
+  return launch_n<FMT, 128, false>(p, sms, stream, msg);
 }
 
 }  // namespace
@@ -556,13 +575,16 @@ bool fp4_quantizes_inside(int64_t B, int64_t M, int64_t N, int64_t K) {
 // 4096, M = 64 5.5 / 9.1, 128 7.1 / 9.4, 256 10.1 / 9.5, 512 11.1 / 9.7; N = K =
 // 8192, M = 128 12.5 / 13.9, 256 15.8 / 14.0; N = K = 2048, M = 256 6.3 / 7.4,
 // 512 8.9 / 7.5; N = 14336, K = 4096, M = 64 9.2 / 9.4, 128 11.0 / 9.9; N = 4096,
-// K = 14336, M = 128 10.2 / 20.0, 256 16.2 / 14.2; two waves of tiles (N =
-// 28672, K = 4096), M = 16 15.0 / 17.0, 64 17.9 / 14.5; 16 x [M, 512, 7168], M =
-// 16 7.8 / 12.2, 128 11.9 / 12.9, 256 14.7 / 13.1.
+// K = 14336, M = 128 10.2 / 20.0, 256 16.2 / 14.2; 16 x [M, 512, 7168], M = 16
+// 7.8 / 12.2, 128 11.9 / 12.9, 256 14.7 / 13.1.  Two CTAs an SM, weights from
+// HBM: N = 28672, K = 4096, M = 16 11.7 / 18.7, 64 13.4 / 18.0, 128 16.2 / 18.6,
+// 192 (448 tiles) 26.8 / 18.9; N = 32000, K = 2048, M = 128 11.8 / 12.9; N =
+// 14336, K = 4096, M = 192 (224 tiles of two token tiles) 13.9 / 11.9; N =
+// 128256, K = 4096 (1002 tiles), M = 32 50.9 / 60.1, 64 56.4 / 52.6.
 bool fp4_use_small(int64_t B, int64_t M, int64_t N, int64_t K) {
   if (M <= 32) return true;
   const int64_t tiles = B * ceil_div(M, 128) * ceil_div(N, ROWS);
-  if (tiles > 152) return false;  // more than one CTA an SM
+  if (tiles > 152) return M <= 128 && tiles <= 304;  // two CTAs an SM, all at once
   const int64_t splits = splits_estimate(tiles);
   const int64_t fixed = M <= 64 ? 440 : (splits == 1 ? 640 : (splits == 2 ? 740 : (splits == 4 ? 590 : 530)));
   return fixed + 31 * ceil_div(ceil_div(K, BK), splits) <= fp4_pair_cost(B, M, N, K);  // 0.01 us
