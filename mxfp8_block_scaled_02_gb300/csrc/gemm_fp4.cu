@@ -90,7 +90,7 @@ struct Cfg {
   static constexpr int OFF_OUT = OFF_SFB + STAGES * SFB_BYTES;
   static constexpr int OFF_BIAS = OFF_OUT + EPI_WARPS * OUT_BOX;
   static constexpr int OFF_BAR = OFF_BIAS + EPI_WARPS * 4 * 32 * 2;
-  static constexpr int OFF_MISC = OFF_BAR + (4 * STAGES + 2) * 8;
+  static constexpr int OFF_MISC = OFF_BAR + (4 * STAGES + 2 + EPI_WARPS) * 8;
   static constexpr int SMEM = OFF_MISC + 16 + 1024;
   static_assert(SMEM <= 232448, "shared memory overflow");
 };
@@ -211,6 +211,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint64_t* sf_ready = sf_full + STAGES;
   uint64_t* acc_full = sf_ready + STAGES;
   uint64_t* acc_free = acc_full + 1;
+  uint64_t* received = acc_free + 1;  // [EPI_WARPS]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
 
@@ -223,16 +224,16 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int pair = blockIdx.x >> 1;
   const int npairs = gridDim.x >> 1;
 
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < STAGES; ++s) {
-      mbar_init(&full[s], 1);     // operands of both CTAs (even CTA's copy is used)
-      mbar_init(&empty[s], 1);    // the even CTA's commit
-      mbar_init(&sf_full[s], 1);  // this CTA's scales in shared memory
-      mbar_init(&sf_ready[s], 2 * SF_WARPS);  // both CTAs' scales in tensor memory (even CTA's copy)
+  if (warp == 0) {
+    // full, empty, sf_full: one arrival (the even CTA's copy of full is used, and
+    // empty is the even CTA's commit); sf_ready: both CTAs' scale writers
+    if (lane < 4 * STAGES) mbar_init(&full[lane], lane < 3 * STAGES ? 1 : 2 * SF_WARPS);
+    if (lane < EPI_WARPS) mbar_init(&received[lane], 1);
+    if (lane == 0) {
+      mbar_init(acc_full, 1);
+      mbar_init(acc_free, 2 * EPI_WARPS);
+      *abort_flag = 0;
     }
-    mbar_init(acc_full, 1);
-    mbar_init(acc_free, 2 * EPI_WARPS);
-    *abort_flag = 0;
     fence_mbar_init();
   }
   if (threadIdx.x == 64) {
@@ -242,9 +243,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     prefetch_tmap(&tmSFA);
     prefetch_tmap(&tmOut);
   }
-  // both CTAs' barriers exist before anyone signals them (this also joins the
-  // threads of the block)
-  cluster_sync();
+  __syncthreads();
+  cluster_arrive_relaxed();
+  cluster_wait();  // both CTAs' barriers exist before anyone signals them
   // This call's reduce waits for this grid itself.  Without a split the next
   // kernel is not let in early: a quantise or activation kernel that starts
   // beside this one keeps its shared-memory split of the SM, and with the L1
@@ -495,9 +496,11 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (BN == 256 && args.exchange) {
       // The pair's sum over its half of K; each of the two pairs of the cluster
       // finishes half of the columns and sends the other half, in fp32, to the
-      // other pair's stage buffers (all their copies and MMAs are done at the
-      // first barrier).  Warp e of a CTA writes what warp e of the other reads:
-      // 32 rows of one group, 16-byte piece q of lane l at 512 q + 16 l.
+      // other pair: staged where its own weight stages were (every copy and MMA
+      // of this pair is done once the accumulator is), copied to where the other
+      // pair's activation stages were (free after the cluster barrier).  Warp e
+      // sends what warp e of the other CTA reads: 32 rows of one group, 16-byte
+      // piece q of lane l at 512 q + 16 l.
       int b, mt, nt, sp, kt_lo, kt_hi;
       unit_coords(pair, args, b, mt, nt, sp, kt_lo, kt_hi);
       const int row0 = (mt * 2 + static_cast<int>(rank)) * BM + quad * 32;
@@ -509,30 +512,42 @@ __global__ void __launch_bounds__(THREADS, 1)
           bias_s[i * 32 + lane] = n < args.N ? args.bias[n] : __float2bfloat16(0.f);
         }
       }
-      const bool got = mbar_wait(acc_full, 0, abort_flag);
-      __syncwarp();
-      cluster_sync();
+      const bool got = __all_sync(0xFFFFFFFFu, mbar_wait(acc_full, 0, abort_flag));
+      cluster_arrive_relaxed();
       const uint32_t acc = tmem + (static_cast<uint32_t>(quad * 32) << 16);
       uint32_t r[2][32];
-      const uint32_t mine = smem_u32(smem + C::OFF_A) + ew * 8192 + lane * 16;
-      const uint32_t theirs = map_shared_rank(mine, crank ^ 2u);
+      uint8_t* out_box = smem + C::OFF_B + ew * 8192;
+      uint8_t* in_box = smem + C::OFF_A + ew * 8192;
       tc_fence_after();
-      if (__all_sync(0xFFFFFFFFu, got)) {
+      if (got) {
         tmem_ld_32x32b_x32(acc + send, r[0]);
         tmem_ld_32x32b_x32(acc + send + 32, r[1]);
         tmem_ld_wait();
+        uint4* o = reinterpret_cast<uint4*>(out_box) + lane;
 #pragma unroll
         for (int q = 0; q < 16; ++q)
-          st_shared_cluster_v4(theirs + q * 512, r[q >> 3][4 * (q & 7)], r[q >> 3][4 * (q & 7) + 1],
-                               r[q >> 3][4 * (q & 7) + 2], r[q >> 3][4 * (q & 7) + 3]);
+          o[q * 32] = make_uint4(r[q >> 3][4 * (q & 7)], r[q >> 3][4 * (q & 7) + 1], r[q >> 3][4 * (q & 7) + 2],
+                                 r[q >> 3][4 * (q & 7) + 3]);
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
+      cluster_wait();
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&received[ew], 8192);
+        if (got)
+          bulk_copy_cluster(map_shared_rank(smem_u32(in_box), crank ^ 2u), out_box, 8192,
+                            map_shared_rank(smem_u32(&received[ew]), crank ^ 2u));
+      }
+      if (got) {
         tmem_ld_32x32b_x32(acc + keep, r[0]);
         tmem_ld_32x32b_x32(acc + keep + 32, r[1]);
         tmem_ld_wait();
       }
       __syncwarp();
-      cluster_sync();
-      if (__all_sync(0xFFFFFFFFu, got)) {
-        const uint4* in = reinterpret_cast<const uint4*>(smem + C::OFF_A + ew * 8192) + lane;
+      // waited for even without a sum of our own: no copy may land after we leave
+      const bool came = __all_sync(0xFFFFFFFFu, mbar_wait(&received[ew], 0, nullptr));
+      if (got && came) {
+        const uint4* in = reinterpret_cast<const uint4*>(in_box) + lane;
 #pragma unroll
         for (int q = 0; q < 16; ++q) {
           const uint4 v = in[q * 32];
@@ -579,6 +594,12 @@ __global__ void __launch_bounds__(THREADS, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive_remote(acc_free_even);
           }
+          if (C::NB == 2 && i == 1 && !partial && u + npairs >= args.units) {
+            // the last tile: its second group goes where activation stages were,
+            // without waiting for the first box to be read
+            box = smem + C::OFF_A + ew * OUT_BOX;
+            pending = false;
+          }
           if (partial) {
             // fp32 partial of this K split: 32 columns a box
 #pragma unroll
@@ -604,11 +625,12 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   tc_fence_before();
   __syncwarp();
-  if (BN == 256 && args.exchange && warp < 4 + SF_WARPS) {  // the epilogue's two barriers
-    cluster_sync();
-    cluster_sync();
+  if (BN == 256 && args.exchange && warp < 4 + SF_WARPS) {  // the epilogue's barrier
+    cluster_arrive_relaxed();
+    cluster_wait();
   }
-  cluster_sync();  // no CTA of the pair leaves while the other may still signal it
+  cluster_arrive_relaxed();
+  cluster_wait();  // no CTA of the cluster leaves while another may still signal it
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, TMEM_COLS);
