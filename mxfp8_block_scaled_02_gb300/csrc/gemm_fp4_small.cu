@@ -14,10 +14,14 @@
 // codes and scales where TMA would have put them, the bytes of the quantise
 // call, which saves a launch and a workspace.
 //
-// The S fp32 partials meet in distributed shared memory: CTA r owns weight rows
-// [r 128/S, (r+1) 128/S) and adds the partials in the order 0..S-1, so the
-// result is the same on every call; with S = 1 the epilogue stores straight
-// from tensor memory.  With more tiles than SMs two CTAs share an SM (kTwo).
+// The S fp32 partials meet in distributed shared memory, by stores that
+// count on an mbarrier of the CTA they go to.  (With a releasing cluster barrier,
+// and every mbarrier made by one thread, N = K = 4096, M = 1 took 4.0 us instead
+// of 3.65; as bulk copies of a warp's partials, M = 128 9.2 instead of 7.1.)  CTA
+// r owns weight rows [r 128/S, (r+1) 128/S) and adds the partials in the order
+// 0..S-1, so the result is the same on every call; with S = 1 the epilogue stores
+// straight from tensor memory.  With more tiles than SMs two CTAs share an SM
+// (kTwo).
 //
 // Measured in a CUDA graph (us, MXFP4 / NVFP4): N = K = 4096, M = 1 3.9 / 4.0
 // (bf16 x 4.2), 16 4.1 / 4.2, 64 5.4 / 5.6, 128 7.1 / 7.2; N = 14336, K = 4096, M
@@ -27,7 +31,8 @@
 //
 // Warps: 0 weight TMA, 1 tensor-memory allocation and MMA issue, 2 token TMA
 // (kQuant: 2..7 quantise the tokens), 4..7 epilogue; all eight reduce.  Every
-// wait is bounded and the cluster barrier is reached on every path.
+// wait is bounded and the cluster barrier (at the start: the CTAs' mbarriers
+// exist) is reached on every path.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -65,7 +70,7 @@ struct Cfg {
   static constexpr int OFF_SFX = OFF_SFW + STAGES * SF_BYTES;
   static constexpr int OFF_RECV = OFF_SFX + STAGES * SF_BYTES;
   static constexpr int OFF_BAR = OFF_RECV + RECV_BYTES;
-  static constexpr int OFF_MISC = OFF_BAR + (3 * STAGES + 1) * 8;
+  static constexpr int OFF_MISC = OFF_BAR + (3 * STAGES + 2) * 8;
   static constexpr int SMEM = OFF_MISC + 16 + 1024;
   static_assert(SMEM <= SMEM_MAX && STAGES >= 3, "shared memory");
   // tensor memory: accumulator, then two scale slots (weight and token atoms)
@@ -159,6 +164,7 @@ __global__ void __launch_bounds__(THREADS, kTwo ? 2 : 1)
   uint64_t* full_x = full_w + C::STAGES;
   uint64_t* empty = full_x + C::STAGES;
   uint64_t* acc_full = empty + C::STAGES;
+  uint64_t* received = acc_full + 1;  // the partials of the rows this CTA owns
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
 
@@ -176,15 +182,13 @@ __global__ void __launch_bounds__(THREADS, kTwo ? 2 : 1)
   const int nk = (rank + 1) * a.KT / a.splits - kt0;  // >= 1: splits <= KT
   const uint32_t base = smem_u32(smem);
 
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < C::STAGES; ++s) {
-      mbar_init(&full_w[s], 1);
-      mbar_init(&full_x[s], 1);
-      mbar_init(&empty[s], 1);
-    }
-    mbar_init(acc_full, 1);
-    *abort_flag = 0;
+  if (warp == 0) {
+    for (int i = lane; i < 3 * C::STAGES + 2; i += 32) mbar_init(&full_w[i], 1);
+    if (lane == 0) *abort_flag = 0;
     fence_mbar_init();
+    __syncwarp();
+    // S partials of 128 / S rows, in chunks of 16 tokens
+    if (lane == 0 && a.splits > 1) mbar_arrive_expect_tx(received, static_cast<uint32_t>((M + 15) / 16 * 16 * ROWS * 4));
   }
   const uint32_t elected = elect_one();
   auto load_w = [&](int i, int st) {
@@ -208,6 +212,7 @@ __global__ void __launch_bounds__(THREADS, kTwo ? 2 : 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (a.splits > 1) cluster_arrive_relaxed();  // this CTA's barriers exist
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
   // the output row this thread finishes: its bias and the weights' scale are
   // read before the dependency wait, like the weights
@@ -381,15 +386,19 @@ __global__ void __launch_bounds__(THREADS, kTwo ? 2 : 1)
     grid_dependency_wait();  // g_x and the output belong to the kernels before
     if (a.gx != nullptr) alpha *= *a.gx;
   }
+  if (a.splits > 1) cluster_wait();  // the other CTAs' barriers do
   if (warp >= 4 && mbar_wait_warp(acc_full, 0, abort_flag)) {
     // ------------------------------------------------ epilogue: lane = weight row
     tc_fence_after();
     const uint32_t lrow = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const int wrow = (warp & 3) * 32 + lane;
     const int owner = wrow / per;
-    const uint32_t dst = a.splits == 1 ? 0u
-                                       : map_shared_rank(base + C::OFF_RECV, static_cast<uint32_t>(owner)) +
-                                             static_cast<uint32_t>(((rank * NTOK) * per + wrow - owner * per) * 4);
+    uint32_t dst = 0, bar = 0;
+    if (a.splits > 1) {
+      dst = map_shared_rank(base + C::OFF_RECV, static_cast<uint32_t>(owner)) +
+            static_cast<uint32_t>(((rank * NTOK) * per + wrow - owner * per) * 4);
+      bar = map_shared_rank(smem_u32(received), static_cast<uint32_t>(owner));
+    }
     for (int c = 0; c < M; c += 16) {
       uint32_t r[16];
       tmem_ld_32x32b_x16(lrow + c, r);
@@ -402,14 +411,14 @@ __global__ void __launch_bounds__(THREADS, kTwo ? 2 : 1)
                 __float2bfloat16_rn(fmaf(__uint_as_float(r[j]), alpha, bias_n));
       } else {
 #pragma unroll
-        for (int j = 0; j < 16; ++j) st_shared_cluster_u32(dst + static_cast<uint32_t>((c + j) * per * 4), r[j]);
+        for (int j = 0; j < 16; ++j) st_async_cluster_u32(dst + static_cast<uint32_t>((c + j) * per * 4), r[j], bar);
       }
     }
   }
 
-  tc_fence_before();
-  cluster_sync();  // all partials are in their owners' buffers
-  if (a.splits > 1 && !*abort_flag && my_n < a.N) {
+  // Every partial of this CTA's rows has come, and none may come after it leaves
+  // (each warp waits, whether or not it goes on).
+  if (a.splits > 1 && mbar_wait_warp(received, 0, nullptr) && !*abort_flag && my_n < a.N) {
     const float* recv = reinterpret_cast<const float*>(smem + C::OFF_RECV);
     const int nl = static_cast<int>(threadIdx.x) % per;
     for (int m = static_cast<int>(threadIdx.x) / per; m < M; m += THREADS / per) {
@@ -418,6 +427,7 @@ __global__ void __launch_bounds__(THREADS, kTwo ? 2 : 1)
       out[static_cast<int64_t>(m) * a.N + my_n] = __float2bfloat16_rn(fmaf(acc, alpha, bias_n));
     }
   }
+  tc_fence_before();
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();

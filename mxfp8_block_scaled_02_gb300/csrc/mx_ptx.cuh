@@ -405,6 +405,13 @@ __device__ __forceinline__ void st_shared_cluster_u32(uint32_t addr, uint32_t v)
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
+// Store to another CTA's shared memory, counted on its mbarrier at `bar`: whoever
+// waits for the bytes there sees them, and nothing has to be flushed.
+__device__ __forceinline__ void st_async_cluster_u32(uint32_t addr, uint32_t v, uint32_t bar) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.u32 [%0], %1, [%2];" ::"r"(addr), "r"(v), "r"(bar)
+               : "memory");
+}
+
 // Copy `bytes` (a multiple of 16) from this CTA's shared memory to another's;
 // they complete on the mbarrier at `bar`, in the CTA that receives them.
 __device__ __forceinline__ void bulk_copy_cluster(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
