@@ -751,37 +751,37 @@ namespace {
 
 // How a product runs on CTA pairs (a function of the shape alone) and what it
 // costs, in 0.01 us: the least of
-//   256-column tiles: 5.4 us + 0.26 us a stage of K (0.36 where a row of K/2
+//   256-column tiles: 4.6 us + 0.26 us a stage of K (0.36 where a row of K/2
 //     bytes is not a whole number of 128-byte lines);
-//   128-column tiles, where one a pair covers the output: 4.7 us + 0.25 (0.29)
+//   128-column tiles, where one a pair covers the output: 4.15 us + 0.25 (0.28)
 //     us a stage.  A CTA still loads 24 of the 32 KB a stage, so only the
 //     epilogue and the misaligned loads get shorter;
 //   256-column tiles with K split in two, the halves meeting in a cluster of two
-//     pairs: 2.2 us + 0.05 us a tile more;
+//     pairs: 1.3 us + 0.04 us a tile more;
 //   256-column tiles with K split over about 64 pairs, at least four stages
-//     each: partial sums and the kernel that adds them cost 2.3 us + 0.16 us a
-//     tile + 0.1 us a split more.
+//     each: partial sums and the kernel that adds them cost 2.9 us + 0.18 us a
+//     tile more.
 // Measured (us, MXFP4, 256 / 128 columns / in two / split): N = K = 4096, M = 512
-// 9.7 / 9.0 / 10.4 / 15.2, M = 768 (one tile a pair / two) 9.8 / 13.5; N = K =
-// 2048, M = 512 7.5 / 6.6 / 8.6 / 10.7; N = 1000, K = 4128, M = 768 11.8 / 9.6 /
-// 10.9 / 11.6; N = 4096, K = 14336, M = 256 20.0 / 18.9 / 15.2 / 14.1, M = 512
-// 20.2 / 19.2 / 16.5 / 20.8; N = 1024, K = 28672, M = 512 34.6 / 33.0 / 22.6 /
-// 13.5; N = 3584, K = 18944, M = 512 25.0 / 23.7 / 18.9 / 21.9.
+// 9.0 / 8.5 / 8.7 / 15.0, M = 768 (one tile a pair / two) 9.8 / 13.5; N = K =
+// 2048, M = 512 6.7 / 6.2 / 7.1 / 10.4; N = K = 8192, M = 256 13.4 / 12.5 / 11.3 /
+// 17.5; N = 1000, K = 4128, M = 768 11.0 / 8.9 / 9.4 / 11.2; N = 4096, K = 14336,
+// M = 256 19.5 / 18.4 / 13.5 / 13.9, M = 512 19.5 / 18.7 / 14.5 / 20.9; N = 1024,
+// K = 28672, M = 512 34.1 / 32.5 / 20.9 / 13.2.
 PairPlan pair_plan(int64_t B, int64_t M, int64_t N, int64_t K, bool may_split) {
   const int64_t stages = ceil_div(K, BK), rows = B * ceil_div(M, 2 * BM), tiles = rows * ceil_div(N, 256);
   const bool lines = K % BK == 0;
   const int64_t stage = lines ? 26 : 36;
-  PairPlan p = {256, 1, false, 540 + stage * stages * (tiles > 76 ? ceil_div(tiles, 76) : 1)};
-  const int64_t narrow = 470 + (lines ? 25 : 29) * stages;
+  PairPlan p = {256, 1, false, 460 + stage * stages * (tiles > 76 ? ceil_div(tiles, 76) : 1)};
+  const int64_t narrow = 415 + (lines ? 25 : 28) * stages;
   if (rows * ceil_div(N, 128) <= 76 && narrow < p.cost) p = {128, 1, false, narrow};
   // 36 clusters of four CTAs run at a time
-  const int64_t exchange = 540 + stage * ceil_div(stages, 2) + 220 + 5 * tiles;
+  const int64_t exchange = 460 + stage * ceil_div(stages, 2) + 130 + 4 * tiles;
   if (tiles <= 36 && stages >= 2 && exchange < p.cost) p = {256, 2, true, exchange};
   int64_t s = tiles > 0 ? 64 / tiles : 1;
   if (s > stages / 4) s = stages / 4;
   if (s > 8) s = 8;
   if (!may_split || s < 2) return p;
-  const int64_t split = 540 + stage * ceil_div(stages, s) + 230 + 16 * tiles + 10 * s;
+  const int64_t split = 460 + stage * ceil_div(stages, s) + 290 + 18 * tiles;
   if (split < p.cost) p = {256, static_cast<int>(s), false, split};
   return p;
 }

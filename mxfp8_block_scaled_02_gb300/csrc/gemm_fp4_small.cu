@@ -579,25 +579,28 @@ bool fp4_quantizes_inside(int64_t B, int64_t M, int64_t N, int64_t K) {
 }
 
 // Where this kernel is the faster one (a function of the shape alone: the
-// workspace size depends on it): its time by the stages of a CTA's K range and
-// by the split, which shares the epilogue out but adds an exchange, against the
-// CTA-pair kernel's.  Measured (us, MXFP4, this kernel / CTA pairs): N = K =
-// 4096, M = 64 5.5 / 9.1, 128 7.1 / 9.4, 256 10.1 / 9.5, 512 11.1 / 9.7; N = K =
-// 8192, M = 128 12.5 / 13.9, 256 15.8 / 14.0; N = K = 2048, M = 256 6.3 / 7.4,
-// 512 8.9 / 7.5; N = 14336, K = 4096, M = 64 9.2 / 9.4, 128 11.0 / 9.9; N = 4096,
-// K = 14336, M = 128 10.2 / 20.0, 256 16.2 / 14.2; 16 x [M, 512, 7168], M = 16
-// 7.8 / 12.2, 128 11.9 / 12.9, 256 14.7 / 13.1.  Two CTAs an SM, weights from
-// HBM: N = 28672, K = 4096, M = 16 11.7 / 18.7, 64 13.4 / 18.0, 128 16.2 / 18.6,
-// 192 (448 tiles) 26.8 / 18.9; N = 32000, K = 2048, M = 128 11.8 / 12.9; N =
-// 14336, K = 4096, M = 192 (224 tiles of two token tiles) 13.9 / 11.9; N =
-// 128256, K = 4096 (1002 tiles), M = 32 50.9 / 60.1, 64 56.4 / 52.6.
+// workspace size depends on it).  Up to 64 tokens always, while two CTAs an SM
+// hold the tiles; above, by its time: 0.26 us a stage of a CTA's K range, and the
+// rest by the split and the tokens, which share the epilogue out but add an
+// exchange.  Measured (us, MXFP4, this kernel / CTA pairs): N = K = 4096, M = 64
+// 5.4 / 8.1, 128 7.3 / 8.2, 256 10.5 / 8.1, 512 9.8 / 8.5; N = K = 8192, M = 64 9.8
+// / 11.0, 128 12.8 / 11.1; N = K = 2048, M = 96 5.4 / 6.2, 256 6.7 / 6.1, 512 9.5 /
+// 6.2; N = 14336, K = 4096, M = 64 8.1 / 8.9, 128 9.8 / 9.2; N = 4096, K = 14336, M
+// = 128 9.9 / 12.1, 256 16.1 / 13.5; 16 x [M, 512, 7168], M = 64 9.4 / 10.3, 128
+// 12.3 / 10.5.  Two CTAs an SM, weights from HBM: N = 28672, K = 4096, M = 16 11.7
+// / 18.7, 64 13.4 / 18.0, 128 16.2 / 18.6, 192 (448 tiles) 26.8 / 18.9; N = 32000,
+// K = 2048, M = 128 11.8 / 12.9; N = 14336, K = 4096, M = 192 (224 tiles of two
+// token tiles) 13.9 / 11.9; N = 128256, K = 4096 (1002 tiles), M = 32 50.9 / 60.1,
+// 64 56.4 / 52.6.
 bool fp4_use_small(int64_t B, int64_t M, int64_t N, int64_t K) {
   if (M <= 32) return true;
   const int64_t tiles = B * ceil_div(M, 128) * ceil_div(N, ROWS);
   if (tiles > 152) return M <= 128 && tiles <= 304;  // two CTAs an SM, all at once
-  const int64_t splits = splits_estimate(tiles);
-  const int64_t fixed = M <= 64 ? 440 : (splits == 1 ? 640 : (splits == 2 ? 740 : (splits == 4 ? 590 : 530)));
-  return fixed + 31 * ceil_div(ceil_div(K, BK), splits) <= fp4_pair_cost(B, M, N, K);  // 0.01 us
+  if (M <= 64) return true;
+  const int64_t splits = splits_estimate(tiles), more = (M < 128 ? M : 128) - 64;
+  const int64_t fixed = splits == 1 ? 375 + 3 * more
+                                    : (splits == 2 ? 510 + 5 * more : (splits == 4 ? 420 : 350) + 3 * more);
+  return fixed + 26 * ceil_div(ceil_div(K, BK), splits) <= fp4_pair_cost(B, M, N, K);  // 0.01 us
 }
 
 cudaError_t launch_gemm_fp4_small(const Fp4Problem& p, int sms, cudaStream_t stream, const char** msg) {
