@@ -25,11 +25,11 @@
 //     ACC1 on) and the scale slots beside them.  The epilogue drains a tile's
 //     shared columns first and releases them, so the next tile's MMAs run while
 //     the rest is drained and stored.
-// What bounds it (M = 4096, N = 14336, K = 4096, MXFP4 71.2 us, 6.8 PFLOP/s;
-// NVFP4 78.7; tensor pipe busy 68 and 61 %): the way between L2 and the SMs,
+// What bounds it (M = 4096, N = 14336, K = 4096, MXFP4 71.0 us, 6.8 PFLOP/s;
+// NVFP4 78.8; tensor pipe busy 68 and 61 %): the way between L2 and the SMs,
 // which operand loads (1.0 GB) and output stores share: without the stores 66
 // of then 76 us, without the loads 68, without both 62; the tensor cores alone
-// need 50.  Longer K writes less: M = 8192, N = 4096, K = 14336 126 us, 7.6
+// need 50.  Longer K writes less: M = 8192, N = 4096, K = 14336 124 us, 7.7
 // PFLOP/s.  192-column tiles with two whole accumulators (86.8 against 73.1 us)
 // load more; clusters of four would share loads, but 144 of the 152 SMs hold
 // them.

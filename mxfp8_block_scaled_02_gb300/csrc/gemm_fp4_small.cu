@@ -23,11 +23,11 @@
 // straight from tensor memory.  With more tiles than SMs two CTAs share an SM
 // (kTwo).
 //
-// Measured in a CUDA graph (us, MXFP4 / NVFP4): N = K = 4096, M = 1 3.9 / 4.0
-// (bf16 x 4.2), 16 4.1 / 4.2, 64 5.4 / 5.6, 128 7.1 / 7.2; N = 14336, K = 4096, M
-// = 16 7.8 / 8.3 (31 MB, 4.0 TB/s: ~3.5 us of chain, then the rate at which the
-// 112 of 152 SMs that hold a row tile take it in); N = 28672, K = 4096, M = 16
-// 11.7 from HBM (62 MB, 5.3 TB/s).  On CTA pairs M = 1 takes 9.6, 13.1 and 21.9.
+// Measured in a CUDA graph (us, MXFP4 / NVFP4): N = K = 4096, M = 1 3.6 / 3.7
+// (bf16 x 3.8), 16 3.7 / 3.9, 64 5.2 / 5.3, 128 7.1 / 7.2; weights from HBM, N =
+// 14336, K = 4096, M = 16 7.2 / 7.5 (31 MB, 4.3 TB/s: ~3 us of chain, then the
+// stream), N = 28672, K = 4096 10.9 / 11.5 (62 MB, 5.7 TB/s).  On CTA pairs M = 1
+// takes 8.5, 13 and 21.
 //
 // Warps: 0 weight TMA, 1 tensor-memory allocation and MMA issue, 2 token TMA
 // (kQuant: 2..7 quantise the tokens), 4..7 epilogue; all eight reduce.  Every
