@@ -701,10 +701,13 @@ cudaError_t launch_t(const Fp4Problem& p, const PairPlan& plan, int sms, cudaStr
   a.exchange = exchange ? 1 : 0;
   a.units = a.B * a.MT * a.NT * splits;
   // Column tiles fastest while a sweep of the weights stays in L2 (two dies:
-  // half of it), else the operand with fewer bytes: M = 4096, N = 14336, K =
-  // 4096 76.2 -> 74.1 us, M = 8192, N = 4096, K = 14336 133.8 -> 126.8 us; at
-  // N = 28672, K = 4096 (59 MB of weights) row tiles fastest 151.9 against 161.5.
-  a.n_fast = p.M >= p.N || p.N * p.K / 2 <= (32ll << 20) ? 1 : 0;
+  // half of it) or they are the operand with fewer bytes: M = 4096, N = 14336, K =
+  // 4096 75.0 -> 71.4 us, M = 8192, N = 4096, K = 14336 132.4 -> 126.8 us; at N =
+  // 28672, K = 4096 (59 MB of weights) row tiles fastest 144.1 against 155.9.  Up
+  // to eight row tiles the first wave would take in all of the weights: row tiles
+  // fastest, weights from HBM, N = 14336, K = 4096, M = 1024 22.5 -> 21.6, M = 2048
+  // 40.8 -> 39.7 us (in L2 20.3 and 38.4 -> 39.4).
+  a.n_fast = a.MT > 8 && (p.M >= p.N || p.N * p.K / 2 <= (32ll << 20)) ? 1 : 0;
   const int pairs = exchange || a.units < sms / 2 ? a.units : sms / 2;
 
   cudaLaunchConfig_t cfg = {};
