@@ -503,7 +503,7 @@ def linear_noalloc(x: torch.Tensor, pw: PackedWeights, bias: torch.Tensor | None
 # ------------------------------------------------------------------ 4-bit layer (MXFP4, NVFP4)
 # On the Grace host a short call costs as much in Python as in its launches, so
 # the functions below look things up once and call few helpers.
-_BF16, _F32, _U8 = torch.bfloat16, torch.float32, torch.uint8
+_BF16, _F32, _U8, _E4M3 = torch.bfloat16, torch.float32, torch.uint8, torch.float8_e4m3fn
 # (MXFP8_QFMT code, elements per code byte, block length) of the quantising formats
 _QSPEC = {"mxfp8": (0, 1, 32), "mxfp4": (1, 2, 32), "nvfp4": (2, 2, 16)}
 
@@ -534,10 +534,12 @@ def quantize_fp4(x: torch.Tensor, fmt: str = "mxfp4", *,
     f = _fmt4(fmt)
     if x.dtype is not _BF16:
         raise TypeError("x must be bfloat16")
-    _require_cuda(x)
+    if not (x.is_cuda and x.is_contiguous()):
+        _require_cuda(x)
     if tensor_scale is not None:
         _check_tensor_scale(fmt, tensor_scale)
-    x = _aligned16(x)
+    if x.data_ptr() & 15:
+        x = _aligned16(x)
     shape, dev = x.shape, x.device
     lead, K = shape[:-1], shape[-1]
     q = torch.empty(lead + (K // 2,), dtype=_U8, device=dev)
@@ -551,12 +553,17 @@ def quantize_fp4(x: torch.Tensor, fmt: str = "mxfp4", *,
 def unpack_fp4(x_q: torch.Tensor) -> torch.Tensor:
     """Packed E2M1 codes [..., K/2] -> the same values as float8_e4m3fn [..., K]
     (with the same scales an MXFP4 tensor is then an MXFP8 one)."""
-    if x_q.dtype != torch.uint8:
+    if x_q.dtype is not _U8:
         raise TypeError("codes must be uint8")
-    _require_cuda(x_q)
-    x_q = _aligned16(x_q)
-    out = torch.empty((*x_q.shape[:-1], 2 * x_q.shape[-1]), dtype=torch.float8_e4m3fn, device=x_q.device)
-    _check(load().mxfp8_fp4_unpack(x_q.data_ptr(), out.numel(), out.data_ptr(), _stream()))
+    if not (x_q.is_cuda and x_q.is_contiguous()):
+        _require_cuda(x_q)
+    src = x_q.data_ptr()
+    if src & 15:
+        x_q = _aligned16(x_q)
+        src = x_q.data_ptr()
+    shape = x_q.shape
+    out = torch.empty(shape[:-1] + (2 * shape[-1],), dtype=_E4M3, device=x_q.device)
+    _check(load().mxfp8_fp4_unpack(src, out.numel(), out.data_ptr(), _stream()))
     return out
 
 
@@ -636,35 +643,63 @@ def linear_fp4(x: torch.Tensor, pw: PackedWeights, bias: torch.Tensor | None = N
     the weights' format), or with ``x_scale`` the codes uint8 [..., K/2] of
     quantize_fp4; ``tensor_scale`` is nvfp4's scale of x either way.  For batched
     weights x is [B, M, ...].  Returns bf16 [..., N]."""
-    fmt, quantized, K, N, B = pw.fmt, x_scale is not None, pw.K, pw.N, pw.B
+    # Most of the host's share of a small call is Python's: one pass, no helper
+    # calls for what is absent or in order (12.5 -> 10.3 us at M = 1)
+    fmt, K, N, B = pw.fmt, pw.K, pw.N, pw.B
     f = _fmt4(fmt)
-    _require_cuda(x, x_scale, bias, out, workspace)
+    quantized = x_scale is not None
+    if not (x.is_cuda and x.is_contiguous()):
+        _require_cuda(x)
+    if x_scale is not None or out is not None or workspace is not None:
+        _require_cuda(x_scale, out, workspace)
+    g_ptr = b_ptr = s_ptr = None
     if tensor_scale is not None:
         _check_tensor_scale(fmt, tensor_scale)
+        g_ptr = tensor_scale.data_ptr()
     if x.dtype is not (_U8 if quantized else _BF16):
         raise TypeError("x must be bfloat16, or uint8 codes with x_scale")
-    shape, dev = x.shape, x.device
+    shape = x.shape
     KX = K // 2 if quantized else K
     if not shape or shape[-1] != KX:
         raise ValueError(f"x {tuple(shape)} does not match weights with K={K}")
     if pw.batched and (len(shape) != 3 or shape[0] != B):
         raise ValueError("batched weights need x of shape [B, M, K]")
     lead = shape[:-1]
-    if quantized and (x_scale.element_size() != 1 or x_scale.shape != lead + (K // QBLOCK[fmt],)):
-        raise ValueError(f"{fmt} activation scale {tuple(x_scale.shape)} for codes {tuple(shape)}")
     rows = x.numel() // KX
-    _product_args(pw, bias, out, rows)
-    x, x_scale, bias = _aligned16(x), _aligned16(x_scale), _aligned16(bias)
+    if bias is not None:
+        if not (bias.is_cuda and bias.is_contiguous()):
+            _require_cuda(bias)
+        if bias.dtype is not _BF16 or bias.dim() != 1 or bias.shape[0] != N:
+            raise ValueError("bias must be bf16 [N]")
+        b_ptr = bias.data_ptr()
+        if b_ptr & 15:
+            bias = _aligned16(bias)
+            b_ptr = bias.data_ptr()
+    if quantized:
+        if x_scale.element_size() != 1 or x_scale.shape != lead + (K // QBLOCK[fmt],):
+            raise ValueError(f"{fmt} activation scale {tuple(x_scale.shape)} for codes {tuple(shape)}")
+        x_scale = _aligned16(x_scale)
+        s_ptr = x_scale.data_ptr()
     if out is None:
-        out = torch.empty(lead + (N,), dtype=_BF16, device=dev)
+        out = torch.empty(lead + (N,), dtype=_BF16, device=x.device)
+    elif out.dtype is not _BF16 or out.numel() != rows * N:
+        raise ValueError(f"out must be bf16 with {rows * N} elements")
     if rows == 0:
         return out
+    x_ptr = x.data_ptr()
+    if x_ptr & 15:
+        x = _aligned16(x)
+        x_ptr = x.data_ptr()
     M = rows // B
-    ws_ptr, ws_bytes, workspace = _workspace(workspace, workspace_size_fp4(B, M, N, K, quantized, fmt), dev)
-    xp = x.data_ptr()
-    _check(load().mxfp8_fp4_linear(f, None if quantized else xp, xp if quantized else None, _ptr(x_scale),
-                                   _ptr(tensor_scale), B, M, N, K, pw.w_packed.data_ptr(), pw.sf_packed.data_ptr(),
-                                   _ptr(pw.tensor_scale), _ptr(bias), out.data_ptr(), ws_ptr, ws_bytes, _stream()))
+    need = workspace_size_fp4(B, M, N, K, quantized, fmt)
+    ws_ptr, ws_bytes = None, 0
+    if workspace is not None or need:
+        ws_ptr, ws_bytes, workspace = _workspace(workspace, need, x.device)
+    wg = pw.tensor_scale
+    _check(load().mxfp8_fp4_linear(f, None if quantized else x_ptr, x_ptr if quantized else None, s_ptr, g_ptr, B, M, N, K,
+                                   pw.w_packed.data_ptr(), pw.sf_packed.data_ptr(),
+                                   None if wg is None else wg.data_ptr(), b_ptr, out.data_ptr(), ws_ptr, ws_bytes,
+                                   _stream()))
     return out
 
 
@@ -790,7 +825,10 @@ def rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tens
         raise TypeError("x and weight must be bfloat16")
     if tensor_scale is not None:
         _check_tensor_scale(fmt, tensor_scale)
-    _require_cuda(weight, residual_out, y)
+    if not (weight.is_cuda and weight.is_contiguous()):
+        _require_cuda(weight)
+    if residual_out is not None or y is not None:
+        _require_cuda(residual_out, y)
     shape = x.shape
     xr, rows, x_stride = _rows2d(x, "x")
     K = shape[-1]
@@ -813,7 +851,8 @@ def rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tens
         raise ValueError("residual_out needs a residual")
     if y is not None and (y.dtype is not _BF16 or y.shape != shape):
         raise ValueError("y must be bf16 with x's shape")
-    weight = _aligned16(weight)
+    if weight.data_ptr() & 15:
+        weight = _aligned16(weight)
     res, q, s = _quantized_out(shape[:-1], dev, rows, K, fmt, tensor_scale, packed)
     _check(load().mxfp8_rmsnorm_quantize(f, xr.data_ptr(), x_stride, r_ptr, r_stride, r_f32, t_ptr, weight.data_ptr(),
                                          eps, None if tensor_scale is None else tensor_scale.data_ptr(), rows, K,

@@ -32,7 +32,9 @@ def test_sizes(lib):
     assert ops.workspace_size_fp4(1, 4096, 14336, 4096, False, "nvfp4") == 4096 * 2048 + 32 * 64 * 512
     assert ops.product_workspace_fp4(1, 4096, 14336, 4096, "nvfp4") == 0
     # few tiles and a long K: fp32 partials
-    assert ops.product_workspace_fp4(1, 256, 4096, 14336, "mxfp4") == 4 * 4 * 256 * 4096
+    assert ops.product_workspace_fp4(1, 256, 1024, 28672, "mxfp4") == 8 * 4 * 256 * 1024
+    # split in two within a cluster: none
+    assert ops.product_workspace_fp4(1, 256, 4096, 14336, "mxfp4") == 0
 
 
 def test_quantise_errors(lib):
