@@ -644,7 +644,8 @@ def linear_fp4(x: torch.Tensor, pw: PackedWeights, bias: torch.Tensor | None = N
     quantize_fp4; ``tensor_scale`` is nvfp4's scale of x either way.  For batched
     weights x is [B, M, ...].  Returns bf16 [..., N]."""
     # Most of the host's share of a small call is Python's: one pass, no helper
-    # calls for what is absent or in order (12.5 -> 10.3 us at M = 1)
+    # calls for what is absent or in order (same box, M = 1 11.5 -> 11.1 us, with
+    # a workspace 18.2 -> 16.9)
     fmt, K, N, B = pw.fmt, pw.K, pw.N, pw.B
     f = _fmt4(fmt)
     quantized = x_scale is not None
