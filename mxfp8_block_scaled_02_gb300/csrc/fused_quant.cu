@@ -19,10 +19,11 @@
 // into the packed atoms cost the activation 5 us of 52 at 4096 x 14336).
 //
 // Measured (us, back to back in a CUDA graph; MXFP8 unless named): rmsnorm with
-// a bf16 residual 8192 x 4096 34.9 (6.76 TB/s), 4 x 4096 1.7; silu_mul 4096 x
-// 14336 44.7 (6.6 TB/s), MXFP4 42.9 (6.2), NVFP4 48.4 (5.5: twice the block
-// scales, each with a reciprocal), 16 x 14336 1.6; fp4 14336 x 4096 23.3 (6.4
-// TB/s), NVFP4 24.5 (6.2); unpack of those codes 12.9 (6.8 TB/s).
+// a bf16 residual 8192 x 4096 34.8 (6.8 TB/s), 4 x 4096 1.7; silu_mul 4096 x 14336
+// 44.5 (6.6 TB/s), MXFP4 42.2 (6.3), NVFP4 44.1 (6.1: twice the block scales, each
+// with a reciprocal), 16 x 14336 1.6; fp4 14336 x 4096 23.2 (6.4 TB/s), NVFP4 23.8
+// (6.3), 8192 x 14336 to packed scales 43.1 (6.9), NVFP4 44.9 (6.7); unpack of
+// 14336 x 4096 codes 12.9 (6.8 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -276,9 +277,11 @@ struct ActArgs {
 };
 
 
-// A CTA takes CH x blockDim.x chunks of one row (a row is `segs` CTAs).
+// A CTA takes CH x blockDim.x chunks of one row (a row is `segs` CTAs).  Twelve
+// CTAs an SM, ten for NVFP4, which spills at twelve (4096 x 14336: 46.0 -> 44.1 us;
+// MXFP4 at ten 42.2 -> 43.7).
 template <int FMT, int CH>
-__global__ void __launch_bounds__(kRowThreads, 12) silu_mul_kernel(const ActArgs a) {
+__global__ void __launch_bounds__(kRowThreads, FMT == kQNV4 ? 10 : 12) silu_mul_kernel(const ActArgs a) {
   launch_dependents();
   const int64_t row = blockIdx.x / a.segs;
   const int c0 = static_cast<int>(blockIdx.x - row * a.segs) * (CH * blockDim.x) + threadIdx.x;
@@ -321,7 +324,7 @@ struct Fp4Args {
 // kEarly as in quantize.cu: only the activation quantise inside a linear call
 // lets the next kernel start early, never the call that may make weights.
 template <int FMT, bool kEarly, int CH>
-__global__ void __launch_bounds__(kRowThreads, CH == 1 ? 12 : 8) quantize_fp4_kernel(const Fp4Args a) {
+__global__ void __launch_bounds__(kRowThreads, CH == 1 ? 12 : 10) quantize_fp4_kernel(const Fp4Args a) {
   if (kEarly) {
     launch_dependents();
     grid_dependency_wait();
@@ -424,9 +427,9 @@ cudaError_t launch_pdl(const void* kern, int64_t grid, int threads, void* args, 
 
 // Chunks a thread, threads and CTAs for M rows of K elements, the CTAs of a row
 // as even as whole warps allow.  `most` chunks a thread keep more bytes in
-// flight on long inputs (4-bit quantise, 14336 x 4096: 25.6 -> 24.1 us, NVFP4
-// 31.4 -> 26.3) and one starts more CTAs on short ones (activation, 512 x 14336:
-// 7.0 -> 6.6 us).
+// flight on long inputs (4-bit quantise, 14336 x 4096: 23.9 -> 23.2 us, NVFP4 28.3
+// -> 23.8; activation, 4096 x 14336 to MXFP8 48.9 -> 44.5) and one starts more CTAs
+// on short ones (activation, 512 x 14336: 7.0 -> 6.6 us).
 int row_split(int64_t M, int64_t K, int most, int* threads, int* segs) {
   const int64_t chunks = K / 16;
   const int ch = chunks >= 32 * most && M * chunks >= 152ll * 32 * 2 * kRowThreads ? most : 1;
