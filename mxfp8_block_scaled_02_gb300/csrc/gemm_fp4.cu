@@ -12,21 +12,21 @@
 // cores.  One instruction reads the same bytes as an 8-bit one and does twice
 // the work, and there are twice (MXFP4) or four times (NVFP4) as many scales
 // per byte, which decides the rest:
-//   scales: one TMA per operand brings a stage's atoms.  A tcgen05.cp moves an
-//     atom to tensor memory in ~64 cycles, so MXFP4's 6 atoms a stage would
-//     just fit beside the MMAs and NVFP4's 12 would not; four warps write
-//     MXFP4's atoms and half of NVFP4's with tcgen05.st instead, into scale
-//     slots ahead of the MMAs.  (All by cp, M = 4096, N = 14336, K = 4096: MXFP4
-//     116 -> 89 us and NVFP4 145 -> 94 us when the writers came in; NVFP4 half by
-//     cp 86.8 -> 80.4.)
+//   scales: one TMA per operand brings a stage's atoms, and four warps write
+//     them to tensor memory with tcgen05.st, a slot a stage, ahead of the MMAs.
+//     (By tcgen05.cp between the MMAs, ~64 cycles an atom, M = 4096, N = 14336,
+//     K = 4096 took 116 us instead of 89 in MXFP4's 6 atoms a stage and 145
+//     instead of 94 in NVFP4's 12.  With fewer slots than stages the warps wait
+//     for commits: half of NVFP4's atoms by cp, three slots, M = 8192, N = 4096, K
+//     = 14336 139 us instead of 132.)
 //   issue: the MMA warp stays converged and its instructions are predicated
 //     (below): 89 -> 79 us.
-//   tensor memory: two accumulators of 256 columns that overlap (from column
-//     ACC1 on) and the scale slots beside them.  The epilogue drains a tile's
+//   tensor memory: the scale slots, and two accumulators of 256 columns that
+//     overlap in what is left (from column ACC1 on).  The epilogue drains a tile's
 //     shared columns first and releases them, so the next tile's MMAs run while
 //     the rest is drained and stored.
 // What bounds it (M = 4096, N = 14336, K = 4096, MXFP4 71.0 us, 6.8 PFLOP/s;
-// NVFP4 78.8; tensor pipe busy 68 and 61 %): the way between L2 and the SMs,
+// NVFP4 77.5; tensor pipe busy 68 %): the way between L2 and the SMs,
 // which operand loads (1.0 GB) and output stores share: without the stores 66
 // of then 76 us, without the loads 68, without both 62; the tensor cores alone
 // need 50.  Longer K writes less: M = 8192, N = 4096, K = 14336 124 us, 7.7
@@ -73,16 +73,13 @@ struct Cfg {
   static constexpr int ATOMS = FMT == kQNV4 ? 4 : 2;
   static constexpr int SFA_BYTES = ATOMS * kAtomBytes;
   static constexpr int SFB_BYTES = ATOMS * NB * kAtomBytes;
-  // tensor memory: scale slots of ATOMS activation and NB ATOMS weight atoms, 4
-  // columns each, above the two accumulators (of 256 columns they overlap)
-  static constexpr int SLOTS = FMT == kQNV4 && BN == 256 ? 3 : STAGES;
+  // Tensor memory: two accumulators, of 256 columns overlapping from column ACC1
+  // on, then the scales: a slot a stage, ATOMS activation and NB ATOMS weight
+  // atoms of 4 columns each.
+  static constexpr int ACC1 = FMT == kQNV4 && BN == 256 ? 16 : 128;  // first column of the odd tiles' accumulator
   static constexpr int SLOT_COLS = ATOMS * 4 * (1 + NB);
-  static constexpr int CP_A = FMT == kQNV4 && BN == 256 ? 4 : 0;
-  static constexpr int CP_B = FMT == kQNV4 && BN == 256 ? 2 : 0;
-  static constexpr int ACC1 = FMT == kQNV4 && BN == 256 ? 96 : 128;  // first column of the odd tiles' accumulator
   static constexpr int T_SF = ACC1 + BN;
-  static_assert(T_SF + SLOTS * SLOT_COLS <= TMEM_COLS, "tensor memory overflow");
-  static_assert(SLOTS <= STAGES, "a slot is freed by a stage's commit");
+  static_assert(T_SF + STAGES * SLOT_COLS <= TMEM_COLS, "tensor memory overflow");
   static constexpr int OFF_A = 0;
   static constexpr int OFF_B = OFF_A + STAGES * A_BYTES;
   static constexpr int OFF_SFA = OFF_B + STAGES * B_BYTES;
@@ -124,16 +121,6 @@ __device__ __forceinline__ void mma_fp4_pair(uint32_t elected, uint32_t d, uint6
         "p;\n\t}" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb), "r"(elected)
         : "memory");
-}
-
-// One scale atom of each CTA's own shared memory (same offset) into 4 columns
-// of its tensor memory, replicated over the four lane quarters.
-__device__ __forceinline__ void cp_sf_pair(uint32_t elected, uint32_t taddr, uint64_t desc) {
-  asm volatile(
-      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
-      "@q tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr),
-      "l"(desc), "r"(elected)
-      : "memory");
 }
 
 __device__ __forceinline__ void commit_pair_elected(uint32_t elected, uint64_t* bar, uint16_t mask) {
@@ -328,7 +315,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       const uint16_t pair_mask = static_cast<uint16_t>(0x3u << even);
       const uint64_t ad0 = sdesc_kmajor_sw128(smem_u32(smem + C::OFF_A));
       const uint64_t bd0 = sdesc_kmajor_sw128(smem_u32(smem + C::OFF_B));
-      int stage = 0, tile_no = 0, slot = 0;
+      int stage = 0, tile_no = 0;
       uint32_t phase = 0;
       bool ok = true;
       for (int u = pair; ok && u < args.units; u += npairs, ++tile_no) {
@@ -352,24 +339,18 @@ __global__ void __launch_bounds__(THREADS, 1)
           const uint64_t ad = ad0 + static_cast<uint32_t>(stage * (A_BYTES >> 4));
           const uint64_t bd = bd0 + static_cast<uint32_t>(stage * (B_BYTES >> 4));
           const int steps = kt == args.KT - 1 ? args.last_steps : BK / MMA_K;
-          const uint32_t t_sfa = tmem + C::T_SF + slot * C::SLOT_COLS;
+          const uint32_t t_sfa = tmem + C::T_SF + stage * C::SLOT_COLS;
           const uint32_t t_sfb = t_sfa + 4 * C::ATOMS;
-          const uint64_t sa = sdesc_sf(smem_u32(smem + C::OFF_SFA)) + static_cast<uint32_t>(stage * (C::SFA_BYTES >> 4));
-          const uint64_t sb = sdesc_sf(smem_u32(smem + C::OFF_SFB)) + static_cast<uint32_t>(stage * (C::SFB_BYTES >> 4));
-#pragma unroll
-          for (int j = 0; j < C::CP_A; ++j) cp_sf_pair(elected, t_sfa + 4 * j, sa + j * (kAtomBytes >> 4));
-#pragma unroll
-          for (int j = 0; j < C::CP_B; ++j) cp_sf_pair(elected, t_sfb + 4 * j, sb + j * (kAtomBytes >> 4));
 #pragma unroll
           for (int kk = 0; kk < BK / MMA_K; ++kk) {
             // MXFP4: two steps share an atom (scale bytes 0-1 and 2-3)
             const int j = FMT == kQNV4 ? kk : kk >> 1;
             const uint32_t id = FMT == kQNV4 ? 0u : static_cast<uint32_t>(kk & 1) * 2u;
             mma_fp4_pair<FMT>(kk < steps ? elected : 0u, acc, ad + 2 * kk, bd + 2 * kk,
-                              idesc_with_sf_id(idesc, id, id), t_sfa + 4 * j, t_sfb + 4 * C::NB * j, ((kt - kt_lo) | kk) != 0);
+                              idesc_with_sf_id(idesc, id, id), t_sfa + 4 * j, t_sfb + 4 * C::NB * j,
+                              ((kt - kt_lo) | kk) != 0);
           }
           commit_pair_elected(elected, &empty[stage], pair_mask);
-          if (++slot == C::SLOTS) slot = 0;
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1u;
@@ -392,30 +373,22 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int sp = u % args.splits;
       total += (sp + 1) * args.KT / args.splits - sp * args.KT / args.splits;
     }
-    int stage = 0, slot = 0, fstage = 0;
-    uint32_t phase = 0, fphase = 0;
+    int stage = 0;
+    uint32_t phase = 0;
     for (int64_t i = 0; i < total; ++i) {
+      // the stage's slot is free: its refill has waited for the MMAs that read it
       if (!mbar_wait(&sf_full[stage], phase, abort_flag)) break;
-      // the MMAs that read this slot last, SLOTS stages ago, are done (with as
-      // many slots as stages, the stage's refill has waited for them already)
-      if (C::SLOTS < STAGES && i >= C::SLOTS) {
-        if (!mbar_wait(&empty[fstage], fphase, abort_flag)) break;
-        if (++fstage == STAGES) {
-          fstage = 0;
-          fphase ^= 1u;
-        }
-      }
       tc_fence_after();
       const uint4* sa = reinterpret_cast<const uint4*>(smem + C::OFF_SFA + stage * C::SFA_BYTES) + lane;
       const uint4* sb = reinterpret_cast<const uint4*>(smem + C::OFF_SFB + stage * C::SFB_BYTES) + lane;
-      const uint32_t t = lane_base + slot * C::SLOT_COLS;
+      const uint32_t t = lane_base + stage * C::SLOT_COLS;
 #pragma unroll
-      for (int j = C::CP_A; j < C::ATOMS; ++j) {
+      for (int j = 0; j < C::ATOMS; ++j) {
         const uint4 v = sa[j * 32];
         tmem_st_32x32b_x4(t + 4 * j, v.x, v.y, v.z, v.w);
       }
 #pragma unroll
-      for (int j = C::CP_B; j < C::NB * C::ATOMS; ++j) {
+      for (int j = 0; j < C::NB * C::ATOMS; ++j) {
         const uint4 v = sb[j * 32];
         tmem_st_32x32b_x4(t + 4 * C::ATOMS + 4 * j, v.x, v.y, v.z, v.w);
       }
@@ -428,7 +401,6 @@ __global__ void __launch_bounds__(THREADS, 1)
         else if (mbar_wait(&full[stage], phase, abort_flag))
           mbar_arrive(&sf_ready[stage]);
       }
-      if (++slot == C::SLOTS) slot = 0;
       if (++stage == STAGES) {
         stage = 0;
         phase ^= 1u;
@@ -579,8 +551,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         tc_fence_after();
         const bool odd = tile_no & 1;
         const uint32_t acc = tmem + (static_cast<uint32_t>(quad * 32) << 16) + (odd ? C::ACC1 : 0);
-        // whether the second group also holds shared columns
-        const bool both = odd ? (half + 2) * 64 < BN - C::ACC1 : (half + 1) * 64 > C::ACC1;
+        // whether the second groups hold shared columns too
+        constexpr int kReleased = C::ACC1 < 64 ? 1 : 0;
 #pragma unroll 1
         for (int i = 0; i < C::NB; ++i) {
           const int up = C::NB == 2 && (i == 0) != odd;  // the upper of this warp's groups
@@ -589,7 +561,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           tmem_ld_32x32b_x32(acc + col, r[0]);
           tmem_ld_32x32b_x32(acc + col + 32, r[1]);
           tmem_ld_wait();
-          if (i == (both ? 1 : 0)) {
+          if (i == kReleased) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_remote(acc_free_even);
