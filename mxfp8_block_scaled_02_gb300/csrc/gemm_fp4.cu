@@ -25,8 +25,8 @@
 //     overlap in what is left (from column ACC1 on).  The epilogue drains a tile's
 //     shared columns first and releases them, so the next tile's MMAs run while
 //     the rest is drained and stored.
-// What bounds it (M = 4096, N = 14336, K = 4096, MXFP4 71.0 us, 6.8 PFLOP/s;
-// NVFP4 77.5; tensor pipe busy 68 %): the way between L2 and the SMs,
+// What bounds it (M = 4096, N = 14336, K = 4096, MXFP4 71.4 us, 6.7 PFLOP/s;
+// NVFP4 77.3; tensor pipe busy 69 and 65 %): the way between L2 and the SMs,
 // which operand loads (1.0 GB) and output stores share: without the stores 66
 // of then 76 us, without the loads 68, without both 62; the tensor cores alone
 // need 50.  Longer K writes less: M = 8192, N = 4096, K = 14336 124 us, 7.7
