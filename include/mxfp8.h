@@ -445,8 +445,8 @@ mxfp8_status mxfp8_fp4_process_weights(int fmt, const uint8_t* w, const uint8_t*
 mxfp8_status mxfp8_fp4_workspace_size(int fmt, int64_t B, int64_t M, int64_t N, int64_t K, int x_is_quantized,
                                       size_t* bytes);
 
-/* Device workspace bytes with which mxfp8_fp4_gemm_packed splits K (0 for the
- * shapes it does not split). */
+/* Device workspace bytes with which mxfp8_fp4_gemm_packed splits K into partial
+ * sums (0 for the shapes where it does not, or splits K inside a cluster). */
 mxfp8_status mxfp8_fp4_product_workspace_size(int fmt, int64_t B, int64_t M, int64_t N, int64_t K, size_t* bytes);
 
 /*

@@ -191,8 +191,8 @@ struct Fp4Problem {
   int splits = 1;
   const void* x_bf16 = nullptr;  // small-M kernel, fp4_quantizes_inside: bf16 x instead of x and sfx
 };
-int fp4_splitk_splits(int64_t B, int64_t M, int64_t N, int64_t K);
-int64_t fp4_pair_cost(int64_t B, int64_t M, int64_t N, int64_t K);  // with that split, in 0.01 us
+int fp4_splitk_splits(int64_t B, int64_t M, int64_t N, int64_t K);  // those that leave partials
+int64_t fp4_pair_cost(int64_t B, int64_t M, int64_t N, int64_t K);  // estimated time in 0.01 us
 cudaError_t launch_gemm_fp4(const Fp4Problem& p, int sms, cudaStream_t stream, const char** msg);
 cudaError_t take_status_fp4(unsigned int* out);
 // A 3-D tensor map: innermost extent d0 in elements of `dtype`, strides s1 and
@@ -200,8 +200,8 @@ cudaError_t take_status_fp4(unsigned int* out);
 bool encode_map3(CUtensorMap* m, CUtensorMapDataType dtype, const void* base, int64_t d0, int64_t d1, int64_t d2,
                  int64_t s1, int64_t s2, int b0, int b1, CUtensorMapSwizzle sw, CUtensorMapL2promotion l2);
 // gemm_fp4_small.cu: the same product on 128 x (16, 32, 64 or 128) tiles of one
-// CTA each, the weights on the MMA's M side and K split over a cluster (part
-// and splits are not used); fp4_use_small: the shapes it is meant for.
+// CTA each, the weights on the MMA's M side, K split over a cluster or two tiles
+// an SM (part and splits are not used); fp4_use_small: the shapes it is meant for.
 bool fp4_quantizes_inside(int64_t B, int64_t M, int64_t N, int64_t K);
 bool fp4_use_small(int64_t B, int64_t M, int64_t N, int64_t K);
 cudaError_t launch_gemm_fp4_small(const Fp4Problem& p, int sms, cudaStream_t stream, const char** msg);
