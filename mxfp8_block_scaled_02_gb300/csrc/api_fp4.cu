@@ -208,7 +208,7 @@ mxfp8_status mxfp8_fp4_workspace_size(int fmt, int64_t B, int64_t M, int64_t N, 
   if (bytes == nullptr) return fail(MXFP8_ERR_INVALID_ARG, "null output pointer");
   mxfp8_status st = check_product(fmt, B, M, N, K);
   if (st != MXFP8_OK) return st;
-  if (x_is_quantized == 0 && mx::fp4_quantizes_inside(B, M, N, K)) {
+  if (x_is_quantized == 0 && mx::fp4_quantizes_inside(B, M)) {
     *bytes = 0;
     return MXFP8_OK;
   }
@@ -241,7 +241,7 @@ mxfp8_status mxfp8_fp4_linear(int fmt, const void* x_bf16, const uint8_t* x_q, c
   if ((st = check_operands(fmt, o)) != MXFP8_OK) return st;
   if (!aligned(x_bf16, 16)) return fail(MXFP8_ERR_INVALID_ARG, "tensor pointers must be 16-byte aligned");
   int sms = 0;
-  if (have_x && mx::fp4_quantizes_inside(B, M, N, K)) {
+  if (have_x && mx::fp4_quantizes_inside(B, M)) {
     if ((st = mx::current_device(&sms)) != MXFP8_OK) return st;
     mx::Fp4Problem p{fmt, nullptr, o.w, nullptr, o.sfw, o.gx, o.gw, o.bias, o.out, B, M, N, K};
     p.x_bf16 = x_bf16;

@@ -135,7 +135,7 @@ __device__ __forceinline__ void expect_tx_elected(uint32_t elected, uint32_t bar
 }
 
 constexpr int QUANT_WARPS = 6;
-constexpr int QUANT_MAX_M = 16;
+constexpr int QUANT_MAX_M = 8;
 constexpr int QUANT_AHEAD = 4;  // loads ahead, in tasks of two rows and a stage
 
 struct Args {
@@ -569,14 +569,13 @@ int64_t splits_estimate(int64_t tiles) { return tiles <= 14 ? 8 : (tiles <= 36 ?
 }  // namespace
 
 // Quantising inside repeats the work in every CTA of the same K range, and
-// saves a launch and the workspace (5 us of host time): used while a CTA's share
-// is small.  Measured in a graph (us, quantise call first / inside, MXFP4):
-// N = K = 4096 (4 stages a CTA), M = 1 4.7 / 4.2, 4 4.7 / 4.5, 8 4.8 / 5.2, 16
-// 5.0 / 6.2; N = 14336, K = 4096 (16 stages), M = 2 8.0 / 8.1, 4 8.0 / 8.7.
-bool fp4_quantizes_inside(int64_t B, int64_t M, int64_t N, int64_t K) {
-  if (B != 1 || M > QUANT_MAX_M) return false;
-  return M <= 2 || M * ceil_div(ceil_div(K, BK), splits_estimate(ceil_div(N, ROWS))) <= 32;
-}
+// saves a launch and the workspace (5 us of host time).  Measured in a graph, the
+// weights from HBM (us, quantise call first / inside, MXFP4; NVFP4): N = K = 4096,
+// M = 1 4.4 / 4.1, 6 4.4 / 4.4, 8 4.6 / 4.6, 16 4.7 / 5.5; 4.7 / 4.2, 4.7 / 4.8, 4.8
+// / 5.3, 5.0 / 6.4; N = 14336, K = 4096, M = 1 7.8 / 7.4, 8 8.1 / 8.3, 16 8.5 / 9.7;
+// N = 28672, K = 4096, M = 8 12.3 / 11.2; 12.8 / 12.1; N = 4096, K = 14336, M = 8
+// 8.9 / 8.6; 9.5 / 9.4, 16 9.1 / 9.8; 9.8 / 12.1.
+bool fp4_quantizes_inside(int64_t B, int64_t M) { return B == 1 && M <= QUANT_MAX_M; }
 
 // Where this kernel is the faster one (a function of the shape alone: the
 // workspace size depends on it).  Up to 64 tokens always, while two CTAs an SM

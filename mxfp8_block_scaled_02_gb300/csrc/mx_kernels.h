@@ -202,7 +202,7 @@ bool encode_map3(CUtensorMap* m, CUtensorMapDataType dtype, const void* base, in
 // gemm_fp4_small.cu: the same product on 128 x (16, 32, 64 or 128) tiles of one
 // CTA each, the weights on the MMA's M side, K split over a cluster or two tiles
 // an SM (part and splits are not used); fp4_use_small: the shapes it is meant for.
-bool fp4_quantizes_inside(int64_t B, int64_t M, int64_t N, int64_t K);
+bool fp4_quantizes_inside(int64_t B, int64_t M);
 bool fp4_use_small(int64_t B, int64_t M, int64_t N, int64_t K);
 cudaError_t launch_gemm_fp4_small(const Fp4Problem& p, int sms, cudaStream_t stream, const char** msg);
 cudaError_t take_status_fp4_small(unsigned int* out);
