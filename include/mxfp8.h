@@ -386,10 +386,11 @@ mxfp8_status mxfp8_linear_fmt(int path, int w_format, const void* x_bf16, const 
  *       E2M1(x / 2^e); an Inf/NaN block gets byte 0xFF and zero codes.
  *     NVFP4: one E4M3 scale per 16 elements and one fp32 scale g per tensor:
  *       s = E4M3(amax / (6 g)) saturating, element = E2M1(x * (1 / (s g)))
- *       in fp32, value = element * s * g.  A block whose s g is zero or below
- *       what can be inverted gets zero codes, one holding Inf/NaN the scale
- *       0x7F (NaN).  g is read on the device (float*, NULL = 1, > 0); choose
- *       it as amax(tensor) / (448 * 6).
+ *       in fp32, value = element * s * g.  A zero block has s = 0, a block
+ *       whose s g is zero or below what can be inverted gets zero codes, one
+ *       holding Inf/NaN the scale 0x7F (NaN).  g is read on the device (float*,
+ *       NULL = 1, >= 0); choose it as amax(tensor) / (448 * 6).  That is 0 for
+ *       an all-zero tensor, and every value is then 0.
  *   Elements round to nearest even and saturate to +-6.
  *   K % 32 == 0 throughout, N % 8 == 0 for the product.
  *   Formats of the quantising calls:

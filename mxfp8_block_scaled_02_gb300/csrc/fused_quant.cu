@@ -20,7 +20,7 @@
 //
 // Measured (us, back to back in a CUDA graph; MXFP8 unless named): rmsnorm with
 // a bf16 residual 8192 x 4096 34.8 (6.8 TB/s), 4 x 4096 1.7; silu_mul 4096 x 14336
-// 44.5 (6.6 TB/s), MXFP4 42.2 (6.3), NVFP4 44.1 (6.1: twice the block scales, each
+// 44.5 (6.6 TB/s), MXFP4 42.2 (6.3), NVFP4 44.5 (6.0: twice the block scales, each
 // with a reciprocal), 16 x 14336 1.6; fp4 14336 x 4096 23.2 (6.4 TB/s), NVFP4 23.8
 // (6.3), 8192 x 14336 to packed scales 43.1 (6.9), NVFP4 44.9 (6.7); unpack of
 // 14336 x 4096 codes 12.9 (6.8 TB/s).

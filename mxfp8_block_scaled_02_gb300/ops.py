@@ -530,7 +530,8 @@ def quantize_fp4(x: torch.Tensor, fmt: str = "mxfp4", *,
     """bf16 x [..., K] -> (x_q uint8 [..., K/2], two E2M1 codes a byte, the even
     element in the low half; x_scale uint8: "mxfp4" E8M0 [..., K/32], "nvfp4"
     E4M3 [..., K/16]).  ``tensor_scale``: nvfp4's fp32 scale of the whole tensor
-    (one element on the device; None is 1), normally amax / (448 * 6)."""
+    (one element on the device, >= 0; None is 1), normally amax / (448 * 6): 0 for
+    an all-zero tensor, whose values are then 0."""
     f = _fmt4(fmt)
     if x.dtype is not _BF16:
         raise TypeError("x must be bfloat16")

@@ -3,7 +3,8 @@ test infrastructure only, plain numpy, no code shared with the library.
 
 MXFP4 (OCP MX v1.0, sections 5.3.3 and 6.3): E2M1 elements, one E8M0 scale
 2**(floor(log2 amax) - 2) per 32.  NVFP4: E2M1 elements, one E4M3 scale per 16,
-one fp32 scale g per tensor; its rule is stated in fp32 steps and follows them.
+one fp32 scale g per tensor; its rule is stated in fp32 steps and follows them
+for every g >= 0 (g = 0, the amax of an all-zero tensor: the value is 0).
 """
 
 from __future__ import annotations
@@ -60,8 +61,9 @@ def quantize4(x: np.ndarray, fmt: str, g: float = 1.0):
         t = safe / np.exp2(e)[..., None]
     else:
         f = np.float32
-        six_g = f(6.0) * f(g)
-        s = e4m3_encode((amax.astype(f) / six_g).astype(np.float64)).astype(np.uint8)
+        with np.errstate(divide="ignore", over="ignore", invalid="ignore"):
+            six_g = np.maximum(f(6.0) * f(g), f(2.0 ** -149))  # a zero block is 0 even for g = 0
+            s = e4m3_encode((amax.astype(f) / six_g).astype(np.float64)).astype(np.uint8)
         unit = e4m3_value(s).astype(f) * f(g)
         with np.errstate(divide="ignore", over="ignore"):
             inv = f(1.0) / unit
