@@ -495,8 +495,7 @@ mxfp8_status mxfp8_fp4_gemm_packed(int fmt, const uint8_t* x_q, const uint8_t* s
  *   residual : device, rows of bf16 (fp32 when residual_is_f32), or NULL with
  *     residual_out NULL: t = x.  residual_out: dense [M, K] of the same type;
  *     it may be the residual itself when that is dense.
- *   weight_bf16 : device, [K] (may be read before the kernel ahead ends, as a
- *     linear layer's weights).
+ *   weight_bf16 : device, [K]; read, like x, after the kernel ahead has finished.
  *   tensor_scale : as mxfp8_fp4_quantize (NVFP4 only).
  *   scale : row-major [M, K/block], or with scale_packed the packed atoms of
  *     (1, M, K), as mxfp8_quantize_packed / mxfp8_fp4_quantize_packed (bytes

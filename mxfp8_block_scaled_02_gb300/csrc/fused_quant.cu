@@ -179,10 +179,11 @@ constexpr int kNormThreads = 512;
 enum { kResNone = 0, kResBf16 = 1, kResF32 = 2 };
 
 // One CTA per row, the row held in registers (CH chunks a thread) between the
-// sum of squares and the output, so x and the residual are read once.  The
-// norm's weight depends on nothing the kernel before this one writes and is
-// read before the dependency wait; the next kernel in the stream may start at
-// once (a GEMM that reads the output after its own wait).
+// sum of squares and the output, so x and the residual are read once.  Nothing
+// is read before the dependency wait: the weight too may be the output of a
+// kernel that let this one start early (an adaptive norm's, from a few-token
+// linear layer).  The next kernel in the stream may start at once (it reads
+// this one's output after its own wait).
 template <int FMT, int CH, int RES>
 __global__ void __launch_bounds__(kNormThreads, CH == 1 ? 3 : (CH == 2 ? 2 : 1)) rmsnorm_kernel(const NormArgs a) {
   __shared__ float part[32];
@@ -190,8 +191,6 @@ __global__ void __launch_bounds__(kNormThreads, CH == 1 ? 3 : (CH == 2 ? 2 : 1))
   const int64_t row = blockIdx.x;
   const int nchunks = static_cast<int>(a.o.K / 16);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  Chunk w = zero_chunk();
-  if (CH == 1) w = static_cast<int>(threadIdx.x) < nchunks ? load16(a.w, threadIdx.x, a.wide) : zero_chunk();
   grid_dependency_wait();
   // all loads first, so that they are in flight together
   const float g = FMT == kQNV4 && a.o.g != nullptr ? *a.o.g : 1.f;
@@ -210,6 +209,8 @@ __global__ void __launch_bounds__(kNormThreads, CH == 1 ? 3 : (CH == 2 ? 2 : 1))
       for (int h = 0; h < (RES == kResF32 ? 2 : 1); ++h) rv[i][h] = valid ? load_32(rp + 8 * h, a.wide) : zero_chunk();
     }
   }
+  Chunk w = zero_chunk();
+  if (CH == 1) w = static_cast<int>(threadIdx.x) < nchunks ? load16(a.w, threadIdx.x, a.wide) : zero_chunk();
   float t[CH][16];
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
