@@ -152,18 +152,21 @@ mxfp8_status mxfp8_workspace_size(int64_t B, int64_t M, int64_t N, int64_t K,
  *   Stream ordering: the GEMM kernels are launched with programmatic stream
  *   serialization.  When the kernel before them in the stream triggers its
  *   dependents early (griddepcontrol.launch_dependents), they may read
- *   w_packed, sf_packed and bias before that kernel ends; x, x_q, x_scale
- *   and out are touched only after it has finished.  The quantise step inside
- *   a linear call is launched the same way and touches nothing before the
- *   kernel ahead of it has finished.  Of this library's
+ *   w_packed and sf_packed before that kernel ends; x, x_q, x_scale, bias, the
+ *   4-bit layer's tensor scales and out are touched only after it has finished,
+ *   so all of those may be its outputs.  The quantise step inside a linear call
+ *   is launched the same way and touches nothing before the kernel ahead of it
+ *   has finished; nor do the norm and activation calls below.  Of this library's
  *   kernels, only these trigger early: the quantise / activation-scale repack
  *   step inside mxfp8_linear, mxfp8_linear_path and mxfp8_linear_noalloc
  *   (whose output only the same call's GEMM reads, after its wait), the
  *   CTA-pair GEMM when it splits K (whose partials only the same call's
- *   reduce reads, after its wait), the small-M GEMM (whose output the
- *   next layer reads as x, after its wait), and the 4-bit layer's counterparts
- *   of these and the norm and activation calls below (whose outputs are
- *   activations, read after the next kernel's wait).
+ *   reduce reads, after its wait), the small-M GEMM, the 4-bit layer's
+ *   counterparts of these, and the norm and activation calls.  What the last
+ *   three write (out, y_q, y_sf, codes, scales, residual_out, y_bf16) may be any
+ *   input of the next call but its w_packed and sf_packed: pass codes and
+ *   scales that are to be weights through mxfp8_process_weights or
+ *   mxfp8_fp4_process_weights.
  *   The standalone calls (mxfp8_quantize, mxfp8_quantize_packed,
  *   mxfp8_pack_scales, mxfp8_process_weights) never do, so weights they write
  *   are complete before a GEMM queued after them starts.  Kernels from other
@@ -462,8 +465,8 @@ mxfp8_status mxfp8_fp4_product_workspace_size(int fmt, int64_t B, int64_t M, int
  *   fp32 accumulation; one rounding to bf16 after the tensor scales and the
  *   bias.  Calls with few output tiles split K and add the fp32 partials in a
  *   fixed order, so a call's result is the same every time.  Stream ordering
- *   as mxfp8_linear: w_packed, sf_packed, bias and w_tensor_scale may be read
- *   before the kernel ahead ends if that kernel triggers its dependents early.
+ *   as mxfp8_linear: w_packed and sf_packed may be read before the kernel ahead
+ *   ends if that kernel triggers its dependents early.
  */
 mxfp8_status mxfp8_fp4_linear(int fmt, const void* x_bf16, const uint8_t* x_q, const uint8_t* x_scale,
                               const float* x_tensor_scale, int64_t B, int64_t M, int64_t N, int64_t K,

@@ -185,11 +185,9 @@ __global__ void __launch_bounds__(THREADS, C::MINB)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  // The bias of the output column this thread reduces (warps 2.. only): read
-  // before the dependency wait, like the weights (the previous kernel in the
-  // stream never writes it), so its latency is off the path after the MMAs
-  // (measured: 6.27 -> 6.02 us per call at M = 1, 9.80 -> 9.48 at M = 64).
-  float bias_n = 0.f;
+  // The bias of the output column this thread reduces (warps 2.. only): loaded
+  // with x, so its latency is off the path after the MMAs.
+  __nv_bfloat16 bias_bf16 = __float2bfloat16_rn(0.f);
 
   if (warp == 0) {
     // ------------------------------------------------ weight producer (TMA)
@@ -278,16 +276,20 @@ __global__ void __launch_bounds__(THREADS, C::MINB)
           *reinterpret_cast<uint32_t*>(smem + C::OFF_SFX + xs * kAtomBytes + (row & 31) * 16 + (row >> 5) * 4) = 0u;
       }
     }
+    // x is written by the previous kernel in the stream, the bias may be: wait for
+    // it to finish, and read nothing of either before.  (With the bias's address
+    // worked out after the wait M = 128 took 14.1 us instead of 13.8.)
+    const __nv_bfloat16* bias_at;
     {
       // the column this thread adds the bias to: in the reduction below, or
       // (one CTA per tile) in the epilogue's direct store, warps 2..5
       const int per = kRows / a.splits;
       const int n = a.splits == 1 ? tile * kRows + (warp & 3) * 32 + lane
                                   : tile * kRows + static_cast<int>(rank) * per + (threadIdx.x - 64) % per;
-      if (a.bias != nullptr && n < a.N) bias_n = __bfloat162float(a.bias[n]);
+      bias_at = a.bias != nullptr && n < a.N ? a.bias + n : nullptr;
     }
-    // x is written by the previous kernel in the stream: wait for it to finish.
     grid_dependency_wait();
+    if (bias_at != nullptr) bias_bf16 = *bias_at;
     // ------------------------------------------------ activation quantiser
     // A task is one 32-element block of x: K tile i, token row r < M, block j
     // of the tile's four, one lane per block (quantize_block32, as in the
@@ -380,6 +382,7 @@ __global__ void __launch_bounds__(THREADS, C::MINB)
       const int quad = warp & 3;
       const int n = tile * kRows + quad * 32 + lane;
       const uint32_t lrow = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+      const float bias_n = __bfloat162float(bias_bf16);
       for (int c = 0; c < a.n_mma; c += 16) {
         uint32_t r[16], r1[16];
         tmem_ld_32x32b_x16(lrow + C::T_ACC + c, r);
@@ -439,7 +442,7 @@ __global__ void __launch_bounds__(THREADS, C::MINB)
     // QTHREADS is a multiple of per, so each thread keeps one output column n
     const int nl = t % per;
     const int n = tile * kRows + static_cast<int>(rank) * per + nl;
-    const float bias = bias_n;  // loaded before the dependency wait (same n)
+    const float bias = __bfloat162float(bias_bf16);  // of the same n
     if (n < a.N) {
 #pragma unroll 4
       for (int m = t / per; m < a.M; m += QTHREADS / per) {

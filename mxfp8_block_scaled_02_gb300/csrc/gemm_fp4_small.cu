@@ -6,8 +6,9 @@
 // (128 rows per CTA) and the tokens its N side (16, 32, 64 or 128 a CTA), no MMA
 // row is padding, and K is split over a cluster of S CTAs so that every SM
 // streams from the start: each holds a ring of 128-row x 128-byte weight tiles
-// in flight before the tokens arrive (they are the previous kernel's output,
-// waited for with griddepcontrol.wait; weights, scales and bias are not).
+// in flight before the tokens arrive (waited for with griddepcontrol.wait, like
+// the bias and the tensor scales: any of them may be the previous kernel's output;
+// the weights and their block scales may not).
 // Codes and scale atoms of both operands come by TMA, the atoms go to tensor
 // memory by tcgen05.cp in the MMA warp's own order.  A few bf16 tokens can
 // also be quantised here (kQuant): six warps load the CTA's K range and write
@@ -214,8 +215,7 @@ __global__ void __launch_bounds__(THREADS, kTwo ? 2 : 1)
   tc_fence_after();
   if (a.splits > 1) cluster_arrive_relaxed();  // this CTA's barriers exist
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
-  // the output row this thread finishes: its bias and the weights' scale are
-  // read before the dependency wait, like the weights
+  // the output row this thread finishes, its bias and the tensor scales
   const int per = ROWS / a.splits;
   const int my_n = a.splits == 1 ? tile * ROWS + (warp & 3) * 32 + lane
                                  : tile * ROWS + rank * per + static_cast<int>(threadIdx.x) % per;
@@ -381,9 +381,10 @@ __global__ void __launch_bounds__(THREADS, kTwo ? 2 : 1)
     __syncwarp();
   }
   if (warp >= 4 || a.splits > 1) {
+    // these, and the output's memory, may belong to the kernels before
+    grid_dependency_wait();
     if (a.bias != nullptr && my_n < a.N) bias_n = __bfloat162float(a.bias[my_n]);
     if (a.gw != nullptr) alpha = *a.gw;
-    grid_dependency_wait();  // g_x and the output belong to the kernels before
     if (a.gx != nullptr) alpha *= *a.gx;
   }
   if (a.splits > 1) cluster_wait();  // the other CTAs' barriers do

@@ -240,8 +240,9 @@ __global__ void __launch_bounds__(F_THREADS, 1)
     uint4* bias_s = reinterpret_cast<uint4*>(smem + F_OFF_BIAS + qw * F_EPI_COLS * 2);
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32) << 16);
 
-    // The bias may be read before the dependency wait (it is a weight-side
-    // input), so it goes to shared memory now.
+    // The bias goes to shared memory now, but not before the dependency wait (the
+    // previous kernel may have written it); x is not there before either.
+    grid_dependency_wait();
     if (a.bias != nullptr && lane < F_EPI_COLS / 8) {
       const int n = nt * FBN + col0 + 8 * lane;
       bias_s[lane] = n < a.N ? *reinterpret_cast<const uint4*>(a.bias + n) : make_uint4(0, 0, 0, 0);

@@ -466,7 +466,9 @@ __global__ void __launch_bounds__(P_THREADS, 1)
       if (live) u += npairs;
       if (live && args.bias != nullptr && args.splits == 1) {
         // this warp's 128 bias values (zero past N) into shared memory while
-        // the tile's MMAs run, so that the drain below reads no global memory
+        // the tile's MMAs run, so that the drain below reads no global memory;
+        // the previous kernel in the stream may have written them
+        grid_dependency_wait();
         if (lane < P_EPI_COLS / 8) {
           const int n = nt * PBN + col0 + 8 * lane;
           bias_s[lane] = n < args.N ? *reinterpret_cast<const uint4*>(args.bias + n) : make_uint4(0, 0, 0, 0);

@@ -39,11 +39,11 @@ __global__ void __launch_bounds__(256) splitk_reduce_kernel(const float* __restr
   const int n0 = static_cast<int>(valid ? t - row * NQ : 0) * 8;
   const int64_t base = row * N + n0;
   // launched with programmatic serialization after the GEMM that writes the
-  // partials: the bias (a weight-side input) is read before the wait, the
-  // partials after it
+  // partials.  The bias too is read after the wait: it may be the output of a
+  // kernel ahead of that GEMM, which this wait covers.
+  grid_dependency_wait();
   uint4 braw = make_uint4(0, 0, 0, 0);
   if (valid && bias != nullptr) braw = __ldg(reinterpret_cast<const uint4*>(bias + n0));
-  grid_dependency_wait();
   float acc[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) acc[i] = 0.f;
