@@ -155,7 +155,7 @@ struct Args {
   const __nv_bfloat16* bias;
   const float* gx;
   const float* gw;
-  int B, M, N, K;
+  int B, N;
   int MT, NT, KT;   // pair tiles, stages of K
   int last_steps;   // MMA steps of the last stage
   int units;        // tiles * splits
@@ -662,9 +662,7 @@ cudaError_t launch_t(const Fp4Problem& p, const PairPlan& plan, int sms, cudaStr
   a.gx = p.gx;
   a.gw = p.gw;
   a.B = static_cast<int>(p.B);
-  a.M = static_cast<int>(p.M);
   a.N = static_cast<int>(p.N);
-  a.K = static_cast<int>(p.K);
   a.MT = static_cast<int>(ceil_div(p.M, 2 * BM));
   a.NT = static_cast<int>(ceil_div(p.N, BN));
   a.KT = static_cast<int>(ceil_div(p.K, BK));
