@@ -517,8 +517,10 @@ mxfp8_status mxfp8_rmsnorm_quantize(int fmt, const void* x_bf16, int64_t x_strid
 
 /*
  * mxfp8_silu_mul_quantize - the gated activation between an MLP's
- * projections, output quantised: y = gate / (1 + exp(-gate)) * up in fp32,
- * (q, scale) = quantise(y).  gate and up: device, M rows of K bf16 with their
+ * projections, output quantised: y = gate / (1 + exp(-gate)) * up in fp32 (by
+ * CUDA's quick exponential and division: y is within (6 + 1.2 |gate|) 2^-23
+ * relative, 1e-5 at |gate| = 64; below -87, where the exponential is subnormal,
+ * its rounding adds to that), (q, scale) = quantise(y).  gate and up: device, M rows of K bf16 with their
  * own strides (for a merged projection, up = gate + K and both strides 2 K).
  * Other arguments as mxfp8_rmsnorm_quantize.
  */

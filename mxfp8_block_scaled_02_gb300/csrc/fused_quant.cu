@@ -19,11 +19,12 @@
 // into the packed atoms cost the activation 5 us of 52 at 4096 x 14336).
 //
 // Measured (us, back to back in a CUDA graph; MXFP8 unless named): rmsnorm with
-// a bf16 residual 8192 x 4096 34.8 (6.8 TB/s), 4 x 4096 1.7; silu_mul 4096 x 14336
-// 44.5 (6.6 TB/s), MXFP4 42.2 (6.3), NVFP4 44.5 (6.0: twice the block scales, each
-// with a reciprocal), 16 x 14336 1.6; fp4 14336 x 4096 23.2 (6.4 TB/s), NVFP4 23.8
-// (6.3), 8192 x 14336 to packed scales 43.1 (6.9), NVFP4 44.9 (6.7); unpack of
-// 14336 x 4096 codes 12.9 (6.8 TB/s).
+// a bf16 residual 8192 x 4096 34.8 (6.8 TB/s), 4 x 4096 1.7, two chunks a thread
+// 2048 x 16384 37.1 (6.4 TB/s), 4 x 16384 3.2, four 1024 x 32768 45.3 (5.2: one
+// CTA an SM); silu_mul 4096 x 14336 44.5 (6.6 TB/s), MXFP4 42.2 (6.3), NVFP4 44.5
+// (6.0: twice the block scales, each with a reciprocal), 16 x 14336 1.6; fp4 14336
+// x 4096 23.2 (6.4 TB/s), NVFP4 23.8 (6.3), 8192 x 14336 to packed scales 43.1
+// (6.9), NVFP4 44.9 (6.7); unpack of 14336 x 4096 codes 12.9 (6.8 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -307,7 +308,10 @@ __global__ void __launch_bounds__(kRowThreads, FMT == kQNV4 ? 10 : 12) silu_mul_
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
       // gate / (1 + exp(-gate)) with the exponential's argument <= 0, so that
-      // nothing overflows and very negative gates keep their value
+      // nothing overflows and very negative gates keep their value.  The quick
+      // exponential and division are off by 2 + 1.2 |gate| and 2 ulp, 1e-5 at
+      // |gate| = 64 and far below an 8-bit element's half step (2^-4); with the
+      // accurate ones NVFP4 4096 x 14336 takes 73.5 us instead of 44.5.
       const float e = __expf(-fabsf(gt[j]));
       gt[j] = gt[j] * __fdividef(gt[j] >= 0.f ? 1.f : e, 1.f + e) * up[j];
     }

@@ -31,8 +31,8 @@
 // of then 76 us, without the loads 68, without both 62; the tensor cores alone
 // need 50.  Longer K writes less: M = 8192, N = 4096, K = 14336 124 us, 7.7
 // PFLOP/s.  192-column tiles with two whole accumulators (86.8 against 73.1 us)
-// load more; clusters of four would share loads, but 144 of the 152 SMs hold
-// them.
+// load more.  Two pairs that share loads (a cluster of four; 144 of the 152 SMs
+// hold them) have not been built, nor has the instruction with K = 96.
 //
 // Warps: 0 weight TMA, 1 tensor-memory allocation and (even CTA) MMA issue,
 // 2 weight-scale TMA, 3 activation and activation-scale TMA, 4..7 scales into

@@ -575,7 +575,8 @@ int64_t splits_estimate(int64_t tiles) { return tiles <= 14 ? 8 : (tiles <= 36 ?
 // M = 1 4.4 / 4.1, 6 4.4 / 4.4, 8 4.6 / 4.6, 16 4.7 / 5.5; 4.7 / 4.2, 4.7 / 4.8, 4.8
 // / 5.3, 5.0 / 6.4; N = 14336, K = 4096, M = 1 7.8 / 7.4, 8 8.1 / 8.3, 16 8.5 / 9.7;
 // N = 28672, K = 4096, M = 8 12.3 / 11.2; 12.8 / 12.1; N = 4096, K = 14336, M = 8
-// 8.9 / 8.6; 9.5 / 9.4, 16 9.1 / 9.8; 9.8 / 12.1.
+// 8.9 / 8.6; 9.5 / 9.4, 16 9.1 / 9.8; 9.8 / 12.1.  So in a graph NVFP4 is up to
+// 10 % the slower one from six tokens on; in eager calls the host's time decides.
 bool fp4_quantizes_inside(int64_t B, int64_t M) { return B == 1 && M <= QUANT_MAX_M; }
 
 // Where this kernel is the faster one (a function of the shape alone: the

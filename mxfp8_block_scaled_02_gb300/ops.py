@@ -192,7 +192,10 @@ def quantize_weights(w: torch.Tensor, fmt: str = "e4m3") -> tuple[torch.Tensor, 
 
 @dataclasses.dataclass
 class PackedWeights:
-    """Weights after the one-time repack: element bytes and scale atoms."""
+    """Weights after the one-time repack (process_weights, process_weights_fp4):
+    element bytes and scale atoms.  A product may read these two before the
+    kernel ahead of it in the stream has finished, so they are not to be another
+    call's outputs (codes that a norm or activation wrote); every other input may."""
 
     w_packed: torch.Tensor   # uint8, B*N*K bytes (3BNK/4 for packed FP6, BNK/2 for FP4)
     sf_packed: torch.Tensor  # uint8, packed scale atoms
