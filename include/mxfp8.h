@@ -557,6 +557,157 @@ mxfp8_status mxfp8_gated_mlp(int fmt, const void* x_bf16, int64_t x_stride, cons
                              void* out_bf16, void* workspace, size_t workspace_bytes, mxfp8_stream_t stream);
 
 /*
+ * Block-128 FP8 layer, products grouped by expert, expert routing.
+ *   No counterpart on the source pages: the E4M3 checkpoints whose scales are
+ *   fp32, one per 128 elements, and what a mixture-of-experts layer needs around
+ *   the products.  Elements are E4M3 throughout.  Formats of the grouped calls:
+ */
+#define MXFP8_GFMT_MXFP8 0   /* one E8M0 scale per 32 elements along K */
+#define MXFP8_GFMT_FP8_128 1 /* fp32 scales: one per 128 of K (rows of x), one per 128 x 128 (weights) */
+
+/*
+ * mxfp8_b128_quantize - bf16 rows -> E4M3 codes and one fp32 scale per block of
+ * 128 elements along K (the last block of a row may be shorter).
+ *   scale = amax / 448 (fp32), code = E4M3(448 x / amax), to nearest even of
+ *   the exact quotient.  A block of zeros has scale 0 and zero codes, one that
+ *   holds Inf or NaN the scale NaN and the codes 0x7F.
+ *   x_bf16  : device, [rows, K];  x_q : device, [rows, K] out;
+ *   x_scale : device, [rows, ceil(K / 128)] fp32 out.
+ *   K % 16 == 0 (else MXFP8_ERR_UNSUPPORTED); pointers 16-byte aligned.
+ *   rows = 0 is a no-op.
+ */
+mxfp8_status mxfp8_b128_quantize(const void* x_bf16, int64_t rows, int64_t K, uint8_t* x_q, float* x_scale,
+                                 mxfp8_stream_t stream);
+
+/*
+ * mxfp8_b128_quantize_weights - the same rule with one scale per 128 x 128
+ * block: w_bf16 [B, N, K] -> w_q [B, N, K], w_scale [B, ceil(N / 128),
+ * ceil(K / 128)] fp32 (the layout of a block-scaled checkpoint).
+ */
+mxfp8_status mxfp8_b128_quantize_weights(const void* w_bf16, int64_t B, int64_t N, int64_t K, uint8_t* w_q,
+                                         float* w_scale, mxfp8_stream_t stream);
+
+/*
+ * mxfp8_b128_silu_mul_quantize - mxfp8_silu_mul_quantize with the output in
+ * fp8_128: q [M, K], scale fp32 [M, ceil(K / 128)].  K % 16 == 0.  The quotients
+ * 448 y / amax are fp32, within 3 ulp.
+ */
+mxfp8_status mxfp8_b128_silu_mul_quantize(const void* gate_bf16, int64_t gate_stride, const void* up_bf16,
+                                          int64_t up_stride, int64_t M, int64_t K, uint8_t* q, float* scale,
+                                          mxfp8_stream_t stream);
+
+/*
+ * mxfp8_b128_linear - out[b, m, n] = bf16( sum_j s_x[b, m, j] s_w[b, n / 128, j]
+ *                     sum_(k in block j) x_q[b, m, k] w[b, n, k]  + bias[n] ).
+ *   Exactly one input form: x_bf16 [B, M, K] (quantised inside the call as
+ *   mxfp8_b128_quantize does), or x_q [B, M, K] with x_scale fp32
+ *   [B, M, ceil(K / 128)].
+ *   w E4M3 [B, N, K] and w_scale fp32 [B, ceil(N / 128), ceil(K / 128)] as a
+ *   checkpoint holds them; no repack is needed.  bias bf16 [N] or NULL.
+ *   workspace : >= mxfp8_b128_workspace_size bytes, 256-byte aligned (NULL for
+ *   a quantised x).
+ *   N % 8 == 0, K % 16 == 0 (else MXFP8_ERR_UNSUPPORTED); pointers 16-byte
+ *   aligned; M = 0 is a no-op.
+ *   Sums within a block and over the blocks are fp32; one rounding, after the
+ *   bias.  Where K is split over CTAs their partial sums are added in the order
+ *   of K: a call's result is the same every time.  w may be read before the
+ *   kernel ahead in the stream ends if that kernel triggers its dependents early
+ *   (the calls of this library that make weights do not).
+ */
+mxfp8_status mxfp8_b128_workspace_size(int64_t B, int64_t M, int64_t N, int64_t K, int x_is_quantized, size_t* bytes);
+mxfp8_status mxfp8_b128_linear(const void* x_bf16, const uint8_t* x_q, const float* x_scale, int64_t B, int64_t M,
+                               int64_t N, int64_t K, const uint8_t* w, const float* w_scale, const void* bias_bf16,
+                               void* out_bf16, void* workspace, size_t workspace_bytes, mxfp8_stream_t stream);
+
+/*
+ * mxfp8_grouped_linear - rows sorted by expert, each times its expert's weights:
+ *   out[r, n] = bf16( sum_k x[r, k] w[e, n, k] + bias[e, n] )
+ *   for r in [offsets[e], offsets[e + 1]), e = 0 .. E - 1.
+ *   fmt     : MXFP8_GFMT_*, of x and w.
+ *   Input   : x_bf16 [T, K], quantised inside the call; row r of the product is
+ *     x[rows[r]] (rows: device int32 [R]; an index outside [0, T) stands for a
+ *     row of zeros), or x[r] with rows NULL and T == R.  Or x_q [R, K] with
+ *     x_scale, E8M0 [R, K / 32] or fp32 [R, ceil(K / 128)].
+ *   offsets : device, int32 [E + 1]; read on the device, so a captured graph
+ *     follows it.  Each is taken as at least 0 and the one before it, and at
+ *     most R, so that groups never overlap.  Rows of out that belong to no group
+ *     are left as they were.
+ *   w       : MXFP8: w_packed of mxfp8_process_weights(B = E) and w_scale its
+ *     sf_packed; FP8_128: E4M3 [E, N, K] and fp32 [E, ceil(N / 128),
+ *     ceil(K / 128)].
+ *   bias    : bf16 [E, N] or NULL.
+ *   workspace : >= mxfp8_grouped_workspace_size bytes, 256-byte aligned (NULL
+ *     for a quantised x).
+ *   E <= 512, N % 8 == 0, K % 128 == 0 (MXFP8) or K % 16 == 0 (FP8_128), else
+ *   MXFP8_ERR_UNSUPPORTED; pointers 16-byte aligned (rows, offsets 4); R = 0 is
+ *   a no-op.  Precision and order as mxfp8_b128_linear; all inputs are read
+ *   after the kernel ahead in the stream has finished.
+ */
+mxfp8_status mxfp8_grouped_workspace_size(int fmt, int64_t E, int64_t R, int64_t N, int64_t K, int x_is_quantized,
+                                          size_t* bytes);
+mxfp8_status mxfp8_grouped_linear(int fmt, const void* x_bf16, int64_t T, const int32_t* rows, const uint8_t* x_q,
+                                  const void* x_scale, const int32_t* offsets, int64_t E, int64_t R, int64_t N,
+                                  int64_t K, const uint8_t* w, const void* w_scale, const void* bias_bf16,
+                                  void* out_bf16, void* workspace, size_t workspace_bytes, mxfp8_stream_t stream);
+
+/*
+ * mxfp8_route - which k experts each of T tokens goes to, and the order of the
+ * T k rows sorted by expert, within an expert by token.
+ *   logits : device, T rows of E fp32 (bf16 when logits_are_bf16), logits_stride
+ *     elements apart.
+ *   The k largest logits, in descending order, ties to the lowest expert.  An
+ *   expert whose logit is -inf or NaN is never chosen; a slot for which none is
+ *   left has id -1, weight 0 and position -1, and no row.
+ *   scoring : the weights, in fp32: softmax over all E (the never-chosen count
+ *     0), or the sigmoid of the logit.
+ *   renormalize : divide by the sum of the token's chosen weights (unless it is
+ *     0); scale : then multiply by this.
+ *   ids [T, k], weights [T, k], positions [T, k] (the row of each slot), offsets
+ *     [E + 1] (the rows of each expert), rows [T k] (the token of each row, -1
+ *     behind the last): device, int32 or fp32, written.
+ *   workspace : >= mxfp8_route_workspace_size bytes, 256-byte aligned (NULL when
+ *     that is 0).
+ *   E <= 512, k <= 32 and k <= E.  T = 0 sets the offsets to 0.
+ */
+#define MXFP8_ROUTE_SOFTMAX 0
+#define MXFP8_ROUTE_SIGMOID 1
+mxfp8_status mxfp8_route_workspace_size(int64_t T, int64_t E, int64_t k, size_t* bytes);
+mxfp8_status mxfp8_route(const void* logits, int64_t logits_stride, int logits_are_bf16, int64_t T, int64_t E, int64_t k,
+                         int scoring, int renormalize, float scale, int32_t* ids, float* weights, int32_t* offsets,
+                         int32_t* rows, int32_t* positions, void* workspace, size_t workspace_bytes,
+                         mxfp8_stream_t stream);
+
+/*
+ * mxfp8_combine - out[t] = bf16( sum_j weights[t, j] y[positions[t, j]] + add[t] )
+ *   in fp32, in the order of the slots, rounded once.  y: device bf16 [R, N];
+ *   positions, weights: device [T, k] as mxfp8_route writes them (a position
+ *   outside [0, R) is left out); add: device, rows of N bf16, add_stride elements
+ *   apart, or NULL; out: device, dense [T, N].  N % 8 == 0, k <= 32.
+ */
+mxfp8_status mxfp8_combine(const void* y_bf16, int64_t R, const int32_t* positions, const float* weights, int64_t T,
+                           int64_t k, int64_t N, const void* add_bf16, int64_t add_stride, void* out_bf16,
+                           mxfp8_stream_t stream);
+
+/*
+ * mxfp8_expert_mlp - a mixture-of-experts gated MLP in one call:
+ *   route (mxfp8_route of the logits), h = grouped product of x's rows with
+ *   gate_up (bf16), c = quantise(silu(h[:, :F]) * h[:, F:]), y = grouped product
+ *   of c with down (bf16), out = combine(y) + add,
+ * by the calls above with the intermediates in the workspace; the output is
+ * theirs bit for bit.
+ *   x_bf16 : device, dense [T, K].  gate_up [E, 2 F, K] (gate rows first) and
+ *   down [E, K, F] as mxfp8_grouped_linear's w; add, out: [T, K].
+ *   workspace : >= mxfp8_expert_mlp_workspace_size bytes, 256-byte aligned.
+ */
+mxfp8_status mxfp8_expert_mlp_workspace_size(int fmt, int64_t T, int64_t E, int64_t k, int64_t K, int64_t F,
+                                             size_t* bytes);
+mxfp8_status mxfp8_expert_mlp(int fmt, const void* x_bf16, int64_t T, int64_t K, const void* logits,
+                              int64_t logits_stride, int logits_are_bf16, int64_t E, int64_t k, int scoring,
+                              int renormalize, float scale, int64_t F, const uint8_t* gate_up, const void* gate_up_scale,
+                              const uint8_t* down, const void* down_scale, const void* add_bf16, int64_t add_stride,
+                              void* out_bf16, void* workspace, size_t workspace_bytes, mxfp8_stream_t stream);
+
+/*
  * Persistable packed weights.
  *   Source: the Mxfp8LinearKernel page: supports_pre_processed_weights and the
  *   weight-cache daemon that hands weights, already processed, to later

@@ -1,0 +1,381 @@
+// grouped_quant.cu - the quantising steps around the grouped and block-128 products:
+// rows of x (in order, or picked by an index) and silu(gate) * up to E4M3 codes, and
+// weights to codes with one scale per 128 x 128 block.
+//
+// fp8_128: a block of 128 elements has the fp32 scale s = amax / 448 and the codes
+// E4M3(448 x / amax), to nearest even, of the exact quotient: x and amax have 8
+// significant bits, so 448 x / amax is either a tie of two codes, which has at
+// most 5, or at least 1 / 7905 away from one (relative; 7905 = 31 * 255).  The fp32
+// product x * (448 / amax) is off by at most 2 ulp, so rounded to 17 bits it is
+// exactly the tie where there is one and on the right side elsewhere; no division
+// per element is needed.  A zero block has s = 0 and zero codes (the signs kept), a
+// block that holds Inf or NaN s = NaN and the codes 0x7F, as MXFP8's blocks.
+//
+// MXFP8: the rule and the bytes of mx_quant.cuh.
+//
+// Bound by reading x and writing the codes.  Sixteen elements a lane (32 bytes in,
+// 16 out: whole sectors), a block of 128 eight lanes, 512 elements a warp and task,
+// UNROLL tasks in flight.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "mx_grouped.h"
+#include "mx_layout.cuh"
+#include "mx_ptx.cuh"
+#include "mx_quant.cuh"
+
+namespace mx {
+
+namespace {
+
+constexpr int THREADS = 256;
+constexpr int UNROLL = 4;
+constexpr int TASK = 512;  // elements of a row per warp and task
+
+// 448 / amax, and what x is multiplied by before it (a power of two: 1 but for an
+// amax so small that the quotient would overflow).
+__device__ __forceinline__ float b128_inverse(float amax, float* pre) {
+  *pre = amax < 0x1p-110f ? 0x1p100f : 1.f;
+  return amax > 0.f ? __fdiv_rn(448.f, amax * *pre) : 0.f;
+}
+
+// x * inv to 17 significant bits (see above); for values that are not of 16 bits
+// this moves a quotient by 2^-17, an E4M3 tie's neighbourhood of 2^-13 of a step.
+__device__ __forceinline__ float b128_quotient(float x, float inv) {
+  return __uint_as_float((__float_as_uint(x * inv) + 0x40u) & 0xFFFFFF80u);
+}
+
+struct Codes {
+  uint32_t w[4];
+};
+
+// Sixteen bf16 of a lane, eight lanes a block of 128 (absent elements are zero):
+// the codes, and the block's scale in each of the eight lanes.
+__device__ __forceinline__ Codes quantize16_b128(const uint32_t (&v)[8], float* scale) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = __vmaxu2(m, v[i] & 0x7FFF7FFFu);
+  m = max(m & 0xFFFFu, m >> 16);
+#pragma unroll
+  for (int d = 1; d < 8; d <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+  const bool nonfinite = m >= 0x7F80u;
+  const float amax = __uint_as_float(m << 16);
+  float pre;
+  const float inv = b128_inverse(amax, &pre);
+  *scale = nonfinite ? __uint_as_float(0x7FC00000u) : __fdiv_rn(amax, 448.f);
+  Codes c;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float f[4];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      f[2 * j] = __uint_as_float(v[2 * i + j] << 16);
+      f[2 * j + 1] = __uint_as_float(v[2 * i + j] & 0xFFFF0000u);
+    }
+    if (pre != 1.f) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f[j] *= pre;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f[j] = b128_quotient(f[j], inv);
+    c.w[i] = nonfinite ? 0x7F7F7F7Fu : cvt_e4m3x2(f[0], f[1]) | (cvt_e4m3x2(f[2], f[3]) << 16);
+  }
+  return c;
+}
+
+// The same of fp32 values (an activation's): no quotient here is close to a tie by
+// construction, and none is snapped to one.
+__device__ __forceinline__ Codes quantize16_b128(const float (&y)[16], float* scale) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(y[i]) & 0x7FFFFFFFu);
+#pragma unroll
+  for (int d = 1; d < 8; d <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+  const bool nonfinite = m >= 0x7F800000u;
+  const float amax = __uint_as_float(m);
+  float pre;
+  const float inv = b128_inverse(amax, &pre);
+  *scale = nonfinite ? __uint_as_float(0x7FC00000u) : __fdiv_rn(amax, 448.f);
+  Codes c;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t a = cvt_e4m3x2(y[4 * i] * pre * inv, y[4 * i + 1] * pre * inv);
+    const uint32_t b = cvt_e4m3x2(y[4 * i + 2] * pre * inv, y[4 * i + 3] * pre * inv);
+    c.w[i] = nonfinite ? 0x7F7F7F7Fu : a | (b << 16);
+  }
+  return c;
+}
+
+// Sixteen bf16 of a lane, two lanes an MXFP8 block: the codes, and in the eight
+// lanes of 128 elements the word of their four scale bytes.
+__device__ __forceinline__ Codes quantize16_mx(const uint32_t (&v)[8], int lane, uint32_t* word) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = __vmaxu2(m, v[i] & 0x7FFF7FFFu);
+  m = max(m & 0xFFFFu, m >> 16);
+  m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+  const bool nonfinite = m >= 0x7F80u;
+  const uint32_t E = m >> 7;
+  const uint32_t sbyte = nonfinite ? 0xFFu : (E > 8u ? E - 8u : 0u);
+  const float mul = __uint_as_float((254u - (nonfinite ? 0u : sbyte)) << 23);
+  uint32_t w = sbyte << (8 * ((lane >> 1) & 3));
+  w |= __shfl_xor_sync(0xFFFFFFFFu, w, 2);
+  w |= __shfl_xor_sync(0xFFFFFFFFu, w, 4);
+  *word = w;
+  Codes c;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t a = cvt_e4m3x2(__uint_as_float(v[2 * i] << 16) * mul, __uint_as_float(v[2 * i] & 0xFFFF0000u) * mul);
+    const uint32_t b =
+        cvt_e4m3x2(__uint_as_float(v[2 * i + 1] << 16) * mul, __uint_as_float(v[2 * i + 1] & 0xFFFF0000u) * mul);
+    c.w[i] = nonfinite ? 0x7F7F7F7Fu : a | (b << 16);
+  }
+  return c;
+}
+
+// 16 bf16 at a 16-byte (wide: 32-byte) aligned address.
+__device__ __forceinline__ void load16(const __nv_bfloat16* p, bool wide, uint32_t (&v)[8]) {
+  if (wide) {
+    ld_global_32(p, v);
+  } else {
+    const uint4 a = reinterpret_cast<const uint4*>(p)[0], b = reinterpret_cast<const uint4*>(p)[1];
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  }
+}
+
+struct RowsArgs {
+  const __nv_bfloat16* x;
+  const int* rows;
+  int64_t T, K;
+  int64_t tasks;  // R * segs
+  int segs;       // tasks a row
+  bool wide;
+  uint8_t* q;
+  uint32_t* s;
+  int64_t s_row, s_kt;
+};
+
+// K % 16 == 0; MXFP8 K % 128 == 0.
+template <int FMT, bool kEarly>
+__global__ void __launch_bounds__(THREADS) quantize_rows_kernel(const RowsArgs a) {
+  if (kEarly) {
+    launch_dependents();
+    grid_dependency_wait();
+  }
+  const int lane = threadIdx.x & 31;
+  const int64_t first = (static_cast<int64_t>(blockIdx.x) * (THREADS / 32) + (threadIdx.x >> 5)) * UNROLL;
+  uint32_t v[UNROLL][8];
+  int64_t row[UNROLL];
+  int k[UNROLL];
+#pragma unroll
+  for (int i = 0; i < UNROLL; ++i) {
+    const int64_t task = first + i;
+    row[i] = task / a.segs;
+    k[i] = static_cast<int>(task - row[i] * a.segs) * TASK + lane * 16;
+    int64_t src = row[i];
+    if (a.rows != nullptr) src = task < a.tasks ? a.rows[row[i]] : -1;
+    if (task < a.tasks && k[i] < a.K && src >= 0 && src < a.T) {
+      load16(a.x + src * a.K + k[i], a.wide, v[i]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] = 0;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < UNROLL; ++i) {
+    if (first + i >= a.tasks) return;  // the whole warp
+    uint32_t word;
+    Codes c;
+    if (FMT == kG8MX) {
+      c = quantize16_mx(v[i], lane, &word);
+    } else {
+      float s;
+      c = quantize16_b128(v[i], &s);
+      word = __float_as_uint(s);
+    }
+    if (k[i] < a.K) {
+      *reinterpret_cast<uint4*>(a.q + row[i] * a.K + k[i]) = make_uint4(c.w[0], c.w[1], c.w[2], c.w[3]);
+      if ((lane & 7) == 0) a.s[row[i] * a.s_row + (k[i] >> 7) * a.s_kt] = word;
+    }
+  }
+}
+
+struct ActArgs {
+  const __nv_bfloat16* gate;
+  const __nv_bfloat16* up;
+  int64_t gate_stride, up_stride, K;
+  int64_t tasks;
+  int segs;
+  bool wide;
+  uint8_t* q;
+  uint32_t* s;
+  int64_t s_row, s_kt;
+};
+
+// y = gate / (1 + exp(-gate)) * up, quantised to fp8_128: the values of
+// silu_mul_kernel (fused_quant.cu).
+template <bool kEarly>
+__global__ void __launch_bounds__(THREADS) silu_mul_rows_kernel(const ActArgs a) {
+  if (kEarly) launch_dependents();
+  const int lane = threadIdx.x & 31;
+  constexpr int U = UNROLL / 2;
+  const int64_t first = (static_cast<int64_t>(blockIdx.x) * (THREADS / 32) + (threadIdx.x >> 5)) * U;
+  grid_dependency_wait();
+  uint32_t g[U][8], u[U][8];
+  int64_t row[U];
+  int k[U];
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    const int64_t task = first + i;
+    row[i] = task / a.segs;
+    k[i] = static_cast<int>(task - row[i] * a.segs) * TASK + lane * 16;
+    if (task < a.tasks && k[i] < a.K) {
+      load16(a.gate + row[i] * a.gate_stride + k[i], a.wide, g[i]);
+      load16(a.up + row[i] * a.up_stride + k[i], a.wide, u[i]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) g[i][j] = u[i][j] = 0;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    if (first + i >= a.tasks) return;
+    float y[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const float gt = __uint_as_float(j & 1 ? g[i][j >> 1] & 0xFFFF0000u : g[i][j >> 1] << 16);
+      const float up = __uint_as_float(j & 1 ? u[i][j >> 1] & 0xFFFF0000u : u[i][j >> 1] << 16);
+      const float e = __expf(-fabsf(gt));
+      y[j] = gt * __fdividef(gt >= 0.f ? 1.f : e, 1.f + e) * up;
+    }
+    float s;
+    const Codes c = quantize16_b128(y, &s);
+    if (k[i] < a.K) {
+      *reinterpret_cast<uint4*>(a.q + row[i] * a.K + k[i]) = make_uint4(c.w[0], c.w[1], c.w[2], c.w[3]);
+      if ((lane & 7) == 0) a.s[row[i] * a.s_row + (k[i] >> 7) * a.s_kt] = __float_as_uint(s);
+    }
+  }
+}
+
+// One CTA per 128 x 128 block: row i of the block in lanes 8 (i % 4).. of warp i / 4 % 8.
+__global__ void __launch_bounds__(THREADS) quantize_weights_b128_kernel(const __nv_bfloat16* __restrict__ w, int64_t N,
+                                                                        int64_t K, int NB, int KT, uint8_t* __restrict__ q,
+                                                                        float* __restrict__ s) {
+  __shared__ uint32_t top[THREADS / 32];
+  const int64_t blk = blockIdx.x;
+  const int kt = static_cast<int>(blk % KT);
+  const int nb = static_cast<int>(blk / KT % NB);
+  const int64_t b = blk / KT / NB;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t k = static_cast<int64_t>(kt) * 128 + (lane & 7) * 16;
+  uint32_t v[4][8], m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t n = static_cast<int64_t>(nb) * 128 + i * 32 + warp * 4 + (lane >> 3);
+    const bool in = n < N && k < K;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[i][j] = 0;
+    if (in) load16(w + (b * N + n) * K + k, false, v[i]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = __vmaxu2(m, v[i][j] & 0x7FFF7FFFu);
+  }
+  m = max(m & 0xFFFFu, m >> 16);
+  m = __reduce_max_sync(0xFFFFFFFFu, m);
+  if (lane == 0) top[warp] = m;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < THREADS / 32; ++i) m = max(m, top[i]);
+  const bool nonfinite = m >= 0x7F80u;
+  const float amax = __uint_as_float(m << 16);
+  float pre;
+  const float inv = b128_inverse(amax, &pre);
+  if (threadIdx.x == 0) s[blk] = nonfinite ? __uint_as_float(0x7FC00000u) : __fdiv_rn(amax, 448.f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t n = static_cast<int64_t>(nb) * 128 + i * 32 + warp * 4 + (lane >> 3);
+    if (n >= N || k >= K) continue;
+    uint32_t c[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t o = 0;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t x = v[i][2 * j + h];
+        o |= cvt_e4m3x2(b128_quotient(__uint_as_float(x << 16) * pre, inv),
+                        b128_quotient(__uint_as_float(x & 0xFFFF0000u) * pre, inv))
+             << (16 * h);
+      }
+      c[j] = nonfinite ? 0x7F7F7F7Fu : o;
+    }
+    *reinterpret_cast<uint4*>(q + (b * N + n) * K + k) = make_uint4(c[0], c[1], c[2], c[3]);
+  }
+}
+
+cudaError_t launch(const void* fn, int64_t blocks, void** args, bool programmatic, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
+  cfg.blockDim = dim3(THREADS, 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = programmatic ? 1 : 0;
+  return cudaLaunchKernelExC(&cfg, fn, args);
+}
+
+inline bool is32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31) == 0; }
+
+}  // namespace
+
+cudaError_t launch_quantize_rows(const QuantRowsProblem& p, cudaStream_t stream) {
+  RowsArgs a;
+  a.x = static_cast<const __nv_bfloat16*>(p.x);
+  a.rows = p.rows;
+  a.T = p.T;
+  a.K = p.K;
+  a.segs = static_cast<int>(ceil_div(p.K, TASK));
+  a.tasks = p.R * a.segs;
+  a.wide = is32(p.x);  // K % 16 == 0: every row then is
+  a.q = p.q;
+  a.s = static_cast<uint32_t*>(p.s);
+  a.s_row = p.s_row;
+  a.s_kt = p.s_kt;
+  const void* fn = p.fmt == kG8MX ? (p.early ? reinterpret_cast<const void*>(quantize_rows_kernel<kG8MX, true>)
+                                             : reinterpret_cast<const void*>(quantize_rows_kernel<kG8MX, false>))
+                                  : (p.early ? reinterpret_cast<const void*>(quantize_rows_kernel<kG8B128, true>)
+                                             : reinterpret_cast<const void*>(quantize_rows_kernel<kG8B128, false>));
+  void* args[] = {&a};
+  return launch(fn, ceil_div(a.tasks, UNROLL * (THREADS / 32)), args, p.early, stream);
+}
+
+cudaError_t launch_silu_mul_rows(const ActRowsProblem& p, cudaStream_t stream) {
+  ActArgs a;
+  a.gate = static_cast<const __nv_bfloat16*>(p.gate);
+  a.up = static_cast<const __nv_bfloat16*>(p.up);
+  a.gate_stride = p.gate_stride;
+  a.up_stride = p.up_stride;
+  a.K = p.K;
+  a.segs = static_cast<int>(ceil_div(p.K, TASK));
+  a.tasks = p.M * a.segs;
+  a.wide = is32(p.gate) && is32(p.up) && p.gate_stride % 16 == 0 && p.up_stride % 16 == 0;
+  a.q = p.q;
+  a.s = static_cast<uint32_t*>(p.s);
+  a.s_row = p.s_row;
+  a.s_kt = p.s_kt;
+  const void* fn = p.early ? reinterpret_cast<const void*>(silu_mul_rows_kernel<true>)
+                           : reinterpret_cast<const void*>(silu_mul_rows_kernel<false>);
+  void* args[] = {&a};
+  return launch(fn, ceil_div(a.tasks, UNROLL / 2 * (THREADS / 32)), args, true, stream);
+}
+
+cudaError_t launch_quantize_weights_b128(const void* w, int64_t B, int64_t N, int64_t K, uint8_t* q, float* s,
+                                         cudaStream_t stream) {
+  const int NB = static_cast<int>(ceil_div(N, 128)), KT = static_cast<int>(ceil_div(K, 128));
+  quantize_weights_b128_kernel<<<static_cast<unsigned>(B * NB * KT), THREADS, 0, stream>>>(
+      static_cast<const __nv_bfloat16*>(w), N, K, NB, KT, q, s);
+  return cudaGetLastError();
+}
+
+}  // namespace mx

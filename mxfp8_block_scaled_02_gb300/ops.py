@@ -79,6 +79,21 @@ SIGNATURES = {
     "mxfp8_gated_mlp_workspace_size": (_INT, [_INT, _I64, _I64, _I64, _SIZE_P]),
     "mxfp8_gated_mlp": (_INT, [_INT, _P, _I64, _P, _I64, _INT, _P, _P, ctypes.c_float, _I64, _I64, _I64, _P, _P, _P,
                                _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "mxfp8_b128_quantize": (_INT, [_P, _I64, _I64, _P, _P, _P]),
+    "mxfp8_b128_quantize_weights": (_INT, [_P, _I64, _I64, _I64, _P, _P, _P]),
+    "mxfp8_b128_silu_mul_quantize": (_INT, [_P, _I64, _P, _I64, _I64, _I64, _P, _P, _P]),
+    "mxfp8_b128_workspace_size": (_INT, [_I64, _I64, _I64, _I64, _INT, _SIZE_P]),
+    "mxfp8_b128_linear": (_INT, [_P, _P, _P, _I64, _I64, _I64, _I64, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "mxfp8_grouped_workspace_size": (_INT, [_INT, _I64, _I64, _I64, _I64, _INT, _SIZE_P]),
+    "mxfp8_grouped_linear": (_INT, [_INT, _P, _I64, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _P, _P, _P, _P, _P,
+                                    ctypes.c_size_t, _P]),
+    "mxfp8_route_workspace_size": (_INT, [_I64, _I64, _I64, _SIZE_P]),
+    "mxfp8_route": (_INT, [_P, _I64, _INT, _I64, _I64, _I64, _INT, _INT, ctypes.c_float, _P, _P, _P, _P, _P, _P,
+                           ctypes.c_size_t, _P]),
+    "mxfp8_combine": (_INT, [_P, _I64, _P, _P, _I64, _I64, _I64, _P, _I64, _P, _P]),
+    "mxfp8_expert_mlp_workspace_size": (_INT, [_INT, _I64, _I64, _I64, _I64, _I64, _SIZE_P]),
+    "mxfp8_expert_mlp": (_INT, [_INT, _P, _I64, _I64, _P, _I64, _INT, _I64, _I64, _INT, _INT, ctypes.c_float, _I64, _P,
+                                _P, _P, _P, _P, _I64, _P, _P, ctypes.c_size_t, _P]),
     "mxfp8_check": (_INT, [_P]),
     "mxfp8_debug_expire_wait": (_INT, [_U64, _P]),
 }
@@ -92,6 +107,10 @@ WFMT = {"e4m3": 0, "e2m3": 1, "e3m2": 2}
 # 4-bit ones are also weight formats of linear_fp4
 QFMT = {"mxfp8": 0, "mxfp4": 1, "nvfp4": 2}
 QBLOCK = {"mxfp8": 32, "mxfp4": 32, "nvfp4": 16}
+
+# formats of the grouped calls (MXFP8_GFMT_*), by PackedWeights.fmt, and the scorings of route
+GFMT = {"e4m3": 0, "fp8_128": 1}
+SCORING = {"softmax": 0, "sigmoid": 1}
 
 
 class MxStatusError(RuntimeError):
@@ -203,7 +222,7 @@ class PackedWeights:
     N: int
     K: int
     batched: bool
-    fmt: str = "e4m3"        # weight element format: "e4m3", "e2m3", "e3m2", or "mxfp4" / "nvfp4"
+    fmt: str = "e4m3"        # weight element format: "e4m3", "e2m3", "e3m2", "mxfp4" / "nvfp4", or "fp8_128"
     tensor_scale: torch.Tensor | None = None  # NVFP4: fp32, one element
 
 
@@ -241,7 +260,8 @@ def process_weights(w_q: torch.Tensor, w_scale: torch.Tensor, fmt: str = "e4m3")
 
 def _not_fp4(pw: PackedWeights, what: str) -> None:
     if pw.fmt not in WFMT:
-        raise ValueError(f"{what} does not take {pw.fmt} weights; use linear_fp4 / gemm_packed_fp4")
+        raise ValueError(f"{what} does not take {pw.fmt} weights; use "
+                         + ("linear_fp8_128 / grouped_linear" if pw.fmt == "fp8_128" else "linear_fp4 / gemm_packed_fp4"))
 
 
 def save_packed(pw: PackedWeights) -> bytes:
@@ -365,7 +385,7 @@ def _mxfp8_only(pa: PackedActivation, what: str) -> None:
 def _e4m3_only(pw: PackedWeights, what: str) -> None:
     if pw.fmt != "e4m3":
         raise ValueError(f"{what} takes E4M3 weights only (these are {pw.fmt}); use "
-                         f"{'linear' if pw.fmt in WFMT else 'linear_fp4'}")
+                         f"{'linear' if pw.fmt in WFMT else 'linear_fp8_128' if pw.fmt == 'fp8_128' else 'linear_fp4'}")
 
 
 @dataclasses.dataclass
@@ -766,7 +786,7 @@ def gemm_packed_fp4(pa: PackedActivation, pw: PackedWeights, bias: torch.Tensor 
 
 
 # ------------------------------------------------------------------ steps that feed a quantised layer
-def _rows2d(x: torch.Tensor, name: str) -> tuple[torch.Tensor, int, int]:
+def _rows2d(x: torch.Tensor, name: str, block: int = BLOCK) -> tuple[torch.Tensor, int, int]:
     """x [..., K] as rows: (tensor, row count, row stride in elements).  A view
     whose rows are evenly spaced (a slice of a wider tensor) is taken as it is
     when its rows start on 16-byte boundaries; anything else is copied."""
@@ -774,8 +794,8 @@ def _rows2d(x: torch.Tensor, name: str) -> tuple[torch.Tensor, int, int]:
         raise ValueError("tensors must be on a CUDA device")
     shape = x.shape
     K = shape[-1] if shape else 0
-    if K == 0 or K % BLOCK:
-        raise ValueError(f"{name} must be [..., K] with K a multiple of {BLOCK}, not {tuple(shape)}")
+    if K == 0 or K % block:
+        raise ValueError(f"{name} must be [..., K] with K a multiple of {block}, not {tuple(shape)}")
     rows = x.numel() // K
     if x.is_contiguous():
         return (x if x.data_ptr() % 16 == 0 else _aligned16(x)), rows, K
@@ -872,7 +892,10 @@ def silu_mul_quantize(gate_up: torch.Tensor, up: torch.Tensor | None = None, *, 
 
     ``gate_up`` bf16 [..., 2 K] holds gate then up along the last axis (a merged
     projection's output); or pass gate [..., K] and ``up`` [..., K].  Returns
-    the quantised result as rmsnorm_quantize does."""
+    the quantised result as rmsnorm_quantize does; ``fmt`` "fp8_128" too, as
+    quantize_fp8_128 returns it (not packed)."""
+    if fmt == "fp8_128":
+        return _silu_mul_fp8_128(gate_up, up, tensor_scale, packed)
     f = _qfmt(fmt)
     if gate_up.dtype is not _BF16 or (up is not None and up.dtype is not _BF16):
         raise TypeError("gate and up must be bfloat16")
@@ -949,6 +972,372 @@ def gated_mlp(x: torch.Tensor, norm_weight: torch.Tensor, gate_up: PackedWeights
                                   _ptr(down.tensor_scale), _ptr(x_tensor_scale), _ptr(h_tensor_scale), out.data_ptr(),
                                   ws_ptr, ws_bytes, _stream()))
     return out, t
+
+
+# ------------------------------------------------------------------ block-128 FP8, grouped products, expert routing
+def _here(*ts: torch.Tensor | None) -> None:
+    """Contiguous tensors on the current CUDA device (whose stream the call goes to)."""
+    for t in ts:
+        if t is not None and not (t.is_cuda and t.is_contiguous() and t.get_device() == torch._C._cuda_getDevice()):
+            _require_cuda(t)
+            raise ValueError(f"tensor on cuda:{t.get_device()}, the current device is cuda:{torch._C._cuda_getDevice()}")
+
+
+def _k_blocks(K: int) -> int:
+    return (K + 127) // 128
+
+
+def quantize_fp8_128(x: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor]:
+    """bf16 x [..., K] (K % 16 == 0) -> (x_q uint8 E4M3 [..., K], x_scale fp32
+    [..., ceil(K/128)]): scale = amax / 448 of each 128 elements along K, code =
+    E4M3(448 x / amax), to nearest even of the exact quotient."""
+    if x.dtype is not _BF16:
+        raise TypeError("x must be bfloat16")
+    _here(x)
+    if x.dim() < 1:
+        raise ValueError("x must have a K dimension")
+    x = _aligned16(x)
+    shape, K = x.shape, x.shape[-1]
+    q = torch.empty(shape, dtype=_U8, device=x.device)
+    s = torch.empty(shape[:-1] + (_k_blocks(K),), dtype=_F32, device=x.device)
+    _check(load().mxfp8_b128_quantize(x.data_ptr(), _rows_of(x, K), K, q.data_ptr(), s.data_ptr(), _stream()))
+    return q, s
+
+
+def quantize_weights_fp8_128(w: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor]:
+    """bf16 weights [N, K] or [B, N, K] -> (codes uint8 of the same shape, fp32
+    scales [..., ceil(N/128), ceil(K/128)]), by quantize_fp8_128's rule on blocks
+    of 128 x 128."""
+    if w.dtype is not _BF16:
+        raise TypeError("w must be bfloat16")
+    if w.dim() not in (2, 3):
+        raise ValueError("w must be [N, K] or [B, N, K]")
+    _here(w)
+    w = _aligned16(w)
+    N, K = w.shape[-2:]
+    B = w.shape[0] if w.dim() == 3 else 1
+    q = torch.empty(w.shape, dtype=_U8, device=w.device)
+    s = torch.empty(w.shape[:-2] + (_k_blocks(N), _k_blocks(K)), dtype=_F32, device=w.device)
+    _check(load().mxfp8_b128_quantize_weights(w.data_ptr(), B, N, K, q.data_ptr(), s.data_ptr(), _stream()))
+    return q, s
+
+
+def process_weights_fp8_128(w_q: torch.Tensor, w_scale: torch.Tensor) -> PackedWeights:
+    """E4M3 weights [N, K] or [B, N, K] (uint8 or float8_e4m3fn) with fp32 scales
+    [..., ceil(N/128), ceil(K/128)], as a block-scaled checkpoint holds them.  The
+    kernels read them as they are: dense, aligned tensors are kept, not copied."""
+    if w_q.dim() not in (2, 3):
+        raise ValueError("w_q must be [N, K] or [B, N, K]")
+    if w_q.dtype not in (_U8, _E4M3) or w_scale.dtype is not _F32:
+        raise TypeError("w_q must be uint8 or float8_e4m3fn, w_scale float32")
+    batched = w_q.dim() == 3
+    B = w_q.shape[0] if batched else 1
+    N, K = w_q.shape[-2:]
+    if K % 16 or N % 8:
+        raise ValueError(f"K={K} must be a multiple of 16 and N={N} of 8")
+    if w_scale.shape != w_q.shape[:-2] + (_k_blocks(N), _k_blocks(K)):
+        raise ValueError(f"weight scale {tuple(w_scale.shape)} does not match weight {tuple(w_q.shape)}")
+    w_q, w_scale = w_q.contiguous(), w_scale.contiguous()
+    _here(w_q, w_scale)
+    return PackedWeights(_bytes(_aligned16(w_q)), _bytes(_aligned16(w_scale)), B, N, K, batched, "fp8_128")
+
+
+@functools.lru_cache(maxsize=4096)
+def workspace_size_fp8_128(B: int, M: int, N: int, K: int, quantized: bool) -> int:
+    n = ctypes.c_size_t()
+    _check(load().mxfp8_b128_workspace_size(B, M, N, K, int(quantized), ctypes.byref(n)))
+    return n.value
+
+
+def _quantised_x(x: torch.Tensor, x_scale: torch.Tensor, fmt: str, K: int) -> tuple[torch.Tensor, torch.Tensor]:
+    """Codes and row-major scales of a quantised x, checked and aligned."""
+    _here(x_scale)
+    if x.dtype not in (_U8, _E4M3):
+        raise TypeError("a pre-quantised x must be uint8 or float8_e4m3fn E4M3 codes")
+    if fmt == "fp8_128":
+        if x_scale.dtype is not _F32 or x_scale.shape != x.shape[:-1] + (_k_blocks(K),):
+            raise ValueError(f"fp8_128 activation scale {x_scale.dtype} {tuple(x_scale.shape)} for codes {tuple(x.shape)}")
+    elif x_scale.element_size() != 1 or x_scale.shape != x.shape[:-1] + (K // BLOCK,):
+        raise ValueError(f"MXFP8 activation scale {tuple(x_scale.shape)} for codes {tuple(x.shape)}")
+    return _aligned16(x), _aligned16(x_scale)
+
+
+def linear_fp8_128(x: torch.Tensor, pw: PackedWeights, bias: torch.Tensor | None = None,
+                   x_scale: torch.Tensor | None = None, *, out: torch.Tensor | None = None,
+                   workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """FP8 linear layer with fp32 scales per block of 128 (weights from
+    process_weights_fp8_128).  ``x`` is bf16 [..., K] (quantised inside the call
+    as quantize_fp8_128 does), or with ``x_scale`` its codes and scales.  For
+    batched weights x is [B, M, K].  Returns bf16 [..., N]."""
+    if pw.fmt != "fp8_128":
+        raise ValueError(f"linear_fp8_128 does not take {pw.fmt} weights")
+    K, N, B = pw.K, pw.N, pw.B
+    quantized = x_scale is not None
+    if not quantized and x.dtype is not _BF16:
+        raise TypeError("x must be bfloat16 (or pass x_scale with a pre-quantised x)")
+    _here(x, bias, out, workspace)
+    shape = x.shape
+    if not shape or shape[-1] != K:
+        raise ValueError(f"x {tuple(shape)} does not match weights with K={K}")
+    if pw.batched and (len(shape) != 3 or shape[0] != B):
+        raise ValueError("batched weights need x of shape [B, M, K]")
+    if bias is not None and (bias.dtype is not _BF16 or tuple(bias.shape) != (N,)):
+        raise ValueError("bias must be bf16 [N]")
+    rows = x.numel() // K
+    if quantized:
+        x, x_scale = _quantised_x(x, x_scale, "fp8_128", K)
+    elif x.data_ptr() & 15:
+        x = _aligned16(x)
+    if out is None:
+        out = torch.empty(shape[:-1] + (N,), dtype=_BF16, device=x.device)
+    elif out.dtype is not _BF16 or out.numel() != rows * N or out.data_ptr() & 15:
+        raise ValueError(f"out must be bf16 with {rows * N} elements, 16-byte aligned")
+    if rows == 0:
+        return out
+    M = rows // B
+    bias = _aligned16(bias)
+    ws_ptr, ws_bytes, workspace = _workspace(workspace, workspace_size_fp8_128(B, M, N, K, quantized), x.device)
+    x_ptr = x.data_ptr()
+    _check(load().mxfp8_b128_linear(None if quantized else x_ptr, x_ptr if quantized else None, _ptr(x_scale), B, M, N, K,
+                                    pw.w_packed.data_ptr(), pw.sf_packed.data_ptr(), _ptr(bias), out.data_ptr(), ws_ptr,
+                                    ws_bytes, _stream()))
+    return out
+
+
+def _silu_mul_fp8_128(gate_up: torch.Tensor, up: torch.Tensor | None, tensor_scale, packed: bool):
+    if tensor_scale is not None:
+        raise ValueError("a tensor scale belongs to nvfp4, not fp8_128")
+    if packed:
+        raise ValueError("fp8_128 scales are row-major; there is no packed form")
+    if gate_up.dtype is not _BF16 or (up is not None and up.dtype is not _BF16):
+        raise TypeError("gate and up must be bfloat16")
+    if up is None:
+        if gate_up.dim() < 1 or gate_up.shape[-1] % 32:
+            raise ValueError(f"gate_up must be [..., 2 K] with K a multiple of 16, not {tuple(gate_up.shape)}")
+        K = gate_up.shape[-1] // 2
+        g, rows, g_stride = _rows2d(gate_up, "gate_up")
+        g_ptr, u_ptr, u_stride = g.data_ptr(), g.data_ptr() + 2 * K, g_stride
+    else:
+        if up.shape != gate_up.shape:
+            raise ValueError("gate and up must have the same shape")
+        g, rows, g_stride = _rows2d(gate_up, "gate", 16)
+        u, _, u_stride = _rows2d(up, "up", 16)
+        K = gate_up.shape[-1]
+        g_ptr, u_ptr = g.data_ptr(), u.data_ptr()
+    lead = gate_up.shape[:-1]
+    q = torch.empty(lead + (K,), dtype=_U8, device=gate_up.device)
+    s = torch.empty(lead + (_k_blocks(K),), dtype=_F32, device=gate_up.device)
+    _check(load().mxfp8_b128_silu_mul_quantize(g_ptr, g_stride, u_ptr, u_stride, rows, K, q.data_ptr(), s.data_ptr(),
+                                               _stream()))
+    return q, s
+
+
+@functools.lru_cache(maxsize=4096)
+def grouped_workspace_size(fmt: str, E: int, R: int, N: int, K: int, quantized: bool) -> int:
+    n = ctypes.c_size_t()
+    _check(load().mxfp8_grouped_workspace_size(GFMT[fmt], E, R, N, K, int(quantized), ctypes.byref(n)))
+    return n.value
+
+
+def _expert_weights(pw: PackedWeights, what: str) -> int:
+    if pw.fmt not in GFMT:
+        raise ValueError(f"{what} takes e4m3 (MXFP8) or fp8_128 weights, not {pw.fmt}")
+    if not pw.batched:
+        raise ValueError(f"{what} takes weights [E, N, K], one matrix an expert")
+    return GFMT[pw.fmt]
+
+
+def _int32(t: torch.Tensor, shape: tuple, name: str) -> int:
+    if t.dtype is not torch.int32 or tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be int32 {list(shape)}, not {t.dtype} {list(t.shape)}")
+    return t.data_ptr()
+
+
+def grouped_linear(x: torch.Tensor, pw: PackedWeights, offsets: torch.Tensor, x_scale: torch.Tensor | None = None, *,
+                   bias: torch.Tensor | None = None, rows: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                   workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Rows sorted by expert, each times its expert's weights: row r of the bf16
+    result [R, N], offsets[e] <= r < offsets[e + 1], is x_r @ w[e].T + bias[e].
+
+    ``pw``: weights [E, N, K] from process_weights (MXFP8) or
+    process_weights_fp8_128.  ``x`` is bf16 [R, K] (quantised inside the call to
+    the weights' format), or with ``x_scale`` its codes; or with ``rows`` (int32
+    [R]) bf16 [T, K], and x_r = x[rows[r]] (a row of zeros for an index outside
+    [0, T)).  ``offsets`` int32 [E + 1] stays on the device.  Rows that belong to
+    no expert are left as they were in ``out``, and undefined in a new tensor."""
+    f = _expert_weights(pw, "grouped_linear")
+    E, N, K = pw.B, pw.N, pw.K
+    quantized = x_scale is not None
+    if not quantized and x.dtype is not _BF16:
+        raise TypeError("x must be bfloat16 (or pass x_scale with a pre-quantised x)")
+    if quantized and rows is not None:
+        raise ValueError("rows go with bf16 x")
+    _here(x, offsets, bias, rows, out, workspace)
+    if x.dim() != 2 or x.shape[1] != K:
+        raise ValueError(f"x {tuple(x.shape)} is not [rows, {K}]")
+    o_ptr = _int32(offsets, (E + 1,), "offsets")
+    T = R = x.shape[0]
+    r_ptr = None
+    if rows is not None:
+        R = rows.numel()
+        r_ptr = _int32(rows, (R,), "rows")
+    if bias is not None and (bias.dtype is not _BF16 or tuple(bias.shape) != (E, N)):
+        raise ValueError(f"bias must be bf16 [{E}, {N}]")
+    if quantized:
+        x, x_scale = _quantised_x(x, x_scale, pw.fmt, K)
+    elif x.data_ptr() & 15:
+        x = _aligned16(x)
+    if out is None:
+        out = torch.empty((R, N), dtype=_BF16, device=x.device)
+    elif out.dtype is not _BF16 or tuple(out.shape) != (R, N) or out.data_ptr() & 15:
+        raise ValueError(f"out must be bf16 [{R}, {N}], 16-byte aligned")
+    if R == 0:
+        return out
+    bias = _aligned16(bias)
+    ws_ptr, ws_bytes, workspace = _workspace(workspace, grouped_workspace_size(pw.fmt, E, R, N, K, quantized), x.device)
+    x_ptr = x.data_ptr()
+    if not x_ptr:  # no token at all: every row is one of zeros
+        x_ptr, T = ws_ptr, 0
+    _check(load().mxfp8_grouped_linear(f, None if quantized else x_ptr, T, r_ptr, x_ptr if quantized else None,
+                                       _ptr(x_scale), o_ptr, E, R, N, K, pw.w_packed.data_ptr(), pw.sf_packed.data_ptr(),
+                                       _ptr(bias), out.data_ptr(), ws_ptr, ws_bytes, _stream()))
+    return out
+
+
+@dataclasses.dataclass
+class Routing:
+    """Which experts T tokens go to (route)."""
+
+    ids: torch.Tensor        # int32 [T, k], by descending logit; -1 where none was left
+    weights: torch.Tensor    # fp32 [T, k]; 0 there
+    offsets: torch.Tensor    # int32 [E + 1]: expert e has the rows [offsets[e], offsets[e + 1])
+    rows: torch.Tensor       # int32 [T k]: the token of each row; -1 behind the last
+    positions: torch.Tensor  # int32 [T, k]: the row of each slot; -1 where none was left
+
+
+def _scoring(scoring: str) -> int:
+    if scoring not in SCORING:
+        raise ValueError(f"scoring must be one of {sorted(SCORING)}, not {scoring!r}")
+    return SCORING[scoring]
+
+
+@functools.lru_cache(maxsize=4096)
+def route_workspace_size(T: int, E: int, k: int) -> int:
+    n = ctypes.c_size_t()
+    _check(load().mxfp8_route_workspace_size(T, E, k, ctypes.byref(n)))
+    return n.value
+
+
+def _logits2d(logits: torch.Tensor) -> tuple[torch.Tensor, int]:
+    """logits [T, E] fp32 or bf16, rows of any stride: (tensor, row stride)."""
+    if not logits.is_cuda or logits.get_device() != torch._C._cuda_getDevice():
+        raise ValueError("tensors must be on the current CUDA device")
+    if logits.dim() != 2 or logits.dtype not in (_F32, _BF16):
+        raise ValueError(f"logits must be fp32 or bf16 [tokens, experts], not {logits.dtype} {tuple(logits.shape)}")
+    if logits.shape[1] > 1 and logits.stride(1) != 1 or (logits.shape[0] > 1 and 0 < logits.stride(0) < logits.shape[1]):
+        logits = logits.contiguous()
+    return logits, logits.stride(0)
+
+
+def route(logits: torch.Tensor, k: int, *, scoring: str = "softmax", renormalize: bool = False, scale: float = 1.0,
+          workspace: torch.Tensor | None = None) -> Routing:
+    """The k experts of each token and the rows sorted by expert, within an expert
+    by token.  ``logits`` fp32 or bf16 [T, E]: the k largest, ties to the lowest
+    expert; -inf and NaN are never chosen.  Weights: softmax over all E or sigmoid
+    of the logits, divided by the token's sum with ``renormalize``, times
+    ``scale``."""
+    sc = _scoring(scoring)
+    logits, stride = _logits2d(logits)
+    _here(workspace)
+    T, E = logits.shape
+    dev = logits.device
+    need = route_workspace_size(T, E, k)  # checks T, E and k
+    r = Routing(torch.empty((T, k), dtype=torch.int32, device=dev), torch.empty((T, k), dtype=_F32, device=dev),
+                torch.empty(E + 1, dtype=torch.int32, device=dev), torch.empty(T * k, dtype=torch.int32, device=dev),
+                torch.empty((T, k), dtype=torch.int32, device=dev))
+    ws_ptr, ws_bytes, workspace = _workspace(workspace, need, dev)
+    _check(load().mxfp8_route(logits.data_ptr(), stride, logits.dtype is _BF16, T, E, k, sc, renormalize, scale,
+                              r.ids.data_ptr(), r.weights.data_ptr(), r.offsets.data_ptr(), r.rows.data_ptr(),
+                              r.positions.data_ptr(), ws_ptr, ws_bytes, _stream()))
+    return r
+
+
+def _added(add: torch.Tensor | None, shape: tuple) -> tuple[torch.Tensor | None, int]:
+    if add is None:
+        return None, 0
+    if add.dtype is not _BF16 or tuple(add.shape) != tuple(shape):
+        raise ValueError(f"add must be bf16 {list(shape)}, not {add.dtype} {list(add.shape)}")
+    add, _, stride = _rows2d(add, "add", 8)
+    return add, stride
+
+
+def combine(y: torch.Tensor, routing: Routing, *, add: torch.Tensor | None = None,
+            out: torch.Tensor | None = None) -> torch.Tensor:
+    """Each token's weighted sum of its rows: out[t] = sum_j weights[t, j]
+    y[positions[t, j]] (+ add[t]), in fp32, rounded once to bf16 [T, N].  ``y`` is
+    bf16 [R, N] in the order of routing.rows, ``add`` bf16 [T, N] (a shared
+    expert's output, a residual)."""
+    if y.dtype is not _BF16 or y.dim() != 2:
+        raise TypeError("y must be bfloat16 [rows, N]")
+    T, k = routing.positions.shape
+    N = y.shape[1]
+    _here(y, routing.positions, routing.weights, out)
+    p_ptr = _int32(routing.positions, (T, k), "positions")
+    if routing.weights.dtype is not _F32 or tuple(routing.weights.shape) != (T, k):
+        raise ValueError("weights must be fp32 like positions")
+    add, add_stride = _added(add, (T, N))
+    _here(out)
+    if out is None:
+        out = torch.empty((T, N), dtype=_BF16, device=y.device)
+    elif out.dtype is not _BF16 or tuple(out.shape) != (T, N) or out.data_ptr() & 15:
+        raise ValueError(f"out must be bf16 [{T}, {N}], 16-byte aligned")
+    y = _aligned16(y)
+    _check(load().mxfp8_combine(y.data_ptr(), y.shape[0], p_ptr, routing.weights.data_ptr(), T, k, N, _ptr(add),
+                                add_stride, out.data_ptr(), _stream()))
+    return out
+
+
+@functools.lru_cache(maxsize=4096)
+def expert_mlp_workspace_size(fmt: str, T: int, E: int, k: int, K: int, F: int) -> int:
+    n = ctypes.c_size_t()
+    _check(load().mxfp8_expert_mlp_workspace_size(GFMT[fmt], T, E, k, K, F, ctypes.byref(n)))
+    return n.value
+
+
+def expert_mlp(x: torch.Tensor, logits: torch.Tensor, gate_up: PackedWeights, down: PackedWeights, k: int, *,
+               scoring: str = "softmax", renormalize: bool = False, scale: float = 1.0,
+               add: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """A mixture-of-experts gated MLP in one call (mxfp8_expert_mlp): route of
+    ``logits`` [..., E], grouped gate_up product of x [..., K], silu(gate) * up,
+    grouped down product, combine (+ ``add`` like x); bf16 like x.  ``gate_up``
+    [E, 2 F, K] (gate rows first) and ``down`` [E, K, F] in one format.
+    mlp.ExpertMLP keeps the weights and checks them once."""
+    f = _expert_weights(gate_up, "expert_mlp")
+    E, K, F = gate_up.B, gate_up.K, down.K
+    if down.fmt != gate_up.fmt or not down.batched or down.B != E or gate_up.N != 2 * F or down.N != K:
+        raise ValueError(f"gate_up [{E}, {gate_up.N}, {K}] {gate_up.fmt} and down [{down.B}, {down.N}, {F}] {down.fmt} "
+                         "are not [E, 2 F, K] and [E, K, F] of one format")
+    sc = _scoring(scoring)
+    if x.dtype is not _BF16:
+        raise TypeError("x must be bfloat16")
+    _here(x, workspace)
+    shape = x.shape
+    if not shape or shape[-1] != K or logits.shape != shape[:-1] + (E,):
+        raise ValueError(f"x {tuple(shape)} and logits {tuple(logits.shape)} are not [..., {K}] and [..., {E}]")
+    T = x.numel() // K
+    logits, l_stride = _logits2d(logits if logits.dim() == 2 else logits.reshape(T, E))
+    add, add_stride = _added(add, shape)
+    out = torch.empty(shape, dtype=_BF16, device=x.device)
+    need = expert_mlp_workspace_size(gate_up.fmt, T, E, k, K, F)  # checks the sizes
+    if T == 0:
+        return out
+    x = _aligned16(x)
+    ws_ptr, ws_bytes, workspace = _workspace(workspace, need, x.device)
+    _check(load().mxfp8_expert_mlp(f, x.data_ptr(), T, K, logits.data_ptr(), l_stride, logits.dtype is _BF16, E, k, sc,
+                                   renormalize, scale, F, gate_up.w_packed.data_ptr(), gate_up.sf_packed.data_ptr(),
+                                   down.w_packed.data_ptr(), down.sf_packed.data_ptr(), _ptr(add), add_stride,
+                                   out.data_ptr(), ws_ptr, ws_bytes, _stream()))
+    return out
 
 
 def check() -> None:

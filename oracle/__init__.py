@@ -11,3 +11,5 @@ from .mx_oracle import (FP6_FORMATS, fp6_emax, fp6_encode, fp6_max, fp6_value,  
                         quantize_fp6)
 from .fp4_oracle import (dequantize4, e2m1_encode, e2m1_value, pack, quantize4,  # noqa: F401,E402
                          quantize_any, rmsnorm, silu_mul, unpack)
+from .grouped_oracle import (combine, dequantize_b128, dequantize_weights_b128, grouped,  # noqa: F401,E402
+                             quantize_b128, quantize_weights_b128, route)
