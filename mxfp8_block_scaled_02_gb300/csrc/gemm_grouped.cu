@@ -29,13 +29,14 @@
 // fragments of bf16 into rows of the output.
 //
 // Warps: 0 weight TMA (and, MXFP8, weight scales), 1 tensor-memory allocation and
-// MMA issue, 2 TMA of x, 3 the group table, 4..7 scales, 8.. epilogue.  Every
-// wait is bounded and the cluster barriers are reached on every path.
+// MMA issue, 2 TMA of x, 3 the group table and the scales of fp8_128; MXFP8: 4..7
+// scales into tensor memory; then the epilogue, 4 or 8 warps.  Every wait is
+// bounded and the cluster barriers are reached on every path.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include "mx_grouped.h"
+#include "mx_grouped.cuh"
 #include "mx_kernels.h"
 #include "mx_layout.cuh"
 #include "mx_ptx.cuh"
@@ -44,11 +45,10 @@ namespace mx {
 
 namespace {
 
-constexpr int ROWS = 128;  // weight rows per CTA
-constexpr int BK = 128;    // bytes (elements) of K per row and stage: one block of fp8_128
+constexpr int ROWS = kGW_Rows, BK = kGBK, BOX = kGBox;
 constexpr int W_BYTES = ROWS * BK;
-constexpr int BOX = 16;    // rows of x per copy of a tile that is not full
-constexpr int SC_WARPS = 4;
+using Args = GroupedArgs;
+using Tile = GroupTile;
 
 template <int FMT, int CG, int TN>
 struct Cfg {
@@ -58,7 +58,9 @@ struct Cfg {
   static constexpr int X_BYTES = XROWS * BK;
   static constexpr int EPI_WARPS = TN >= 128 ? 8 : 4;
   static constexpr int EPI_COLS = TN / (EPI_WARPS / 4);  // columns per epilogue warp
-  static constexpr int THREADS = 256 + 32 * EPI_WARPS;
+  static constexpr int SC_WARPS = MX ? 4 : 1;       // warps that prepare scales
+  static constexpr int EPI_FIRST = MX ? 8 : 4;       // first epilogue warp
+  static constexpr int THREADS = 32 * (EPI_FIRST + EPI_WARPS);
   static constexpr int SF_BYTES = MX ? kAtomBytes : 0;  // weight scales of a stage
   static constexpr int SLOTS = MX ? 0 : 8;              // fp8_128: blocks of K whose scales are staged
   static constexpr int RECV_BYTES = CG == 1 && TN <= 64 ? 32768 : 0;
@@ -93,90 +95,6 @@ struct Cfg {
   static_assert(SMEM <= 232448 && STAGES >= 4, "shared memory");
 };
 
-// ---------------------------------------------------------------- instructions issued by one elected lane
-// as predicated instructions of a converged warp (see gemm_fp4.cu)
-template <int CG>
-__device__ __forceinline__ void mma_mxf8(uint32_t elected, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                         uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
-  if (CG == 2)
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %7, 0;\n\t"
-        "@q tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
-            d),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb), "r"(elected)
-        : "memory");
-  else
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %7, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
-            d),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb), "r"(elected)
-        : "memory");
-}
-
-template <int CG>
-__device__ __forceinline__ void mma_f8(uint32_t elected, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                       uint32_t accumulate) {
-  if (CG == 2)
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(elected)
-        : "memory");
-  else
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(elected)
-        : "memory");
-}
-
-// Arrive on `bar` when all earlier MMAs of this lane are done: in both CTAs of a pair, or here.
-template <int CG>
-__device__ __forceinline__ void commit(uint32_t elected, uint64_t* bar) {
-  if (CG == 2)
-    asm volatile(
-        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
-        "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(
-            smem_u32(bar)),
-        "h"(static_cast<uint16_t>(3)), "r"(elected)
-        : "memory");
-  else
-    asm volatile(
-        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
-        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
-        "r"(elected)
-        : "memory");
-}
-
-// bar: shared-window address; on a pair the even CTA's.
-template <int CG>
-__device__ __forceinline__ void tma_load(uint32_t elected, uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0,
-                                         int c1, int c2) {
-  if (CG == 2)
-    asm volatile(
-        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %6, 0;\n\t"
-        "@q cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4, %5}], [%2];\n\t}" ::"r"(dst),
-        "l"(m), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(elected)
-        : "memory");
-  else
-    asm volatile(
-        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %6, 0;\n\t"
-        "@q cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], "
-        "[%2];\n\t}" ::"r"(dst),
-        "l"(m), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(elected)
-        : "memory");
-}
-
-__device__ __forceinline__ void expect_tx(uint32_t elected, uint64_t* bar, uint32_t bytes) {
-  asm volatile(
-      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
-      "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(smem_u32(bar)),
-      "r"(bytes), "r"(elected)
-      : "memory");
-}
-
 // ---------------------------------------------------------------- fragments
 // 16 lanes x 8 NG columns: thread t receives, of group g of 8 columns, r[4g],
 // r[4g+1] = lane t/4, columns 2 (t%4) and the next; r[4g+2], r[4g+3] = lane t/4 + 8.
@@ -202,123 +120,15 @@ __device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t m0, ui
                : "memory");
 }
 
-// (a0, a1) += (p0, p1) * (s0, s1)
-__device__ __forceinline__ void fma2(uint64_t& a, uint32_t p0, uint32_t p1, float s0, float s1) {
-  asm("{\n\t.reg .b64 p, s;\n\tmov.b64 p, {%1, %2};\n\tmov.b64 s, {%3, %4};\n\tfma.rn.f32x2 %0, p, s, %0;\n\t}"
-      : "+l"(a)
-      : "r"(p0), "r"(p1), "f"(s0), "f"(s1));
+// a += p * s; volatile, so that it stays behind the wait for p's load
+__device__ __forceinline__ void add_scaled(float& a, uint32_t p, float s) {
+  asm volatile("fma.rn.f32 %0, %1, %2, %0;" : "+f"(a) : "f"(__uint_as_float(p)), "f"(s));
 }
-__device__ __forceinline__ float lo32(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v)); }
-__device__ __forceinline__ float hi32(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
 
 __device__ __forceinline__ void st_async_v4(uint32_t addr, float a, float b, float c, float d, uint32_t bar) {
   asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(addr),
                "r"(__float_as_uint(a)), "r"(__float_as_uint(b)), "r"(__float_as_uint(c)), "r"(__float_as_uint(d)), "r"(bar)
                : "memory");
-}
-
-template <int N>
-__device__ __forceinline__ void set_registers_inc() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void set_registers_dec() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-
-// mbar_wait without a call: the epilogue's sums would have to be saved around one.
-__device__ __forceinline__ bool mbar_wait_inline(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const unsigned long long t0 = globaltimer();
-  while (true) {
-#pragma unroll 1
-    for (int i = 0; i < 64; ++i)
-      if (mbar_try_wait(bar, parity)) return true;
-    if (*abort) return false;
-    if (globaltimer() - t0 > kWaitLimitNs) {
-      atomicOr(&g_status, kStatusTimeout);
-      *abort = 1;
-      return false;
-    }
-  }
-}
-
-// ---------------------------------------------------------------- tiles
-struct Args {
-  const int* offsets;     // [groups + 1] on the device, or nullptr: every group has M rows
-  int groups;
-  int M;                  // rows of each group without offsets
-  int R;                  // rows of x and out
-  int N;
-  int WT;                 // weight tiles of CG * 128 rows
-  int KT;                 // stages of K
-  int splits;             // K splits = cluster size (CG = 1)
-  int w_fast;             // 1: weight tiles vary fastest within a group, 0: tiles of x
-  const uint32_t* xs;     // scales of x: word (r, kt) at r * xs_row + kt * xs_kt holds the
-  int64_t xs_row, xs_kt;  // four E8M0 bytes (MXFP8) or the fp32 (fp8_128) of 128 elements
-  const void* ws;         // MXFP8: packed atoms; fp8_128: fp32 [groups][NB][KT]
-  int RTW;                // weight row tiles of 128 (atoms), NB of fp8_128
-  const __nv_bfloat16* bias;
-  int64_t bias_stride;    // of a group: N, or 0 for one bias
-  __nv_bfloat16* out;
-};
-
-// The groups' first rows, row counts and the tiles before them.
-struct Table {
-  int* start;
-  int* count;
-  int* before;  // [groups + 1]
-};
-
-struct Tile {
-  int e, wt;        // group, weight tile
-  int row0, rows;   // first row of x, rows
-  int width;        // MMA columns: rows rounded up to STEP
-};
-
-// Unit u: of group e, tiles (x tile, weight tile).  A group's rows are shared out
-// evenly: n rows over T = ceil(n / TN) tiles of ceil(n / T), rounded up to STEP
-// (TN / STEP is a power of two up to 8, for which every tile keeps a row).
-template <int STEP, int TN>
-__device__ __forceinline__ Tile tile_of(int u, const Args& a, const Table& t) {
-  Tile r;
-  int start, n, tiles, v;
-  if (a.offsets == nullptr) {
-    n = a.M;
-    tiles = (n + TN - 1) / TN;
-    const int per = tiles * a.WT;
-    r.e = u / per;
-    v = u - r.e * per;
-    start = r.e * a.M;
-  } else {
-    const int q = u / a.WT;  // before[e] <= q < before[e + 1]
-    int lo = 0, hi = a.groups;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (t.before[mid] <= q)
-        lo = mid;
-      else
-        hi = mid;
-    }
-    r.e = lo;
-    n = t.count[lo];
-    start = t.start[lo];
-    tiles = t.before[lo + 1] - t.before[lo];
-    v = u - t.before[lo] * a.WT;
-  }
-  int xt;
-  if (a.w_fast) {
-    xt = v / a.WT;
-    r.wt = v - xt * a.WT;
-  } else {
-    r.wt = v / tiles;
-    xt = v - r.wt * tiles;
-  }
-  const int share = ((n + tiles - 1) / tiles + STEP - 1) / STEP * STEP;
-  r.row0 = start + xt * share;
-  r.rows = min(share, n - xt * share);
-  r.width = (r.rows + STEP - 1) / STEP * STEP;
-  return r;
 }
 
 template <int FMT, int CG, int TN>
@@ -341,7 +151,7 @@ __global__ void __launch_bounds__(Cfg<FMT, CG, TN>::THREADS, 1)
   uint64_t* received = sc_free + SLOTS;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
-  Table table;
+  GroupTable table;
   table.start = reinterpret_cast<int*>(smem + C::OFF_TABLE);
   table.count = table.start + kMaxGroups;
   table.before = table.count + kMaxGroups;
@@ -360,9 +170,9 @@ __global__ void __launch_bounds__(Cfg<FMT, CG, TN>::THREADS, 1)
     for (int i = lane; i < C::NBARS; i += 32) {
       uint32_t n = 1;
       uint64_t* b = &full[i];
-      if (MX && b >= sf_ready && b < buf_full) n = CG * SC_WARPS;
+      if (MX && b >= sf_ready && b < buf_full) n = CG * C::SC_WARPS;
       if (b >= buf_free && b < sc_full) n = CG * C::EPI_WARPS;
-      if (!MX && b >= sc_full && b < sc_free) n = SC_WARPS;
+      if (!MX && b >= sc_full && b < sc_free) n = C::SC_WARPS;
       if (!MX && b >= sc_free && b < received) n = C::EPI_WARPS;
       mbar_init(b, n);
     }
@@ -384,47 +194,14 @@ __global__ void __launch_bounds__(Cfg<FMT, CG, TN>::THREADS, 1)
     }
   }
   if (a.offsets != nullptr) {
-    // Whatever the offsets hold, no row outside of x is touched.
     grid_dependency_wait();
-    for (int e = threadIdx.x; e <= a.groups; e += C::THREADS) table.before[e] = min(max(a.offsets[e], 0), a.R);
+    load_offsets(a, table, C::THREADS);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   if (a.offsets != nullptr) {
-    if (warp == 3) {
-      // ... and each offset is at least the one before it: groups never overlap, and
-      // there are at most grouped_max_tiles tiles.  (before[e + 1] is read before
-      // before[e] is overwritten.)
-      int sum = 0, top = 0;
-      for (int e0 = 0; e0 < a.groups; e0 += 32) {
-        const int e = e0 + lane;
-        int start = e < a.groups ? table.before[e] : 0;
-        const int next = e < a.groups ? table.before[e + 1] : 0;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          const int o = __shfl_up_sync(0xFFFFFFFFu, start, d);
-          if (lane >= d) start = max(start, o);
-        }
-        start = max(start, top);
-        const int count = e < a.groups ? max(next - start, 0) : 0;
-        top = __shfl_sync(0xFFFFFFFFu, start + count, 31);
-        const int mine = (count + TN - 1) / TN;
-        int upto = mine;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          const int o = __shfl_up_sync(0xFFFFFFFFu, upto, d);
-          if (lane >= d) upto += o;
-        }
-        if (e < a.groups) {
-          table.start[e] = start;
-          table.count[e] = count;
-          table.before[e] = sum + upto - mine;
-        }
-        sum += __shfl_sync(0xFFFFFFFFu, upto, 31);
-      }
-      if (lane == 0) table.before[a.groups] = sum;
-    }
+    if (warp == 3) fill_table<TN>(a, table, lane);
     __syncthreads();
   }
   if (csize > 1) {
@@ -433,15 +210,10 @@ __global__ void __launch_bounds__(Cfg<FMT, CG, TN>::THREADS, 1)
   }
   if (CG == 1) launch_dependents();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
-  const int units =
-      (a.offsets != nullptr ? table.before[a.groups] : a.groups * ((a.M + TN - 1) / TN)) * a.WT;
+  const int units = unit_count<TN>(a, table);
   const uint32_t base = smem_u32(smem);
 
-  // fp8_128 on pairs: the epilogue holds 128 sums a thread; 2 (40 + 216) = 4 * 128
-  constexpr bool SPLIT_REGS = !MX && CG == 2;
-
   if (warp < 4) {
-    if (SPLIT_REGS) set_registers_dec<40>();
     if (warp == 0 || warp == 2) {
     // ------------------------------------------------------------ producers
     // Both CTAs' operands complete on the even CTA's `full`, whose bytes the even
@@ -571,133 +343,54 @@ __global__ void __launch_bounds__(Cfg<FMT, CG, TN>::THREADS, 1)
       if (!ok) __nanosleep(200000);  // let issued tensor-core work retire
     }
     __syncwarp();
-    }
-  } else if (warp < 4 + SC_WARPS) {
-    if (SPLIT_REGS) set_registers_dec<40>();
-    grid_dependency_wait();  // x's scales are the previous kernel's output
-    if constexpr (MX) {
-      // ---------------------------------------------------------- MXFP8 scales into tensor memory
-      // Line l of an atom (rows l, l + 32, l + 64, l + 96) goes to lane l of each
-      // quarter, one quarter a warp.  The words of x's rows are loaded AHEAD stages early.
-      constexpr int NW = TN < 32 ? 1 : TN / 32, AHEAD = 2;
-      const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + C::T_SF;
-      const uint32_t ready = CG == 2 ? map_shared_rank(smem_u32(sf_ready), 0) : smem_u32(sf_ready);
-      int f_u = worker, f_kt = kt0, f_rows = 0;
-      const uint32_t* f_p = a.xs;
-      auto start = [&]() {
-        if (f_u >= units) return;
-        const Tile t = tile_of<STEP, TN>(f_u, a, table);
-        f_rows = t.rows;
-        f_p = a.xs + static_cast<int64_t>(t.row0 + lane) * a.xs_row;
-      };
-      start();
-      auto fetch = [&](uint32_t (&w)[NW]) {
-        if (f_u >= units) return;
-        const uint32_t* p = f_p + f_kt * a.xs_kt;
-#pragma unroll
-        for (int i = 0; i < NW; ++i) w[i] = lane + 32 * i < f_rows ? __ldg(p + 32 * i * a.xs_row) : 0u;
-        if (++f_kt == kt1) {
-          f_kt = kt0;
-          f_u += nworkers;
-          start();
-        }
-      };
-      uint32_t w[AHEAD][NW] = {};
-#pragma unroll
-      for (int d = 0; d < AHEAD; ++d) fetch(w[d]);
-      int stage = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      int64_t left = 0;
-      for (int u = worker; u < units; u += nworkers) left += kt1 - kt0;
-      while (ok && left > 0) {
-#pragma unroll
-        for (int d = 0; d < AHEAD; ++d, --left) {
-          if (!ok || left <= 0) break;
-          // the stage's slot is free: its refill has waited for the MMAs that read it
-          if (!__all_sync(0xFFFFFFFFu, mbar_wait(&sf_full[stage], phase, abort_flag))) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint4 v = reinterpret_cast<const uint4*>(smem + C::OFF_SFW + stage * C::SF_BYTES)[lane];
-          const uint32_t ts = lane_base + stage * C::SLOT_COLS;
-          tmem_st_32x32b_x4(ts, v.x, v.y, v.z, v.w);
-#pragma unroll
-          for (int i = 0; i < NW; i += 4)
-            tmem_st_32x32b_x4(ts + 4 + i, w[d][i], i + 1 < NW ? w[d][i + 1 < NW ? i + 1 : 0] : 0u,
-                              i + 2 < NW ? w[d][i + 2 < NW ? i + 2 : 0] : 0u,
-                              i + 3 < NW ? w[d][i + 3 < NW ? i + 3 : 0] : 0u);
-          fetch(w[d]);
-          tmem_st_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            if (!leader)
-              mbar_arrive_remote(ready + static_cast<uint32_t>(stage * 8));
-            else if (mbar_wait(&full[stage], phase, abort_flag))
-              mbar_arrive(&sf_ready[stage]);
-          }
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1u;
-          }
-        }
-      }
-    } else {
+    } else if (!MX && warp == 3) {
       // ---------------------------------------------------------- fp8_128: s_x s_w of a block of K and each row of x
-      // Thread i prepares rows i and i + 128 of the tile.  Column c = 16 J + 8 g +
-      // 2 q + b goes to position 16 J + 4 q + 2 g + b: 16 bytes are what a thread
-      // of the epilogue (q) needs for 16 columns.
-      constexpr int NR = TN > 128 ? 2 : 1, AHEAD = 4;
-      const int i0 = static_cast<int>(threadIdx.x) - 128;
-      const int pos = (i0 & ~15) | ((i0 & 6) << 1) | ((i0 & 8) >> 2) | (i0 & 1);
-      const bool has = i0 < TN;
+      // Lane l prepares rows l, l + 32, ...  Column c = 16 J + 8 g + 2 q + b goes to
+      // position 16 J + 4 q + 2 g + b: 16 bytes are what a thread of the epilogue
+      // (q) needs for 16 columns.
+      constexpr int NR = TN < 32 ? 1 : TN / 32;
+      grid_dependency_wait();  // x's scales are the previous kernel's output
+      const int pos = (lane & ~15) | ((lane & 6) << 1) | ((lane & 8) >> 2) | (lane & 1);
       float* slots = reinterpret_cast<float*>(smem + C::OFF_SC);
+      int slot = 0;
+      uint32_t phase = 1;
+      bool ok = true;
+      float x[NR] = {}, w = 0.f;  // of the block ahead
       int f_u = worker, f_kt = kt0, f_rows = 0;
       const float *f_x = nullptr, *f_w = nullptr;
       auto start = [&]() {
         if (f_u >= units) return;
         const Tile t = tile_of<STEP, TN>(f_u, a, table);
         f_rows = t.rows;
-        f_x = reinterpret_cast<const float*>(a.xs) + static_cast<int64_t>(t.row0 + i0) * a.xs_row;
+        f_x = reinterpret_cast<const float*>(a.xs) + static_cast<int64_t>(t.row0 + lane) * a.xs_row;
         const int rt = min(t.wt * CG + rank, a.RTW - 1);
         f_w = static_cast<const float*>(a.ws) + (static_cast<int64_t>(t.e) * a.RTW + rt) * a.KT;
       };
-      start();
-      auto fetch = [&](float (&x)[NR], float& w) {
+      auto fetch = [&]() {
         if (f_u >= units) return;
         w = __ldg(f_w + f_kt);
         const float* p = f_x + f_kt * a.xs_kt;
 #pragma unroll
-        for (int i = 0; i < NR; ++i) x[i] = i0 + 128 * i < f_rows ? __ldg(p + 128 * i * a.xs_row) : 0.f;
+        for (int i = 0; i < NR; ++i) x[i] = lane + 32 * i < f_rows ? __ldg(p + 32 * i * a.xs_row) : 0.f;
         if (++f_kt == kt1) {
           f_kt = kt0;
           f_u += nworkers;
           start();
         }
       };
-      float x[AHEAD][NR] = {}, w[AHEAD] = {};
-#pragma unroll
-      for (int d = 0; d < AHEAD; ++d) fetch(x[d], w[d]);
-      int64_t left = 0;
-      for (int u = worker; u < units; u += nworkers) left += kt1 - kt0;
-      int slot = 0;
-      uint32_t phase = 1;
-      bool ok = true;
-      while (ok && left > 0) {
-#pragma unroll
-        for (int d = 0; d < AHEAD; ++d, --left) {
-          if (!ok || left <= 0) break;
-          if (!__all_sync(0xFFFFFFFFu, mbar_wait(&sc_free[slot], phase, abort_flag))) {
+      start();
+      fetch();
+      for (int u = worker; ok && u < units; u += nworkers) {
+        for (int kt = kt0; kt < kt1; ++kt) {
+          if (!mbar_wait_warp(&sc_free[slot], phase, abort_flag)) {
             ok = false;
             break;
           }
-          if (has) {
+          if (TN >= 32 || lane < TN) {
 #pragma unroll
-            for (int i = 0; i < NR; ++i) slots[slot * TN + pos + 128 * i] = x[d][i] * w[d];
+            for (int i = 0; i < NR; ++i) slots[slot * TN + pos + 32 * i] = x[i] * w;
           }
-          fetch(x[d], w[d]);
+          fetch();
           __syncwarp();
           if (lane == 0) mbar_arrive(&sc_full[slot]);
           if (++slot == SLOTS) {
@@ -707,15 +400,85 @@ __global__ void __launch_bounds__(Cfg<FMT, CG, TN>::THREADS, 1)
         }
       }
     }
+  } else if (MX && warp < 8) {
+    grid_dependency_wait();  // x's scales are the previous kernel's output
+    // ---------------------------------------------------------- MXFP8 scales into tensor memory
+    // Line l of an atom (rows l, l + 32, l + 64, l + 96) goes to lane l of each
+    // quarter, one quarter a warp.  The words of x's rows are loaded AHEAD stages early.
+    constexpr int NW = TN < 32 ? 1 : TN / 32, AHEAD = 2;
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + C::T_SF;
+    const uint32_t ready = CG == 2 ? map_shared_rank(smem_u32(sf_ready), 0) : smem_u32(sf_ready);
+    int f_u = worker, f_kt = kt0, f_rows = 0;
+    const uint32_t* f_p = a.xs;
+    auto start = [&]() {
+      if (f_u >= units) return;
+      const Tile t = tile_of<STEP, TN>(f_u, a, table);
+      f_rows = t.rows;
+      f_p = a.xs + static_cast<int64_t>(t.row0 + lane) * a.xs_row;
+    };
+    start();
+    auto fetch = [&](uint32_t (&w)[NW]) {
+      if (f_u >= units) return;
+      const uint32_t* p = f_p + f_kt * a.xs_kt;
+#pragma unroll
+      for (int i = 0; i < NW; ++i) w[i] = lane + 32 * i < f_rows ? __ldg(p + 32 * i * a.xs_row) : 0u;
+      if (++f_kt == kt1) {
+        f_kt = kt0;
+        f_u += nworkers;
+        start();
+      }
+    };
+    uint32_t w[AHEAD][NW] = {};
+#pragma unroll
+    for (int d = 0; d < AHEAD; ++d) fetch(w[d]);
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    int64_t left = 0;
+    for (int u = worker; u < units; u += nworkers) left += kt1 - kt0;
+    while (ok && left > 0) {
+#pragma unroll
+      for (int d = 0; d < AHEAD; ++d, --left) {
+        if (!ok || left <= 0) break;
+        // the stage's slot is free: its refill has waited for the MMAs that read it
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(&sf_full[stage], phase, abort_flag))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint4 v = reinterpret_cast<const uint4*>(smem + C::OFF_SFW + stage * C::SF_BYTES)[lane];
+        const uint32_t ts = lane_base + stage * C::SLOT_COLS;
+        tmem_st_32x32b_x4(ts, v.x, v.y, v.z, v.w);
+#pragma unroll
+        for (int i = 0; i < NW; i += 4)
+          tmem_st_32x32b_x4(ts + 4 + i, w[d][i], i + 1 < NW ? w[d][i + 1 < NW ? i + 1 : 0] : 0u,
+                            i + 2 < NW ? w[d][i + 2 < NW ? i + 2 : 0] : 0u,
+                            i + 3 < NW ? w[d][i + 3 < NW ? i + 3 : 0] : 0u);
+        fetch(w[d]);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (!leader)
+            mbar_arrive_remote(ready + static_cast<uint32_t>(stage * 8));
+          else if (mbar_wait(&full[stage], phase, abort_flag))
+            mbar_arrive(&sf_ready[stage]);
+        }
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
   } else {
     // ------------------------------------------------------------ epilogue
-    if (SPLIT_REGS) set_registers_inc<216>();
     constexpr int COLS = C::EPI_COLS;
     constexpr int CH = COLS < 32 ? COLS : 32;  // columns per load
     constexpr int NCH = COLS / CH, NG = CH / 8;
     const int quad = warp & 3;
-    const int col_base = (warp - 8) / 4 * COLS;
-    uint8_t* box = smem + C::OFF_OUT + (warp - 8) * 1024;
+    const int ew = warp - C::EPI_FIRST;
+    const int col_base = ew / 4 * COLS;
+    uint8_t* box = smem + C::OFF_OUT + ew * 1024;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16) + col_base;
     const uint32_t free_bar = CG == 2 ? map_shared_rank(smem_u32(buf_free), 0) : smem_u32(buf_free);
     auto release = [&](int b) {
@@ -733,8 +496,8 @@ __global__ void __launch_bounds__(Cfg<FMT, CG, TN>::THREADS, 1)
     const uint8_t* ld_addr = box + (lane >> 2) * 64 + ((((lane & 3) ^ (lane >> 3)) & 3) << 4);
     int flip = 0;
     grid_dependency_wait();  // the bias may be the previous kernel's output
-    // Eight columns (rows of x) of this warp's 32 weight rows, v[h][..] the fragment
-    // of lanes 16 h..: rounded, transposed, stored.
+    // Eight columns (rows of x) of this warp's 32 weight rows, v[4 h ..] the fragment
+    // of lanes 16 h ..: rounded, transposed, stored.
     Tile t;
     float bias[4];
     int n_lane = 0;
@@ -748,11 +511,10 @@ __global__ void __launch_bounds__(Cfg<FMT, CG, TN>::THREADS, 1)
         bias[i] = a.bias != nullptr && n < a.N ? __bfloat162float(a.bias[t.e * a.bias_stride + n]) : 0.f;
       }
     };
-    auto emit = [&](int col, const float (&v)[2][4]) {
+    auto emit = [&](int col, const float (&v)[8]) {
       uint32_t m[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        m[i] = pack_bf16x2(v[i >> 1][2 * (i & 1)] + bias[i], v[i >> 1][2 * (i & 1) + 1] + bias[i]);
+      for (int i = 0; i < 4; ++i) m[i] = pack_bf16x2(v[2 * i] + bias[i], v[2 * i + 1] + bias[i]);
       stmatrix_x4_trans(st_addr + flip, m[0], m[1], m[2], m[3]);
       __syncwarp();
       const uint4 o = *reinterpret_cast<const uint4*>(ld_addr + flip);
@@ -764,29 +526,29 @@ __global__ void __launch_bounds__(Cfg<FMT, CG, TN>::THREADS, 1)
     // K splits: group j of 8 columns is finished by CTA j % S of the cluster; the
     // partial sums of all S go to its slot j / S, and are added in the order of K.
     float* recv = reinterpret_cast<float*>(smem + C::OFF_RECV);
-    auto send = [&](int col, const float (&v)[2][4]) {
+    auto send = [&](int col, const float (&v)[8]) {
       const int j = col >> 3, S = a.splits;
       const int owner = j % S;
       float* at = recv + ((j / S * S + cta) * 4 + quad) * 256 + lane * 8;
       const uint32_t dst = map_shared_rank(smem_u32(at), owner);
       const uint32_t bar = map_shared_rank(smem_u32(received), owner);
-      st_async_v4(dst, v[0][0], v[0][1], v[0][2], v[0][3], bar);
-      st_async_v4(dst + 16, v[1][0], v[1][1], v[1][2], v[1][3], bar);
+      st_async_v4(dst, v[0], v[1], v[2], v[3], bar);
+      st_async_v4(dst + 16, v[4], v[5], v[6], v[7], bar);
     };
     auto finish_split = [&]() {
       const int S = a.splits, groups = (t.rows + 7) >> 3;
       const int owned = groups > cta ? (groups - cta + S - 1) / S : 0;
       if (owned == 0) return;
-      if (warp == 8 && lane == 0) mbar_arrive_expect_tx(received, static_cast<uint32_t>(owned * S * 4096));
+      if (ew == 0 && lane == 0) mbar_arrive_expect_tx(received, static_cast<uint32_t>(owned * S * 4096));
       // waited for in any case: no store may land after this CTA has left
       if (!__all_sync(0xFFFFFFFFu, mbar_wait(received, 0, nullptr))) return;
       for (int i = 0; i < owned; ++i) {
-        float v[2][4] = {};
+        float v[8] = {};
         for (int s = 0; s < S; ++s) {
           const float4* p = reinterpret_cast<const float4*>(recv + ((i * S + s) * 4 + quad) * 256 + lane * 8);
           const float4 p0 = p[0], p1 = p[1];
-          v[0][0] += p0.x, v[0][1] += p0.y, v[0][2] += p0.z, v[0][3] += p0.w;
-          v[1][0] += p1.x, v[1][1] += p1.y, v[1][2] += p1.z, v[1][3] += p1.w;
+          v[0] += p0.x, v[1] += p0.y, v[2] += p0.z, v[3] += p0.w;
+          v[4] += p1.x, v[5] += p1.y, v[6] += p1.z, v[7] += p1.w;
         }
         emit((i * S + cta) * 8, v);
       }
@@ -822,9 +584,9 @@ __global__ void __launch_bounds__(Cfg<FMT, CG, TN>::THREADS, 1)
           if (at + col_base < t.width) {
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
-              float v[2][4];
+              float v[8];
 #pragma unroll
-              for (int k = 0; k < 8; ++k) v[k >> 2][k & 3] = __uint_as_float(r[k >> 2][4 * g + (k & 3)]);
+              for (int k = 0; k < 8; ++k) v[k] = __uint_as_float(r[k >> 2][4 * g + (k & 3)]);
               const int col = col_base + at + 8 * g;
               if (col < t.rows) {
                 if (split)
@@ -841,70 +603,88 @@ __global__ void __launch_bounds__(Cfg<FMT, CG, TN>::THREADS, 1)
       int slot = 0;
       uint32_t sphase = 0;
       for (int u = worker; ok && u < units; u += nworkers) {
-        start_tile(u);
-        const int cols = t.width - col_base;  // of this warp, if positive
-        uint64_t acc[2][NCH * NG][2];
+        // columns of this warp that are in use, if positive
+        const int cols = tile_of<STEP, TN>(u, a, table).width - col_base;
+        float acc[NCH][2][4 * NG];  // as the fragments
 #pragma unroll
-        for (int i = 0; i < 2 * NCH * NG * 2; ++i) (&acc[0][0][0])[i] = 0;
-        for (int kt = kt0; kt < kt1; ++kt, ++n) {
-          const int b = n % BUFS;
-          if (!__all_sync(0xFFFFFFFFu, mbar_wait_inline(&sc_full[slot], sphase, abort_flag)) ||
-              !__all_sync(0xFFFFFFFFu, mbar_wait_inline(&buf_full[b], static_cast<uint32_t>((n / BUFS) & 1), abort_flag))) {
-            ok = false;
-            break;
-          }
+        for (int i = 0; i < NCH * 8 * NG; ++i) (&acc[0][0][0])[i] = 0.f;
+        // CH columns of all 32 lanes at a time: the next ones are on their way while
+        // one lot is added, also over the end of a block of K.
+        constexpr int RB = NCH > 1 ? 2 : 1;
+        uint32_t r[RB][2][4 * NG];
+        float4 f[RB][CH / 16];
+        auto load = [&](int blk, int sl, int i) {
+          const uint32_t src = lanes + (blk % BUFS) * C::ACOLS + i * CH;
+          tmem_ld_frag(src, r[i % RB][0]);
+          tmem_ld_frag(src + (16u << 16), r[i % RB][1]);
+          const float4* sc =
+              reinterpret_cast<const float4*>(smem + C::OFF_SC) + (sl * TN + col_base + i * CH) / 4 + (lane & 3);
+#pragma unroll
+          for (int k = 0; k < CH / 16; ++k) f[i % RB][k] = sc[4 * k];
+        };
+        // block blk of K (in buffer blk % BUFS) and its scales have come
+        auto arrived = [&](int blk, int sl, uint32_t ph) {
+          const int b = blk % BUFS;
+          const uint32_t bp = static_cast<uint32_t>((blk / BUFS) & 1);
+          bool come = __all_sync(0xFFFFFFFFu, mbar_try_wait(&sc_full[sl], ph) && mbar_try_wait(&buf_full[b], bp));
+          if (!come)
+            come = __all_sync(0xFFFFFFFFu, mbar_wait_inline(&sc_full[sl], ph, abort_flag) &&
+                                               mbar_wait_inline(&buf_full[b], bp, abort_flag));
           tc_fence_after();
-          const uint32_t src = lanes + b * C::ACOLS;
-          const float4* sc = reinterpret_cast<const float4*>(smem + C::OFF_SC) + (slot * TN + col_base) / 4 + (lane & 3);
-          uint32_t r[2][4 * NG];
-          if (cols > 0) tmem_ld_frag(src, r[0]);
+          return come;
+        };
+        ok = arrived(n, slot, sphase);
+        if (ok && cols > 0) load(n, slot, 0);
+        for (int kt = kt0; ok && kt < kt1; ++kt, ++n) {
+          int next_slot = slot + 1;
+          uint32_t next_phase = sphase;
+          if (next_slot == SLOTS) {
+            next_slot = 0;
+            next_phase ^= 1u;
+          }
 #pragma unroll
           for (int i = 0; i < NCH; ++i) {
-            float4 s[CH / 16];
-#pragma unroll
-            for (int k = 0; k < CH / 16; ++k) s[k] = sc[(i * CH + 16 * k) / 4];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              tmem_ld_wait();
-              if (i * CH < cols) {
-                // the next fragment is on its way while this one is added
-                if (h == 0)
-                  tmem_ld_frag(src + i * CH + (16u << 16), r[1]);
-                else if (i + 1 < NCH && (i + 1) * CH < cols)
-                  tmem_ld_frag(src + (i + 1) * CH, r[0]);
+            tmem_ld_wait();
+            if (i + 1 < NCH) {
+              if ((i + 1) * CH < cols) load(n, slot, i + 1);
+            } else {
+              release(n % BUFS);
+              if (lane == 0) mbar_arrive(&sc_free[slot]);
+              if (RB == 2 && kt + 1 < kt1) {
+                ok = arrived(n + 1, next_slot, next_phase);
+                if (cols > 0) load(n + 1, next_slot, 0);
               }
-              if (i == NCH - 1 && h == 1) release(b);
-              if (i * CH < cols) {
+            }
+            if (i * CH < cols) {
 #pragma unroll
-                for (int g = 0; g < NG; ++g) {
-                  const float4 f = s[g >> 1];
-                  const float s0 = g & 1 ? f.z : f.x, s1 = g & 1 ? f.w : f.y;
-                  fma2(acc[h][i * NG + g][0], r[h][4 * g], r[h][4 * g + 1], s0, s1);
-                  fma2(acc[h][i * NG + g][1], r[h][4 * g + 2], r[h][4 * g + 3], s0, s1);
+              for (int g = 0; g < NG; ++g) {
+                const float4 q = f[i % RB][g >> 1];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {  // the four sums of a column one after the other
+                  const float sc = g & 1 ? (c ? q.w : q.z) : (c ? q.y : q.x);
+#pragma unroll
+                  for (int k = 0; k < 4; ++k)
+                    add_scaled(acc[i][k >> 1][4 * g + 2 * (k & 1) + c], r[i % RB][k >> 1][4 * g + 2 * (k & 1) + c], sc);
                 }
               }
             }
+            if (RB == 1 && kt + 1 < kt1) {
+              ok = arrived(n + 1, next_slot, next_phase);
+              if (cols > 0) load(n + 1, next_slot, 0);
+            }
           }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sc_free[slot]);
-          if (++slot == SLOTS) {
-            slot = 0;
-            sphase ^= 1u;
-          }
+          slot = next_slot;
+          sphase = next_phase;
         }
         if (!ok) break;
+        start_tile(u);
 #pragma unroll
-        for (int g = 0; g < NCH * NG; ++g) {
+        for (int g = 0; g < COLS / 8; ++g) {
           const int col = col_base + 8 * g;
           if (col < t.rows) {
-            float v[2][4];
+            float v[8];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              v[h][0] = lo32(acc[h][g][0]);
-              v[h][1] = hi32(acc[h][g][0]);
-              v[h][2] = lo32(acc[h][g][1]);
-              v[h][3] = hi32(acc[h][g][1]);
-            }
+            for (int k = 0; k < 8; ++k) v[k] = acc[g / NG][k >> 2][4 * (g % NG) + (k & 3)];
             if (split)
               send(col, v);
             else
@@ -948,33 +728,11 @@ cudaError_t launch_t(const GroupedProblem& p, int splits, int sms, cudaStream_t 
     if (dev >= 0 && dev < 64) attr_set[dev] = true;
   }
   CUtensorMap mw, mx, mbox;
-  const auto u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
-  const auto sw = CU_TENSOR_MAP_SWIZZLE_128B;
-  const auto l2 = CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
-  if (!encode_map3(&mw, u8, p.w, p.K, p.N, p.E, p.K, p.N * p.K, BK, ROWS, sw, l2) ||
-      !encode_map3(&mx, u8, p.x, p.K, p.R, 1, p.K, p.R * p.K, BK, C::XROWS, sw, l2) ||
-      !encode_map3(&mbox, u8, p.x, p.K, p.R, 1, p.K, p.R * p.K, BK, BOX, sw, l2)) {
+  if (!grouped_maps(p, C::XROWS, &mw, &mx, &mbox)) {
     *msg = "cuTensorMapEncodeTiled rejected an operand of the grouped product";
     return cudaErrorInvalidValue;
   }
-  Args a;
-  a.offsets = p.offsets;
-  a.groups = static_cast<int>(p.E);
-  a.M = p.offsets != nullptr ? 0 : static_cast<int>(p.R / p.E);
-  a.R = static_cast<int>(p.R);
-  a.N = static_cast<int>(p.N);
-  a.WT = static_cast<int>(ceil_div(p.N, CG * ROWS));
-  a.KT = static_cast<int>(ceil_div(p.K, BK));
-  a.splits = splits;
-  a.w_fast = p.R / p.E >= p.N ? 1 : 0;
-  a.xs = static_cast<const uint32_t*>(p.xs);
-  a.xs_row = p.xs_row;
-  a.xs_kt = p.xs_kt;
-  a.ws = p.ws;
-  a.RTW = static_cast<int>(ceil_div(p.N, ROWS));
-  a.bias = static_cast<const __nv_bfloat16*>(p.bias);
-  a.bias_stride = p.bias_stride;
-  a.out = static_cast<__nv_bfloat16*>(p.out);
+  const Args a = grouped_args(p, CG, splits);
   const int64_t units = grouped_max_tiles(p.E, p.R, p.offsets != nullptr, TN) * a.WT;
   const int csize = CG == 2 ? 2 : splits;
   int64_t workers = splits > 1 ? units : (units < sms / CG ? units : sms / CG);
@@ -1000,7 +758,12 @@ cudaError_t launch_t(const GroupedProblem& p, int splits, int sms, cudaStream_t 
 template <int FMT>
 cudaError_t launch_fmt(const GroupedProblem& p, const GroupedPlan& plan, int sms, cudaStream_t stream,
                        const char** msg) {
-  if (plan.cg == 2) return launch_t<FMT, 2, 256>(p, 1, sms, stream, msg);
+  if (plan.cg == 2) {
+    if constexpr (FMT == kG8MX)
+      return launch_t<FMT, 2, 256>(p, 1, sms, stream, msg);
+    else
+      return launch_gemm_b128_pair(p, sms, stream, msg);
+  }
   if (plan.tn == 16) return launch_t<FMT, 1, 16>(p, plan.splits, sms, stream, msg);
   if (plan.tn == 32) return launch_t<FMT, 1, 32>(p, plan.splits, sms, stream, msg);
   if (plan.tn == 64) return launch_t<FMT, 1, 64>(p, plan.splits, sms, stream, msg);
@@ -1008,6 +771,38 @@ cudaError_t launch_fmt(const GroupedProblem& p, const GroupedPlan& plan, int sms
 }
 
 }  // namespace
+
+// Tensor maps of the weights, and of x in boxes of box_rows and of kGBox rows.
+bool grouped_maps(const GroupedProblem& p, int box_rows, CUtensorMap* mw, CUtensorMap* mx, CUtensorMap* mbox) {
+  const auto u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  const auto sw = CU_TENSOR_MAP_SWIZZLE_128B;
+  const auto l2 = CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
+  return encode_map3(mw, u8, p.w, p.K, p.N, p.E, p.K, p.N * p.K, kGBK, kGW_Rows, sw, l2) &&
+         encode_map3(mx, u8, p.x, p.K, p.R, 1, p.K, p.R * p.K, kGBK, box_rows, sw, l2) &&
+         encode_map3(mbox, u8, p.x, p.K, p.R, 1, p.K, p.R * p.K, kGBK, kGBox, sw, l2);
+}
+
+GroupedArgs grouped_args(const GroupedProblem& p, int cg, int splits) {
+  GroupedArgs a;
+  a.offsets = p.offsets;
+  a.groups = static_cast<int>(p.E);
+  a.M = p.offsets != nullptr ? 0 : static_cast<int>(p.R / p.E);
+  a.R = static_cast<int>(p.R);
+  a.N = static_cast<int>(p.N);
+  a.WT = static_cast<int>(ceil_div(p.N, cg * kGW_Rows));
+  a.KT = static_cast<int>(ceil_div(p.K, kGBK));
+  a.splits = splits;
+  a.w_fast = p.R / p.E >= p.N ? 1 : 0;
+  a.xs = static_cast<const uint32_t*>(p.xs);
+  a.xs_row = p.xs_row;
+  a.xs_kt = p.xs_kt;
+  a.ws = p.ws;
+  a.RTW = static_cast<int>(ceil_div(p.N, kGW_Rows));
+  a.bias = static_cast<const __nv_bfloat16*>(p.bias);
+  a.bias_stride = p.bias_stride;
+  a.out = static_cast<__nv_bfloat16*>(p.out);
+  return a;
+}
 
 int64_t grouped_max_tiles(int64_t E, int64_t R, bool ragged, int tn) {
   if (!ragged) return E * ceil_div(R / E, tn);

@@ -39,6 +39,9 @@ int64_t grouped_max_tiles(int64_t E, int64_t R, bool ragged, int tn);
 cudaError_t launch_gemm_grouped(const GroupedProblem& p, const GroupedPlan& plan, int sms, cudaStream_t stream,
                                 const char** msg);
 cudaError_t take_status_grouped(unsigned int* out);
+// gemm_b128_pair.cu: fp8_128 on CTA pairs.
+cudaError_t launch_gemm_b128_pair(const GroupedProblem& p, int sms, cudaStream_t stream, const char** msg);
+cudaError_t take_status_b128_pair(unsigned int* out);
 
 // grouped_quant.cu.  Row r of the output is x[rows[r]] (rows null: x[r]), a row
 // index outside [0, T) gives zeros.  Codes [R, K]; the scales' 4-byte words (as

@@ -226,3 +226,28 @@ def test_rows_past_31_bits_of_elements():
     ops.check()
     tail = ops.grouped_linear(x[R - 700:].contiguous(), pw, to_dev(np.array([0, 0, 400, 700], dtype=np.int32), dev))
     assert torch.equal(out[R - 700:], tail)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_many_small_last_tiles_back_to_back(fmt):
+    """Groups whose last tile holds a few rows, so that one CTA of a pair has none of them, next to full
+    ones, many calls in a row: the pipelines of the two CTAs stay together."""
+    dev = device()
+    rng = np.random.default_rng(12)
+    counts = [242, 266, 258, 235, 251, 261, 246, 258, 278, 263, 1, 513] * 3
+    E, N, K, R = len(counts), 1024, 1024, sum(counts)
+    wq = torch.randint(0, 100, (E, N, K), dtype=torch.uint8, device=dev)
+    ws = (torch.rand(E, N // 128, K // 128, device=dev) + 0.5 if fmt == "fp8_128" else
+          torch.randint(120, 130, (E, N, K // 32), dtype=torch.uint8, device=dev))
+    pw = ops.process_weights_fp8_128(wq, ws) if fmt == "fp8_128" else ops.process_weights(wq, ws)
+    x = to_bf16(bf16_round(rng.standard_normal((R, K))), dev)
+    off = to_dev(offsets_of(counts), dev)
+    want = ops.grouped_linear(x, pw, off)
+    ops.check()
+    for _ in range(5):
+        outs = [ops.grouped_linear(x, pw, off) for _ in range(20)]
+        ops.check()
+        assert all(torch.equal(o, want) for o in outs)
+    lo, hi = 242 + 266, 242 + 266 + 258
+    alone = ops.grouped_linear(x[lo:hi].contiguous(), pw, to_dev(np.array([0, 0, 0] + [258] * (E - 2), dtype=np.int32), dev))
+    assert torch.equal(want[lo:hi], alone)
