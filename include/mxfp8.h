@@ -637,7 +637,7 @@ mxfp8_status mxfp8_b128_linear(const void* x_bf16, const uint8_t* x_q, const flo
  *     ceil(K / 128)].
  *   bias    : bf16 [E, N] or NULL.
  *   workspace : >= mxfp8_grouped_workspace_size bytes, 256-byte aligned (NULL
- *     for a quantised x).
+ *     when that is 0).
  *   E <= 512, N % 8 == 0, K % 128 == 0 (MXFP8) or K % 16 == 0 (FP8_128), else
  *   MXFP8_ERR_UNSUPPORTED; pointers 16-byte aligned (rows, offsets 4); R = 0 is
  *   a no-op.  Precision and order as mxfp8_b128_linear; all inputs are read

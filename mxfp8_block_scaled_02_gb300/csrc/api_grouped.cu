@@ -86,6 +86,14 @@ struct Product {
   void* out;
 };
 
+// Scale words of a quantised x that a product wants K-block major: a warp reads those
+// of 32 rows and one block at once, which row-major are in 32 cache lines.  On pairs in
+// MXFP8 every one of four warps reads all of a tile's, and 16384 rows, 16 experts of
+// 4096 x 4096 take 392 us instead of 210.
+int64_t turned_bytes(int fmt, int64_t E, int64_t R, int64_t N, int64_t K, bool ragged) {
+  return fmt == MXFP8_GFMT_MXFP8 && mx::grouped_plan(fmt, E, R, N, K, ragged).cg == 2 ? round_up(4 * R * ceil_div(K, 128), 256) : 0;
+}
+
 // The checks of a product call, then its launches.
 mxfp8_status run_product(const Product& p, void* workspace, size_t workspace_bytes, mxfp8_stream_t stream) {
   mxfp8_status st;
@@ -101,11 +109,15 @@ mxfp8_status run_product(const Product& p, void* workspace, size_t workspace_byt
   if (!aligned(p.rows, 4) || !aligned(p.offsets, 4))
     return fail(MXFP8_ERR_INVALID_ARG, "rows and offsets must be 4-byte aligned");
   const XLayout l = x_layout(p.R, p.K);
+  const int64_t turned = have_q ? turned_bytes(p.fmt, p.E, p.R, p.N, p.K, p.offsets != nullptr) : 0;
+  const int64_t need = have_x ? l.total : turned;
   if (have_x) {
     if (p.T < 0 || p.T > kMaxRows || (p.rows == nullptr && p.T != p.R))
       return fail(MXFP8_ERR_INVALID_ARG, "x has %lld rows for %lld of the product", (ll)p.T, (ll)p.R);
-    if (static_cast<int64_t>(workspace_bytes) < l.total)
-      return fail(MXFP8_ERR_INVALID_ARG, "workspace has %zu bytes, needs %lld", workspace_bytes, (ll)l.total);
+  }
+  if (need > 0) {
+    if (static_cast<int64_t>(workspace_bytes) < need)
+      return fail(MXFP8_ERR_INVALID_ARG, "workspace has %zu bytes, needs %lld", workspace_bytes, (ll)need);
     if (workspace == nullptr || !aligned(workspace, 256))
       return fail(MXFP8_ERR_INVALID_ARG, "workspace must be non-null and 256-byte aligned");
   }
@@ -135,6 +147,12 @@ mxfp8_status run_product(const Product& p, void* workspace, size_t workspace_byt
     if (e != cudaSuccess) return cuda_fail(e, "quantise launch");
     g.x = ws;
     g.xs = ws + l.s;
+    g.xs_row = 1;
+    g.xs_kt = p.R;
+  } else if (turned > 0) {
+    cudaError_t e = mx::launch_transpose_words(p.x_scale, p.R, KT, workspace, as_stream(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "activation scale repack launch");
+    g.xs = workspace;
     g.xs_row = 1;
     g.xs_kt = p.R;
   }
@@ -265,7 +283,7 @@ mxfp8_status mxfp8_b128_silu_mul_quantize(const void* gate_bf16, int64_t gate_st
     return fail(MXFP8_ERR_INVALID_ARG, "tensor pointers must be 16-byte aligned");
   int sms = 0;
   if ((st = mx::current_device(&sms)) != MXFP8_OK) return st;
-  const mx::ActRowsProblem p{mx::kG8B128, gate_bf16, gate_stride, up_bf16, up_stride, M, K, q, scale, ceil_div(K, 128), 1, true};
+  const mx::ActRowsProblem p{mx::kG8B128, gate_bf16, gate_stride, up_bf16, up_stride, M, K, q, scale, ceil_div(K, 128), 1};
   cudaError_t e = mx::launch_silu_mul_rows(p, as_stream(stream));
   return e == cudaSuccess ? MXFP8_OK : cuda_fail(e, "activation launch");
 }
@@ -296,7 +314,8 @@ mxfp8_status mxfp8_grouped_workspace_size(int fmt, int64_t E, int64_t R, int64_t
                                           size_t* bytes) {
   if (bytes == nullptr) return fail(MXFP8_ERR_INVALID_ARG, "null output pointer");
   mxfp8_status st = check_product(fmt, E, R, N, K, true);
-  if (st == MXFP8_OK) *bytes = x_is_quantized ? 0 : static_cast<size_t>(x_layout(R, K).total);
+  if (st == MXFP8_OK)
+    *bytes = static_cast<size_t>(R == 0 ? 0 : x_is_quantized ? turned_bytes(fmt, E, R, N, K, true) : x_layout(R, K).total);
   return st;
 }
 
@@ -434,17 +453,8 @@ mxfp8_status mxfp8_expert_mlp(int fmt, const void* x_bf16, int64_t T, int64_t K,
   if ((e = mx::launch_gemm_grouped(g, mx::grouped_plan(fmt, E, R, 2 * F, K, true), sms, as_stream(stream), &msg)) !=
       cudaSuccess)
     return cuda_fail(e, msg);
-  if (fmt == MXFP8_GFMT_FP8_128) {
-    const mx::ActRowsProblem c{fmt, h, 2 * F, h + 2 * F, 2 * F, R, F, cq, ws + w.cs, 1, R, true};
-    e = mx::launch_silu_mul_rows(c, as_stream(stream));
-    g.xs_row = 1;
-    g.xs_kt = R;
-  } else {
-    const mx::ActProblem c{MXFP8_QFMT_MXFP8, h, 2 * F, h + 2 * F, 2 * F, nullptr, R, F, cq, ws + w.cs, false};
-    e = mx::launch_silu_mul_quantize(c, as_stream(stream));
-    g.xs_row = F / 128;
-    g.xs_kt = 1;
-  }
+  const mx::ActRowsProblem c{fmt, h, 2 * F, h + 2 * F, 2 * F, R, F, cq, ws + w.cs, 1, R};
+  e = mx::launch_silu_mul_rows(c, as_stream(stream));
   if (e != cudaSuccess) return cuda_fail(e, "activation launch");
   g.x = cq;
   g.xs = ws + w.cs;

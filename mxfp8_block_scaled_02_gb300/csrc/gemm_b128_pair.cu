@@ -40,13 +40,15 @@ constexpr int EPI_WARPS = 8;
 constexpr int THREADS = 128 + 32 * EPI_WARPS;
 constexpr int OFF_W = 0;
 constexpr int OFF_X = OFF_W + STAGES * HALF_BYTES;
-constexpr int OFF_TABLE = OFF_X + STAGES * HALF_BYTES;
+constexpr int OUT_BOX = 32 * 64;  // staging of an epilogue warp: 32 rows x 32 columns
+constexpr int OFF_OUT = OFF_X + STAGES * HALF_BYTES;
+constexpr int OFF_TABLE = OFF_OUT + EPI_WARPS * OUT_BOX;
 constexpr int OFF_BAR = (OFF_TABLE + (3 * kMaxGroups + 1) * 4 + 7) / 8 * 8;
 constexpr int NBARS = 2 * STAGES + 2 * BUFS;
 constexpr int OFF_MISC = OFF_BAR + NBARS * 8;
 constexpr int SMEM = OFF_MISC + 16 + 1024;
 constexpr int TMEM_COLS = 512;
-static_assert(SMEM <= 232448, "shared memory");
+static_assert(SMEM <= 232448 && BUFS == 2, "shared memory; the epilogue flips between two buffers");
 
 // a += p * s; volatile, so that it stays behind the wait for p's load
 __device__ __forceinline__ void add_scaled(float& a, uint32_t p, float s) {
@@ -187,8 +189,8 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
             for (int kk = 0; kk < BK / 32; ++kk)
               mma_f8<2>(elected, tmem + b * TILE, xd + 2 * kk, wd + 2 * kk, idesc, kk != 0);
-            commit<2>(elected, &empty[stage]);
             commit<2>(elected, &buf_full[b]);
+            commit<2>(elected, &empty[stage]);
             if (++stage == STAGES) {
               stage = 0;
               phase ^= 1u;
@@ -215,120 +217,106 @@ __global__ void __launch_bounds__(THREADS, 1)
     grid_dependency_wait();  // x's scales and the bias may be the previous kernel's output
     int b = 0;
     uint32_t bphase = 0;
-    bool ok = true;
-    // whether the sums of the next block have come, asked early and, if not, waited for
-    auto ask = [&]() { return mbar_try_wait(&buf_full[b], bphase); };
-    auto arrived = [&](bool come) {
-      come = __all_sync(0xFFFFFFFFu, come);
-      if (!come) come = __all_sync(0xFFFFFFFFu, mbar_wait_inline(&buf_full[b], bphase, abort_flag));
+    // The loop below runs at the pace of its instructions: two warps a scheduler, 128
+    // multiply-adds a block and warp.  So it has no branches on the tile (rows that
+    // are not the group's are added like the others and not stored), and a wait that
+    // ran out only makes the later ones return at once.
+    auto arrived = [&]() {
+      if (!mbar_try_wait(&buf_full[b], bphase)) mbar_wait_inline(&buf_full[b], bphase, abort_flag);
+      __syncwarp();
       tc_fence_after();
-      return come;
     };
-    for (int u = pair; ok && u < units; u += npairs) {
+    for (int u = pair; u < units; u += npairs) {
       const GroupTile t = tile_of<0, TILE>(u, a, table);
-      const int rows = t.rows - rank * BM;         // of this CTA
-      const bool active = (warp & 3) * 32 < rows;  // of this warp
+      const int rows = t.rows - rank * BM;  // of this CTA
       // this row's scales and those of the 128 x 128 blocks of the weights, two blocks
       // of K ahead
       const float* xp = reinterpret_cast<const float*>(a.xs) +
-                        (my_row < rows ? static_cast<int64_t>(t.row0 + rank * BM + my_row) * a.xs_row : 0);
+                        static_cast<int64_t>(t.row0 + (my_row < rows ? rank * BM + my_row : 0)) * a.xs_row;
       const float* wp = static_cast<const float*>(a.ws) +
                         (static_cast<int64_t>(t.e) * a.RTW + min(2 * t.wt + half, a.RTW - 1)) * a.KT;
-      float x1 = 0.f, w1 = 0.f, x2 = 0.f, w2 = 0.f;
-      if (active) {
-        x1 = __ldg(xp);
-        w1 = __ldg(wp);
-        if (a.KT > 1) {
-          x2 = __ldg(xp + a.xs_kt);
-          w2 = __ldg(wp + 1);
-        }
-      }
+      float x1 = __ldg(xp), w1 = __ldg(wp), x2 = 0.f, w2 = 0.f;
       float acc[128];
 #pragma unroll
       for (int i = 0; i < 128; ++i) acc[i] = 0.f;
       // 32 columns at a time: the next ones are on their way while one lot is added,
       // also over the end of a block.
       uint32_t r[2][2][16];
-      ok = arrived(ask());
-      if (ok && active) {
-        tmem_ld_32x32b_x16(src + b * TILE, r[0][0]);
-        tmem_ld_32x32b_x16(src + b * TILE + 16, r[0][1]);
+      int left = a.KT - 1;  // blocks after this one
+      if (left > 0) {
+        xp += a.xs_kt;
+        x2 = __ldg(xp);
+        w2 = __ldg(++wp);
       }
-      for (int kt = 0; ok && kt < a.KT; ++kt) {
+      arrived();
+      tmem_ld_32x32b_x16(src + b * TILE, r[0][0]);
+      tmem_ld_32x32b_x16(src + b * TILE + 16, r[0][1]);
+      while (true) {
         const float s = x1 * w1;
         x1 = x2;
         w1 = w2;
-        if (active && kt + 2 < a.KT) {
-          x2 = __ldg(xp + (kt + 2) * a.xs_kt);
-          w2 = __ldg(wp + kt + 2);
+        if (left > 1) {
+          xp += a.xs_kt;
+          x2 = __ldg(xp);
+          w2 = __ldg(++wp);
         }
-        bool come = false;
+        const uint32_t at = src + b * TILE;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           tmem_ld_wait();
           if (i < 3) {
-            if (active) {
-              tmem_ld_32x32b_x16(src + b * TILE + 32 * (i + 1), r[(i + 1) & 1][0]);
-              tmem_ld_32x32b_x16(src + b * TILE + 32 * (i + 1) + 16, r[(i + 1) & 1][1]);
-            }
+            tmem_ld_32x32b_x16(at + 32 * (i + 1), r[(i + 1) & 1][0]);
+            tmem_ld_32x32b_x16(at + 32 * (i + 1) + 16, r[(i + 1) & 1][1]);
           } else {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_remote(free_bar + static_cast<uint32_t>(b * 8));
-            if (++b == BUFS) {
-              b = 0;
-              bphase ^= 1u;
-            }
-            if (kt + 1 < a.KT) come = ask();
+            b ^= 1;
+            bphase ^= b ^ 1;
           }
-          if (active) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              if (i == 3 && j == 16 && kt + 1 < a.KT) {
-                ok = arrived(come);
-                tmem_ld_32x32b_x16(src + b * TILE, r[0][0]);
-                tmem_ld_32x32b_x16(src + b * TILE + 16, r[0][1]);
-              }
-              add_scaled(acc[32 * i + j], r[i & 1][j >> 4][j & 15], s);
-            }
-          } else if (i == 3 && kt + 1 < a.KT) {
-            ok = arrived(come);
-          }
+          for (int j = 0; j < 32; ++j) add_scaled(acc[32 * i + j], r[i & 1][j >> 4][j & 15], s);
         }
+        if (left-- == 0) break;
+        arrived();
+        tmem_ld_32x32b_x16(src + b * TILE, r[0][0]);
+        tmem_ld_32x32b_x16(src + b * TILE + 16, r[0][1]);
       }
-      if (!ok) break;
-      // This thread's row: 128 columns, 32 bytes at a time.
-      const int n0 = t.wt * TILE + half * BM;
-      if (my_row < rows) {
-        __nv_bfloat16* out = a.out + static_cast<int64_t>(t.row0 + rank * BM + my_row) * a.N + n0;
+      // 32 columns at a time: this thread's row to shared memory, 16-byte pieces
+      // swizzled; from there four lanes a row.  (From registers, a lane a row of 32
+      // lines an instruction, a tile took 1.9 us.)
+      if ((warp & 3) * 32 < rows) {
+        const int n0 = t.wt * TILE + half * BM;
+        const int row0 = (warp & 3) * 32;
+        __nv_bfloat16* out = a.out + static_cast<int64_t>(t.row0 + rank * BM + row0) * a.N + n0;
         const __nv_bfloat16* bias = a.bias != nullptr ? a.bias + t.e * a.bias_stride + n0 : nullptr;
-        const bool wide = (a.N & 15) == 0 && (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
+        uint8_t* box = smem + OFF_OUT + ew * OUT_BOX;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          uint32_t o[8];
+        for (int q = 0; q < 4; ++q) {
+          if (n0 + 32 * q >= a.N) break;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int c = 16 * i + 8 * h;
-            if (n0 + c >= a.N) continue;
+          for (int p = 0; p < 4; ++p) {
+            const int c = 32 * q + 8 * p;
             uint4 bv = make_uint4(0, 0, 0, 0);
-            if (bias != nullptr) bv = __ldg(reinterpret_cast<const uint4*>(bias + c));
+            if (bias != nullptr && n0 + c < a.N) bv = __ldg(reinterpret_cast<const uint4*>(bias + c));
             const uint32_t bw[4] = {bv.x, bv.y, bv.z, bv.w};
+            uint32_t o[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              o[4 * h + k] = pack_bf16x2(acc[c + 2 * k] + __uint_as_float(bw[k] << 16),
-                                         acc[c + 2 * k + 1] + __uint_as_float(bw[k] & 0xFFFF0000u));
+              o[k] = pack_bf16x2(acc[c + 2 * k] + __uint_as_float(bw[k] << 16),
+                                 acc[c + 2 * k + 1] + __uint_as_float(bw[k] & 0xFFFF0000u));
+            *reinterpret_cast<uint4*>(box + lane * 64 + (((p ^ (lane >> 1)) & 3) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
           }
-          if (wide && n0 + 16 * i < a.N) {
-            st_global_32(out + 16 * i, o);
-          } else {
+          __syncwarp();
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-              if (n0 + 16 * i + 8 * h < a.N)
-                *reinterpret_cast<uint4*>(out + 16 * i + 8 * h) = make_uint4(o[4 * h], o[4 * h + 1], o[4 * h + 2], o[4 * h + 3]);
+          for (int p = 0; p < 4; ++p) {
+            const int r = 8 * p + (lane >> 2), c = 32 * q + 8 * (lane & 3);
+            const uint4 v = *reinterpret_cast<const uint4*>(box + r * 64 + ((((lane & 3) ^ (r >> 1)) & 3) << 4));
+            if (row0 + r < rows && n0 + c < a.N) *reinterpret_cast<uint4*>(out + static_cast<int64_t>(r) * a.N + c) = v;
           }
+          __syncwarp();
         }
       }
-      __syncwarp();
     }
   }
 

@@ -134,6 +134,47 @@ __device__ __forceinline__ Codes quantize16_mx(const uint32_t (&v)[8], int lane,
   return c;
 }
 
+// The same of fp32 values, whose exponent decides as bf16's does.
+__device__ __forceinline__ Codes quantize16_mx(const float (&y)[16], int lane, uint32_t* word) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(y[i]) & 0x7FFFFFFFu);
+  m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+  const bool nonfinite = m >= 0x7F800000u;
+  const uint32_t E = m >> 23;
+  const uint32_t sbyte = nonfinite ? 0xFFu : (E > 8u ? E - 8u : 0u);
+  const float mul = __uint_as_float((254u - (nonfinite ? 0u : sbyte)) << 23);
+  uint32_t w = sbyte << (8 * ((lane >> 1) & 3));
+  w |= __shfl_xor_sync(0xFFFFFFFFu, w, 2);
+  w |= __shfl_xor_sync(0xFFFFFFFFu, w, 4);
+  *word = w;
+  Codes c;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t a = cvt_e4m3x2(y[4 * i] * mul, y[4 * i + 1] * mul);
+    const uint32_t b = cvt_e4m3x2(y[4 * i + 2] * mul, y[4 * i + 3] * mul);
+    c.w[i] = nonfinite ? 0x7F7F7F7Fu : a | (b << 16);
+  }
+  return c;
+}
+
+// Scale words [R][KT] -> [KT][R], 32 x 32 a CTA.
+__global__ void __launch_bounds__(THREADS) transpose_words_kernel(const uint32_t* __restrict__ in, int64_t R, int KT,
+                                                                  uint32_t* __restrict__ out) {
+  __shared__ uint32_t box[32][33];
+  launch_dependents();
+  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * 32;
+  const int k0 = blockIdx.y * 32, x = threadIdx.x & 31, y = threadIdx.x >> 5;
+  grid_dependency_wait();
+#pragma unroll
+  for (int i = 0; i < 32; i += THREADS / 32)
+    if (r0 + y + i < R && k0 + x < KT) box[y + i][x] = in[(r0 + y + i) * KT + k0 + x];
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 32; i += THREADS / 32)
+    if (r0 + x < R && k0 + y + i < KT) out[static_cast<int64_t>(k0 + y + i) * R + r0 + x] = box[x][y + i];
+}
+
 // 16 bf16 at a 16-byte (wide: 32-byte) aligned address.
 __device__ __forceinline__ void load16(const __nv_bfloat16* p, bool wide, uint32_t (&v)[8]) {
   if (wide) {
@@ -213,11 +254,11 @@ struct ActArgs {
   int64_t s_row, s_kt;
 };
 
-// y = gate / (1 + exp(-gate)) * up, quantised to fp8_128: the values of
-// silu_mul_kernel (fused_quant.cu).
-template <bool kEarly>
+// y = gate / (1 + exp(-gate)) * up, quantised: the values of silu_mul_kernel
+// (fused_quant.cu), and in MXFP8 its bytes.
+template <int FMT>
 __global__ void __launch_bounds__(THREADS) silu_mul_rows_kernel(const ActArgs a) {
-  if (kEarly) launch_dependents();
+  launch_dependents();
   const int lane = threadIdx.x & 31;
   constexpr int U = UNROLL / 2;
   const int64_t first = (static_cast<int64_t>(blockIdx.x) * (THREADS / 32) + (threadIdx.x >> 5)) * U;
@@ -249,11 +290,18 @@ __global__ void __launch_bounds__(THREADS) silu_mul_rows_kernel(const ActArgs a)
       const float e = __expf(-fabsf(gt));
       y[j] = gt * __fdividef(gt >= 0.f ? 1.f : e, 1.f + e) * up;
     }
-    float s;
-    const Codes c = quantize16_b128(y, &s);
+    uint32_t word;
+    Codes c;
+    if (FMT == kG8MX) {
+      c = quantize16_mx(y, lane, &word);
+    } else {
+      float s;
+      c = quantize16_b128(y, &s);
+      word = __float_as_uint(s);
+    }
     if (k[i] < a.K) {
       *reinterpret_cast<uint4*>(a.q + row[i] * a.K + k[i]) = make_uint4(c.w[0], c.w[1], c.w[2], c.w[3]);
-      if ((lane & 7) == 0) a.s[row[i] * a.s_row + (k[i] >> 7) * a.s_kt] = __float_as_uint(s);
+      if ((lane & 7) == 0) a.s[row[i] * a.s_row + (k[i] >> 7) * a.s_kt] = word;
     }
   }
 }
@@ -364,10 +412,24 @@ cudaError_t launch_silu_mul_rows(const ActRowsProblem& p, cudaStream_t stream) {
   a.s = static_cast<uint32_t*>(p.s);
   a.s_row = p.s_row;
   a.s_kt = p.s_kt;
-  const void* fn = p.early ? reinterpret_cast<const void*>(silu_mul_rows_kernel<true>)
-                           : reinterpret_cast<const void*>(silu_mul_rows_kernel<false>);
+  const void* fn = p.fmt == kG8MX ? reinterpret_cast<const void*>(silu_mul_rows_kernel<kG8MX>)
+                                  : reinterpret_cast<const void*>(silu_mul_rows_kernel<kG8B128>);
   void* args[] = {&a};
   return launch(fn, ceil_div(a.tasks, UNROLL / 2 * (THREADS / 32)), args, true, stream);
+}
+
+cudaError_t launch_transpose_words(const void* in, int64_t R, int64_t KT, void* out, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(ceil_div(R, 32)), static_cast<unsigned>(ceil_div(KT, 32)), 1);
+  cfg.blockDim = dim3(THREADS, 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, transpose_words_kernel, static_cast<const uint32_t*>(in), R, static_cast<int>(KT),
+                            static_cast<uint32_t*>(out));
 }
 
 cudaError_t launch_quantize_weights_b128(const void* w, int64_t B, int64_t N, int64_t K, uint8_t* q, float* s,

@@ -57,7 +57,8 @@ struct QuantRowsProblem {
   bool early;            // let the next kernel in the stream start before this one ends
 };
 cudaError_t launch_quantize_rows(const QuantRowsProblem& p, cudaStream_t stream);
-// silu(gate) * up with the output quantised; rows of 16-byte aligned bf16.
+// silu(gate) * up with the output quantised; rows of 16-byte aligned bf16.  Lets the
+// next kernel in the stream start early.
 struct ActRowsProblem {
   int fmt;
   const void* gate;
@@ -68,9 +69,10 @@ struct ActRowsProblem {
   uint8_t* q;
   void* s;
   int64_t s_row, s_kt;
-  bool early;
 };
 cudaError_t launch_silu_mul_rows(const ActRowsProblem& p, cudaStream_t stream);
+// Scale words [R][KT] -> [KT][R] (KT at most 2^21).
+cudaError_t launch_transpose_words(const void* in, int64_t R, int64_t KT, void* out, cudaStream_t stream);
 // bf16 weights [B, N, K] -> E4M3 codes and fp32 scales [B, ceil(N / 128), ceil(K / 128)].
 cudaError_t launch_quantize_weights_b128(const void* w, int64_t B, int64_t N, int64_t K, uint8_t* q, float* s,
                                          cudaStream_t stream);
