@@ -25,7 +25,7 @@ typedef long long ll;
 cudaStream_t as_stream(mxfp8_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
 
 constexpr int64_t kMaxRows = 1ll << 30;
-constexpr int64_t kMaxExtent = 1ll << 29;
+constexpr int64_t kMaxExtent = 1ll << 27;
 
 mxfp8_status check_gfmt(int fmt) {
   if (fmt != MXFP8_GFMT_MXFP8 && fmt != MXFP8_GFMT_FP8_128) return fail(MXFP8_ERR_INVALID_ARG, "format %d", fmt);

@@ -31,10 +31,10 @@ namespace mx {
 
 namespace {
 
-constexpr int THREADS = 512;
+constexpr int THREADS = 1024;
 constexpr int WARPS = THREADS / 32;
 constexpr int GROUP = 64;          // tokens ranked at a time
-constexpr int MAX_BLOCKS = 152;    // CTAs whose counts a CTA adds up
+constexpr int MAX_BLOCKS = 160;    // CTAs whose counts a CTA adds up, a multiple of 32
 
 struct Args {
   const void* logits;
@@ -50,7 +50,7 @@ struct Args {
   int* offsets;
   int* rows;
   int* positions;
-  int* counts;  // [blocks][E]
+  int* counts;  // [E][MAX_BLOCKS]
 };
 
 __device__ __forceinline__ float load_logit(const Args& a, int64_t t, int e) {
@@ -74,17 +74,25 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// NL: logits a lane.  One token by one warp.
+// One token by one warp; key[i]: of expert 32 i + lane.  A lane keeps its largest
+// (the first of equals); a round is a warp maximum, the lowest expert that has it,
+// and a new largest in the lane it came from.
 template <int NL>
-__device__ __forceinline__ void select_token(const Args& a, int64_t t, int lane, int* counts) {
-  uint32_t key[NL];
-#pragma unroll
-  for (int i = 0; i < NL; ++i) key[i] = i * 32 + lane < a.E ? order_key(load_logit(a, t, i * 32 + lane)) : 0u;
+__device__ __forceinline__ void select_token(const Args& a, int64_t t, int lane, uint32_t (&key)[NL], int* counts) {
   uint32_t best = 0;
+  int at = 0;
+  auto largest = [&]() {
+    best = key[0];
+    at = 0;
 #pragma unroll
-  for (int i = 0; i < NL; ++i) best = max(best, key[i]);
-  const uint32_t top_key = __reduce_max_sync(0xFFFFFFFFu, best);
-  const float top = key_value(top_key);
+    for (int i = 1; i < NL; ++i) {
+      if (key[i] > best) at = i;
+      best = max(best, key[i]);
+    }
+  };
+  largest();
+  uint32_t most = __reduce_max_sync(0xFFFFFFFFu, best);
+  const float top = key_value(most);
   float sum = 1.f;
   if (!a.sigmoid) {
     sum = 0.f;
@@ -94,34 +102,30 @@ __device__ __forceinline__ void select_token(const Args& a, int64_t t, int lane,
     sum = warp_sum(sum);
   }
   int my_id = -1;  // lane j keeps slot j
-  float my_w = 0.f;
-  uint32_t most = top_key;
+  uint32_t my_key = 0;
   for (int j = 0; j < a.k; ++j) {
     if (j > 0) most = __reduce_max_sync(0xFFFFFFFFu, best);
     if (most == 0) break;  // none is left
-    int at = 0x7FFFFFFF;
-#pragma unroll
-    for (int i = NL - 1; i >= 0; --i)
-      if (key[i] == most) at = i * 32 + lane;
-    const int id = __reduce_min_sync(0xFFFFFFFFu, at);
+    const int id = __reduce_min_sync(0xFFFFFFFFu, best == most ? at * 32 + lane : 0x7FFFFFFF);
     if (lane == j) {
-      const float v = key_value(most);
       my_id = id;
-      my_w = a.sigmoid ? 1.f / (1.f + expf(-v)) : expf(v - top) / sum;
+      my_key = most;
     }
     if ((id & 31) == lane) {
-      best = 0;
 #pragma unroll
-      for (int i = 0; i < NL; ++i) {
-        if (i == id >> 5) key[i] = 0;
-        best = max(best, key[i]);
-      }
-      if (counts != nullptr) atomicAdd(&counts[id], 1);
+      for (int i = 0; i < NL; ++i)
+        if (i == at) key[i] = 0;
+      largest();
+      atomicAdd(&counts[id], 1);
     }
   }
+  float my_w = 0.f;
+  if (my_id >= 0) {
+    const float v = key_value(my_key);
+    my_w = a.sigmoid ? 1.f / (1.f + expf(-v)) : expf(v - top) / sum;
+  }
   if (a.renormalize) {
-    float total = 0.f;
-    for (int j = 0; j < a.k; ++j) total += __shfl_sync(0xFFFFFFFFu, my_w, j);
+    const float total = warp_sum(my_w);
     my_w = total > 0.f ? my_w / total : my_w;  // all zero: stay so
   }
   if (lane < a.k) {
@@ -130,10 +134,23 @@ __device__ __forceinline__ void select_token(const Args& a, int64_t t, int lane,
   }
 }
 
+// The next token's logits are on their way while one is sorted.
 template <int NL>
 __device__ __forceinline__ void select_range(const Args& a, int64_t t0, int64_t t1, int* counts) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int64_t t = t0 + warp; t < t1; t += WARPS) select_token<NL>(a, t, lane, counts);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  float next[NL];
+  auto fetch = [&](int64_t t) {
+#pragma unroll
+    for (int i = 0; i < NL; ++i) next[i] = t < t1 && i * 32 + lane < a.E ? load_logit(a, t, i * 32 + lane) : 0.f;
+  };
+  fetch(t0 + warp);
+  for (int64_t t = t0 + warp; t < t1; t += warps) {
+    uint32_t key[NL];
+#pragma unroll
+    for (int i = 0; i < NL; ++i) key[i] = i * 32 + lane < a.E ? order_key(next[i]) : 0u;
+    fetch(t + warps);
+    select_token<NL>(a, t, lane, key, counts);
+  }
 }
 
 __device__ __forceinline__ void select_any(const Args& a, int64_t t0, int64_t t1, int* counts) {
@@ -212,7 +229,7 @@ __global__ void __launch_bounds__(THREADS) route_select_kernel(const Args a) {
   select_any(a, t0, t1, counts);
   __syncthreads();  // counts and (kOne) this CTA's ids
   if (!kOne) {
-    for (int e = threadIdx.x; e < a.E; e += THREADS) a.counts[static_cast<int64_t>(blockIdx.x) * a.E + e] = counts[e];
+    for (int e = threadIdx.x; e < a.E; e += THREADS) a.counts[e * MAX_BLOCKS + blockIdx.x] = counts[e];
     return;
   }
   int all;
@@ -231,25 +248,44 @@ __global__ void __launch_bounds__(THREADS) route_select_kernel(const Args a) {
 
 __global__ void __launch_bounds__(THREADS) route_place_kernel(const Args a) {
   __shared__ int next[kRouteMaxE];
+  __shared__ int totals[kRouteMaxE];
   __shared__ uint32_t mask[2 * kRouteMaxE];
   __shared__ int warp_sums[WARPS];
   launch_dependents();
+  const int mine = static_cast<int>(blockIdx.x), lane = threadIdx.x & 31;
   grid_dependency_wait();
-  int total = 0, before = 0;
-  const int e = threadIdx.x;
-  if (e < a.E) {
-    const int mine = static_cast<int>(blockIdx.x);
-#pragma unroll 8
-    for (int b = 0; b < a.blocks; ++b) {
-      const int c = a.counts[static_cast<int64_t>(b) * a.E + e];
-      total += c;
-      if (b < mine) before += c;
+  // a warp an expert, a lane every 32nd CTA; four experts' counts in flight
+  for (int e0 = (threadIdx.x >> 5) * 4; e0 < a.E; e0 += 4 * WARPS) {
+    int c[4][MAX_BLOCKS / 32];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+      for (int j = 0; j < MAX_BLOCKS / 32; ++j)
+        c[i][j] = e0 + i < a.E && 32 * j + lane < a.blocks ? a.counts[(e0 + i) * MAX_BLOCKS + 32 * j + lane] : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      int total = 0, before = 0;
+#pragma unroll
+      for (int j = 0; j < MAX_BLOCKS / 32; ++j) {
+        total += c[i][j];
+        if (32 * j + lane < mine) before += c[i][j];
+      }
+      total = __reduce_add_sync(0xFFFFFFFFu, total);
+      before = __reduce_add_sync(0xFFFFFFFFu, before);
+      if (lane == 0 && e0 + i < a.E) {
+        totals[e0 + i] = total;
+        next[e0 + i] = before;
+      }
     }
   }
+  __syncthreads();
+  const int e = threadIdx.x;
+  const int total = e < a.E ? totals[e] : 0;
   int all;
   const int first = scan(total, warp_sums, &all);
   if (e < a.E) {
-    next[e] = first + before;
+    next[e] += first;
     if (blockIdx.x == 0) a.offsets[e] = first;
   }
   if (blockIdx.x == 0 && e == 0) a.offsets[a.E] = all;
@@ -341,7 +377,7 @@ cudaError_t launch(const void* fn, int64_t blocks, int threads, void** args, cud
 
 int64_t route_count_bytes(int64_t T, int E) {
   const int64_t blocks = ceil_div(T, tokens_per_block(T > 0 ? T : 1));
-  return blocks > 1 ? 4 * blocks * E : 0;
+  return blocks > 1 ? 4ll * MAX_BLOCKS * E : 0;
 }
 
 cudaError_t launch_route(const RouteProblem& p, cudaStream_t stream) {
