@@ -149,12 +149,14 @@ mxfp8_status run_product(const Product& p, void* workspace, size_t workspace_byt
     g.xs = ws + l.s;
     g.xs_row = 1;
     g.xs_kt = p.R;
+    g.offsets_ready = 1;
   } else if (turned > 0) {
     cudaError_t e = mx::launch_transpose_words(p.x_scale, p.R, KT, workspace, as_stream(stream));
     if (e != cudaSuccess) return cuda_fail(e, "activation scale repack launch");
     g.xs = workspace;
     g.xs_row = 1;
     g.xs_kt = p.R;
+    g.offsets_ready = 1;
   }
   const char* msg = "";
   cudaError_t e = mx::launch_gemm_grouped(g, mx::grouped_plan(p.fmt, p.E, p.R, p.N, p.K, p.offsets != nullptr), sms,
@@ -446,6 +448,7 @@ mxfp8_status mxfp8_expert_mlp(int fmt, const void* x_bf16, int64_t T, int64_t K,
   g.bias_stride = 0;
   g.out = h;
   g.offsets = offsets;
+  g.offsets_ready = 1;
   g.E = E;
   g.R = R;
   g.N = 2 * F;

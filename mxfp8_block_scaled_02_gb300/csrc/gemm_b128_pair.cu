@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     tmem_relinquish_pair();
   }
   if (a.offsets != nullptr) {
-    grid_dependency_wait();
+    if (!a.offsets_ready) grid_dependency_wait();
     load_offsets(a, table, THREADS);
   }
   tc_fence_before();

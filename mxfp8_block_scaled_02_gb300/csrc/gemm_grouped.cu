@@ -178,6 +178,35 @@ __global__ void __launch_bounds__(Cfg<FMT, CG, TN>::THREADS, 1)
     }
     if (lane == 0) *abort_flag = 0;
     fence_mbar_init();
+    __syncwarp();
+  }
+  // The weights of stage s at K tile kt of tile t, and what the stage waits for.  Both
+  // CTAs' operands complete on the even CTA's `full`, whose bytes the even CTA alone
+  // posts.  (They may land before the post, not a phase early: the stage was freed by
+  // a commit behind the MMA that waited for the last phase.)
+  const uint32_t base = smem_u32(smem);
+  const uint32_t elected = elect_one();
+  auto load_weights = [&](int s, int kt, const Tile& t) {
+    const int rt = t.wt * CG + rank;
+    const uint32_t bar = (CG == 2 ? map_shared_rank(smem_u32(full), 0) : smem_u32(full)) + s * 8;
+    expect_tx(leader ? elected : 0u, &full[s], CG * W_BYTES + t.width * BK);
+    tma_load<CG>(elected, base + C::OFF_W + s * W_BYTES, &tmW, bar, kt * BK, rt * ROWS, t.e);
+    if (MX && elected) {
+      mbar_arrive_expect_tx(&sf_full[s], kAtomBytes);
+      bulk_load(smem + C::OFF_SFW + s * C::SF_BYTES,
+                static_cast<const uint8_t*>(a.ws) +
+                    ((static_cast<int64_t>(t.e) * a.KT + kt) * a.RTW + min(rt, a.RTW - 1)) * kAtomBytes,
+                kAtomBytes, &sf_full[s]);
+    }
+    __syncwarp();
+  };
+  // Without offsets the first round of weights needs nothing but this warp's barriers
+  // (one CTA a tile; on a pair, the other CTA's too).
+  int early = 0;
+  if (CG == 1 && warp == 0 && a.offsets == nullptr && worker < unit_count<TN>(a, table)) {
+    const Tile t = tile_of<STEP, TN>(worker, a, table);
+    early = min(STAGES, kt1 - kt0);
+    for (int s = 0; s < early; ++s) load_weights(s, kt0 + s, t);
   }
   if (threadIdx.x == 96) {
     prefetch_tmap(&tmW);
@@ -194,7 +223,7 @@ __global__ void __launch_bounds__(Cfg<FMT, CG, TN>::THREADS, 1)
     }
   }
   if (a.offsets != nullptr) {
-    grid_dependency_wait();
+    if (!a.offsets_ready) grid_dependency_wait();
     load_offsets(a, table, C::THREADS);
   }
   tc_fence_before();
@@ -211,16 +240,10 @@ __global__ void __launch_bounds__(Cfg<FMT, CG, TN>::THREADS, 1)
   if (CG == 1) launch_dependents();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
   const int units = unit_count<TN>(a, table);
-  const uint32_t base = smem_u32(smem);
 
   if (warp < 4) {
     if (warp == 0 || warp == 2) {
     // ------------------------------------------------------------ producers
-    // Both CTAs' operands complete on the even CTA's `full`, whose bytes the even
-    // CTA alone posts.  (They may land before the post, not a phase early: the
-    // stage was freed by a commit behind the MMA that waited for the last phase.)
-    const uint32_t elected = elect_one();
-    const uint32_t poster = leader ? elected : 0u;
     const uint32_t full_bar = CG == 2 ? map_shared_rank(smem_u32(full), 0) : smem_u32(full);
     if (warp == 2) grid_dependency_wait();
     int stage = 0;
@@ -231,10 +254,6 @@ __global__ void __launch_bounds__(Cfg<FMT, CG, TN>::THREADS, 1)
       const Tile t = tile_of<STEP, TN>(u, a, table);
       const int mine = t.width / CG;  // rows of x this CTA stages
       const int x0 = t.row0 + rank * mine;
-      const int rt = t.wt * CG + rank;
-      const uint8_t* atoms = MX ? static_cast<const uint8_t*>(a.ws) +
-                                      (static_cast<int64_t>(t.e) * a.KT * a.RTW + min(rt, a.RTW - 1)) * kAtomBytes
-                                : nullptr;
       for (int kt = kt0; kt < kt1; ++kt, ++issued) {
         if (!mbar_wait_warp(&empty[stage], phase, abort_flag)) {
           ok = false;
@@ -242,14 +261,7 @@ __global__ void __launch_bounds__(Cfg<FMT, CG, TN>::THREADS, 1)
         }
         const uint32_t bar = full_bar + stage * 8;
         if (warp == 0) {
-          expect_tx(poster, &full[stage], CG * (W_BYTES + mine * BK));
-          tma_load<CG>(elected, base + C::OFF_W + stage * W_BYTES, &tmW, bar, kt * BK, rt * ROWS, t.e);
-          if (MX && elected) {
-            mbar_arrive_expect_tx(&sf_full[stage], kAtomBytes);
-            bulk_load(smem + C::OFF_SFW + stage * C::SF_BYTES, atoms + static_cast<int64_t>(kt) * a.RTW * kAtomBytes,
-                      kAtomBytes, &sf_full[stage]);
-          }
-          __syncwarp();
+          if (issued >= early) load_weights(stage, kt, t);
         } else if (mine == C::XROWS) {
           tma_load<CG>(elected, base + C::OFF_X + stage * C::X_BYTES, &tmX, bar, kt * BK, x0, 0);
         } else {
@@ -275,7 +287,6 @@ __global__ void __launch_bounds__(Cfg<FMT, CG, TN>::THREADS, 1)
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (even CTA)
     if (leader) {
-      const uint32_t elected = elect_one();
       const uint64_t wd0 = sdesc_kmajor_sw128(base + C::OFF_W), xd0 = sdesc_kmajor_sw128(base + C::OFF_X);
       int stage = 0, n = 0;  // n: accumulators begun (MXFP8), blocks of K (fp8_128)
       uint32_t phase = 0;
@@ -362,16 +373,16 @@ __global__ void __launch_bounds__(Cfg<FMT, CG, TN>::THREADS, 1)
         if (f_u >= units) return;
         const Tile t = tile_of<STEP, TN>(f_u, a, table);
         f_rows = t.rows;
-        f_x = reinterpret_cast<const float*>(a.xs) + static_cast<int64_t>(t.row0 + lane) * a.xs_row;
+        f_x = reinterpret_cast<const float*>(a.xs) + static_cast<int64_t>(t.row0 + lane) * a.xs_row + kt0 * a.xs_kt;
         const int rt = min(t.wt * CG + rank, a.RTW - 1);
-        f_w = static_cast<const float*>(a.ws) + (static_cast<int64_t>(t.e) * a.RTW + rt) * a.KT;
+        f_w = static_cast<const float*>(a.ws) + (static_cast<int64_t>(t.e) * a.RTW + rt) * a.KT + kt0;
       };
       auto fetch = [&]() {
         if (f_u >= units) return;
-        w = __ldg(f_w + f_kt);
-        const float* p = f_x + f_kt * a.xs_kt;
+        w = __ldg(f_w++);
 #pragma unroll
-        for (int i = 0; i < NR; ++i) x[i] = lane + 32 * i < f_rows ? __ldg(p + 32 * i * a.xs_row) : 0.f;
+        for (int i = 0; i < NR; ++i) x[i] = lane + 32 * i < f_rows ? __ldg(f_x + 32 * i * a.xs_row) : 0.f;
+        f_x += a.xs_kt;
         if (++f_kt == kt1) {
           f_kt = kt0;
           f_u += nworkers;
@@ -556,7 +567,6 @@ __global__ void __launch_bounds__(Cfg<FMT, CG, TN>::THREADS, 1)
     const bool split = CG == 1 && TN <= 64 && a.splits > 1;
 
     int n = 0;  // accumulators (MXFP8) or blocks of K (fp8_128) so far
-    bool ok = true;
     if constexpr (MX) {
       for (int u = worker; u < units; u += nworkers, ++n) {
         start_tile(u);
@@ -602,81 +612,61 @@ __global__ void __launch_bounds__(Cfg<FMT, CG, TN>::THREADS, 1)
     } else {
       int slot = 0;
       uint32_t sphase = 0;
-      for (int u = worker; ok && u < units; u += nworkers) {
-        // columns of this warp that are in use, if positive
-        const int cols = tile_of<STEP, TN>(u, a, table).width - col_base;
+      for (int u = worker; u < units; u += nworkers) {
         float acc[NCH][2][4 * NG];  // as the fragments
 #pragma unroll
         for (int i = 0; i < NCH * 8 * NG; ++i) (&acc[0][0][0])[i] = 0.f;
-        // CH columns of all 32 lanes at a time: the next ones are on their way while
-        // one lot is added, also over the end of a block of K.
+        // CH columns of all 32 lanes at a time (those that are not the tile's are added
+        // like the others and not stored): the next ones are on their way while one lot
+        // is added.
         constexpr int RB = NCH > 1 ? 2 : 1;
         uint32_t r[RB][2][4 * NG];
         float4 f[RB][CH / 16];
-        auto load = [&](int blk, int sl, int i) {
-          const uint32_t src = lanes + (blk % BUFS) * C::ACOLS + i * CH;
+        auto load = [&](int i) {
+          const uint32_t src = lanes + (n % BUFS) * C::ACOLS + i * CH;
           tmem_ld_frag(src, r[i % RB][0]);
           tmem_ld_frag(src + (16u << 16), r[i % RB][1]);
           const float4* sc =
-              reinterpret_cast<const float4*>(smem + C::OFF_SC) + (sl * TN + col_base + i * CH) / 4 + (lane & 3);
+              reinterpret_cast<const float4*>(smem + C::OFF_SC) + (slot * TN + col_base + i * CH) / 4 + (lane & 3);
 #pragma unroll
           for (int k = 0; k < CH / 16; ++k) f[i % RB][k] = sc[4 * k];
         };
-        // block blk of K (in buffer blk % BUFS) and its scales have come
-        auto arrived = [&](int blk, int sl, uint32_t ph) {
-          const int b = blk % BUFS;
-          const uint32_t bp = static_cast<uint32_t>((blk / BUFS) & 1);
-          bool come = __all_sync(0xFFFFFFFFu, mbar_try_wait(&sc_full[sl], ph) && mbar_try_wait(&buf_full[b], bp));
-          if (!come)
-            come = __all_sync(0xFFFFFFFFu, mbar_wait_inline(&sc_full[sl], ph, abort_flag) &&
-                                               mbar_wait_inline(&buf_full[b], bp, abort_flag));
+        for (int kt = kt0; kt < kt1; ++kt) {
+          // the sums of block n (in buffer n % BUFS) and its scales; a wait that ran out
+          // only makes the later ones return at once
+          const uint32_t bp = static_cast<uint32_t>((n / BUFS) & 1);
+          if (!mbar_try_wait(&sc_full[slot], sphase)) mbar_wait_inline(&sc_full[slot], sphase, abort_flag);
+          if (!mbar_try_wait(&buf_full[n % BUFS], bp)) mbar_wait_inline(&buf_full[n % BUFS], bp, abort_flag);
+          __syncwarp();
           tc_fence_after();
-          return come;
-        };
-        ok = arrived(n, slot, sphase);
-        if (ok && cols > 0) load(n, slot, 0);
-        for (int kt = kt0; ok && kt < kt1; ++kt, ++n) {
-          int next_slot = slot + 1;
-          uint32_t next_phase = sphase;
-          if (next_slot == SLOTS) {
-            next_slot = 0;
-            next_phase ^= 1u;
-          }
+          load(0);
 #pragma unroll
           for (int i = 0; i < NCH; ++i) {
             tmem_ld_wait();
             if (i + 1 < NCH) {
-              if ((i + 1) * CH < cols) load(n, slot, i + 1);
+              load(i + 1);
             } else {
               release(n % BUFS);
               if (lane == 0) mbar_arrive(&sc_free[slot]);
-              if (RB == 2 && kt + 1 < kt1) {
-                ok = arrived(n + 1, next_slot, next_phase);
-                if (cols > 0) load(n + 1, next_slot, 0);
-              }
             }
-            if (i * CH < cols) {
 #pragma unroll
-              for (int g = 0; g < NG; ++g) {
-                const float4 q = f[i % RB][g >> 1];
+            for (int g = 0; g < NG; ++g) {
+              const float4 q = f[i % RB][g >> 1];
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {  // the four sums of a column one after the other
-                  const float sc = g & 1 ? (c ? q.w : q.z) : (c ? q.y : q.x);
+              for (int c = 0; c < 2; ++c) {  // the four sums of a column one after the other
+                const float sc = g & 1 ? (c ? q.w : q.z) : (c ? q.y : q.x);
 #pragma unroll
-                  for (int k = 0; k < 4; ++k)
-                    add_scaled(acc[i][k >> 1][4 * g + 2 * (k & 1) + c], r[i % RB][k >> 1][4 * g + 2 * (k & 1) + c], sc);
-                }
+                for (int k = 0; k < 4; ++k)
+                  add_scaled(acc[i][k >> 1][4 * g + 2 * (k & 1) + c], r[i % RB][k >> 1][4 * g + 2 * (k & 1) + c], sc);
               }
-            }
-            if (RB == 1 && kt + 1 < kt1) {
-              ok = arrived(n + 1, next_slot, next_phase);
-              if (cols > 0) load(n + 1, next_slot, 0);
             }
           }
-          slot = next_slot;
-          sphase = next_phase;
+          ++n;
+          if (++slot == SLOTS) {
+            slot = 0;
+            sphase ^= 1u;
+          }
         }
-        if (!ok) break;
         start_tile(u);
 #pragma unroll
         for (int g = 0; g < COLS / 8; ++g) {
@@ -792,6 +782,7 @@ GroupedArgs grouped_args(const GroupedProblem& p, int cg, int splits) {
   a.WT = static_cast<int>(ceil_div(p.N, cg * kGW_Rows));
   a.KT = static_cast<int>(ceil_div(p.K, kGBK));
   a.splits = splits;
+  a.offsets_ready = p.offsets_ready;
   a.w_fast = p.R / p.E >= p.N ? 1 : 0;
   a.xs = static_cast<const uint32_t*>(p.xs);
   a.xs_row = p.xs_row;
@@ -809,19 +800,50 @@ int64_t grouped_max_tiles(int64_t E, int64_t R, bool ragged, int tn) {
   return (E < R ? E : R) + R / tn;
 }
 
-// The kernel for a shape, by the rows a group has on average (with offsets the
-// host knows no more) and the tiles there can be.
+namespace {
+
+// Estimated time of a shape on one CTA a tile with up to tn rows of x and K split s
+// ways, or on pairs (tn = 256), in 0.01 us.  Measured (us, fp8_128, weights from HBM;
+// the quantise kernel and the launches, 6 to 8, included): a stage of K takes 0.24 to
+// 0.26 with up to 64 rows, 0.36 with 128 and on pairs; N = K = 4096, M = 1, one to
+// eight splits 13.7 / 11.0 / 10.9 / 21.6 (two waves of clusters); M = 200, 64 rows a
+// tile 17.6, 128 20.5, pairs 23.0; M = 512 25.9 / 20.2 / 20.3; N = 14336, K = 4096,
+// M = 48 18.6 / 18.7 / 22.0, M = 256 34.6 / 31.1 / 22.1; N = 1000, K = 4096, M = 333,
+// 64 rows and two splits 15.1, one 16.2, 128 rows 20.1, pairs 22.3.
+int64_t plan_cost(int64_t groups, int64_t rows, int64_t N, int64_t K, int tn, int splits) {
+  const int64_t stages = ceil_div(K, kGBK);
+  const int64_t workers = tn == 256 ? 76 : 152;
+  const int64_t tiles = groups * ceil_div(rows, tn) * ceil_div(N, tn == 256 ? 256 : 128) * splits;
+  const int64_t stage = tn >= 128 ? 36 : (tn == 64 ? 26 : 24);
+  const int64_t tile = stage * ceil_div(stages, splits) + (splits > 1 ? 230 : 150);
+  const int64_t bytes = groups * N * K / 65000;  // the weights at 6.5 TB/s
+  const int64_t t = ceil_div(tiles, workers) * tile;
+  return t > bytes ? t : bytes + tn;  // bound by the weights: the narrowest
+}
+
+}  // namespace
+
+// With offsets the host knows the rows a group has only on average, and groups
+// without rows only where there are fewer rows than groups.
 GroupedPlan grouped_plan(int fmt, int64_t E, int64_t R, int64_t N, int64_t K, bool ragged) {
   (void)fmt;
-  GroupedPlan p = {2, 256, 1};
-  const int64_t rows = ceil_div(R, E);
-  if (rows > 128) return p;
-  p.cg = 1;
-  p.tn = rows <= 16 ? 16 : (rows <= 32 ? 32 : (rows <= 64 ? 64 : 128));
-  const int64_t tiles = grouped_max_tiles(E, R, ragged, p.tn) * ceil_div(N, ROWS);
-  const int64_t stages = ceil_div(K, BK);
-  while (p.tn <= 64 && p.splits < 8 && tiles * p.splits * 2 <= 144 && stages >= 2 * p.splits * 2) p.splits *= 2;
-  return p;
+  const int64_t groups = E < R ? E : (R > 0 ? R : 1), rows = ceil_div(R, groups);
+  GroupedPlan best = {2, 256, 1};
+  int64_t least = plan_cost(groups, rows, N, K, 256, 1);
+  for (int tn = 128; tn >= 16; tn >>= 1) {
+    // at most eight tiles of x a group: each reads the weights again, from L2
+    if (ceil_div(rows, tn) > 8) break;
+    for (int s = 1; s <= (tn <= 64 ? 8 : 1); s <<= 1) {
+      // split, a cluster does one tile: all of them, however the rows fall, at once
+      if (s > 1 && (grouped_max_tiles(E, R, ragged, tn) * ceil_div(N, kGW_Rows) * s > 152 || ceil_div(K, kGBK) < 2 * s)) break;
+      const int64_t c = plan_cost(groups, rows, N, K, tn, s);
+      if (c <= least) {
+        least = c;
+        best = {1, tn, s};
+      }
+    }
+  }
+  return best;
 }
 
 cudaError_t launch_gemm_grouped(const GroupedProblem& p, const GroupedPlan& plan, int sms, cudaStream_t stream,

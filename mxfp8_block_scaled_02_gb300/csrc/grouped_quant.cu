@@ -32,6 +32,7 @@ namespace {
 constexpr int THREADS = 256;
 constexpr int UNROLL = 4;
 constexpr int TASK = 512;  // elements of a row per warp and task
+constexpr int FEW_TASKS = 152 * 8 * 2;  // up to so many a warp has one: latency, not bandwidth
 
 // 448 / amax, and what x is multiplied by before it (a power of two: 1 but for an
 // amax so small that the quotient would overflow).
@@ -162,10 +163,10 @@ __device__ __forceinline__ Codes quantize16_mx(const float (&y)[16], int lane, u
 __global__ void __launch_bounds__(THREADS) transpose_words_kernel(const uint32_t* __restrict__ in, int64_t R, int KT,
                                                                   uint32_t* __restrict__ out) {
   __shared__ uint32_t box[32][33];
-  launch_dependents();
   const int64_t r0 = static_cast<int64_t>(blockIdx.x) * 32;
   const int k0 = blockIdx.y * 32, x = threadIdx.x & 31, y = threadIdx.x >> 5;
   grid_dependency_wait();
+  launch_dependents();  // in this order, as above
 #pragma unroll
   for (int i = 0; i < 32; i += THREADS / 32)
     if (r0 + y + i < R && k0 + x < KT) box[y + i][x] = in[(r0 + y + i) * KT + k0 + x];
@@ -198,19 +199,21 @@ struct RowsArgs {
 };
 
 // K % 16 == 0; MXFP8 K % 128 == 0.
-template <int FMT, bool kEarly>
+template <int FMT, bool kEarly, int U>
 __global__ void __launch_bounds__(THREADS) quantize_rows_kernel(const RowsArgs a) {
+  // In this order: when the next kernel starts, all before this one is done, and it
+  // may read what this one does not write (GroupedProblem::offsets_ready).
   if (kEarly) {
-    launch_dependents();
     grid_dependency_wait();
+    launch_dependents();
   }
   const int lane = threadIdx.x & 31;
-  const int64_t first = (static_cast<int64_t>(blockIdx.x) * (THREADS / 32) + (threadIdx.x >> 5)) * UNROLL;
-  uint32_t v[UNROLL][8];
-  int64_t row[UNROLL];
-  int k[UNROLL];
+  const int64_t first = (static_cast<int64_t>(blockIdx.x) * (THREADS / 32) + (threadIdx.x >> 5)) * U;
+  uint32_t v[U][8];
+  int64_t row[U];
+  int k[U];
 #pragma unroll
-  for (int i = 0; i < UNROLL; ++i) {
+  for (int i = 0; i < U; ++i) {
     const int64_t task = first + i;
     row[i] = task / a.segs;
     k[i] = static_cast<int>(task - row[i] * a.segs) * TASK + lane * 16;
@@ -224,7 +227,7 @@ __global__ void __launch_bounds__(THREADS) quantize_rows_kernel(const RowsArgs a
     }
   }
 #pragma unroll
-  for (int i = 0; i < UNROLL; ++i) {
+  for (int i = 0; i < U; ++i) {
     if (first + i >= a.tasks) return;  // the whole warp
     uint32_t word;
     Codes c;
@@ -256,13 +259,12 @@ struct ActArgs {
 
 // y = gate / (1 + exp(-gate)) * up, quantised: the values of silu_mul_kernel
 // (fused_quant.cu), and in MXFP8 its bytes.
-template <int FMT>
+template <int FMT, int U>
 __global__ void __launch_bounds__(THREADS) silu_mul_rows_kernel(const ActArgs a) {
-  launch_dependents();
   const int lane = threadIdx.x & 31;
-  constexpr int U = UNROLL / 2;
   const int64_t first = (static_cast<int64_t>(blockIdx.x) * (THREADS / 32) + (threadIdx.x >> 5)) * U;
   grid_dependency_wait();
+  launch_dependents();  // in this order, as above
   uint32_t g[U][8], u[U][8];
   int64_t row[U];
   int k[U];
@@ -373,6 +375,21 @@ cudaError_t launch(const void* fn, int64_t blocks, void** args, bool programmati
   return cudaLaunchKernelExC(&cfg, fn, args);
 }
 
+template <int FMT, bool kEarly>
+const void* rows_kernel_of(bool few) {
+  return few ? reinterpret_cast<const void*>(quantize_rows_kernel<FMT, kEarly, 1>)
+             : reinterpret_cast<const void*>(quantize_rows_kernel<FMT, kEarly, UNROLL>);
+}
+const void* rows_kernel(int fmt, bool early, bool few) {
+  if (fmt == kG8MX) return early ? rows_kernel_of<kG8MX, true>(few) : rows_kernel_of<kG8MX, false>(few);
+  return early ? rows_kernel_of<kG8B128, true>(few) : rows_kernel_of<kG8B128, false>(few);
+}
+template <int U>
+const void* act_kernel(int fmt) {
+  return fmt == kG8MX ? reinterpret_cast<const void*>(silu_mul_rows_kernel<kG8MX, U>)
+                      : reinterpret_cast<const void*>(silu_mul_rows_kernel<kG8B128, U>);
+}
+
 inline bool is32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31) == 0; }
 
 }  // namespace
@@ -390,12 +407,10 @@ cudaError_t launch_quantize_rows(const QuantRowsProblem& p, cudaStream_t stream)
   a.s = static_cast<uint32_t*>(p.s);
   a.s_row = p.s_row;
   a.s_kt = p.s_kt;
-  const void* fn = p.fmt == kG8MX ? (p.early ? reinterpret_cast<const void*>(quantize_rows_kernel<kG8MX, true>)
-                                             : reinterpret_cast<const void*>(quantize_rows_kernel<kG8MX, false>))
-                                  : (p.early ? reinterpret_cast<const void*>(quantize_rows_kernel<kG8B128, true>)
-                                             : reinterpret_cast<const void*>(quantize_rows_kernel<kG8B128, false>));
+  const bool few = a.tasks <= FEW_TASKS;
+  const void* fn = rows_kernel(p.fmt, p.early, few);
   void* args[] = {&a};
-  return launch(fn, ceil_div(a.tasks, UNROLL * (THREADS / 32)), args, p.early, stream);
+  return launch(fn, ceil_div(a.tasks, (few ? 1 : UNROLL) * (THREADS / 32)), args, p.early, stream);
 }
 
 cudaError_t launch_silu_mul_rows(const ActRowsProblem& p, cudaStream_t stream) {
@@ -412,10 +427,10 @@ cudaError_t launch_silu_mul_rows(const ActRowsProblem& p, cudaStream_t stream) {
   a.s = static_cast<uint32_t*>(p.s);
   a.s_row = p.s_row;
   a.s_kt = p.s_kt;
-  const void* fn = p.fmt == kG8MX ? reinterpret_cast<const void*>(silu_mul_rows_kernel<kG8MX>)
-                                  : reinterpret_cast<const void*>(silu_mul_rows_kernel<kG8B128>);
+  const bool few = a.tasks <= FEW_TASKS;
+  const void* fn = few ? act_kernel<1>(p.fmt) : act_kernel<UNROLL / 2>(p.fmt);
   void* args[] = {&a};
-  return launch(fn, ceil_div(a.tasks, UNROLL / 2 * (THREADS / 32)), args, true, stream);
+  return launch(fn, ceil_div(a.tasks, (few ? 1 : UNROLL / 2) * (THREADS / 32)), args, true, stream);
 }
 
 cudaError_t launch_transpose_words(const void* in, int64_t R, int64_t KT, void* out, cudaStream_t stream) {

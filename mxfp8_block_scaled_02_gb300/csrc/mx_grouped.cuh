@@ -136,6 +136,7 @@ struct GroupedArgs {
   int WT;                 // weight tiles of CG * 128 rows
   int KT;                 // stages of K
   int splits;             // K splits = cluster size (CG = 1)
+  int offsets_ready;      // GroupedProblem::offsets_ready
   int w_fast;             // 1: weight tiles vary fastest within a group, 0: tiles of x
   const uint32_t* xs;     // scales of x: word (r, kt) at r * xs_row + kt * xs_kt holds the
   int64_t xs_row, xs_kt;  // four E8M0 bytes (MXFP8) or the fp32 (fp8_128) of 128 elements

@@ -27,6 +27,10 @@ struct GroupedProblem {
   void* out;              // bf16 [R, N]
   const int* offsets;     // device, [E + 1], or nullptr
   int64_t E, R, N, K;
+  // 1: the kernel before this one in the stream does not write the offsets and lets
+  // this one start only when all before it is done (the kernels of grouped_quant.cu):
+  // offsets, weights and their scales are read without waiting for it
+  int offsets_ready = 0;
 };
 // How a shape is run: a CTA pair (cg = 2) or one CTA a tile, the rows of x a tile
 // takes at most, and the K splits.
