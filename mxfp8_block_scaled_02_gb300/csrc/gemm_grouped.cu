@@ -768,8 +768,9 @@ bool grouped_maps(const GroupedProblem& p, int box_rows, CUtensorMap* mw, CUtens
   const auto sw = CU_TENSOR_MAP_SWIZZLE_128B;
   const auto l2 = CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
   return encode_map3(mw, u8, p.w, p.K, p.N, p.E, p.K, p.N * p.K, kGBK, kGW_Rows, sw, l2) &&
-         encode_map3(mx, u8, p.x, p.K, p.R, 1, p.K, p.R * p.K, kGBK, box_rows, sw, l2) &&
-         encode_map3(mbox, u8, p.x, p.K, p.R, 1, p.K, p.R * p.K, kGBK, kGBox, sw, l2);
+         encode_map3(mbox, u8, p.x, p.K, p.R, 1, p.K, p.R * p.K, kGBK, kGBox, sw, l2) &&
+         (box_rows == kGBox ? (*mx = *mbox, true)
+                            : encode_map3(mx, u8, p.x, p.K, p.R, 1, p.K, p.R * p.K, kGBK, box_rows, sw, l2));
 }
 
 GroupedArgs grouped_args(const GroupedProblem& p, int cg, int splits) {

@@ -978,9 +978,12 @@ def gated_mlp(x: torch.Tensor, norm_weight: torch.Tensor, gate_up: PackedWeights
 def _here(*ts: torch.Tensor | None) -> None:
     """Contiguous tensors on the current CUDA device (whose stream the call goes to)."""
     for t in ts:
-        if t is not None and not (t.is_cuda and t.is_contiguous() and t.get_device() == torch._C._cuda_getDevice()):
+        if t is not None and not (t.is_cuda and t.is_contiguous() and t.get_device() == _current_device()):
             _require_cuda(t)
-            raise ValueError(f"tensor on cuda:{t.get_device()}, the current device is cuda:{torch._C._cuda_getDevice()}")
+            raise ValueError(f"tensor on cuda:{t.get_device()}, the current device is cuda:{_current_device()}")
+
+
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else (lambda: -1)
 
 
 def _k_blocks(K: int) -> int:
@@ -1071,35 +1074,55 @@ def linear_fp8_128(x: torch.Tensor, pw: PackedWeights, bias: torch.Tensor | None
     batched weights x is [B, M, K].  Returns bf16 [..., N]."""
     if pw.fmt != "fp8_128":
         raise ValueError(f"linear_fp8_128 does not take {pw.fmt} weights")
+    # one pass, few helper calls, as linear_fp4
     K, N, B = pw.K, pw.N, pw.B
     quantized = x_scale is not None
     if not quantized and x.dtype is not _BF16:
         raise TypeError("x must be bfloat16 (or pass x_scale with a pre-quantised x)")
-    _here(x, bias, out, workspace)
+    if not (x.is_cuda and x.is_contiguous() and x.get_device() == _current_device()):
+        _here(x)
     shape = x.shape
     if not shape or shape[-1] != K:
         raise ValueError(f"x {tuple(shape)} does not match weights with K={K}")
     if pw.batched and (len(shape) != 3 or shape[0] != B):
         raise ValueError("batched weights need x of shape [B, M, K]")
-    if bias is not None and (bias.dtype is not _BF16 or tuple(bias.shape) != (N,)):
-        raise ValueError("bias must be bf16 [N]")
     rows = x.numel() // K
+    b_ptr = s_ptr = None
+    if bias is not None:
+        _here(bias)
+        if bias.dtype is not _BF16 or bias.dim() != 1 or bias.shape[0] != N:
+            raise ValueError("bias must be bf16 [N]")
+        b_ptr = bias.data_ptr()
+        if b_ptr & 15:
+            bias = _aligned16(bias)
+            b_ptr = bias.data_ptr()
     if quantized:
         x, x_scale = _quantised_x(x, x_scale, "fp8_128", K)
-    elif x.data_ptr() & 15:
-        x = _aligned16(x)
+        s_ptr = x_scale.data_ptr()
+    dev = x.device
     if out is None:
-        out = torch.empty(shape[:-1] + (N,), dtype=_BF16, device=x.device)
-    elif out.dtype is not _BF16 or out.numel() != rows * N or out.data_ptr() & 15:
-        raise ValueError(f"out must be bf16 with {rows * N} elements, 16-byte aligned")
+        out = torch.empty(shape[:-1] + (N,), dtype=_BF16, device=dev)
+    else:
+        _here(out)
+        if out.dtype is not _BF16 or out.numel() != rows * N or out.data_ptr() & 15:
+            raise ValueError(f"out must be bf16 with {rows * N} elements, 16-byte aligned")
     if rows == 0:
         return out
     M = rows // B
-    bias = _aligned16(bias)
-    ws_ptr, ws_bytes, workspace = _workspace(workspace, workspace_size_fp8_128(B, M, N, K, quantized), x.device)
     x_ptr = x.data_ptr()
-    _check(load().mxfp8_b128_linear(None if quantized else x_ptr, x_ptr if quantized else None, _ptr(x_scale), B, M, N, K,
-                                    pw.w_packed.data_ptr(), pw.sf_packed.data_ptr(), _ptr(bias), out.data_ptr(), ws_ptr,
+    if x_ptr & 15:
+        x = _aligned16(x)
+        x_ptr = x.data_ptr()
+    need = 0 if quantized else workspace_size_fp8_128(B, M, N, K, False)
+    ws_ptr, ws_bytes = None, 0
+    if workspace is not None:
+        _here(workspace)
+        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    elif need:
+        workspace = torch.empty(need, dtype=_U8, device=dev)
+        ws_ptr, ws_bytes = workspace.data_ptr(), need
+    _check(load().mxfp8_b128_linear(None if quantized else x_ptr, x_ptr if quantized else None, s_ptr, B, M, N, K,
+                                    pw.w_packed.data_ptr(), pw.sf_packed.data_ptr(), b_ptr, out.data_ptr(), ws_ptr,
                                     ws_bytes, _stream()))
     return out
 
@@ -1147,8 +1170,11 @@ def _expert_weights(pw: PackedWeights, what: str) -> int:
     return GFMT[pw.fmt]
 
 
+_I32 = torch.int32
+
+
 def _int32(t: torch.Tensor, shape: tuple, name: str) -> int:
-    if t.dtype is not torch.int32 or tuple(t.shape) != shape:
+    if t.dtype is not _I32 or t.shape != shape:
         raise ValueError(f"{name} must be int32 {list(shape)}, not {t.dtype} {list(t.shape)}")
     return t.data_ptr()
 
@@ -1172,35 +1198,50 @@ def grouped_linear(x: torch.Tensor, pw: PackedWeights, offsets: torch.Tensor, x_
         raise TypeError("x must be bfloat16 (or pass x_scale with a pre-quantised x)")
     if quantized and rows is not None:
         raise ValueError("rows go with bf16 x")
-    _here(x, offsets, bias, rows, out, workspace)
-    if x.dim() != 2 or x.shape[1] != K:
-        raise ValueError(f"x {tuple(x.shape)} is not [rows, {K}]")
+    _here(x, offsets)
+    shape = x.shape
+    if len(shape) != 2 or shape[1] != K:
+        raise ValueError(f"x {tuple(shape)} is not [rows, {K}]")
     o_ptr = _int32(offsets, (E + 1,), "offsets")
-    T = R = x.shape[0]
-    r_ptr = None
+    T = R = shape[0]
+    r_ptr = b_ptr = s_ptr = None
     if rows is not None:
+        _here(rows)
         R = rows.numel()
         r_ptr = _int32(rows, (R,), "rows")
-    if bias is not None and (bias.dtype is not _BF16 or tuple(bias.shape) != (E, N)):
-        raise ValueError(f"bias must be bf16 [{E}, {N}]")
+    if bias is not None:
+        _here(bias)
+        if bias.dtype is not _BF16 or bias.shape != (E, N):
+            raise ValueError(f"bias must be bf16 [{E}, {N}]")
+        bias = _aligned16(bias)
+        b_ptr = bias.data_ptr()
     if quantized:
         x, x_scale = _quantised_x(x, x_scale, pw.fmt, K)
-    elif x.data_ptr() & 15:
-        x = _aligned16(x)
+        s_ptr = x_scale.data_ptr()
+    dev = x.device
     if out is None:
-        out = torch.empty((R, N), dtype=_BF16, device=x.device)
-    elif out.dtype is not _BF16 or tuple(out.shape) != (R, N) or out.data_ptr() & 15:
-        raise ValueError(f"out must be bf16 [{R}, {N}], 16-byte aligned")
+        out = torch.empty((R, N), dtype=_BF16, device=dev)
+    else:
+        _here(out)
+        if out.dtype is not _BF16 or out.shape != (R, N) or out.data_ptr() & 15:
+            raise ValueError(f"out must be bf16 [{R}, {N}], 16-byte aligned")
     if R == 0:
         return out
-    bias = _aligned16(bias)
-    ws_ptr, ws_bytes, workspace = _workspace(workspace, grouped_workspace_size(pw.fmt, E, R, N, K, quantized), x.device)
     x_ptr = x.data_ptr()
+    if x_ptr & 15:
+        x = _aligned16(x)
+        x_ptr = x.data_ptr()
+    need = grouped_workspace_size(pw.fmt, E, R, N, K, quantized)
+    ws_ptr, ws_bytes = None, 0
+    if workspace is not None or need:
+        if workspace is not None:
+            _here(workspace)
+        ws_ptr, ws_bytes, workspace = _workspace(workspace, need, dev)
     if not x_ptr:  # no token at all: every row is one of zeros
         x_ptr, T = ws_ptr, 0
-    _check(load().mxfp8_grouped_linear(f, None if quantized else x_ptr, T, r_ptr, x_ptr if quantized else None,
-                                       _ptr(x_scale), o_ptr, E, R, N, K, pw.w_packed.data_ptr(), pw.sf_packed.data_ptr(),
-                                       _ptr(bias), out.data_ptr(), ws_ptr, ws_bytes, _stream()))
+    _check(load().mxfp8_grouped_linear(f, None if quantized else x_ptr, T, r_ptr, x_ptr if quantized else None, s_ptr,
+                                       o_ptr, E, R, N, K, pw.w_packed.data_ptr(), pw.sf_packed.data_ptr(), b_ptr,
+                                       out.data_ptr(), ws_ptr, ws_bytes, _stream()))
     return out
 
 
@@ -1230,10 +1271,13 @@ def route_workspace_size(T: int, E: int, k: int) -> int:
 
 def _logits2d(logits: torch.Tensor) -> tuple[torch.Tensor, int]:
     """logits [T, E] fp32 or bf16, rows of any stride: (tensor, row stride)."""
-    if not logits.is_cuda or logits.get_device() != torch._C._cuda_getDevice():
+    if not logits.is_cuda or logits.get_device() != _current_device():
         raise ValueError("tensors must be on the current CUDA device")
-    if logits.dim() != 2 or logits.dtype not in (_F32, _BF16):
-        raise ValueError(f"logits must be fp32 or bf16 [tokens, experts], not {logits.dtype} {tuple(logits.shape)}")
+    dtype = logits.dtype
+    if logits.dim() != 2 or not (dtype is _F32 or dtype is _BF16):
+        raise ValueError(f"logits must be fp32 or bf16 [tokens, experts], not {dtype} {tuple(logits.shape)}")
+    if logits.is_contiguous():
+        return logits, logits.shape[1]
     if logits.shape[1] > 1 and logits.stride(1) != 1 or (logits.shape[0] > 1 and 0 < logits.stride(0) < logits.shape[1]):
         logits = logits.contiguous()
     return logits, logits.stride(0)
@@ -1248,24 +1292,30 @@ def route(logits: torch.Tensor, k: int, *, scoring: str = "softmax", renormalize
     ``scale``."""
     sc = _scoring(scoring)
     logits, stride = _logits2d(logits)
-    _here(workspace)
     T, E = logits.shape
     dev = logits.device
     need = route_workspace_size(T, E, k)  # checks T, E and k
-    r = Routing(torch.empty((T, k), dtype=torch.int32, device=dev), torch.empty((T, k), dtype=_F32, device=dev),
-                torch.empty(E + 1, dtype=torch.int32, device=dev), torch.empty(T * k, dtype=torch.int32, device=dev),
-                torch.empty((T, k), dtype=torch.int32, device=dev))
-    ws_ptr, ws_bytes, workspace = _workspace(workspace, need, dev)
+    empty, slots = torch.empty, (T, k)
+    ids = empty(slots, dtype=_I32, device=dev)
+    weights = empty(slots, dtype=_F32, device=dev)
+    offsets = empty(E + 1, dtype=_I32, device=dev)
+    rows = empty(T * k, dtype=_I32, device=dev)
+    positions = empty(slots, dtype=_I32, device=dev)
+    ws_ptr, ws_bytes = None, 0
+    if workspace is not None or need:
+        if workspace is not None:
+            _here(workspace)
+        ws_ptr, ws_bytes, workspace = _workspace(workspace, need, dev)
     _check(load().mxfp8_route(logits.data_ptr(), stride, logits.dtype is _BF16, T, E, k, sc, renormalize, scale,
-                              r.ids.data_ptr(), r.weights.data_ptr(), r.offsets.data_ptr(), r.rows.data_ptr(),
-                              r.positions.data_ptr(), ws_ptr, ws_bytes, _stream()))
-    return r
+                              ids.data_ptr(), weights.data_ptr(), offsets.data_ptr(), rows.data_ptr(),
+                              positions.data_ptr(), ws_ptr, ws_bytes, _stream()))
+    return Routing(ids, weights, offsets, rows, positions)
 
 
 def _added(add: torch.Tensor | None, shape: tuple) -> tuple[torch.Tensor | None, int]:
     if add is None:
         return None, 0
-    if add.dtype is not _BF16 or tuple(add.shape) != tuple(shape):
+    if add.dtype is not _BF16 or add.shape != shape:
         raise ValueError(f"add must be bf16 {list(shape)}, not {add.dtype} {list(add.shape)}")
     add, _, stride = _rows2d(add, "add", 8)
     return add, stride
@@ -1279,21 +1329,28 @@ def combine(y: torch.Tensor, routing: Routing, *, add: torch.Tensor | None = Non
     expert's output, a residual)."""
     if y.dtype is not _BF16 or y.dim() != 2:
         raise TypeError("y must be bfloat16 [rows, N]")
-    T, k = routing.positions.shape
-    N = y.shape[1]
-    _here(y, routing.positions, routing.weights, out)
-    p_ptr = _int32(routing.positions, (T, k), "positions")
-    if routing.weights.dtype is not _F32 or tuple(routing.weights.shape) != (T, k):
-        raise ValueError("weights must be fp32 like positions")
-    add, add_stride = _added(add, (T, N))
-    _here(out)
+    positions, weights = routing.positions, routing.weights
+    _here(y, positions, weights)
+    T, k = slots = positions.shape
+    R, N = y.shape
+    if positions.dtype is not _I32 or weights.dtype is not _F32 or weights.shape != slots:
+        raise ValueError("positions must be int32 [T, k] and weights fp32 of the same shape")
+    a_ptr, add_stride = None, 0
+    if add is not None:
+        add, add_stride = _added(add, (T, N))
+        a_ptr = add.data_ptr()
     if out is None:
         out = torch.empty((T, N), dtype=_BF16, device=y.device)
-    elif out.dtype is not _BF16 or tuple(out.shape) != (T, N) or out.data_ptr() & 15:
-        raise ValueError(f"out must be bf16 [{T}, {N}], 16-byte aligned")
-    y = _aligned16(y)
-    _check(load().mxfp8_combine(y.data_ptr(), y.shape[0], p_ptr, routing.weights.data_ptr(), T, k, N, _ptr(add),
-                                add_stride, out.data_ptr(), _stream()))
+    else:
+        _here(out)
+        if out.dtype is not _BF16 or out.shape != (T, N) or out.data_ptr() & 15:
+            raise ValueError(f"out must be bf16 [{T}, {N}], 16-byte aligned")
+    y_ptr = y.data_ptr()
+    if y_ptr & 15:
+        y = _aligned16(y)
+        y_ptr = y.data_ptr()
+    _check(load().mxfp8_combine(y_ptr, R, positions.data_ptr(), weights.data_ptr(), T, k, N, a_ptr, add_stride,
+                                out.data_ptr(), _stream()))
     return out
 
 
