@@ -604,8 +604,9 @@ mxfp8_status mxfp8_b128_silu_mul_quantize(const void* gate_bf16, int64_t gate_st
  *   [B, M, ceil(K / 128)].
  *   w E4M3 [B, N, K] and w_scale fp32 [B, ceil(N / 128), ceil(K / 128)] as a
  *   checkpoint holds them; no repack is needed.  bias bf16 [N] or NULL.
- *   workspace : >= mxfp8_b128_workspace_size bytes, 256-byte aligned (NULL for
- *   a quantised x).
+ *   workspace : >= mxfp8_b128_workspace_size bytes, 256-byte aligned (NULL when
+ *   that is 0: a quantised x, or B = 1 and up to eight rows of bf16 x, which the
+ *   product's kernel quantises to the same bytes).
  *   N % 8 == 0, K % 16 == 0 (else MXFP8_ERR_UNSUPPORTED); pointers 16-byte
  *   aligned; M = 0 is a no-op.
  *   Sums within a block and over the blocks are fp32; one rounding, after the

@@ -110,7 +110,9 @@ mxfp8_status run_product(const Product& p, void* workspace, size_t workspace_byt
     return fail(MXFP8_ERR_INVALID_ARG, "rows and offsets must be 4-byte aligned");
   const XLayout l = x_layout(p.R, p.K);
   const int64_t turned = have_q ? turned_bytes(p.fmt, p.E, p.R, p.N, p.K, p.offsets != nullptr) : 0;
-  const int64_t need = have_x ? l.total : turned;
+  const bool inside = have_x && p.fmt == MXFP8_GFMT_FP8_128 && p.rows == nullptr &&
+                      mx::b128_quantizes_inside(p.offsets != nullptr, p.E, p.R);
+  const int64_t need = inside ? 0 : (have_x ? l.total : turned);
   if (have_x) {
     if (p.T < 0 || p.T > kMaxRows || (p.rows == nullptr && p.T != p.R))
       return fail(MXFP8_ERR_INVALID_ARG, "x has %lld rows for %lld of the product", (ll)p.T, (ll)p.R);
@@ -140,7 +142,9 @@ mxfp8_status run_product(const Product& p, void* workspace, size_t workspace_byt
   g.R = p.R;
   g.N = p.N;
   g.K = p.K;
-  if (have_x) {
+  if (inside) {
+    g.x_bf16 = p.x_bf16;
+  } else if (have_x) {
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     const mx::QuantRowsProblem q{p.fmt, p.x_bf16, p.rows, p.T, p.R, p.K, ws, ws + l.s, 1, p.R, true};
     cudaError_t e = mx::launch_quantize_rows(q, as_stream(stream));
@@ -295,7 +299,8 @@ mxfp8_status mxfp8_b128_workspace_size(int64_t B, int64_t M, int64_t N, int64_t 
   if (B < 1 || M < 0 || M > kMaxRows || B > kMaxRows)
     return fail(MXFP8_ERR_INVALID_ARG, "B=%lld M=%lld", (ll)B, (ll)M);
   mxfp8_status st = check_product(MXFP8_GFMT_FP8_128, B, B * M, N, K, false);
-  if (st == MXFP8_OK) *bytes = x_is_quantized ? 0 : static_cast<size_t>(x_layout(B * M, K).total);
+  if (st == MXFP8_OK)
+    *bytes = x_is_quantized || mx::b128_quantizes_inside(false, B, B * M) ? 0 : static_cast<size_t>(x_layout(B * M, K).total);
   return st;
 }
 

@@ -36,6 +36,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "mx_block128.cuh"
 #include "mx_grouped.cuh"
 #include "mx_kernels.h"
 #include "mx_layout.cuh"
@@ -131,8 +132,20 @@ __device__ __forceinline__ void st_async_v4(uint32_t addr, float a, float b, flo
                : "memory");
 }
 
-template <int FMT, int CG, int TN>
-__global__ void __launch_bounds__(Cfg<FMT, CG, TN>::THREADS, 1)
+// kQuant: few rows of bf16 x of one group, quantised here (fp8_128): four more warps
+// load each stage's rows and write the codes where TMA would have put them and the
+// scales where warp 3 would, the bytes of the quantise kernel.  That saves a launch, a
+// workspace and the way through memory.
+constexpr int QUANT_WARPS = 4;
+constexpr int QUANT_ROWS = 8;
+
+template <int FMT, int CG, int TN, bool kQuant>
+constexpr int threads_of() {
+  return Cfg<FMT, CG, TN>::THREADS + (kQuant ? 32 * QUANT_WARPS : 0);
+}
+
+template <int FMT, int CG, int TN, bool kQuant>
+__global__ void __launch_bounds__(threads_of<FMT, CG, TN, kQuant>(), 1)
     gemm_grouped_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                         const __grid_constant__ CUtensorMap tmXbox, const Args a) {
   using C = Cfg<FMT, CG, TN>;
@@ -170,6 +183,7 @@ __global__ void __launch_bounds__(Cfg<FMT, CG, TN>::THREADS, 1)
     for (int i = lane; i < C::NBARS; i += 32) {
       uint32_t n = 1;
       uint64_t* b = &full[i];
+      if (kQuant && b < empty) n = 2;  // the copies, and the quantising warp
       if (MX && b >= sf_ready && b < buf_full) n = CG * C::SC_WARPS;
       if (b >= buf_free && b < sc_full) n = CG * C::EPI_WARPS;
       if (!MX && b >= sc_full && b < sc_free) n = C::SC_WARPS;
@@ -189,7 +203,7 @@ __global__ void __launch_bounds__(Cfg<FMT, CG, TN>::THREADS, 1)
   auto load_weights = [&](int s, int kt, const Tile& t) {
     const int rt = t.wt * CG + rank;
     const uint32_t bar = (CG == 2 ? map_shared_rank(smem_u32(full), 0) : smem_u32(full)) + s * 8;
-    expect_tx(leader ? elected : 0u, &full[s], CG * W_BYTES + t.width * BK);
+    expect_tx(leader ? elected : 0u, &full[s], CG * W_BYTES + (kQuant ? 0 : t.width * BK));
     tma_load<CG>(elected, base + C::OFF_W + s * W_BYTES, &tmW, bar, kt * BK, rt * ROWS, t.e);
     if (MX && elected) {
       mbar_arrive_expect_tx(&sf_full[s], kAtomBytes);
@@ -224,7 +238,7 @@ __global__ void __launch_bounds__(Cfg<FMT, CG, TN>::THREADS, 1)
   }
   if (a.offsets != nullptr) {
     if (!a.offsets_ready) grid_dependency_wait();
-    load_offsets(a, table, C::THREADS);
+    load_offsets(a, table, threads_of<FMT, CG, TN, kQuant>());
   }
   tc_fence_before();
   __syncthreads();
@@ -242,7 +256,7 @@ __global__ void __launch_bounds__(Cfg<FMT, CG, TN>::THREADS, 1)
   const int units = unit_count<TN>(a, table);
 
   if (warp < 4) {
-    if (warp == 0 || warp == 2) {
+    if (warp == 0 || (warp == 2 && !kQuant)) {
     // ------------------------------------------------------------ producers
     const uint32_t full_bar = CG == 2 ? map_shared_rank(smem_u32(full), 0) : smem_u32(full);
     if (warp == 2) grid_dependency_wait();
@@ -354,7 +368,7 @@ __global__ void __launch_bounds__(Cfg<FMT, CG, TN>::THREADS, 1)
       if (!ok) __nanosleep(200000);  // let issued tensor-core work retire
     }
     __syncwarp();
-    } else if (!MX && warp == 3) {
+    } else if (!MX && !kQuant && warp == 3) {
       // ---------------------------------------------------------- fp8_128: s_x s_w of a block of K and each row of x
       // Lane l prepares rows l, l + 32, ...  Column c = 16 J + 8 g + 2 q + b goes to
       // position 16 J + 4 q + 2 g + b: 16 bytes are what a thread of the epilogue
@@ -478,6 +492,68 @@ __global__ void __launch_bounds__(Cfg<FMT, CG, TN>::THREADS, 1)
         if (++stage == STAGES) {
           stage = 0;
           phase ^= 1u;
+        }
+      }
+    }
+  } else if (kQuant && warp >= C::EPI_FIRST + C::EPI_WARPS) {
+    if constexpr (kQuant) {
+      // ---------------------------------------------------------- quantisers
+      // Warp q takes every QUANT_WARPS-th stage: eight lanes a row, four rows at a
+      // time, sixteen elements a lane.  (It waits for a slot that was freed at most
+      // one round ago: the stages and slots are at least QUANT_WARPS.)
+      static_assert(!MX && CG == 1 && TN == 16 && STAGES >= QUANT_WARPS && SLOTS >= QUANT_WARPS, "few rows, fp8_128");
+      const int first = warp - C::EPI_FIRST - C::EPI_WARPS;
+      const int c = lane & 7;
+      float* slots = reinterpret_cast<float*>(smem + C::OFF_SC);
+      grid_dependency_wait();
+      for (int u = worker; u < units; u += nworkers) {
+        const Tile t = tile_of<STEP, TN>(u, a, table);
+        const float* wp = static_cast<const float*>(a.ws) + static_cast<int64_t>(min(t.wt, a.RTW - 1)) * a.KT;
+        const int base_i = (u - worker) / nworkers * (kt1 - kt0);  // stages of the units before
+        uint32_t v[2][8];
+        float w = 0.f;
+        auto fetch = [&](int at) {
+          const int k = at * BK + 16 * c;
+          w = at < kt1 ? __ldg(wp + at) : 0.f;
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            const int r = 4 * p + (lane >> 3);
+            if (at < kt1 && r < t.rows && k < a.K) {
+              load16(a.x + static_cast<int64_t>(t.row0 + r) * a.K + k, false, v[p]);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 8; ++j) v[p][j] = 0;
+            }
+          }
+        };
+        int at = kt0 + (first - base_i % QUANT_WARPS + QUANT_WARPS) % QUANT_WARPS;
+        fetch(at);
+        for (; at < kt1; at += QUANT_WARPS) {
+          const int i = base_i + at - kt0;
+          const int stage = i % STAGES, slot = i % SLOTS;
+          Codes codes[2];
+          float scale[2];
+#pragma unroll
+          for (int p = 0; p < 2; ++p) codes[p] = quantize16_b128(v[p], &scale[p]);
+          const float sw = w;
+          fetch(at + QUANT_WARPS);
+          if (!mbar_wait_warp(&empty[stage], static_cast<uint32_t>((i / STAGES) & 1) ^ 1u, abort_flag) ||
+              !mbar_wait_warp(&sc_free[slot], static_cast<uint32_t>((i / SLOTS) & 1) ^ 1u, abort_flag))
+            break;
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            const int r = 4 * p + (lane >> 3);
+            if (r < t.rows)  // 128-byte rows, 16-byte pieces swizzled as TMA does
+              *reinterpret_cast<uint4*>(smem + C::OFF_X + stage * C::X_BYTES + r * BK + ((c ^ r) << 4)) =
+                  make_uint4(codes[p].w[0], codes[p].w[1], codes[p].w[2], codes[p].w[3]);
+            if (c == 0) slots[slot * TN + (((r & 6) << 1) | (r & 1))] = scale[p] * sw;
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&full[stage]);
+            mbar_arrive(&sc_full[slot]);
+          }
         }
       }
     }
@@ -702,7 +778,7 @@ __global__ void __launch_bounds__(Cfg<FMT, CG, TN>::THREADS, 1)
   }
 }
 
-template <int FMT, int CG, int TN>
+template <int FMT, int CG, int TN, bool kQuant = false>
 cudaError_t launch_t(const GroupedProblem& p, int splits, int sms, cudaStream_t stream, const char** msg) {
   using C = Cfg<FMT, CG, TN>;
   static bool attr_set[64] = {};
@@ -710,7 +786,7 @@ cudaError_t launch_t(const GroupedProblem& p, int splits, int sms, cudaStream_t 
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64 || !attr_set[dev]) {
     cudaError_t e =
-        cudaFuncSetAttribute(gemm_grouped_kernel<FMT, CG, TN>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+        cudaFuncSetAttribute(gemm_grouped_kernel<FMT, CG, TN, kQuant>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) {
       *msg = "cudaFuncSetAttribute(max dynamic shared memory) failed";
       return e;
@@ -718,7 +794,7 @@ cudaError_t launch_t(const GroupedProblem& p, int splits, int sms, cudaStream_t 
     if (dev >= 0 && dev < 64) attr_set[dev] = true;
   }
   CUtensorMap mw, mx, mbox;
-  if (!grouped_maps(p, C::XROWS, &mw, &mx, &mbox)) {
+  if (!grouped_maps(p, kQuant ? 0 : C::XROWS, &mw, &mx, &mbox)) {
     *msg = "cuTensorMapEncodeTiled rejected an operand of the grouped product";
     return cudaErrorInvalidValue;
   }
@@ -728,7 +804,7 @@ cudaError_t launch_t(const GroupedProblem& p, int splits, int sms, cudaStream_t 
   int64_t workers = splits > 1 ? units : (units < sms / CG ? units : sms / CG);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(workers * csize), 1, 1);
-  cfg.blockDim = dim3(C::THREADS, 1, 1);
+  cfg.blockDim = dim3(threads_of<FMT, CG, TN, kQuant>(), 1, 1);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
@@ -740,7 +816,7 @@ cudaError_t launch_t(const GroupedProblem& p, int splits, int sms, cudaStream_t 
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, gemm_grouped_kernel<FMT, CG, TN>, mw, mx, mbox, a);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, gemm_grouped_kernel<FMT, CG, TN, kQuant>, mw, mx, mbox, a);
   if (e != cudaSuccess) *msg = "grouped product launch failed";
   return e;
 }
@@ -753,6 +829,9 @@ cudaError_t launch_fmt(const GroupedProblem& p, const GroupedPlan& plan, int sms
       return launch_t<FMT, 2, 256>(p, 1, sms, stream, msg);
     else
       return launch_gemm_b128_pair(p, sms, stream, msg);
+  }
+  if constexpr (FMT == kG8B128) {
+    if (p.x_bf16 != nullptr) return launch_t<FMT, 1, 16, true>(p, plan.splits, sms, stream, msg);
   }
   if (plan.tn == 16) return launch_t<FMT, 1, 16>(p, plan.splits, sms, stream, msg);
   if (plan.tn == 32) return launch_t<FMT, 1, 32>(p, plan.splits, sms, stream, msg);
@@ -767,8 +846,12 @@ bool grouped_maps(const GroupedProblem& p, int box_rows, CUtensorMap* mw, CUtens
   const auto u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
   const auto sw = CU_TENSOR_MAP_SWIZZLE_128B;
   const auto l2 = CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
-  return encode_map3(mw, u8, p.w, p.K, p.N, p.E, p.K, p.N * p.K, kGBK, kGW_Rows, sw, l2) &&
-         encode_map3(mbox, u8, p.x, p.K, p.R, 1, p.K, p.R * p.K, kGBK, kGBox, sw, l2) &&
+  if (!encode_map3(mw, u8, p.w, p.K, p.N, p.E, p.K, p.N * p.K, kGBK, kGW_Rows, sw, l2)) return false;
+  if (box_rows == 0) {  // x is not copied
+    *mx = *mbox = *mw;
+    return true;
+  }
+  return encode_map3(mbox, u8, p.x, p.K, p.R, 1, p.K, p.R * p.K, kGBK, kGBox, sw, l2) &&
          (box_rows == kGBox ? (*mx = *mbox, true)
                             : encode_map3(mx, u8, p.x, p.K, p.R, 1, p.K, p.R * p.K, kGBK, box_rows, sw, l2));
 }
@@ -793,6 +876,8 @@ GroupedArgs grouped_args(const GroupedProblem& p, int cg, int splits) {
   a.bias = static_cast<const __nv_bfloat16*>(p.bias);
   a.bias_stride = p.bias_stride;
   a.out = static_cast<__nv_bfloat16*>(p.out);
+  a.x = static_cast<const __nv_bfloat16*>(p.x_bf16);
+  a.K = static_cast<int>(p.K);
   return a;
 }
 
@@ -824,14 +909,16 @@ int64_t plan_cost(int64_t groups, int64_t rows, int64_t N, int64_t K, int tn, in
 
 }  // namespace
 
+bool b128_quantizes_inside(bool ragged, int64_t E, int64_t R) { return !ragged && E == 1 && R <= QUANT_ROWS; }
+
 // With offsets the host knows the rows a group has only on average, and groups
 // without rows only where there are fewer rows than groups.
 GroupedPlan grouped_plan(int fmt, int64_t E, int64_t R, int64_t N, int64_t K, bool ragged) {
-  (void)fmt;
   const int64_t groups = E < R ? E : (R > 0 ? R : 1), rows = ceil_div(R, groups);
+  const bool few = fmt == kG8B128 && b128_quantizes_inside(ragged, E, R);
   GroupedPlan best = {2, 256, 1};
-  int64_t least = plan_cost(groups, rows, N, K, 256, 1);
-  for (int tn = 128; tn >= 16; tn >>= 1) {
+  int64_t least = few ? INT64_MAX : plan_cost(groups, rows, N, K, 256, 1);
+  for (int tn = few ? 16 : 128; tn >= 16; tn >>= 1) {
     // at most eight tiles of x a group: each reads the weights again, from L2
     if (ceil_div(rows, tn) > 8) break;
     for (int s = 1; s <= (tn <= 64 ? 8 : 1); s <<= 1) {

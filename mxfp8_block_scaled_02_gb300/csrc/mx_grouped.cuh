@@ -145,6 +145,8 @@ struct GroupedArgs {
   const __nv_bfloat16* bias;
   int64_t bias_stride;    // of a group: N, or 0 for one bias
   __nv_bfloat16* out;
+  const __nv_bfloat16* x;  // quantised inside: bf16 [R, K]
+  int K;
 };
 
 // The groups' first rows, row counts and the tiles before them.

@@ -31,12 +31,16 @@ struct GroupedProblem {
   // this one start only when all before it is done (the kernels of grouped_quant.cu):
   // offsets, weights and their scales are read without waiting for it
   int offsets_ready = 0;
+  // b128_quantizes_inside: bf16 x [R, K] instead of x and xs
+  const void* x_bf16 = nullptr;
 };
 // How a shape is run: a CTA pair (cg = 2) or one CTA a tile, the rows of x a tile
 // takes at most, and the K splits.
 struct GroupedPlan {
   int cg, tn, splits;
 };
+// Whether fp8_128 products of bf16 x quantise it in their own kernel: few rows, no groups.
+bool b128_quantizes_inside(bool ragged, int64_t E, int64_t R);
 GroupedPlan grouped_plan(int fmt, int64_t E, int64_t R, int64_t N, int64_t K, bool ragged);
 // Tiles of up to tn rows of x that R rows in E groups can come to.
 int64_t grouped_max_tiles(int64_t E, int64_t R, bool ragged, int tn);

@@ -35,6 +35,8 @@ def test_sizes(lib):
     assert ops.workspace_size_fp8_128(2, 3, 128, 400, False) == up(6 * 400) + up(4 * 6 * 4)
     assert ops.workspace_size_fp8_128(1, 4096, 14336, 4096, False) == 4096 * 4096 + 4 * 4096 * 32
     assert ops.workspace_size_fp8_128(1, 4096, 14336, 4096, True) == 0
+    # one to eight rows are quantised in the product's kernel
+    assert ops.workspace_size_fp8_128(1, 8, 256, 512, False) == 0 and ops.workspace_size_fp8_128(1, 9, 256, 512, False) > 0
     assert ops.grouped_workspace_size("e4m3", 8, 100, 256, 512, False) == up(100 * 512) + up(4 * 100 * 4)
     assert ops.grouped_workspace_size("fp8_128", 8, 100, 256, 512, True) == 0
     assert ops.route_workspace_size(64, 128, 8) == 0          # one CTA
@@ -60,7 +62,7 @@ def test_quantise_errors(lib):
 
 def test_linear_errors(lib):
     #       x     xq    xs    B  M  N    K    w     ws    bias  out   workspace  bytes stream
-    ok = [FAKE, None, None, 1, 4, 256, 512, FAKE, FAKE, None, FAKE, P(0x10100), 1 << 20, None]
+    ok = [FAKE, None, None, 1, 40, 256, 512, FAKE, FAKE, None, FAKE, P(0x10100), 1 << 20, None]
     call = caller(lib.mxfp8_b128_linear, ok)
     assert call(_3=0) == INVALID and call(_4=-1) == INVALID and call(_5=0) == INVALID and call(_6=0) == INVALID
     assert call(_5=12) == UNSUPPORTED and call(_6=520) == UNSUPPORTED
