@@ -61,7 +61,10 @@ struct Cfg {
   static constexpr int EPI_COLS = TN / (EPI_WARPS / 4);  // columns per epilogue warp
   static constexpr int SC_WARPS = MX ? 4 : 1;       // warps that prepare scales
   static constexpr int EPI_FIRST = MX ? 8 : 4;       // first epilogue warp
-  static constexpr int THREADS = 32 * (EPI_FIRST + EPI_WARPS);
+  // MXFP8 on pairs: two sets of scale warps, each every other stage (a stage's chain
+  // of load, tensor-memory store and its completion is longer than its MMAs)
+  static constexpr int SC_SETS = MX && CG == 2 ? 2 : 1;
+  static constexpr int THREADS = 32 * (EPI_FIRST + EPI_WARPS + (SC_SETS - 1) * SC_WARPS);
   static constexpr int SF_BYTES = MX ? kAtomBytes : 0;  // weight scales of a stage
   static constexpr int SLOTS = MX ? 0 : 8;              // fp8_128: blocks of K whose scales are staged
   static constexpr int RECV_BYTES = CG == 1 && TN <= 64 ? 32768 : 0;
@@ -325,7 +328,8 @@ __global__ void __launch_bounds__(threads_of<FMT, CG, TN, kQuant>(), 1)
           }
         }
         for (int kt = kt0; kt < kt1; ++kt) {
-          if (!mbar_wait_warp(MX ? &sf_ready[stage] : &full[stage], phase, abort_flag)) {
+          if ((MX && !mbar_wait_warp(&sf_ready[stage], phase, abort_flag)) ||
+              !mbar_wait_warp(&full[stage], phase, abort_flag)) {
             ok = false;
             break;
           }
@@ -425,7 +429,7 @@ __global__ void __launch_bounds__(threads_of<FMT, CG, TN, kQuant>(), 1)
         }
       }
     }
-  } else if (MX && warp < 8) {
+  } else if (MX && (warp < 8 || warp >= C::EPI_FIRST + C::EPI_WARPS)) {
     grid_dependency_wait();  // x's scales are the previous kernel's output
     // ---------------------------------------------------------- MXFP8 scales into tensor memory
     // Line l of an atom (rows l, l + 32, l + 64, l + 96) goes to lane l of each
@@ -433,40 +437,44 @@ __global__ void __launch_bounds__(threads_of<FMT, CG, TN, kQuant>(), 1)
     constexpr int NW = TN < 32 ? 1 : TN / 32, AHEAD = 2;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + C::T_SF;
     const uint32_t ready = CG == 2 ? map_shared_rank(smem_u32(sf_ready), 0) : smem_u32(sf_ready);
-    int f_u = worker, f_kt = kt0, f_rows = 0;
+    constexpr int SETS = C::SC_SETS;
+    const int set = warp < 8 ? 0 : 1, nk = kt1 - kt0;
+    int f_u = worker, f_kt = kt0 + set, f_rows = 0;
     const uint32_t* f_p = a.xs;
-    auto start = [&]() {
+    auto start = [&]() {  // the tile that stage f_kt counted from f_u's first falls into
+      while (f_kt >= kt1 && f_u < units) {
+        f_kt -= nk;
+        f_u += nworkers;
+      }
       if (f_u >= units) return;
       const Tile t = tile_of<STEP, TN>(f_u, a, table);
-      f_rows = t.rows;
-      f_p = a.xs + static_cast<int64_t>(t.row0 + lane) * a.xs_row;
+      f_rows = t.rows - lane;
+      f_p = a.xs + static_cast<int64_t>(t.row0 + lane) * a.xs_row + f_kt * a.xs_kt;
     };
     start();
     auto fetch = [&](uint32_t (&w)[NW]) {
       if (f_u >= units) return;
-      const uint32_t* p = f_p + f_kt * a.xs_kt;
 #pragma unroll
-      for (int i = 0; i < NW; ++i) w[i] = lane + 32 * i < f_rows ? __ldg(p + 32 * i * a.xs_row) : 0u;
-      if (++f_kt == kt1) {
-        f_kt = kt0;
-        f_u += nworkers;
-        start();
-      }
+      for (int i = 0; i < NW; ++i) w[i] = 32 * i < f_rows ? __ldg(f_p + 32 * i * a.xs_row) : 0u;
+      f_p += SETS * a.xs_kt;
+      f_kt += SETS;
+      if (f_kt >= kt1) start();
     };
     uint32_t w[AHEAD][NW] = {};
 #pragma unroll
     for (int d = 0; d < AHEAD; ++d) fetch(w[d]);
-    int stage = 0;
+    int stage = set;
     uint32_t phase = 0;
     bool ok = true;
-    int64_t left = 0;
-    for (int u = worker; u < units; u += nworkers) left += kt1 - kt0;
+    int64_t left = -set;  // stages of this set
+    for (int u = worker; u < units; u += nworkers) left += nk;
+    left = (left + SETS - 1) / SETS;
     while (ok && left > 0) {
 #pragma unroll
       for (int d = 0; d < AHEAD; ++d, --left) {
         if (!ok || left <= 0) break;
         // the stage's slot is free: its refill has waited for the MMAs that read it
-        if (!__all_sync(0xFFFFFFFFu, mbar_wait(&sf_full[stage], phase, abort_flag))) {
+        if (!mbar_wait_warp(&sf_full[stage], phase, abort_flag)) {
           ok = false;
           break;
         }
@@ -486,11 +494,12 @@ __global__ void __launch_bounds__(threads_of<FMT, CG, TN, kQuant>(), 1)
         if (lane == 0) {
           if (!leader)
             mbar_arrive_remote(ready + static_cast<uint32_t>(stage * 8));
-          else if (mbar_wait(&full[stage], phase, abort_flag))
+          else
             mbar_arrive(&sf_ready[stage]);
         }
-        if (++stage == STAGES) {
-          stage = 0;
+        stage += SETS;
+        if (stage >= STAGES) {
+          stage -= STAGES;
           phase ^= 1u;
         }
       }
