@@ -437,7 +437,7 @@ mxfp8_status mxfp8_expert_mlp(int fmt, const void* x_bf16, int64_t T, int64_t K,
                    reinterpret_cast<int32_t*>(ws + w.ids), weights, offsets, rows, positions, ws + w.counts,
                    static_cast<size_t>(mx::route_count_bytes(T, static_cast<int>(E))), stream);
   if (st != MXFP8_OK) return st;
-  const mx::QuantRowsProblem q{fmt, x_bf16, rows, T, R, K, xq, ws + w.xs, 1, R, true};
+  const mx::QuantRowsProblem q{fmt, x_bf16, nullptr, T, R, K, xq, ws + w.xs, 1, R, true, positions, static_cast<int>(k)};
   cudaError_t e = mx::launch_quantize_rows(q, as_stream(stream));
   if (e != cudaSuccess) return cuda_fail(e, "quantise launch");
   const char* msg = "";

@@ -7,8 +7,10 @@
 // MXFP8: the rule and the bytes of mx_quant.cuh.
 //
 // Bound by reading x and writing the codes.  Sixteen elements a lane (32 bytes in,
-// 16 out: whole sectors), a block of 128 eight lanes, 512 elements a warp and task,
-// UNROLL tasks in flight.
+// 16 out: whole sectors), a block of 128 eight lanes, 512 elements a warp; one task a
+// warp, many warps.  (Two or four tasks a warp with their loads first are slower: 4096
+// x 14336 silu 52.4 us with one, 57.0 with two; 16384 rows of 4096 picked from 2048
+// tokens 30.3, 30.6 with two, 31.6 with four.)
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -24,9 +26,7 @@ namespace mx {
 namespace {
 
 constexpr int THREADS = 256;
-constexpr int UNROLL = 4;
 constexpr int TASK = 512;  // elements of a row per warp and task
-constexpr int FEW_TASKS = 152 * 8 * 2;  // up to so many a warp has one: latency, not bandwidth
 
 // Sixteen bf16 of a lane, two lanes an MXFP8 block: the codes, and in the eight
 // lanes of 128 elements the word of their four scale bytes.
@@ -99,8 +99,10 @@ __global__ void __launch_bounds__(THREADS) transpose_words_kernel(const uint32_t
 struct RowsArgs {
   const __nv_bfloat16* x;
   const int* rows;
-  int64_t T, K;
-  int64_t tasks;  // R * segs
+  const int* positions;
+  int k;          // positions a row of x
+  int64_t T, R, K;
+  int64_t tasks;  // (R, or T with positions) * segs
   int segs;       // tasks a row
   bool wide;
   uint8_t* q;
@@ -109,7 +111,7 @@ struct RowsArgs {
 };
 
 // K % 16 == 0; MXFP8 K % 128 == 0.
-template <int FMT, bool kEarly, int U>
+template <int FMT, bool kEarly>
 __global__ void __launch_bounds__(THREADS) quantize_rows_kernel(const RowsArgs a) {
   // In this order: when the next kernel starts, all before this one is done, and it
   // may read what this one does not write (GroupedProblem::offsets_ready).
@@ -118,39 +120,36 @@ __global__ void __launch_bounds__(THREADS) quantize_rows_kernel(const RowsArgs a
     launch_dependents();
   }
   const int lane = threadIdx.x & 31;
-  const int64_t first = (static_cast<int64_t>(blockIdx.x) * (THREADS / 32) + (threadIdx.x >> 5)) * U;
-  uint32_t v[U][8];
-  int64_t row[U];
-  int k[U];
-#pragma unroll
-  for (int i = 0; i < U; ++i) {
-    const int64_t task = first + i;
-    row[i] = task / a.segs;
-    k[i] = static_cast<int>(task - row[i] * a.segs) * TASK + lane * 16;
-    int64_t src = row[i];
-    if (a.rows != nullptr) src = task < a.tasks ? a.rows[row[i]] : -1;
-    if (task < a.tasks && k[i] < a.K && src >= 0 && src < a.T) {
-      load16(a.x + src * a.K + k[i], a.wide, v[i]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = 0;
-    }
+  const int64_t task = static_cast<int64_t>(blockIdx.x) * (THREADS / 32) + (threadIdx.x >> 5);
+  if (task >= a.tasks) return;  // the whole warp
+  const int64_t row = task / a.segs;
+  const int k = static_cast<int>(task - row * a.segs) * TASK + lane * 16;
+  const int64_t src = a.rows != nullptr ? a.rows[row] : row;
+  int pos = -1;  // lane j: where copy j of this row goes
+  if (a.positions != nullptr && lane < a.k) pos = a.positions[row * a.k + lane];
+  uint32_t v[8] = {};
+  if (k < a.K && src >= 0 && src < a.T) load16(a.x + src * a.K + k, a.wide, v);
+  uint32_t word;
+  Codes c;
+  if (FMT == kG8MX) {
+    c = quantize16_mx(v, lane, &word);
+  } else {
+    float s;
+    c = quantize16_b128(v, &s);
+    word = __float_as_uint(s);
   }
-#pragma unroll
-  for (int i = 0; i < U; ++i) {
-    if (first + i >= a.tasks) return;  // the whole warp
-    uint32_t word;
-    Codes c;
-    if (FMT == kG8MX) {
-      c = quantize16_mx(v[i], lane, &word);
-    } else {
-      float s;
-      c = quantize16_b128(v[i], &s);
-      word = __float_as_uint(s);
+  auto store = [&](int64_t r) {
+    if (k < a.K) {
+      *reinterpret_cast<uint4*>(a.q + r * a.K + k) = make_uint4(c.w[0], c.w[1], c.w[2], c.w[3]);
+      if ((lane & 7) == 0) a.s[r * a.s_row + (k >> 7) * a.s_kt] = word;
     }
-    if (k[i] < a.K) {
-      *reinterpret_cast<uint4*>(a.q + row[i] * a.K + k[i]) = make_uint4(c.w[0], c.w[1], c.w[2], c.w[3]);
-      if ((lane & 7) == 0) a.s[row[i] * a.s_row + (k[i] >> 7) * a.s_kt] = word;
+  };
+  if (a.positions == nullptr) {
+    store(row);
+  } else {
+    for (int j = 0; j < a.k; ++j) {
+      const int p = __shfl_sync(0xFFFFFFFFu, pos, j);
+      if (p >= 0 && p < a.R) store(p);
     }
   }
 }
@@ -169,52 +168,40 @@ struct ActArgs {
 
 // y = gate / (1 + exp(-gate)) * up, quantised: the values of silu_mul_kernel
 // (fused_quant.cu), and in MXFP8 its bytes.
-template <int FMT, int U>
+template <int FMT>
 __global__ void __launch_bounds__(THREADS) silu_mul_rows_kernel(const ActArgs a) {
-  const int lane = threadIdx.x & 31;
-  const int64_t first = (static_cast<int64_t>(blockIdx.x) * (THREADS / 32) + (threadIdx.x >> 5)) * U;
   grid_dependency_wait();
   launch_dependents();  // in this order, as above
-  uint32_t g[U][8], u[U][8];
-  int64_t row[U];
-  int k[U];
-#pragma unroll
-  for (int i = 0; i < U; ++i) {
-    const int64_t task = first + i;
-    row[i] = task / a.segs;
-    k[i] = static_cast<int>(task - row[i] * a.segs) * TASK + lane * 16;
-    if (task < a.tasks && k[i] < a.K) {
-      load16(a.gate + row[i] * a.gate_stride + k[i], a.wide, g[i]);
-      load16(a.up + row[i] * a.up_stride + k[i], a.wide, u[i]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) g[i][j] = u[i][j] = 0;
-    }
+  const int lane = threadIdx.x & 31;
+  const int64_t task = static_cast<int64_t>(blockIdx.x) * (THREADS / 32) + (threadIdx.x >> 5);
+  if (task >= a.tasks) return;
+  const int64_t row = task / a.segs;
+  const int k = static_cast<int>(task - row * a.segs) * TASK + lane * 16;
+  uint32_t g[8] = {}, u[8] = {};
+  if (k < a.K) {
+    load16(a.gate + row * a.gate_stride + k, a.wide, g);
+    load16(a.up + row * a.up_stride + k, a.wide, u);
   }
+  float y[16];
 #pragma unroll
-  for (int i = 0; i < U; ++i) {
-    if (first + i >= a.tasks) return;
-    float y[16];
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const float gt = __uint_as_float(j & 1 ? g[i][j >> 1] & 0xFFFF0000u : g[i][j >> 1] << 16);
-      const float up = __uint_as_float(j & 1 ? u[i][j >> 1] & 0xFFFF0000u : u[i][j >> 1] << 16);
-      const float e = __expf(-fabsf(gt));
-      y[j] = gt * __fdividef(gt >= 0.f ? 1.f : e, 1.f + e) * up;
-    }
-    uint32_t word;
-    Codes c;
-    if (FMT == kG8MX) {
-      c = quantize16_mx(y, lane, &word);
-    } else {
-      float s;
-      c = quantize16_b128(y, &s);
-      word = __float_as_uint(s);
-    }
-    if (k[i] < a.K) {
-      *reinterpret_cast<uint4*>(a.q + row[i] * a.K + k[i]) = make_uint4(c.w[0], c.w[1], c.w[2], c.w[3]);
-      if ((lane & 7) == 0) a.s[row[i] * a.s_row + (k[i] >> 7) * a.s_kt] = word;
-    }
+  for (int j = 0; j < 16; ++j) {
+    const float gt = __uint_as_float(j & 1 ? g[j >> 1] & 0xFFFF0000u : g[j >> 1] << 16);
+    const float up = __uint_as_float(j & 1 ? u[j >> 1] & 0xFFFF0000u : u[j >> 1] << 16);
+    const float e = __expf(-fabsf(gt));
+    y[j] = gt * __fdividef(gt >= 0.f ? 1.f : e, 1.f + e) * up;
+  }
+  uint32_t word;
+  Codes c;
+  if (FMT == kG8MX) {
+    c = quantize16_mx(y, lane, &word);
+  } else {
+    float s;
+    c = quantize16_b128(y, &s);
+    word = __float_as_uint(s);
+  }
+  if (k < a.K) {
+    *reinterpret_cast<uint4*>(a.q + row * a.K + k) = make_uint4(c.w[0], c.w[1], c.w[2], c.w[3]);
+    if ((lane & 7) == 0) a.s[row * a.s_row + (k >> 7) * a.s_kt] = word;
   }
 }
 
@@ -285,21 +272,6 @@ cudaError_t launch(const void* fn, int64_t blocks, void** args, bool programmati
   return cudaLaunchKernelExC(&cfg, fn, args);
 }
 
-template <int FMT, bool kEarly>
-const void* rows_kernel_of(bool few) {
-  return few ? reinterpret_cast<const void*>(quantize_rows_kernel<FMT, kEarly, 1>)
-             : reinterpret_cast<const void*>(quantize_rows_kernel<FMT, kEarly, UNROLL>);
-}
-const void* rows_kernel(int fmt, bool early, bool few) {
-  if (fmt == kG8MX) return early ? rows_kernel_of<kG8MX, true>(few) : rows_kernel_of<kG8MX, false>(few);
-  return early ? rows_kernel_of<kG8B128, true>(few) : rows_kernel_of<kG8B128, false>(few);
-}
-template <int U>
-const void* act_kernel(int fmt) {
-  return fmt == kG8MX ? reinterpret_cast<const void*>(silu_mul_rows_kernel<kG8MX, U>)
-                      : reinterpret_cast<const void*>(silu_mul_rows_kernel<kG8B128, U>);
-}
-
 inline bool is32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31) == 0; }
 
 }  // namespace
@@ -308,19 +280,24 @@ cudaError_t launch_quantize_rows(const QuantRowsProblem& p, cudaStream_t stream)
   RowsArgs a;
   a.x = static_cast<const __nv_bfloat16*>(p.x);
   a.rows = p.rows;
+  a.positions = p.positions;
+  a.k = p.k;
   a.T = p.T;
+  a.R = p.R;
   a.K = p.K;
   a.segs = static_cast<int>(ceil_div(p.K, TASK));
-  a.tasks = p.R * a.segs;
+  a.tasks = (p.positions != nullptr ? p.T : p.R) * a.segs;
   a.wide = is32(p.x);  // K % 16 == 0: every row then is
   a.q = p.q;
   a.s = static_cast<uint32_t*>(p.s);
   a.s_row = p.s_row;
   a.s_kt = p.s_kt;
-  const bool few = a.tasks <= FEW_TASKS;
-  const void* fn = rows_kernel(p.fmt, p.early, few);
+  const void* fn = p.fmt == kG8MX ? (p.early ? reinterpret_cast<const void*>(quantize_rows_kernel<kG8MX, true>)
+                                             : reinterpret_cast<const void*>(quantize_rows_kernel<kG8MX, false>))
+                                  : (p.early ? reinterpret_cast<const void*>(quantize_rows_kernel<kG8B128, true>)
+                                             : reinterpret_cast<const void*>(quantize_rows_kernel<kG8B128, false>));
   void* args[] = {&a};
-  return launch(fn, ceil_div(a.tasks, (few ? 1 : UNROLL) * (THREADS / 32)), args, p.early, stream);
+  return launch(fn, ceil_div(a.tasks, THREADS / 32), args, p.early, stream);
 }
 
 cudaError_t launch_silu_mul_rows(const ActRowsProblem& p, cudaStream_t stream) {
@@ -337,10 +314,10 @@ cudaError_t launch_silu_mul_rows(const ActRowsProblem& p, cudaStream_t stream) {
   a.s = static_cast<uint32_t*>(p.s);
   a.s_row = p.s_row;
   a.s_kt = p.s_kt;
-  const bool few = a.tasks <= FEW_TASKS;
-  const void* fn = few ? act_kernel<1>(p.fmt) : act_kernel<UNROLL / 2>(p.fmt);
+  const void* fn = p.fmt == kG8MX ? reinterpret_cast<const void*>(silu_mul_rows_kernel<kG8MX>)
+                                  : reinterpret_cast<const void*>(silu_mul_rows_kernel<kG8B128>);
   void* args[] = {&a};
-  return launch(fn, ceil_div(a.tasks, (few ? 1 : UNROLL / 2) * (THREADS / 32)), args, true, stream);
+  return launch(fn, ceil_div(a.tasks, THREADS / 32), args, true, stream);
 }
 
 cudaError_t launch_transpose_words(const void* in, int64_t R, int64_t KT, void* out, cudaStream_t stream) {

@@ -52,7 +52,8 @@ cudaError_t launch_gemm_b128_pair(const GroupedProblem& p, int sms, cudaStream_t
 cudaError_t take_status_b128_pair(unsigned int* out);
 
 // grouped_quant.cu.  Row r of the output is x[rows[r]] (rows null: x[r]), a row
-// index outside [0, T) gives zeros.  Codes [R, K]; the scales' 4-byte words (as
+// index outside [0, T) gives zeros; or, with positions, row t of x goes to the rows
+// positions[t][0 .. k) that are in [0, R) (read once, written k times).  Codes [R, K]; the scales' 4-byte words (as
 // GroupedProblem::xs) at r * s_row + kt * s_kt.
 struct QuantRowsProblem {
   int fmt;
@@ -63,6 +64,8 @@ struct QuantRowsProblem {
   void* s;
   int64_t s_row, s_kt;
   bool early;            // let the next kernel in the stream start before this one ends
+  const int* positions = nullptr;  // device [T, k]; rows null
+  int k = 0;                       // at most 32
 };
 cudaError_t launch_quantize_rows(const QuantRowsProblem& p, cudaStream_t stream);
 // silu(gate) * up with the output quantised; rows of 16-byte aligned bf16.  Lets the
