@@ -13,8 +13,9 @@
 // because the groups are ragged in x: a tile takes as many columns as its group
 // has rows left, in steps of 16 (32 on a pair), and a group's rows are shared out
 // evenly over its tiles, so hardly any MMA column is padding.  Two shapes:
-//   CG = 2: 256 weight rows x up to 256 rows of x on a pair of CTAs
-//           (cta_group::2), where the tensor cores or L2 bound the product;
+//   CG = 2: 256 weight rows x up to 256 rows of x on a pair of CTAs (cta_group::2;
+//           MXFP8, fp8_128 has gemm_b128_pair.cu), where the way between L2 and the
+//           SMs bounds the product: 64 KB a stage and pair;
 //   CG = 1: 128 weight rows x up to 16, 32, 64 or 128 on one CTA, where reading
 //           the weights does.  With few tiles K is split over a cluster of S CTAs,
 //           whose partial sums meet in distributed shared memory (TN <= 64).
@@ -28,10 +29,19 @@
 // lane per row every thread would read all of them), and stmatrix.trans turns the
 // fragments of bf16 into rows of the output.
 //
+// Measured (us, weights from HBM, in a CUDA graph, x quantised before): MXFP8, 128
+// rows on 54 of 64 experts of 2048 x 4096 73 (6.4 TB/s of weights); 16384 rows on 13
+// of 16 experts of 4096 x 4096 186 (2.95 PFLOP/s; 205 before the MMA warp waited for
+// the operands itself and a second set of scale warps took every other stage, 167
+// without the scales' tensor-memory stores).  fp8_128: eight rows on eight experts of
+// 2048 x 4096 15.7 (4.3 TB/s: 128 tiles on 152 SMs, and ~4 us of chain); one row, N =
+// K = 4096, bf16 x 8.8, of which two thirds are the chain from launch to the exchange.
+//
 // Warps: 0 weight TMA (and, MXFP8, weight scales), 1 tensor-memory allocation and
 // MMA issue, 2 TMA of x, 3 the group table and the scales of fp8_128; MXFP8: 4..7
-// scales into tensor memory; then the epilogue, 4 or 8 warps.  Every wait is
-// bounded and the cluster barriers are reached on every path.
+// (on pairs the last four too) scales into tensor memory; the epilogue, 4 or 8
+// warps; with kQuant four that quantise x.  Every wait is bounded and the cluster
+// barriers are reached on every path.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -83,14 +93,14 @@ struct Cfg {
   // on) and a slot of scales a stage; fp8_128 a ring of sums of one block of K
   static constexpr int ACOLS = TN < 32 ? 32 : TN;
   static constexpr bool OVERLAP = MX && CG == 2;
-  static constexpr int BUFS = MX ? 2 : (TN == 256 ? 2 : 4);
+  static constexpr int BUFS = MX ? 2 : 4;
   static constexpr int ACC_STEP = OVERLAP ? 128 : ACOLS;
   static constexpr int T_SF = OVERLAP ? 384 : 2 * ACOLS;
   static constexpr int SFX_COLS = TN > 128 ? 8 : 4;
   static constexpr int SLOT_COLS = 4 + SFX_COLS;
   static constexpr int T_END = MX ? T_SF + STAGES * SLOT_COLS : BUFS * ACOLS;
   static constexpr int TMEM_COLS = T_END <= 128 ? 128 : (T_END <= 256 ? 256 : 512);
-  static_assert(T_END <= 512, "tensor memory");
+  static_assert(T_END <= 512 && (MX || CG == 1), "tensor memory");
   // barriers: full, empty; MXFP8 sf_full, sf_ready a stage; buf_full, buf_free a
   // buffer; sc_full, sc_free a slot; received
   static constexpr int NBARS = (MX ? 4 : 2) * STAGES + 2 * BUFS + 2 * SLOTS + 1;
@@ -260,118 +270,118 @@ __global__ void __launch_bounds__(threads_of<FMT, CG, TN, kQuant>(), 1)
 
   if (warp < 4) {
     if (warp == 0 || (warp == 2 && !kQuant)) {
-    // ------------------------------------------------------------ producers
-    const uint32_t full_bar = CG == 2 ? map_shared_rank(smem_u32(full), 0) : smem_u32(full);
-    if (warp == 2) grid_dependency_wait();
-    int stage = 0;
-    uint32_t phase = 1;  // the first round's stages are free
-    int64_t issued = 0;
-    bool ok = true;
-    for (int u = worker; ok && u < units; u += nworkers) {
-      const Tile t = tile_of<STEP, TN>(u, a, table);
-      const int mine = t.width / CG;  // rows of x this CTA stages
-      const int x0 = t.row0 + rank * mine;
-      for (int kt = kt0; kt < kt1; ++kt, ++issued) {
-        if (!mbar_wait_warp(&empty[stage], phase, abort_flag)) {
-          ok = false;
-          break;
-        }
-        const uint32_t bar = full_bar + stage * 8;
-        if (warp == 0) {
-          if (issued >= early) load_weights(stage, kt, t);
-        } else if (mine == C::XROWS) {
-          tma_load<CG>(elected, base + C::OFF_X + stage * C::X_BYTES, &tmX, bar, kt * BK, x0, 0);
-        } else {
-          for (int i = 0; i < mine; i += BOX)
-            tma_load<CG>(elected, base + C::OFF_X + stage * C::X_BYTES + i * BK, &tmXbox, bar, kt * BK, x0 + i, 0);
-        }
-        if (++stage == STAGES) {
-          stage = 0;
-          phase ^= 1u;
-        }
-      }
-    }
-    // Before exit: every commit to this CTA's empty barriers has arrived, and with
-    // it the copies that the MMAs before it waited for.
-    if (lane == 0) {
-      for (int s = 0; s < STAGES; ++s) {
-        if (issued <= s) continue;
-        const int64_t last = (issued - 1 - s) / STAGES;
-        mbar_wait(&empty[s], static_cast<uint32_t>(last & 1), nullptr);
-      }
-    }
-    __syncwarp();
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer (even CTA)
-    if (leader) {
-      const uint64_t wd0 = sdesc_kmajor_sw128(base + C::OFF_W), xd0 = sdesc_kmajor_sw128(base + C::OFF_X);
-      int stage = 0, n = 0;  // n: accumulators begun (MXFP8), blocks of K (fp8_128)
-      uint32_t phase = 0;
+      // ------------------------------------------------------------ producers
+      const uint32_t full_bar = CG == 2 ? map_shared_rank(smem_u32(full), 0) : smem_u32(full);
+      if (warp == 2) grid_dependency_wait();
+      int stage = 0;
+      uint32_t phase = 1;  // the first round's stages are free
+      int64_t issued = 0;
       bool ok = true;
       for (int u = worker; ok && u < units; u += nworkers) {
         const Tile t = tile_of<STEP, TN>(u, a, table);
-        // fp32 accumulation (MXFP8: UE8M0 scales), E4M3 operands, N >> 3 at bit 17, M >> 4 at bit 24
-        const uint32_t idesc =
-            MX ? idesc_mxf8(CG * ROWS, t.width)
-               : (1u << 4) | (static_cast<uint32_t>(t.width >> 3) << 17) | (static_cast<uint32_t>(CG * ROWS >> 4) << 24);
-        uint32_t acc = 0;
-        if (MX) {
-          const int b = n & 1;
-          acc = tmem + b * C::ACC_STEP;
-          // overlapping accumulators: the last tile's shared columns are drained;
-          // else the tile before that
-          const bool wait = C::OVERLAP ? n > 0 : n > 1;
-          if (wait && !mbar_wait_warp(&buf_free[C::OVERLAP ? b ^ 1 : b],
-                                      static_cast<uint32_t>(((n - (C::OVERLAP ? 1 : 2)) >> 1) & 1), abort_flag)) {
+        const int mine = t.width / CG;  // rows of x this CTA stages
+        const int x0 = t.row0 + rank * mine;
+        for (int kt = kt0; kt < kt1; ++kt, ++issued) {
+          if (!mbar_wait_warp(&empty[stage], phase, abort_flag)) {
             ok = false;
             break;
           }
-        }
-        for (int kt = kt0; kt < kt1; ++kt) {
-          if ((MX && !mbar_wait_warp(&sf_ready[stage], phase, abort_flag)) ||
-              !mbar_wait_warp(&full[stage], phase, abort_flag)) {
-            ok = false;
-            break;
-          }
-          if (!MX) {
-            const int b = n % BUFS;
-            acc = tmem + b * C::ACOLS;
-            if (!mbar_wait_warp(&buf_free[b], static_cast<uint32_t>(((n / BUFS) & 1) ^ 1), abort_flag)) {
-              ok = false;
-              break;
-            }
-          }
-          tc_fence_after();
-          const uint64_t wd = wd0 + static_cast<uint32_t>(stage * (W_BYTES >> 4));
-          const uint64_t xd = xd0 + static_cast<uint32_t>(stage * (C::X_BYTES >> 4));
-          const uint32_t t_sfw = tmem + C::T_SF + stage * C::SLOT_COLS;
-#pragma unroll
-          for (int kk = 0; kk < BK / 32; ++kk) {
-            if (MX)
-              mma_mxf8<CG>(elected, acc, wd + 2 * kk, xd + 2 * kk, idesc_with_sf_id(idesc, kk, kk), t_sfw, t_sfw + 4,
-                           ((kt - kt0) | kk) != 0);
-            else
-              mma_f8<CG>(elected, acc, wd + 2 * kk, xd + 2 * kk, idesc, kk != 0);
-          }
-          commit<CG>(elected, &empty[stage]);
-          if (!MX) {
-            commit<CG>(elected, &buf_full[n % BUFS]);
-            ++n;
+          const uint32_t bar = full_bar + stage * 8;
+          if (warp == 0) {
+            if (issued >= early) load_weights(stage, kt, t);
+          } else if (mine == C::XROWS) {
+            tma_load<CG>(elected, base + C::OFF_X + stage * C::X_BYTES, &tmX, bar, kt * BK, x0, 0);
+          } else {
+            for (int i = 0; i < mine; i += BOX)
+              tma_load<CG>(elected, base + C::OFF_X + stage * C::X_BYTES + i * BK, &tmXbox, bar, kt * BK, x0 + i, 0);
           }
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1u;
           }
         }
-        if (!ok) break;
-        if (MX) {
-          commit<CG>(elected, &buf_full[n & 1]);
-          ++n;
+      }
+      // Before exit: every commit to this CTA's empty barriers has arrived, and with
+      // it the copies that the MMAs before it waited for.
+      if (lane == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+          if (issued <= s) continue;
+          const int64_t last = (issued - 1 - s) / STAGES;
+          mbar_wait(&empty[s], static_cast<uint32_t>(last & 1), nullptr);
         }
       }
-      if (!ok) __nanosleep(200000);  // let issued tensor-core work retire
-    }
-    __syncwarp();
+      __syncwarp();
+    } else if (warp == 1) {
+      // ------------------------------------------------------------ MMA issuer (even CTA)
+      if (leader) {
+        const uint64_t wd0 = sdesc_kmajor_sw128(base + C::OFF_W), xd0 = sdesc_kmajor_sw128(base + C::OFF_X);
+        int stage = 0, n = 0;  // n: accumulators begun (MXFP8), blocks of K (fp8_128)
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int u = worker; ok && u < units; u += nworkers) {
+          const Tile t = tile_of<STEP, TN>(u, a, table);
+          // fp32 accumulation (MXFP8: UE8M0 scales), E4M3 operands, N >> 3 at bit 17, M >> 4 at bit 24
+          const uint32_t idesc =
+              MX ? idesc_mxf8(CG * ROWS, t.width)
+                 : (1u << 4) | (static_cast<uint32_t>(t.width >> 3) << 17) | (static_cast<uint32_t>(CG * ROWS >> 4) << 24);
+          uint32_t acc = 0;
+          if (MX) {
+            const int b = n & 1;
+            acc = tmem + b * C::ACC_STEP;
+            // overlapping accumulators: the last tile's shared columns are drained;
+            // else the tile before that
+            const bool wait = C::OVERLAP ? n > 0 : n > 1;
+            if (wait && !mbar_wait_warp(&buf_free[C::OVERLAP ? b ^ 1 : b],
+                                        static_cast<uint32_t>(((n - (C::OVERLAP ? 1 : 2)) >> 1) & 1), abort_flag)) {
+              ok = false;
+              break;
+            }
+          }
+          for (int kt = kt0; kt < kt1; ++kt) {
+            if ((MX && !mbar_wait_warp(&sf_ready[stage], phase, abort_flag)) ||
+                !mbar_wait_warp(&full[stage], phase, abort_flag)) {
+              ok = false;
+              break;
+            }
+            if (!MX) {
+              const int b = n % BUFS;
+              acc = tmem + b * C::ACOLS;
+              if (!mbar_wait_warp(&buf_free[b], static_cast<uint32_t>(((n / BUFS) & 1) ^ 1), abort_flag)) {
+                ok = false;
+                break;
+              }
+            }
+            tc_fence_after();
+            const uint64_t wd = wd0 + static_cast<uint32_t>(stage * (W_BYTES >> 4));
+            const uint64_t xd = xd0 + static_cast<uint32_t>(stage * (C::X_BYTES >> 4));
+            const uint32_t t_sfw = tmem + C::T_SF + stage * C::SLOT_COLS;
+#pragma unroll
+            for (int kk = 0; kk < BK / 32; ++kk) {
+              if (MX)
+                mma_mxf8<CG>(elected, acc, wd + 2 * kk, xd + 2 * kk, idesc_with_sf_id(idesc, kk, kk), t_sfw, t_sfw + 4,
+                             ((kt - kt0) | kk) != 0);
+              else
+                mma_f8<CG>(elected, acc, wd + 2 * kk, xd + 2 * kk, idesc, kk != 0);
+            }
+            commit<CG>(elected, &empty[stage]);
+            if (!MX) {
+              commit<CG>(elected, &buf_full[n % BUFS]);
+              ++n;
+            }
+            if (++stage == STAGES) {
+              stage = 0;
+              phase ^= 1u;
+            }
+          }
+          if (!ok) break;
+          if (MX) {
+            commit<CG>(elected, &buf_full[n & 1]);
+            ++n;
+          }
+        }
+        if (!ok) __nanosleep(200000);  // let issued tensor-core work retire
+      }
+      __syncwarp();
     } else if (!MX && !kQuant && warp == 3) {
       // ---------------------------------------------------------- fp8_128: s_x s_w of a block of K and each row of x
       // Lane l prepares rows l, l + 32, ...  Column c = 16 J + 8 g + 2 q + b goes to

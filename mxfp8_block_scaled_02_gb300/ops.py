@@ -986,6 +986,11 @@ def _here(*ts: torch.Tensor | None) -> None:
 _current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else (lambda: -1)
 
 
+def _weights_here(pw: PackedWeights) -> None:
+    if pw.w_packed.get_device() != _current_device():
+        raise ValueError(f"weights on {pw.w_packed.device}, the current device is cuda:{_current_device()}")
+
+
 def _k_blocks(K: int) -> int:
     return (K + 127) // 128
 
@@ -1081,6 +1086,7 @@ def linear_fp8_128(x: torch.Tensor, pw: PackedWeights, bias: torch.Tensor | None
         raise TypeError("x must be bfloat16 (or pass x_scale with a pre-quantised x)")
     if not (x.is_cuda and x.is_contiguous() and x.get_device() == _current_device()):
         _here(x)
+    _weights_here(pw)
     shape = x.shape
     if not shape or shape[-1] != K:
         raise ValueError(f"x {tuple(shape)} does not match weights with K={K}")
@@ -1199,6 +1205,7 @@ def grouped_linear(x: torch.Tensor, pw: PackedWeights, offsets: torch.Tensor, x_
     if quantized and rows is not None:
         raise ValueError("rows go with bf16 x")
     _here(x, offsets)
+    _weights_here(pw)
     shape = x.shape
     if len(shape) != 2 or shape[1] != K:
         raise ValueError(f"x {tuple(shape)} is not [rows, {K}]")
@@ -1378,6 +1385,8 @@ def expert_mlp(x: torch.Tensor, logits: torch.Tensor, gate_up: PackedWeights, do
     if x.dtype is not _BF16:
         raise TypeError("x must be bfloat16")
     _here(x, workspace)
+    _weights_here(gate_up)
+    _weights_here(down)
     shape = x.shape
     if not shape or shape[-1] != K or logits.shape != shape[:-1] + (E,):
         raise ValueError(f"x {tuple(shape)} and logits {tuple(logits.shape)} are not [..., {K}] and [..., {E}]")
