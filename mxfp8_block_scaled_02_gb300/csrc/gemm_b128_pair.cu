@@ -8,9 +8,25 @@
 // scale s_x s_w is one number for a whole block of K.  (With the weights on the M
 // side, as for MXFP8, ragged rows leave no MMA column unused, but each
 // multiply-add reads a sum, an addend and a scale of its own from the register
-// file, which delivers two operands a cycle: 412 cycles a block and scheduler
-// where a scale that stays takes 262, and the scales have to be read from shared
-// memory by every warp.  M = 4096, N = 14336, K = 4096 took 271 us so.)
+// file, which delivers two operands a cycle: 128 of them a warp, two warps a
+// scheduler, take 412 cycles a block where a scale that stays takes 262, and the
+// scales have to be read from shared memory by every warp.  M = 4096, N = 14336, K
+// = 4096 took 271 us so.)
+//
+// Bound by the round of the two buffers: 512 cycles of MMAs, their commit, the load
+// of a buffer into registers (its first half is added before the second has room)
+// and the way back to the MMA warp, ~1.6 us for two blocks, a little over what the
+// operands need from L2 (0.37 us a block) and the multiply-adds of two warps a
+// scheduler (~320 cycles).  M = 4096, N = 14336, K = 4096 166 us, 2.9 PFLOP/s, tensor
+// pipe 59 % busy (ncu), issue slots 58 %; 24576 rows on 61 of 64 experts of 4096 x
+// 2048 226 us: 16 blocks a tile, and a tile's start and output cost 1.3 us more.
+// Steps, the first of those shapes: rows of x in lanes 231 -> scales loaded by the
+// thread that needs them 214 -> output through shared memory 210 -> no branch on the
+// tile in the loop 179 -> the wait for the next block after the additions 172 -> 64
+// columns at a time, the buffer given back before the last are added 166.  Not kept:
+// the columns as two MMAs of 128 with a barrier each, so that the two warps of a
+// scheduler come apart (273: such an MMA takes as long as one of 256); test_wait
+// spins (+0); the next tile's first scales before the output (+1 %).
 //
 // A cluster of two CTAs computes 256 rows x 256 weight rows with cta_group::2: CTA r
 // stages rows [128 r, +128) of both tiles and receives the sums of its rows of x.
@@ -239,19 +255,22 @@ __global__ void __launch_bounds__(THREADS, 1)
       float acc[128];
 #pragma unroll
       for (int i = 0; i < 128; ++i) acc[i] = 0.f;
-      // 32 columns at a time: the next ones are on their way while one lot is added,
-      // also over the end of a block.
-      uint32_t r[2][2][16];
+      // 64 columns at a time; the buffer is given back once the second lot is in
+      // registers, before it is added.
+      uint32_t r[4][16];
+      auto load = [&](uint32_t at) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_ld_32x32b_x16(at + 16 * q, r[q]);
+      };
       int left = a.KT - 1;  // blocks after this one
       if (left > 0) {
         xp += a.xs_kt;
         x2 = __ldg(xp);
         w2 = __ldg(++wp);
       }
-      arrived();
-      tmem_ld_32x32b_x16(src + b * TILE, r[0][0]);
-      tmem_ld_32x32b_x16(src + b * TILE + 16, r[0][1]);
       while (true) {
+        arrived();
+        load(src + b * TILE);
         const float s = x1 * w1;
         x1 = x2;
         w1 = w2;
@@ -260,27 +279,19 @@ __global__ void __launch_bounds__(THREADS, 1)
           x2 = __ldg(xp);
           w2 = __ldg(++wp);
         }
-        const uint32_t at = src + b * TILE;
+        tmem_ld_wait();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          tmem_ld_wait();
-          if (i < 3) {
-            tmem_ld_32x32b_x16(at + 32 * (i + 1), r[(i + 1) & 1][0]);
-            tmem_ld_32x32b_x16(at + 32 * (i + 1) + 16, r[(i + 1) & 1][1]);
-          } else {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_remote(free_bar + static_cast<uint32_t>(b * 8));
-            b ^= 1;
-            bphase ^= b ^ 1;
-          }
+        for (int j = 0; j < 64; ++j) add_scaled(acc[j], r[j >> 4][j & 15], s);
+        load(src + b * TILE + 64);
+        tmem_ld_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(free_bar + static_cast<uint32_t>(b * 8));
+        b ^= 1;
+        bphase ^= b ^ 1;
 #pragma unroll
-          for (int j = 0; j < 32; ++j) add_scaled(acc[32 * i + j], r[i & 1][j >> 4][j & 15], s);
-        }
+        for (int j = 0; j < 64; ++j) add_scaled(acc[64 + j], r[j >> 4][j & 15], s);
         if (left-- == 0) break;
-        arrived();
-        tmem_ld_32x32b_x16(src + b * TILE, r[0][0]);
-        tmem_ld_32x32b_x16(src + b * TILE + 16, r[0][1]);
       }
       // 32 columns at a time: this thread's row to shared memory, 16-byte pieces
       // swizzled; from there four lanes a row.  (From registers, a lane a row of 32
