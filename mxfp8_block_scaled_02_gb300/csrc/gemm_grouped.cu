@@ -35,7 +35,9 @@
 // the operands itself and a second set of scale warps took every other stage, 167
 // without the scales' tensor-memory stores).  fp8_128: eight rows on eight experts of
 // 2048 x 4096 15.7 (4.3 TB/s: 128 tiles on 152 SMs, and ~4 us of chain); one row, N =
-// K = 4096, bf16 x 8.8, of which two thirds are the chain from launch to the exchange.
+// K = 4096, bf16 x quantised inside 7.9 (8.6 with a warp a stage, which loaded x cold and
+// met the instruction cache's misses after the kernel before had ended), of which two
+// thirds are the chain from launch to the exchange.
 //
 // Warps: 0 weight TMA (and, MXFP8, weight scales), 1 tensor-memory allocation and
 // MMA issue, 2 TMA of x, 3 the group table and the scales of fp8_128; MXFP8: 4..7
@@ -196,10 +198,10 @@ __global__ void __launch_bounds__(threads_of<FMT, CG, TN, kQuant>(), 1)
     for (int i = lane; i < C::NBARS; i += 32) {
       uint32_t n = 1;
       uint64_t* b = &full[i];
-      if (kQuant && b < empty) n = 2;  // the copies, and the quantising warp
+      if (kQuant && b < empty) n = 1 + a.R;  // the copies, and each row's codes
       if (MX && b >= sf_ready && b < buf_full) n = CG * C::SC_WARPS;
       if (b >= buf_free && b < sc_full) n = CG * C::EPI_WARPS;
-      if (!MX && b >= sc_full && b < sc_free) n = C::SC_WARPS;
+      if (!MX && b >= sc_full && b < sc_free) n = kQuant ? a.R : C::SC_WARPS;
       if (!MX && b >= sc_free && b < received) n = C::EPI_WARPS;
       mbar_init(b, n);
     }
@@ -517,62 +519,61 @@ __global__ void __launch_bounds__(threads_of<FMT, CG, TN, kQuant>(), 1)
   } else if (kQuant && warp >= C::EPI_FIRST + C::EPI_WARPS) {
     if constexpr (kQuant) {
       // ---------------------------------------------------------- quantisers
-      // Warp q takes every QUANT_WARPS-th stage: eight lanes a row, four rows at a
-      // time, sixteen elements a lane.  (It waits for a slot that was freed at most
-      // one round ago: the stages and slots are at least QUANT_WARPS.)
-      static_assert(!MX && CG == 1 && TN == 16 && STAGES >= QUANT_WARPS && SLOTS >= QUANT_WARPS, "few rows, fp8_128");
-      const int first = warp - C::EPI_FIRST - C::EPI_WARPS;
-      const int c = lane & 7;
+      // Eight lanes a task, a row of a stage: task i is row i % R of stage i / R,
+      // counted on over this worker's units (one group of rows, so unit u is weight
+      // tile u), and group g of up to 16 takes every groups-th.  From one task of a
+      // group to its next are eight stages at the most, no more than there are stages
+      // and slots: the place the next waits for has been freed up to the fill before
+      // last, so that the wait's parity is right; and none waits for what a later task
+      // of its warp would free.  A first round without effect, before x may be read,
+      // brings the code into the instruction cache.
+      static_assert(!MX && CG == 1 && TN == 16 && STAGES >= 8 && SLOTS >= 8, "few rows, fp8_128");
+      const int group = (warp - C::EPI_FIRST - C::EPI_WARPS) * 4 + (lane >> 3);
+      const int groups = min(4 * QUANT_WARPS, 8 * a.R), c = lane & 7;
       float* slots = reinterpret_cast<float*>(smem + C::OFF_SC);
-      grid_dependency_wait();
-      for (int u = worker; u < units; u += nworkers) {
-        const Tile t = tile_of<STEP, TN>(u, a, table);
-        const float* wp = static_cast<const float*>(a.ws) + static_cast<int64_t>(min(t.wt, a.RTW - 1)) * a.KT;
-        const int base_i = (u - worker) / nworkers * (kt1 - kt0);  // stages of the units before
-        uint32_t v[2][8];
-        float w = 0.f;
-        auto fetch = [&](int at) {
-          const int k = at * BK + 16 * c;
-          w = at < kt1 ? __ldg(wp + at) : 0.f;
+      const int nk = kt1 - kt0;
+      const int stages = units > worker ? ((units - 1 - worker) / nworkers + 1) * nk : 0;
+      uint32_t v[8] = {};
+      float w = 0.f;
+      auto fetch = [&](int i) {
+        const int at = i / a.R, r = i - at * a.R;
+        const int nth = at / nk, st = kt0 + at - nth * nk, k = st * BK + 16 * c;
+        const bool in = group < groups && at < stages;
+        if (in) w = __ldg(static_cast<const float*>(a.ws) + static_cast<int64_t>(worker + nth * nworkers) * a.KT + st);
+        if (in && k < a.K) {
+          load16(a.x + static_cast<int64_t>(r) * a.K + k, false, v);
+        } else {
 #pragma unroll
-          for (int p = 0; p < 2; ++p) {
-            const int r = 4 * p + (lane >> 3);
-            if (at < kt1 && r < t.rows && k < a.K) {
-              load16(a.x + static_cast<int64_t>(t.row0 + r) * a.K + k, false, v[p]);
-            } else {
-#pragma unroll
-              for (int j = 0; j < 8; ++j) v[p][j] = 0;
-            }
-          }
-        };
-        int at = kt0 + (first - base_i % QUANT_WARPS + QUANT_WARPS) % QUANT_WARPS;
-        fetch(at);
-        for (; at < kt1; at += QUANT_WARPS) {
-          const int i = base_i + at - kt0;
-          const int stage = i % STAGES, slot = i % SLOTS;
-          Codes codes[2];
-          float scale[2];
-#pragma unroll
-          for (int p = 0; p < 2; ++p) codes[p] = quantize16_b128(v[p], &scale[p]);
-          const float sw = w;
-          fetch(at + QUANT_WARPS);
-          if (!mbar_wait_warp(&empty[stage], static_cast<uint32_t>((i / STAGES) & 1) ^ 1u, abort_flag) ||
-              !mbar_wait_warp(&sc_free[slot], static_cast<uint32_t>((i / SLOTS) & 1) ^ 1u, abort_flag))
-            break;
-#pragma unroll
-          for (int p = 0; p < 2; ++p) {
-            const int r = 4 * p + (lane >> 3);
-            if (r < t.rows)  // 128-byte rows, 16-byte pieces swizzled as TMA does
-              *reinterpret_cast<uint4*>(smem + C::OFF_X + stage * C::X_BYTES + r * BK + ((c ^ r) << 4)) =
-                  make_uint4(codes[p].w[0], codes[p].w[1], codes[p].w[2], codes[p].w[3]);
-            if (c == 0) slots[slot * TN + (((r & 6) << 1) | (r & 1))] = scale[p] * sw;
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&full[stage]);
-            mbar_arrive(&sc_full[slot]);
-          }
+          for (int j = 0; j < 8; ++j) v[j] = 0;
+        }
+      };
+      // the warp's groups go round together; one without a task is idle
+      const int last = (stages * a.R + groups - 1) / groups * groups;
+      for (int i = group - groups; i < last; i += groups) {
+        float scale;
+        const Codes codes = quantize16_b128(v, &scale);
+        const float sw = w;
+        if (i < group) grid_dependency_wait();
+        fetch(i + groups);
+        const int at = i / a.R, r = i - at * a.R;
+        const bool task = i >= 0 && group < groups && at < stages;
+        const int stage = at % STAGES, slot = at % SLOTS;
+        bool free = true;
+        if (task)
+          free = mbar_wait(&empty[stage], static_cast<uint32_t>((at / STAGES) & 1) ^ 1u, abort_flag) &&
+                 mbar_wait(&sc_free[slot], static_cast<uint32_t>((at / SLOTS) & 1) ^ 1u, abort_flag);
+        if (!__all_sync(0xFFFFFFFFu, free)) break;
+        if (task) {
+          // 128-byte rows, 16-byte pieces swizzled as TMA does
+          *reinterpret_cast<uint4*>(smem + C::OFF_X + stage * C::X_BYTES + r * BK + ((c ^ r) << 4)) =
+              make_uint4(codes.w[0], codes.w[1], codes.w[2], codes.w[3]);
+          if (c == 0) slots[slot * TN + (((r & 6) << 1) | (r & 1))] = scale * sw;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (task && c == 0) {
+          mbar_arrive(&full[stage]);
+          mbar_arrive(&sc_full[slot]);
         }
       }
     }

@@ -156,7 +156,8 @@ def test_batches(B, M, N, K):
 
 
 @pytest.mark.parametrize("M,N,K", [(1, 1000, 4112), (2, 8, 16), (3, 520, 2064), (4, 264, 8192), (5, 4096, 384), (7, 256, 512),
-                                   (8, 1032, 1040), (9, 1032, 1040), (8, 20000, 256), (48, 520, 1040), (120, 264, 784), (333, 1000, 4112)])
+                                   (8, 1032, 1040), (9, 1032, 1040), (8, 20000, 256),
+                                   (1, 20000, 1152), (3, 20000, 1152), (5, 40000, 528), (8, 20000, 1152), (48, 520, 1040), (120, 264, 784), (333, 1000, 4112)])
 @pytest.mark.parametrize("with_bias", [False, True])
 def test_bf16_x(M, N, K, with_bias):
     dev = device()
