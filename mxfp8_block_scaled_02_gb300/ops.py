@@ -986,6 +986,13 @@ def _here(*ts: torch.Tensor | None) -> None:
 _current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else (lambda: -1)
 
 
+def _device_here(*ts: torch.Tensor | None) -> None:
+    """Tensors of any strides on the current CUDA device."""
+    for t in ts:
+        if t is not None and not (t.is_cuda and t.get_device() == _current_device()):
+            raise ValueError("tensors must be on the current CUDA device")
+
+
 def _weights_here(pw: PackedWeights) -> None:
     if pw.w_packed.get_device() != _current_device():
         raise ValueError(f"weights on {pw.w_packed.device}, the current device is cuda:{_current_device()}")
@@ -1140,6 +1147,7 @@ def _silu_mul_fp8_128(gate_up: torch.Tensor, up: torch.Tensor | None, tensor_sca
         raise ValueError("fp8_128 scales are row-major; there is no packed form")
     if gate_up.dtype is not _BF16 or (up is not None and up.dtype is not _BF16):
         raise TypeError("gate and up must be bfloat16")
+    _device_here(gate_up, up)
     if up is None:
         if gate_up.dim() < 1 or gate_up.shape[-1] % 32:
             raise ValueError(f"gate_up must be [..., 2 K] with K a multiple of 16, not {tuple(gate_up.shape)}")
@@ -1278,8 +1286,7 @@ def route_workspace_size(T: int, E: int, k: int) -> int:
 
 def _logits2d(logits: torch.Tensor) -> tuple[torch.Tensor, int]:
     """logits [T, E] fp32 or bf16, rows of any stride: (tensor, row stride)."""
-    if not logits.is_cuda or logits.get_device() != _current_device():
-        raise ValueError("tensors must be on the current CUDA device")
+    _device_here(logits)
     dtype = logits.dtype
     if logits.dim() != 2 or not (dtype is _F32 or dtype is _BF16):
         raise ValueError(f"logits must be fp32 or bf16 [tokens, experts], not {dtype} {tuple(logits.shape)}")
@@ -1322,6 +1329,7 @@ def route(logits: torch.Tensor, k: int, *, scoring: str = "softmax", renormalize
 def _added(add: torch.Tensor | None, shape: tuple) -> tuple[torch.Tensor | None, int]:
     if add is None:
         return None, 0
+    _device_here(add)
     if add.dtype is not _BF16 or add.shape != shape:
         raise ValueError(f"add must be bf16 {list(shape)}, not {add.dtype} {list(add.shape)}")
     add, _, stride = _rows2d(add, "add", 8)

@@ -217,3 +217,33 @@ def test_no_tokens():
     block = mlp.ExpertMLP(pack(ops, q1, s1, "mxfp8", dev), pack(ops, q2, s2, "mxfp8", dev), 1)
     out = block(torch.empty(0, 128, dtype=torch.bfloat16, device=dev), torch.empty(0, 2, device=dev))
     assert tuple(out.shape) == (0, 128)
+
+
+def test_tensors_of_another_device(monkeypatch):
+    # calls go to the current device's stream: tensors elsewhere are refused
+    dev = device()
+    rng = np.random.default_rng(0)
+    fmt, bf = "fp8_128", torch.bfloat16
+    q1, s1, _ = weights(rng, fmt, 2, 256, 128)
+    q2, s2, _ = weights(rng, fmt, 2, 128, 128)
+    w1, w2 = pack(ops, q1, s1, fmt, dev), pack(ops, q2, s2, fmt, dev)
+    x, z = torch.ones(4, 128, dtype=bf, device=dev), torch.zeros(4, 2, device=dev)
+    r = ops.route(z, 1)
+    y = ops.grouped_linear(x, w2, r.offsets)
+    calls = [lambda: ops.quantize_fp8_128(x), lambda: ops.quantize_weights_fp8_128(x), lambda: ops.silu_mul_quantize(x, fmt=fmt),
+             lambda: ops.silu_mul_quantize(x, x, fmt=fmt), lambda: ops.linear_fp8_128(x[None].expand(2, 4, 128).contiguous(), w2),
+             lambda: ops.grouped_linear(x, w2, r.offsets), lambda: ops.route(z, 1), lambda: ops.combine(y, r),
+             lambda: ops.expert_mlp(x, z, w1, w2, 1)]
+    for call in calls:
+        call()
+    for call in (lambda: ops.combine(y, r, add=y.cpu()), lambda: ops.expert_mlp(x, z, w1, w2, 1, add=x.cpu()),
+                 lambda: ops.silu_mul_quantize(x, x.cpu(), fmt=fmt), lambda: ops.grouped_linear(x, w2, r.offsets.cpu()),
+                 lambda: ops.expert_mlp(x, z.cpu(), w1, w2, 1)):
+        with pytest.raises(ValueError, match="CUDA device"):
+            call()
+    with monkeypatch.context() as m:
+        m.setattr(ops, "_current_device", lambda: dev.index + 1 if dev.index is not None else 1)
+        for call in calls:
+            with pytest.raises(ValueError, match="current"):
+                call()
+    ops.check()
