@@ -63,6 +63,11 @@ constexpr int W_BYTES = ROWS * BK;
 using Args = GroupedArgs;
 using Tile = GroupTile;
 
+// K splits: what a CTA of a cluster of S receives, 4 KB of each CTA for each group of 8
+// columns that it finishes, and the room for it.
+constexpr int received_bytes(int tn, int splits) { return (tn / 8 + splits - 1) / splits * splits * 4096; }
+constexpr int recv_bytes(int tn) { return tn == 64 ? 40960 : (tn <= 32 ? 32768 : 0); }
+
 template <int FMT, int CG, int TN>
 struct Cfg {
   static constexpr bool MX = FMT == kG8MX;
@@ -79,7 +84,7 @@ struct Cfg {
   static constexpr int THREADS = 32 * (EPI_FIRST + EPI_WARPS + (SC_SETS - 1) * SC_WARPS);
   static constexpr int SF_BYTES = MX ? kAtomBytes : 0;  // weight scales of a stage
   static constexpr int SLOTS = MX ? 0 : 8;              // fp8_128: blocks of K whose scales are staged
-  static constexpr int RECV_BYTES = CG == 1 && TN <= 64 ? 32768 : 0;
+  static constexpr int RECV_BYTES = CG == 1 ? recv_bytes(TN) : 0;
   static constexpr int FIXED = SLOTS * TN * 4 + RECV_BYTES + EPI_WARPS * 1024 + (3 * kMaxGroups + 1) * 4 + 512;
   static constexpr int FIT = (232448 - 1024 - FIXED) / (W_BYTES + X_BYTES + SF_BYTES);
   static constexpr int STAGES = FIT < 12 ? FIT : 12;
@@ -941,9 +946,16 @@ GroupedPlan grouped_plan(int fmt, int64_t E, int64_t R, int64_t N, int64_t K, bo
   for (int tn = few ? 16 : 128; tn >= 16; tn >>= 1) {
     // at most eight tiles of x a group: each reads the weights again, from L2
     if (ceil_div(rows, tn) > 8) break;
-    for (int s = 1; s <= (tn <= 64 ? 8 : 1); s <<= 1) {
-      // split, a cluster does one tile: all of them, however the rows fall, at once
-      if (s > 1 && (grouped_max_tiles(E, R, ragged, tn) * ceil_div(N, kGW_Rows) * s > 152 || ceil_div(K, kGBK) < 2 * s)) break;
+    for (int s = 1; s <= 8; ++s) {
+      // split, a cluster does one tile: all of them, however the rows fall, at once.
+      // kClusterSMs: what the occupancy calculator says that clusters of s fill (M = 64, N
+      // = 2048, K = 16384, 128 CTAs in clusters of 8 20.0 us, of 4 13.0, of 5 12.4; M = 1,
+      // N = 2048, K = 4096 clusters of 8 10.4, of 4 5.6; M = 16, N = K = 5120 clusters of
+      // 2 8.3, of 3 7.6).
+      constexpr int kClusterSMs[9] = {0, 152, 152, 138, 144, 140, 138, 105, 120};
+      if (s > 1 && (received_bytes(tn, s) > recv_bytes(tn) || ceil_div(K, kGBK) < 2 * s ||
+                    grouped_max_tiles(E, R, ragged, tn) * ceil_div(N, kGW_Rows) * s > kClusterSMs[s]))
+        continue;
       const int64_t c = plan_cost(groups, rows, N, K, tn, s);
       if (c <= least) {
         least = c;

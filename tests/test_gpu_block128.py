@@ -144,6 +144,18 @@ def test_exact_sums(M, N, K):
     assert np.array_equal(f64(out), bf16_round(ref + bias))
 
 
+# K split over clusters of 2 to 8 CTAs, tiles of 16, 32 and 64 rows
+SPLITS = [(1, 4736, 1152), (1, 3000, 2048), (1, 2040, 2048), (1, 120, 1152), (1, 120, 2048), (9, 3000, 2048), (9, 2040, 2048),
+          (9, 120, 2048), (24, 3000, 2048), (24, 2040, 2048), (100, 504, 2048), (100, 760, 1152), (150, 120, 1152),
+          (150, 120, 2048), (150, 1000, 1152), (150, 1016, 2048), (150, 1272, 1152), (150, 1656, 1152), (150, 2040, 1152)]
+
+
+@pytest.mark.parametrize("M,N,K", SPLITS)
+def test_exact_sums_of_split_k(M, N, K):
+    test_exact_sums(M, N, K)
+    test_bf16_x(M, N, K, True)
+
+
 @pytest.mark.parametrize("B,M,N,K", [(2, 1, 128, 256), (3, 40, 136, 400), (4, 130, 264, 384), (16, 9, 1000, 512), (2, 300, 520, 272)])
 def test_batches(B, M, N, K):
     dev = device()

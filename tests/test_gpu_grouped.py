@@ -60,6 +60,26 @@ def test_exact_sums(fmt, case):
     assert np.array_equal(f64(out_b), bf16_round(oracle.grouped(x, w, off, bias)))
 
 
+# K split over clusters of 2 to 8 CTAs, tiles of 16, 32 and 64 rows
+SPLITS = [((1, 0, 3, 1, 0, 2, 1, 0), 768, 1152), ((37, 63), 640, 1152), ((1, 1, 1), 128, 1152), ((2, 0, 0, 1, 1, 0, 3, 1), 384, 2048),
+          ((1,) * 8, 256, 2048), ((0, 3, 0), 128, 2048), ((3, 40, 0, 20, 7), 1152, 1152), ((14,) * 5, 768, 1152),
+          ((99, 1), 768, 1152), ((30, 0, 30), 896, 2048), ((0, 0, 70, 0, 0), 384, 2048), ((50, 50), 256, 2048),
+          ((64, 1, 0, 0, 5), 1408, 1152), ((10, 20, 5, 35, 0), 896, 1152), ((1, 99), 1280, 1152), ((65, 35), 1024, 2048),
+          ((20, 20, 20), 512, 2048)]
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("counts,N,K", SPLITS)
+def test_exact_sums_of_split_k(fmt, counts, N, K):
+    dev = device()
+    rng = np.random.default_rng(len(counts) * N + K)
+    xq, xs, wq, ws, x, w = exact_case(rng, fmt, counts, N, K)
+    off = offsets_of(counts)
+    out = ops.grouped_linear(to_dev(xq, dev), pack(ops, wq, ws, fmt, dev), to_dev(off, dev), to_dev(xs, dev))
+    ops.check()
+    assert np.array_equal(f64(out), bf16_round(oracle.grouped(x, w, off)))
+
+
 def test_exact_sums_of_a_ragged_k():
     """fp8_128 with a last block of 16 along K and of 8 along N."""
     dev = device()
