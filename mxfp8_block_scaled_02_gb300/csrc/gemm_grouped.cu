@@ -289,7 +289,9 @@ __global__ void __launch_bounds__(threads_of<FMT, CG, TN, kQuant>(), 1)
         const int mine = t.width / CG;  // rows of x this CTA stages
         const int x0 = t.row0 + rank * mine;
         for (int kt = kt0; kt < kt1; ++kt, ++issued) {
-          if (!mbar_wait_warp(&empty[stage], phase, abort_flag)) {
+          // (Not for weights on their way since the start: the MMAs of such a stage may be
+          // over before this warp comes by, and the next phase waits for this warp.)
+          if (issued >= early && !mbar_wait_warp(&empty[stage], phase, abort_flag)) {
             ok = false;
             break;
           }

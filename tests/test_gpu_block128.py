@@ -271,6 +271,29 @@ def test_graph_and_streams(M):
         assert all(torch.equal(o, want[i]) for o in outs[i])
 
 
+@pytest.mark.parametrize("M", [1, 20, 40, 100])
+def test_beside_kernels_that_hold_the_sms(M):
+    """Warps that come late (the SMs are shared with another stream's kernels) meet every wait in time."""
+    dev = device()
+    rng = np.random.default_rng(M)
+    q, s, _ = weights(rng, "fp8_128", 1000, 1040)
+    pw = ops.process_weights_fp8_128(to_dev(q, dev), to_dev(s, dev))
+    x = to_bf16(bf16_round(rng.standard_normal((M, 1040))), dev)
+    xq, xs = ops.quantize_fp8_128(x)
+    want = ops.linear_fp8_128(x, pw)
+    other, st = torch.rand(1 << 24, device=dev), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(20):
+        for _ in range(4):
+            other = torch.sin(other)
+        with torch.cuda.stream(st):
+            outs += [ops.linear_fp8_128(x, pw) for _ in range(5)] + [ops.linear_fp8_128(xq, pw, x_scale=xs) for _ in range(5)]
+    torch.cuda.synchronize()
+    ops.check()
+    assert all(torch.equal(o, want) for o in outs)
+
+
 @pytest.mark.parametrize("what", ["quantised x", "bias"])
 def test_inputs_the_kernel_ahead_has_just_written(what):
     """x from the quantise call and the bias from a few-token product, back to back, many times."""
