@@ -922,15 +922,19 @@ namespace {
 // eight splits 13.7 / 11.0 / 10.9 / 21.6 (two waves of clusters); M = 200, 64 rows a
 // tile 17.6, 128 20.5, pairs 23.0; M = 512 25.9 / 20.2 / 20.3; N = 14336, K = 4096,
 // M = 48 18.6 / 18.7 / 22.0, M = 256 34.6 / 31.1 / 22.1; N = 1000, K = 4096, M = 333,
-// 64 rows and two splits 15.1, one 16.2, 128 rows 20.1, pairs 22.3.
+// 64 rows and two splits 15.1, one 16.2, 128 rows 20.1, pairs 22.3.  A split costs the
+// exchange, more of it in larger clusters, and once two calls in a row do not fit the
+// SMs together their overlap; pairs start 2 us later.  Over 1500 shapes, 1 to 24576
+// rows, the choice took 2.0 % more time on average than the best that was tried (5 % of
+// them 10 to 36 %, most of those with few of the experts at work).
 int64_t plan_cost(int64_t groups, int64_t rows, int64_t N, int64_t K, int tn, int splits) {
   const int64_t stages = ceil_div(K, kGBK);
   const int64_t workers = tn == 256 ? 76 : 152;
   const int64_t tiles = groups * ceil_div(rows, tn) * ceil_div(N, tn == 256 ? 256 : 128) * splits;
-  const int64_t stage = tn >= 128 ? 36 : (tn == 64 ? 26 : 24);
-  const int64_t tile = stage * ceil_div(stages, splits) + (splits > 1 ? 230 : 150);
+  const int64_t stage = tn == 256 ? 40 : (tn == 128 ? 36 : (tn == 64 ? 26 : 24));
+  const int64_t tile = stage * ceil_div(stages, splits) + (splits > 1 ? 150 + 20 * splits + tn + (tiles > 76 ? 60 : 0) : (tn == 256 ? 130 : 150));
   const int64_t bytes = groups * N * K / 65000;  // the weights at 6.5 TB/s
-  const int64_t t = ceil_div(tiles, workers) * tile;
+  const int64_t t = ceil_div(tiles, workers) * tile + (tn == 256 ? 200 : 0);
   return t > bytes ? t : bytes + tn;  // bound by the weights: the narrowest
 }
 
@@ -939,22 +943,27 @@ int64_t plan_cost(int64_t groups, int64_t rows, int64_t N, int64_t K, int tn, in
 bool b128_quantizes_inside(bool ragged, int64_t E, int64_t R) { return !ragged && E == 1 && R <= QUANT_ROWS; }
 
 // With offsets the host knows the rows a group has only on average, and groups
-// without rows only where there are fewer rows than groups.
+// without rows only where there are fewer rows than groups: it counts on twice as many,
+// because a tile that is too wide costs less than a second one (108 experts, 55 of them
+// with the 1416 rows, 1216 x 1744, fp8_128, 64 rows a tile 27.5 us, 16, enough for the
+// average, 37.0).
 GroupedPlan grouped_plan(int fmt, int64_t E, int64_t R, int64_t N, int64_t K, bool ragged) {
-  const int64_t groups = E < R ? E : (R > 0 ? R : 1), rows = ceil_div(R, groups);
+  const int64_t groups = E < R ? E : (R > 0 ? R : 1), mean = ceil_div(R, groups), rows = ragged && mean > 1 ? 2 * mean : mean;
   const bool few = fmt == kG8B128 && b128_quantizes_inside(ragged, E, R);
   GroupedPlan best = {2, 256, 1};
   int64_t least = few ? INT64_MAX : plan_cost(groups, rows, N, K, 256, 1);
   for (int tn = few ? 16 : 128; tn >= 16; tn >>= 1) {
-    // at most eight tiles of x a group: each reads the weights again, from L2
-    if (ceil_div(rows, tn) > 8) break;
+    // at most eight tiles of x a group, unless all tiles run at once: each reads the
+    // weights again, from L2
+    const int64_t tiles = ceil_div(rows, tn);
+    if (tiles > 8 && groups * tiles * ceil_div(N, kGW_Rows) > 152) break;
     for (int s = 1; s <= 8; ++s) {
       // split, a cluster does one tile: all of them, however the rows fall, at once.
-      // kClusterSMs: what the occupancy calculator says that clusters of s fill (M = 64, N
+      // kClusterSMs: one cluster less than the occupancy calculator has room for (M = 64, N
       // = 2048, K = 16384, 128 CTAs in clusters of 8 20.0 us, of 4 13.0, of 5 12.4; M = 1,
       // N = 2048, K = 4096 clusters of 8 10.4, of 4 5.6; M = 16, N = K = 5120 clusters of
-      // 2 8.3, of 3 7.6).
-      constexpr int kClusterSMs[9] = {0, 152, 152, 138, 144, 140, 138, 105, 120};
+      // 2 8.3, of 3 7.6).  Of 7 there are no more than of 8.
+      constexpr int kClusterSMs[9] = {0, 152, 152, 135, 140, 135, 132, 0, 112};
       if (s > 1 && (received_bytes(tn, s) > recv_bytes(tn) || ceil_div(K, kGBK) < 2 * s ||
                     grouped_max_tiles(E, R, ragged, tn) * ceil_div(N, kGW_Rows) * s > kClusterSMs[s]))
         continue;

@@ -145,9 +145,10 @@ def test_exact_sums(M, N, K):
 
 
 # K split over clusters of 2 to 8 CTAs, tiles of 16, 32 and 64 rows
-SPLITS = [(1, 4736, 1152), (1, 3000, 2048), (1, 2040, 2048), (1, 120, 1152), (1, 120, 2048), (9, 3000, 2048), (9, 2040, 2048),
-          (9, 120, 2048), (24, 3000, 2048), (24, 2040, 2048), (100, 504, 2048), (100, 760, 1152), (150, 120, 1152),
-          (150, 120, 2048), (150, 1000, 1152), (150, 1016, 2048), (150, 1272, 1152), (150, 1656, 1152), (150, 2040, 1152)]
+SPLITS = [(1, 3240, 1152), (1, 120, 1152), (1, 120, 2048), (1, 1560, 4096), (1, 1160, 4096), (1, 120, 4096), (9, 3240, 1152),
+          (9, 120, 1152), (9, 120, 2048), (9, 120, 4096), (24, 3000, 2048), (24, 2040, 2048), (100, 504, 2048), (150, 120, 4096),
+          (150, 120, 8192), (150, 200, 2048), (150, 200, 4096), (150, 1000, 1152), (200, 120, 4096), (200, 200, 1152),
+          (200, 200, 4096), (200, 200, 8192), (200, 280, 4096), (200, 440, 1152), (200, 440, 2048), (200, 1080, 2048)]
 
 
 @pytest.mark.parametrize("M,N,K", SPLITS)

@@ -61,11 +61,10 @@ def test_exact_sums(fmt, case):
 
 
 # K split over clusters of 2 to 8 CTAs, tiles of 16, 32 and 64 rows
-SPLITS = [((1, 0, 3, 1, 0, 2, 1, 0), 768, 1152), ((37, 63), 640, 1152), ((1, 1, 1), 128, 1152), ((2, 0, 0, 1, 1, 0, 3, 1), 384, 2048),
-          ((1,) * 8, 256, 2048), ((0, 3, 0), 128, 2048), ((3, 40, 0, 20, 7), 1152, 1152), ((14,) * 5, 768, 1152),
-          ((99, 1), 768, 1152), ((30, 0, 30), 896, 2048), ((0, 0, 70, 0, 0), 384, 2048), ((50, 50), 256, 2048),
-          ((64, 1, 0, 0, 5), 1408, 1152), ((10, 20, 5, 35, 0), 896, 1152), ((1, 99), 1280, 1152), ((65, 35), 1024, 2048),
-          ((20, 20, 20), 512, 2048)]
+SPLITS = [((1, 0, 3, 1, 0, 2, 1, 0), 512, 1152), ((1, 1, 1), 128, 1152), ((0, 3, 0), 128, 2048), ((1, 1, 1), 128, 4096),
+          ((37, 63), 128, 4096), ((3, 40, 0, 20, 7), 128, 4096), ((99, 1), 512, 1152), ((50, 50), 256, 1152), ((100, 0), 256, 2048),
+          ((14,) * 5, 384, 4096), ((0, 0, 70, 0, 0), 256, 4096), ((64, 1, 0, 0, 5), 1408, 2048), ((65, 35), 640, 1152),
+          ((1, 99), 512, 2048), ((50, 50), 384, 4096), ((20, 20, 20), 512, 2048), ((1,) * 8, 256, 2048)]
 
 
 @pytest.mark.parametrize("fmt", FMTS)
