@@ -280,24 +280,25 @@ __global__ void __launch_bounds__(threads_of<FMT, CG, TN, kQuant>(), 1)
       // ------------------------------------------------------------ producers
       const uint32_t full_bar = CG == 2 ? map_shared_rank(smem_u32(full), 0) : smem_u32(full);
       if (warp == 2) grid_dependency_wait();
-      int stage = 0;
-      uint32_t phase = 1;  // the first round's stages are free
-      int64_t issued = 0;
+      // Behind the weights that are on their way since the start.  (Their stages are not
+      // waited for: the MMAs of one may be over before this warp comes by, and its next
+      // phase waits for this warp.)
+      int stage = early % STAGES, kt = kt0 + early;
+      uint32_t phase = early < STAGES ? 1 : 0;  // the first round's stages are free
+      int64_t issued = early;
       bool ok = true;
-      for (int u = worker; ok && u < units; u += nworkers) {
+      for (int u = worker; ok && u < units; u += nworkers, kt = kt0) {
         const Tile t = tile_of<STEP, TN>(u, a, table);
         const int mine = t.width / CG;  // rows of x this CTA stages
         const int x0 = t.row0 + rank * mine;
-        for (int kt = kt0; kt < kt1; ++kt, ++issued) {
-          // (Not for weights on their way since the start: the MMAs of such a stage may be
-          // over before this warp comes by, and the next phase waits for this warp.)
-          if (issued >= early && !mbar_wait_warp(&empty[stage], phase, abort_flag)) {
+        for (; kt < kt1; ++kt, ++issued) {
+          if (!mbar_wait_warp(&empty[stage], phase, abort_flag)) {
             ok = false;
             break;
           }
           const uint32_t bar = full_bar + stage * 8;
           if (warp == 0) {
-            if (issued >= early) load_weights(stage, kt, t);
+            load_weights(stage, kt, t);
           } else if (mine == C::XROWS) {
             tma_load<CG>(elected, base + C::OFF_X + stage * C::X_BYTES, &tmX, bar, kt * BK, x0, 0);
           } else {
