@@ -59,14 +59,23 @@ mxfp8_status check_product(int fmt, int64_t E, int64_t R, int64_t N, int64_t K, 
 }
 
 // Codes and scale words of x quantised inside a call: [R, K], then [ceil(K / 128)][R].
+// Where many rows are picked from at most half as many tokens, the tokens are quantised
+// first, [T, K] and [T][ceil(K / 128)], and their codes picked (MXFP8, 16384 rows picked
+// from 2048 tokens, 16 experts of 4096 x 4096, the whole call 213 -> 204 us; for fewer
+// rows the launch costs more than it saves).
 struct XLayout {
-  int64_t s, total;
+  int64_t s, tq, ts, total;
 };
 
-XLayout x_layout(int64_t R, int64_t K) {
+bool picks_codes(int64_t R, int64_t K) { return R * K >= 1ll << 24; }
+
+XLayout x_layout(int64_t R, int64_t K, bool ragged) {
+  const int64_t half = ragged && picks_codes(R, K) ? R / 2 : 0, KT = ceil_div(K, 128);
   XLayout w;
   w.s = round_up(R * K, 256);
-  w.total = w.s + round_up(4 * R * ceil_div(K, 128), 256);
+  w.tq = w.s + round_up(4 * R * KT, 256);
+  w.ts = w.tq + round_up(half * K, 256);
+  w.total = w.ts + round_up(4 * half * KT, 256);
   return w;
 }
 
@@ -108,7 +117,7 @@ mxfp8_status run_product(const Product& p, void* workspace, size_t workspace_byt
     return fail(MXFP8_ERR_INVALID_ARG, "tensor pointers must be 16-byte aligned");
   if (!aligned(p.rows, 4) || !aligned(p.offsets, 4))
     return fail(MXFP8_ERR_INVALID_ARG, "rows and offsets must be 4-byte aligned");
-  const XLayout l = x_layout(p.R, p.K);
+  const XLayout l = x_layout(p.R, p.K, p.offsets != nullptr);
   const int64_t turned = have_q ? turned_bytes(p.fmt, p.E, p.R, p.N, p.K, p.offsets != nullptr) : 0;
   const bool inside = have_x && p.fmt == MXFP8_GFMT_FP8_128 && p.rows == nullptr &&
                       mx::b128_quantizes_inside(p.offsets != nullptr, p.E, p.R);
@@ -146,8 +155,12 @@ mxfp8_status run_product(const Product& p, void* workspace, size_t workspace_byt
     g.x_bf16 = p.x_bf16;
   } else if (have_x) {
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    const mx::QuantRowsProblem q{p.fmt, p.x_bf16, p.rows, p.T, p.R, p.K, ws, ws + l.s, 1, p.R, true};
+    const bool pick = p.rows != nullptr && p.T > 0 && p.T <= p.R / 2 && picks_codes(p.R, p.K);
+    mx::QuantRowsProblem q{p.fmt, p.x_bf16, p.rows, p.T, p.R, p.K, ws, ws + l.s, 1, p.R, true};
+    if (pick) q = mx::QuantRowsProblem{p.fmt, p.x_bf16, nullptr, p.T, p.T, p.K, ws + l.tq, ws + l.ts, KT, 1, true};
     cudaError_t e = mx::launch_quantize_rows(q, as_stream(stream));
+    if (e == cudaSuccess && pick)
+      e = mx::launch_gather_rows(ws + l.tq, ws + l.ts, p.rows, p.T, p.R, p.K, ws, ws + l.s, as_stream(stream));
     if (e != cudaSuccess) return cuda_fail(e, "quantise launch");
     g.x = ws;
     g.xs = ws + l.s;
@@ -300,7 +313,7 @@ mxfp8_status mxfp8_b128_workspace_size(int64_t B, int64_t M, int64_t N, int64_t 
     return fail(MXFP8_ERR_INVALID_ARG, "B=%lld M=%lld", (ll)B, (ll)M);
   mxfp8_status st = check_product(MXFP8_GFMT_FP8_128, B, B * M, N, K, false);
   if (st == MXFP8_OK)
-    *bytes = x_is_quantized || mx::b128_quantizes_inside(false, B, B * M) ? 0 : static_cast<size_t>(x_layout(B * M, K).total);
+    *bytes = x_is_quantized || mx::b128_quantizes_inside(false, B, B * M) ? 0 : static_cast<size_t>(x_layout(B * M, K, false).total);
   return st;
 }
 
@@ -322,7 +335,7 @@ mxfp8_status mxfp8_grouped_workspace_size(int fmt, int64_t E, int64_t R, int64_t
   if (bytes == nullptr) return fail(MXFP8_ERR_INVALID_ARG, "null output pointer");
   mxfp8_status st = check_product(fmt, E, R, N, K, true);
   if (st == MXFP8_OK)
-    *bytes = static_cast<size_t>(R == 0 ? 0 : x_is_quantized ? turned_bytes(fmt, E, R, N, K, true) : x_layout(R, K).total);
+    *bytes = static_cast<size_t>(R == 0 ? 0 : x_is_quantized ? turned_bytes(fmt, E, R, N, K, true) : x_layout(R, K, true).total);
   return st;
 }
 

@@ -82,6 +82,10 @@ struct ActRowsProblem {
   int64_t s_row, s_kt;
 };
 cudaError_t launch_silu_mul_rows(const ActRowsProblem& p, cudaStream_t stream);
+// Codes [T, K] and scale words [T][KT] -> those of rows [R], words as [KT][R]; a row of
+// zeros for an index outside [0, T).
+cudaError_t launch_gather_rows(const void* xq, const void* xs, const int* rows, int64_t T, int64_t R, int64_t K, uint8_t* q,
+                               void* s, cudaStream_t stream);
 // Scale words [R][KT] -> [KT][R] (KT at most 2^21).
 cudaError_t launch_transpose_words(const void* in, int64_t R, int64_t KT, void* out, cudaStream_t stream);
 // bf16 weights [B, N, K] -> E4M3 codes and fp32 scales [B, ceil(N / 128), ceil(K / 128)].

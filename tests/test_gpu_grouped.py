@@ -125,6 +125,30 @@ def test_bf16_x_in_order_and_picked(fmt, counts, N, K):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("T,R", [(1, 4099), (300, 4100), (2050, 4100), (2051, 4100)])
+def test_many_rows_picked_from_few_tokens(fmt, T, R):
+    """Both sides of the rule that quantises the tokens and picks their codes: the bytes are those of x[rows]."""
+    dev = device()
+    rng = np.random.default_rng(T)
+    N, K = 136, 4096 if fmt == "mxfp8" else 4112
+    q, s, _ = weights(rng, fmt, 3, N, K)
+    pw = pack(ops, q, s, fmt, dev)
+    x = to_bf16(bf16_round(rng.standard_normal((T, K))), dev)
+    rows = torch.from_numpy(rng.integers(-2, T + 2, R).astype(np.int32)).to(dev)
+    off = torch.tensor([0, 1500, 1500, R - 3], dtype=torch.int32, device=dev)
+    out = ops.grouped_linear(x, pw, off, rows=rows)
+    inside = (rows >= 0) & (rows < T)
+    picked = torch.where(inside[:, None], x[rows.clamp(0, T - 1).long()], torch.zeros((), dtype=x.dtype, device=dev))
+    want = ops.grouped_linear(picked, pw, off)
+    band, need = 4096, ops.grouped_workspace_size(pw.fmt, 3, R, N, K, False)
+    ws = torch.full((2 * band + need,), 0xA5, dtype=torch.uint8, device=dev)
+    again = ops.grouped_linear(x, pw, off, rows=rows, workspace=ws[band:band + need])
+    ops.check()
+    assert torch.equal(out[:R - 3], want[:R - 3]) and torch.equal(again[:R - 3], want[:R - 3])
+    assert (ws[:band] == 0xA5).all() and (ws[band + need:] == 0xA5).all()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("R,first,last", [(40, 5, 33), (400, 1, 399), (100, 0, 0)])
 def test_rows_of_no_expert_are_left(fmt, R, first, last):
     dev = device()
