@@ -39,8 +39,8 @@ def test_sizes(lib):
     assert ops.workspace_size_fp8_128(1, 8, 256, 512, False) == 0 and ops.workspace_size_fp8_128(1, 9, 256, 512, False) > 0
     assert ops.grouped_workspace_size("e4m3", 8, 100, 256, 512, False) == up(100 * 512) + up(4 * 100 * 4)
     assert ops.grouped_workspace_size("fp8_128", 8, 100, 256, 512, True) == 0
-    assert ops.route_workspace_size(64, 128, 8) == 0          # one CTA
-    assert ops.route_workspace_size(65, 128, 8) == ops.route_workspace_size(1 << 20, 128, 8) == 160 * 128 * 4
+    assert ops.route_workspace_size(32, 128, 8) == 0          # one CTA
+    assert ops.route_workspace_size(33, 128, 8) == ops.route_workspace_size(1 << 20, 128, 8) == 160 * 128 * 4
     assert ops.route_workspace_size(0, 8, 2) == 0
     assert ops.expert_mlp_workspace_size("fp8_128", 0, 8, 2, 256, 128) >= 0
 

@@ -23,7 +23,8 @@ def assert_routing(r: ops.Routing, want: dict, z: np.ndarray, scale: float = 1.0
     assert (np.abs(w - want["weights"]) <= rel * np.abs(want["weights"]) + 2.0 ** -126 * abs(scale)).all()
 
 
-SIZES = [(1, 1, 1), (1, 8, 8), (3, 5, 2), (16, 64, 8), (64, 33, 4), (65, 128, 6), (200, 256, 8), (1000, 512, 32), (130, 100, 1),
+SIZES = [(1, 1, 1), (1, 8, 8), (3, 5, 2), (16, 64, 8), (32, 64, 8), (33, 64, 8), (64, 33, 4), (65, 128, 6), (1281, 40, 3),
+         (200, 256, 8), (1000, 512, 32), (130, 100, 1),
          (20000, 16, 2)]
 
 
