@@ -630,8 +630,9 @@ mxfp8_status mxfp8_b128_linear(const void* x_bf16, const uint8_t* x_q, const flo
  *     row of zeros), or x[r] with rows NULL and T == R.  Or x_q [R, K] with
  *     x_scale, E8M0 [R, K / 32] or fp32 [R, ceil(K / 128)].
  *   offsets : device, int32 [E + 1]; read on the device, so a captured graph
- *     follows it.  Each is taken as at least 0 and the one before it, and at
- *     most R, so that groups never overlap.  Rows of out that belong to no group
+ *     follows it (several CTAs read it: it must not change during the call).
+ *     Each is taken as at least 0 and the one before it, and at most R, so that
+ *     groups never overlap.  Rows of out that belong to no group
  *     are left as they were.
  *   w       : MXFP8: w_packed of mxfp8_process_weights(B = E) and w_scale its
  *     sf_packed; FP8_128: E4M3 [E, N, K] and fp32 [E, ceil(N / 128),

@@ -294,3 +294,28 @@ def test_many_small_last_tiles_back_to_back(fmt):
     lo, hi = 242 + 266, 242 + 266 + 258
     alone = ops.grouped_linear(x[lo:hi].contiguous(), pw, to_dev(np.array([0, 0, 0] + [258] * (E - 2), dtype=np.int32), dev))
     assert torch.equal(want[lo:hi], alone)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("counts,N,K", [((1, 0, 3, 1, 2), 512, 1152), ((9, 40, 0, 20), 392, 1024), ((300, 0, 129, 700), 520, 640),
+                                        ((1100, 64, 0, 900), 392, 1152)])
+def test_beside_kernels_that_hold_the_sms(fmt, counts, N, K):
+    """Warps that come late (the SMs are shared with another stream's kernels) meet every wait in time."""
+    dev = device()
+    rng = np.random.default_rng(N)
+    q, s, _ = weights(rng, fmt, len(counts), N, K)
+    pw, off = pack(ops, q, s, fmt, dev), to_dev(offsets_of(counts), dev)
+    x = to_bf16(bf16_round(rng.standard_normal((sum(counts), K))), dev)
+    xq, xs = ops.quantize_fp8_128(x) if fmt == "fp8_128" else ops.quantize(x)
+    want = ops.grouped_linear(x, pw, off)
+    other, st = torch.rand(1 << 24, device=dev), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(20):
+        for _ in range(4):
+            other = torch.sin(other)
+        with torch.cuda.stream(st):
+            outs += [ops.grouped_linear(x, pw, off) for _ in range(5)] + [ops.grouped_linear(xq, pw, off, xs) for _ in range(5)]
+    torch.cuda.synchronize()
+    ops.check()
+    assert all(torch.equal(o, want) for o in outs)

@@ -138,9 +138,12 @@ def restated_steps(x, logits, gate_up, down, k, add, **how):
 
 
 @pytest.mark.parametrize("fmt", ["mxfp8", "fp8_128"])
-@pytest.mark.parametrize("T,E,k,K,F", [(1, 8, 2, 256, 128), (5, 16, 4, 384, 256), (70, 8, 8, 256, 384), (600, 4, 2, 512, 256)])
+@pytest.mark.parametrize("T,E,k,K,F", [(1, 8, 2, 256, 128), (5, 16, 4, 384, 256), (70, 8, 8, 256, 384), (600, 4, 2, 512, 256),
+                                       (3000, 4, 2, 256, 384), (2500, 9, 4, 512, 128), (1700, 3, 1, 640, 400)])
 def test_expert_mlp_is_its_steps(fmt, T, E, k, K, F):
     """Bit for bit the calls it is made of, and near the fp64 block."""
+    if fmt == "mxfp8" and F % 128:
+        pytest.skip("K is a multiple of 128 in MXFP8")
     dev = device()
     rng = np.random.default_rng(T + F)
     q1, s1, w1 = weights(rng, fmt, E, 2 * F, K)
