@@ -108,12 +108,14 @@ struct Cfg {
   static constexpr int T_END = MX ? T_SF + STAGES * SLOT_COLS : BUFS * ACOLS;
   static constexpr int TMEM_COLS = T_END <= 128 ? 128 : (T_END <= 256 ? 256 : 512);
   static_assert(T_END <= 512 && (MX || CG == 1), "tensor memory");
-  // barriers: full, empty; MXFP8 sf_full, sf_ready a stage; buf_full, buf_free a
-  // buffer; sc_full, sc_free a slot; received
+  // barriers: full, empty; MXFP8 sf_full, sf_ready a stage; buf_full (MXFP8), buf_free a
+  // buffer; sc_full, sc_free a slot; received.  fp8_128: the commit that frees a stage
+  // also says that the block's sums are there (one commit a block less: M = 1, N = 2048,
+  // K = 4096 5.7 -> 5.5 us); a stage's next phase is further off than the buffers reach.
   static constexpr int NBARS = (MX ? 4 : 2) * STAGES + 2 * BUFS + 2 * SLOTS + 1;
   static constexpr int OFF_MISC = OFF_BAR + NBARS * 8;
   static constexpr int SMEM = OFF_MISC + 16 + 1024;
-  static_assert(SMEM <= 232448 && STAGES >= 4, "shared memory");
+  static_assert(SMEM <= 232448 && STAGES >= (MX ? 4 : BUFS + 1), "shared memory");
 };
 
 // ---------------------------------------------------------------- fragments
@@ -374,10 +376,7 @@ __global__ void __launch_bounds__(threads_of<FMT, CG, TN, kQuant>(), 1)
                 mma_f8<CG>(elected, acc, wd + 2 * kk, xd + 2 * kk, idesc, kk != 0);
             }
             commit<CG>(elected, &empty[stage]);
-            if (!MX) {
-              commit<CG>(elected, &buf_full[n % BUFS]);
-              ++n;
-            }
+            if (!MX) ++n;
             if (++stage == STAGES) {
               stage = 0;
               phase ^= 1u;
@@ -738,9 +737,9 @@ __global__ void __launch_bounds__(threads_of<FMT, CG, TN, kQuant>(), 1)
         for (int kt = kt0; kt < kt1; ++kt) {
           // the sums of block n (in buffer n % BUFS) and its scales; a wait that ran out
           // only makes the later ones return at once
-          const uint32_t bp = static_cast<uint32_t>((n / BUFS) & 1);
+          const uint32_t bp = static_cast<uint32_t>((n / STAGES) & 1);
           if (!mbar_try_wait(&sc_full[slot], sphase)) mbar_wait_inline(&sc_full[slot], sphase, abort_flag);
-          if (!mbar_try_wait(&buf_full[n % BUFS], bp)) mbar_wait_inline(&buf_full[n % BUFS], bp, abort_flag);
+          if (!mbar_try_wait(&empty[n % STAGES], bp)) mbar_wait_inline(&empty[n % STAGES], bp, abort_flag);
           __syncwarp();
           tc_fence_after();
           load(0);
