@@ -59,10 +59,11 @@ mxfp8_status check_product(int fmt, int64_t E, int64_t R, int64_t N, int64_t K, 
 }
 
 // Codes and scale words of x quantised inside a call: [R, K], then [ceil(K / 128)][R].
-// Where many rows are picked from at most half as many tokens, the tokens are quantised
-// first, [T, K] and [T][ceil(K / 128)], and their codes picked (MXFP8, 16384 rows picked
-// from 2048 tokens, 16 experts of 4096 x 4096, the whole call 213 -> 204 us; for fewer
-// rows the launch costs more than it saves).
+// Where many rows are picked from at most a quarter as many tokens, the tokens are
+// quantised first, [T, K] and [T][ceil(K / 128)], and their codes picked (us, the whole
+// call in one step and in two, MXFP8, 16 experts of 2048 x 4096: 16384 rows from 2048
+// tokens 118 / 107, from 8192 118 / 120; 4096 rows from 512 42.7 / 41.2, from 2048 42.6 /
+// 44.0; 2048 rows from 256 34.6 / 35.5).
 struct XLayout {
   int64_t s, tq, ts, total;
 };
@@ -70,12 +71,12 @@ struct XLayout {
 bool picks_codes(int64_t R, int64_t K) { return R * K >= 1ll << 24; }
 
 XLayout x_layout(int64_t R, int64_t K, bool ragged) {
-  const int64_t half = ragged && picks_codes(R, K) ? R / 2 : 0, KT = ceil_div(K, 128);
+  const int64_t most = ragged && picks_codes(R, K) ? R / 4 : 0, KT = ceil_div(K, 128);
   XLayout w;
   w.s = round_up(R * K, 256);
   w.tq = w.s + round_up(4 * R * KT, 256);
-  w.ts = w.tq + round_up(half * K, 256);
-  w.total = w.ts + round_up(4 * half * KT, 256);
+  w.ts = w.tq + round_up(most * K, 256);
+  w.total = w.ts + round_up(4 * most * KT, 256);
   return w;
 }
 
@@ -155,7 +156,7 @@ mxfp8_status run_product(const Product& p, void* workspace, size_t workspace_byt
     g.x_bf16 = p.x_bf16;
   } else if (have_x) {
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    const bool pick = p.rows != nullptr && p.T > 0 && p.T <= p.R / 2 && picks_codes(p.R, p.K);
+    const bool pick = p.rows != nullptr && p.T > 0 && p.T <= p.R / 4 && picks_codes(p.R, p.K);
     mx::QuantRowsProblem q{p.fmt, p.x_bf16, p.rows, p.T, p.R, p.K, ws, ws + l.s, 1, p.R, true};
     if (pick) q = mx::QuantRowsProblem{p.fmt, p.x_bf16, nullptr, p.T, p.T, p.K, ws + l.tq, ws + l.ts, KT, 1, true};
     cudaError_t e = mx::launch_quantize_rows(q, as_stream(stream));
