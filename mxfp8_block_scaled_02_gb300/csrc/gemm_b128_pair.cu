@@ -18,7 +18,7 @@
 // and the way back to the MMA warp, ~1.6 us for two blocks, a little over what the
 // operands need from L2 (0.37 us a block) and the multiply-adds of two warps a
 // scheduler (~320 cycles).  M = 4096, N = 14336, K = 4096 166 us, 2.9 PFLOP/s, tensor
-// pipe 59 % busy (ncu), issue slots 58 %; 24576 rows on 61 of 64 experts of 4096 x
+// pipe 61 % busy (ncu), issue slots 57 %; 24576 rows on 61 of 64 experts of 4096 x
 // 2048 226 us: 16 blocks a tile, and a tile's start and output cost 1.3 us more.
 // Steps, the first of those shapes: rows of x in lanes 231 -> scales loaded by the
 // thread that needs them 214 -> output through shared memory 210 -> no branch on the
