@@ -15,7 +15,7 @@
 //
 // Bound by the round of the two buffers: 512 cycles of MMAs, their commit, the load
 // of a buffer into registers (its first half is added before the second has room)
-// and the way back to the MMA warp, ~1.6 us for two blocks, a little over what the
+// and the way back to the MMA warp, ~0.85 us for two blocks, a little over what the
 // operands need from L2 (0.37 us a block) and the multiply-adds of two warps a
 // scheduler (~320 cycles).  M = 4096, N = 14336, K = 4096 166 us, 2.9 PFLOP/s, tensor
 // pipe 61 % busy (ncu), issue slots 57 %; 24576 rows on 61 of 64 experts of 4096 x
