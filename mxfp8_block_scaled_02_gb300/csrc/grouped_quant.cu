@@ -9,8 +9,10 @@
 // Bound by reading x and writing the codes.  Sixteen elements a lane (32 bytes in,
 // 16 out: whole sectors), a block of 128 eight lanes, 512 elements a warp; one task a
 // warp, many warps.  (Two or four tasks a warp with their loads first are slower: 4096
-// x 14336 silu 52.4 us with one, 57.0 with two, both of six CTAs an SM; 16384 rows of 4096 picked from 2048
-// tokens 30.3, 30.6 with two, 31.6 with four.)
+// x 14336 silu 52.4 us with one, 57.0 with two, both at six CTAs an SM; 16384 rows of
+// 4096 picked from 2048 tokens 30.3, 30.6 with two, 31.6 with four.  16384 x 4096
+// quantised 39.2 us, 5.2 TB/s: the issue slots are 85 % busy, 38.8 with CTAs of 128
+// threads, 40.8 of 512, 39.1 with fewer instructions a division or an index.)
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
