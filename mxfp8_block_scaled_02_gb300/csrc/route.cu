@@ -167,11 +167,12 @@ __device__ __forceinline__ void select_any(const Args& a, int64_t t0, int64_t t1
 }
 
 // Rows and positions of tokens [t0, t1), whose experts are in a.ids; next[e]: the row
-// of the first of them (shared; advanced).
+// of the first of them (shared; advanced).  A thread clears the words whose bits it has
+// just counted: nobody else touches them between the two barriers around that.
 __device__ __forceinline__ void place_range(const Args& a, int64_t t0, int64_t t1, int* next, uint32_t* mask) {
+  for (int e = threadIdx.x; e < 2 * a.E; e += THREADS) mask[e] = 0;
   for (int64_t g0 = t0; g0 < t1; g0 += GROUP) {
     const int slots = static_cast<int>(min(static_cast<int64_t>(GROUP), t1 - g0)) * a.k;
-    for (int e = threadIdx.x; e < 2 * a.E; e += THREADS) mask[e] = 0;
     __syncthreads();
     for (int i = threadIdx.x; i < slots; i += THREADS) {
       const int e = a.ids[g0 * a.k + i], t = i / a.k;
@@ -189,7 +190,10 @@ __device__ __forceinline__ void place_range(const Args& a, int64_t t0, int64_t t
       a.positions[g0 * a.k + i] = pos;
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < a.E; e += THREADS) next[e] += __popc(mask[2 * e]) + __popc(mask[2 * e + 1]);
+    for (int e = threadIdx.x; e < a.E; e += THREADS) {
+      next[e] += __popc(mask[2 * e]) + __popc(mask[2 * e + 1]);
+      mask[2 * e] = mask[2 * e + 1] = 0;
+    }
   }
 }
 
