@@ -336,8 +336,9 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   tc_fence_before();
   __syncthreads();
-  cluster_arrive_relaxed();
-  cluster_wait();  // neither CTA leaves while the other may still signal it
+  // Neither CTA leaves while the other may still signal it; the odd CTA's last arrivals
+  // on buf_free, which nobody waits for, are ordered by this barrier.
+  cluster_sync();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, TMEM_COLS);

@@ -601,8 +601,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     cluster_arrive_relaxed();
     cluster_wait();
   }
-  cluster_arrive_relaxed();
-  cluster_wait();  // no CTA of the cluster leaves while another may still signal it
+  // No CTA of the cluster leaves while another may still signal it; the odd CTA's last
+  // arrival on acc_free, which nobody waits for, is ordered by this barrier.
+  cluster_sync();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, TMEM_COLS);

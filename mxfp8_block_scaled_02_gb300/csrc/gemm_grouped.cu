@@ -792,9 +792,14 @@ __global__ void __launch_bounds__(threads_of<FMT, CG, TN, kQuant>(), 1)
 
   tc_fence_before();
   __syncthreads();
-  if (csize > 1) {
+  // No CTA of the cluster leaves while another may still signal it.  Pairs: the odd CTA's
+  // last arrivals on buf_free are waited for by nobody, so this barrier has to order them.
+  // K splits: all that is sent is waited for above.
+  if (CG == 2) {
+    cluster_sync();
+  } else if (csize > 1) {
     cluster_arrive_relaxed();
-    cluster_wait();  // no CTA of the cluster leaves while another may still signal it
+    cluster_wait();
   }
   if (warp == 1) {
     tc_fence_after();
