@@ -674,7 +674,11 @@ __global__ void __launch_bounds__(threads_of<FMT, CG, TN, kQuant>(), 1)
       for (int u = worker; u < units; u += nworkers, ++n) {
         start_tile(u);
         const int b = n & 1;
-        if (!__all_sync(0xFFFFFFFFu, mbar_wait(&buf_full[b], static_cast<uint32_t>((n >> 1) & 1), abort_flag))) break;
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(&buf_full[b], static_cast<uint32_t>((n >> 1) & 1), abort_flag))) {
+          // without a sum of its own a CTA still waits for those of its cluster's others
+          if (split) finish_split();
+          break;
+        }
         tc_fence_after();
         const uint32_t acc = lanes + b * C::ACC_STEP;
         // Pairs: the columns shared with the next tile's accumulator first (the

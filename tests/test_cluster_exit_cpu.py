@@ -39,3 +39,14 @@ def test_the_last_cluster_barrier_orders_the_signals(name):
 
 def test_some_kernels_signal():
     assert {"gemm_b128_pair.cu", "gemm_grouped.cu", "gemm_pair.cu", "gemm_fp4.cu"} <= set(kernels_that_signal())
+
+
+def test_a_wait_that_ran_out_still_waits_for_what_others_send():
+    """The grouped product's K splits: no partial sum may land after the CTA that it was sent to has left."""
+    with open(os.path.join(build.CSRC, "gemm_grouped.cu")) as f:
+        text = re.sub(r"//[^\n]*", "", f.read())
+    epilogue = text[text.index("auto finish_split ="):]
+    epilogue = epilogue[epilogue.index("const bool split"):epilogue.index("__syncthreads();")]
+    for leave in re.finditer(r"\bbreak;", epilogue):
+        before = epilogue[:leave.start()].rstrip()
+        assert before.endswith("finish_split();"), before[-200:]
