@@ -162,8 +162,10 @@ mxfp8_status mxfp8_workspace_size(int64_t B, int64_t M, int64_t N, int64_t K,
  *   (whose output only the same call's GEMM reads, after its wait), the
  *   CTA-pair GEMM when it splits K (whose partials only the same call's
  *   reduce reads, after its wait), the small-M GEMM, the 4-bit layer's
- *   counterparts of these, and the norm and activation calls.  What the last
- *   three write (out, y_q, y_sf, codes, scales, residual_out, y_bf16) may be any
+ *   counterparts of these, the norm and activation calls, and the block-128,
+ *   grouped, routing and weighted-sum calls (not mxfp8_b128_quantize and
+ *   mxfp8_b128_quantize_weights).  What all but the first two write (out, y_q,
+ *   y_sf, codes, scales, residual_out, y_bf16, a routing) may be any
  *   input of the next call but its w_packed and sf_packed: pass codes and
  *   scales that are to be weights through mxfp8_process_weights or
  *   mxfp8_fp4_process_weights.
@@ -611,9 +613,12 @@ mxfp8_status mxfp8_b128_silu_mul_quantize(const void* gate_bf16, int64_t gate_st
  *   aligned; M = 0 is a no-op.
  *   Sums within a block and over the blocks are fp32; one rounding, after the
  *   bias.  Where K is split over CTAs their partial sums are added in the order
- *   of K: a call's result is the same every time.  w may be read before the
- *   kernel ahead in the stream ends if that kernel triggers its dependents early
- *   (the calls of this library that make weights do not).
+ *   of K: a call's result is the same every time.
+ *   Stream ordering as mxfp8_linear: w and w_scale may be read before the
+ *   kernels ahead in the stream end if those trigger their dependents early
+ *   (with nine rows of bf16 x or more they are read afterwards).  A copy, or
+ *   mxfp8_b128_quantize_weights, directly ahead is in order; the outputs of
+ *   mxfp8_b128_silu_mul_quantize are not to be weights.
  */
 mxfp8_status mxfp8_b128_workspace_size(int64_t B, int64_t M, int64_t N, int64_t K, int x_is_quantized, size_t* bytes);
 mxfp8_status mxfp8_b128_linear(const void* x_bf16, const uint8_t* x_q, const float* x_scale, int64_t B, int64_t M,

@@ -211,10 +211,11 @@ def quantize_weights(w: torch.Tensor, fmt: str = "e4m3") -> tuple[torch.Tensor, 
 
 @dataclasses.dataclass
 class PackedWeights:
-    """Weights after the one-time repack (process_weights, process_weights_fp4):
-    element bytes and scale atoms.  A product may read these two before the
-    kernel ahead of it in the stream has finished, so they are not to be another
-    call's outputs (codes that a norm or activation wrote); every other input may."""
+    """Weights after the one-time repack (process_weights, process_weights_fp4) or as
+    they are (process_weights_fp8_128): element bytes and scale atoms or scales.  A
+    product may read these two before the kernel ahead of it in the stream has
+    finished, so they are not to be another call's outputs (codes that a norm or
+    activation wrote); every other input may."""
 
     w_packed: torch.Tensor   # uint8, B*N*K bytes (3BNK/4 for packed FP6, BNK/2 for FP4)
     sf_packed: torch.Tensor  # uint8, packed scale atoms
@@ -1083,7 +1084,12 @@ def linear_fp8_128(x: torch.Tensor, pw: PackedWeights, bias: torch.Tensor | None
     """FP8 linear layer with fp32 scales per block of 128 (weights from
     process_weights_fp8_128).  ``x`` is bf16 [..., K] (quantised inside the call
     as quantize_fp8_128 does), or with ``x_scale`` its codes and scales.  For
-    batched weights x is [B, M, K].  Returns bf16 [..., N]."""
+    batched weights x is [B, M, K].  Returns bf16 [..., N].
+
+    The weights may be read before the kernels ahead in the stream have finished
+    if those let later kernels start early, as most calls of this library do
+    (PackedWeights).  Weights that a copy or quantize_weights_fp8_128 has just
+    written are in order: neither does that."""
     if pw.fmt != "fp8_128":
         raise ValueError(f"linear_fp8_128 does not take {pw.fmt} weights")
     # one pass, few helper calls, as linear_fp4
