@@ -392,6 +392,13 @@ __device__ __forceinline__ void cluster_sync() {
 __device__ __forceinline__ void cluster_arrive_relaxed() {
   asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 }
+// The first half before exit, for a CTA whose signals to others have all been waited
+// for; after a wait that ran out, with a fence that orders them instead.
+__device__ __forceinline__ void cluster_arrive_last(bool gave_up) {
+  if (gave_up) asm volatile("fence.acq_rel.cluster;" ::: "memory");
+  __syncwarp();
+  cluster_arrive_relaxed();
+}
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 // Address of the same shared-memory location in CTA `rank` of the cluster.

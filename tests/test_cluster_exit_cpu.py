@@ -1,8 +1,8 @@
 """Signals to another CTA's barriers and the end of the kernel, by the text of the sources.
 
-A CTA's shared memory must not be signalled once it has left.  Arrivals on another CTA's barrier that
-this CTA does not wait for before it leaves are ordered by the cluster barrier at the end alone, and
-only by its releasing form."""
+A CTA's shared memory must not be signalled once it has left.  So either the cluster barrier before the end
+is the releasing one, which orders every signal ahead of it, or the CTA that is signalled has waited for the
+last of them (and the barrier has a fence for a kernel in which a wait ran out)."""
 
 import glob
 import os
@@ -30,11 +30,14 @@ def test_the_last_cluster_barrier_orders_the_signals(name):
     text = kernels_that_signal()[name]
     end = text[text.rindex(SIGNAL):]
     end = end[:end.index("tmem_dealloc_pair")]
-    last = max(end.rfind("cluster_arrive_relaxed();"), end.rfind("cluster_sync();"))
-    assert last >= 0, "no cluster barrier before the end"
-    # on pairs (the kernels that signal): a releasing barrier
-    pairs = re.search(r"if \(CG == 2\)\s*\{?\s*cluster_sync\(\);", end)
-    assert pairs or end.startswith("cluster_sync();", last), "the barrier before the end orders no signal"
+    halves = [m.group() for m in re.finditer(r"cluster_sync\(\);|cluster_arrive_\w+\([^;]*\);", end)]
+    assert halves, "no cluster barrier before the end"
+    if re.search(r"if \(CG == 2\)\s*\{?\s*cluster_sync\(\);", end) or halves[-1] == "cluster_sync();":
+        return  # releasing, on pairs at least (the kernels that signal)
+    assert halves[-1] == "cluster_arrive_last(*abort_flag);", "the barrier before the end orders no signal"
+    issuer = text[text.rindex("commit_pair_elected(elected, acc_full"):]
+    issuer = issuer[:issuer.index("__nanosleep")]
+    assert re.search(r"if \(ok &&[^;]*mbar_wait_warp\(acc_free,", issuer), "the last signals are not waited for"
 
 
 def test_some_kernels_signal():
