@@ -236,10 +236,10 @@ __global__ void __launch_bounds__(threads_of<FMT, CG, TN, kQuant>(), 1)
     }
     __syncwarp();
   };
-  // Without offsets the first round of weights needs nothing but this warp's barriers
-  // (one CTA a tile; on a pair, the other CTA's too).
+  // Without offsets (fp8_128 alone) the first round of weights needs nothing but this
+  // warp's barriers (one CTA a tile; on a pair, the other CTA's too).
   int early = 0;
-  if (CG == 1 && warp == 0 && a.offsets == nullptr && worker < unit_count<TN>(a, table)) {
+  if (!MX && CG == 1 && warp == 0 && a.offsets == nullptr && worker < unit_count<TN>(a, table)) {
     const Tile t = tile_of<STEP, TN>(worker, a, table);
     early = min(STAGES, kt1 - kt0);
     for (int s = 0; s < early; ++s) load_weights(s, kt0 + s, t);
@@ -924,6 +924,9 @@ int64_t grouped_max_tiles(int64_t E, int64_t R, bool ragged, int tn) {
 
 namespace {
 
+// The counts below are GB300's: 152 SMs, 76 pairs, the clusters that fit at once.  With
+// others the choice is slower, never wrong: no kernel needs its CTAs to run together
+// but for the clusters.
 // Estimated time of a shape on one CTA a tile with up to tn rows of x and K split s
 // ways, or on pairs (tn = 256), in 0.01 us.  Measured (us, fp8_128, weights from HBM;
 // the quantise kernel and the launches, 6 to 8, included): a stage of K takes 0.24 to
