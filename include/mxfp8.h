@@ -611,7 +611,8 @@ mxfp8_status mxfp8_b128_silu_mul_quantize(const void* gate_bf16, int64_t gate_st
  *   product's kernel quantises to the same bytes).
  *   N % 8 == 0, K % 16 == 0 (else MXFP8_ERR_UNSUPPORTED); pointers 16-byte
  *   aligned; M = 0 is a no-op.
- *   Sums within a block and over the blocks are fp32; one rounding, after the
+ *   Sums within a block and over the blocks are fp32, and so is the product
+ *   s_x s_w of a block, which has to lie in fp32's range; one rounding, after the
  *   bias.  Where K is split over CTAs their partial sums are added in the order
  *   of K: a call's result is the same every time.
  *   Stream ordering as mxfp8_linear: w and w_scale may be read before the

@@ -17,19 +17,19 @@
 // of a buffer into registers (its first half is added before the second has room)
 // and the way back to the MMA warp, ~0.85 us for two blocks, a little over what the
 // operands need from L2 (0.37 us a block) and the multiply-adds of two warps a
-// scheduler (~320 cycles).  M = 4096, N = 14336, K = 4096 166 us, 2.9 PFLOP/s, tensor
+// scheduler (~320 cycles).  M = 4096, N = 14336, K = 4096 168 us, 2.9 PFLOP/s, tensor
 // pipe 61 % busy (ncu), issue slots 57 %; 24576 rows on 61 of 64 experts of 4096 x
-// 2048 226 us: 16 blocks a tile, and a tile's start and output cost 1.3 us more.
+// 2048 229 us: 16 blocks a tile, and a tile's start and output cost 1.3 us more.
 // Steps, the first of those shapes: rows of x in lanes 231 -> scales loaded by the
 // thread that needs them 214 -> output through shared memory 210 -> no branch on the
 // tile in the loop 179 -> the wait for the next block after the additions 172 -> 64
 // columns at a time, the buffer given back before the last are added 166.  Not kept:
 // the columns as two MMAs of 128 with a barrier each, so that the two warps of a
-// scheduler come apart (273: such an MMA takes as long as one of 256); test_wait
-// spins (+0); the next tile's first scales before the output (+1 %); a group's last
+// scheduler come apart (273; what of it the narrower MMAs cost and what the second
+// barrier was not told apart); test_wait spins (+0); the next tile's first scales before the output (+1 %); a group's last
 // tile of up to 128 rows with the weights on the M side and its rows in as few columns
 // as hold them (64 groups of 272 rows, N = K = 2048, 115 instead of 119 us, of 384 rows
-// 143 instead of 120: the round of the two buffers stays, whatever the width).
+// 143 instead of 120).
 //
 // A cluster of two CTAs computes 256 rows x 256 weight rows with cta_group::2: CTA r
 // stages rows [128 r, +128) of both tiles and receives the sums of its rows of x.

@@ -9,10 +9,10 @@
 // Bound by reading x and writing the codes.  Sixteen elements a lane (32 bytes in,
 // 16 out: whole sectors), a block of 128 eight lanes, 512 elements a warp; one task a
 // warp, many warps.  (Two or four tasks a warp with their loads first are slower: 4096
-// x 14336 silu 52.4 us with one, 57.0 with two, both at six CTAs an SM; 16384 rows of
-// 4096 picked from 2048 tokens 30.3, 30.6 with two, 31.6 with four.  16384 x 4096
-// quantised 39.2 us, 5.2 TB/s: the issue slots are 85 % busy, 38.8 with CTAs of 128
-// threads, 40.8 of 512, 39.1 with fewer instructions a division or an index.)
+// x 14336 silu 52.4 us with one, 57.0 with two, both at six CTAs an SM; picked
+// rows +1 % with two, +4 % with four.  16384 x 4096 quantised 39.2 us, 5.2 TB/s: the issue
+// slots are 85 % busy, 38.8 with CTAs of 128 threads, 40.8 of 512, 39.1 with fewer
+// instructions a division or an index.)
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -157,8 +157,8 @@ __global__ void __launch_bounds__(THREADS) quantize_rows_kernel(const RowsArgs a
 }
 
 // Rows of codes and scale words picked by an index: where rows repeat, cheaper than
-// quantising each again (16384 rows of 4096 picked from 2048 tokens 27 us in one
-// step, 18 in two).  A warp a row, eight rows a CTA, whose words of a block of K are one
+// quantising each again (16384 rows of 4096 picked from 2048 tokens, MXFP8 28.0 us in one
+// step, 17.9 in two; fp8_128 36.6 and 18.9).  A warp a row, eight rows a CTA, whose words of a block of K are one
 // sector.  An index outside [0, T) gives a row of zeros with scales of zero.
 __global__ void __launch_bounds__(THREADS)
     gather_rows_kernel(const uint8_t* __restrict__ xq, const uint32_t* __restrict__ xs, const int* __restrict__ rows,
@@ -205,7 +205,8 @@ struct ActArgs {
 
 // y = gate / (1 + exp(-gate)) * up, quantised: the values of silu_mul_kernel
 // (fused_quant.cu), and in MXFP8 its bytes.  Eight CTAs an SM: 4096 x 14336 51.0 us, 53.3
-// with the six that 40 registers leave.
+// with the six that 40 registers leave (fp8_128 at 32 registers spills 8 bytes: in the
+// 51.0).
 template <int FMT>
 __global__ void __launch_bounds__(THREADS, 8) silu_mul_rows_kernel(const ActArgs a) {
   grid_dependency_wait();
