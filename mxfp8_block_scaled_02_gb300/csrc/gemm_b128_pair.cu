@@ -26,10 +26,10 @@
 // columns at a time, the buffer given back before the last are added 166.  Not kept:
 // the columns as two MMAs of 128 with a barrier each, so that the two warps of a
 // scheduler come apart (273; what of it the narrower MMAs cost and what the second
-// barrier was not told apart); test_wait spins (+0); the next tile's first scales before the output (+1 %); a group's last
-// tile of up to 128 rows with the weights on the M side and its rows in as few columns
-// as hold them (64 groups of 272 rows, N = K = 2048, 115 instead of 119 us, of 384 rows
-// 143 instead of 120).
+// barrier was not told apart); test_wait spins (+0); the next tile's first scales
+// before the output (+1 %); a group's last tile of up to 128 rows with the weights on
+// the M side and its rows in as few columns as hold them (64 groups of 272 rows, N = K =
+// 2048, 115 instead of 119 us, of 384 rows 143 instead of 120).
 //
 // A cluster of two CTAs computes 256 rows x 256 weight rows with cta_group::2: CTA r
 // stages rows [128 r, +128) of both tiles and receives the sums of its rows of x.

@@ -33,11 +33,12 @@
 // rows on 54 of 64 experts of 2048 x 4096 73 (6.4 TB/s of weights); 16384 rows on 13
 // of 16 experts of 4096 x 4096 185 with the repack of x's scale words (2.97 PFLOP/s;
 // 205 before the MMA warp waited for the operands itself and a second set of scale
-// warps took every other stage, 167 without the scales' tensor-memory stores).  fp8_128: eight rows on eight experts of
-// 2048 x 4096 15.7 (4.3 TB/s: 128 tiles on 152 SMs, and ~4 us of chain); one row, N =
-// K = 4096, bf16 x quantised inside 7.8 (8.6 with a warp a stage, which loaded x cold and
-// met the instruction cache's misses after the kernel before had ended), of which two
-// thirds are the chain from launch to the exchange.
+// warps took every other stage, 167 without the scales' tensor-memory stores).
+// fp8_128: eight rows on eight experts of 2048 x 4096 15.7 (4.3 TB/s: 128 tiles on 152
+// SMs, and ~4 us of chain); one row, N = K = 4096, bf16 x quantised inside 7.8 (8.6 with
+// a warp a stage, which loaded x cold and met the instruction cache's misses after the
+// kernel before had ended), of which two thirds are the chain from launch to the
+// exchange.
 //
 // Warps: 0 weight TMA (and, MXFP8, weight scales), 1 tensor-memory allocation and
 // MMA issue, 2 TMA of x, 3 the group table and the scales of fp8_128; MXFP8: 4..7

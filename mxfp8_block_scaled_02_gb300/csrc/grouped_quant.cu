@@ -157,9 +157,10 @@ __global__ void __launch_bounds__(THREADS) quantize_rows_kernel(const RowsArgs a
 }
 
 // Rows of codes and scale words picked by an index: where rows repeat, cheaper than
-// quantising each again (16384 rows of 4096 picked from 2048 tokens, MXFP8 28.0 us in one
-// step, 17.9 in two; fp8_128 36.6 and 18.9).  A warp a row, eight rows a CTA, whose words of a block of K are one
-// sector.  An index outside [0, T) gives a row of zeros with scales of zero.
+// quantising each again (16384 rows of 4096 picked from 2048 tokens, MXFP8 28.0 us in
+// one step, 17.9 in two; fp8_128 36.6 and 18.9).  A warp a row, eight rows a CTA, whose
+// words of a block of K are one sector.  An index outside [0, T) gives a row of zeros
+// with scales of zero.
 __global__ void __launch_bounds__(THREADS)
     gather_rows_kernel(const uint8_t* __restrict__ xq, const uint32_t* __restrict__ xs, const int* __restrict__ rows,
                        int64_t T, int64_t R, int64_t K, int KT, uint8_t* __restrict__ q, uint32_t* __restrict__ s) {
